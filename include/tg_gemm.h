@@ -20,9 +20,9 @@
  * device.  The caller owns all three buffers and the library keeps no
  * pointer to them after a call returns.  No call allocates or frees device
  * memory at run time.  Scratch memory comes from two places:
- *   - the caller: tg_gemm_relu_f16_ws, tg_gemm_relu_f16_ex and
- *     tg_gemm_relu_w4a16 take an optional (or, for some layouts, required)
- *     workspace pointer and size;
+ *   - the caller: tg_gemm_relu_f16_ws, tg_gemm_relu_f16_ex,
+ *     tg_gemm_relu_w4a16, tg_gated and tg_gated_backward take an optional (or,
+ *     for some layouts, required) workspace pointer and size;
  *   - one fixed module buffer of TG_STATIC_WORKSPACE_BYTES (16 MiB) that the
  *     library holds on every GPU where it is loaded, until the process
  *     exits; only tg_gemm_relu_f16_static_ws uses it.
@@ -427,6 +427,115 @@ TG_API int64_t tg_w4a16_workspace_size(int64_t M, int64_t N, int64_t K, int32_t 
  * above.  Same requirements on Wq, scales, K and group. */
 TG_API tg_status tg_dequant_w4_f16(const void *Wq, const void *scales, void *W, int64_t N, int64_t K,
                                    int32_t group, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Gated feed-forward block
+ *
+ *   G = X . Wg^T,  U = X . Wu^T,  H = act(G) * U            (tg_gated)
+ *   dG = dH * U * act'(G),  dU = dH * act(G),
+ *   dX = dG . Wg + dU . Wu,  dWg = dG^T . X,  dWu = dU^T . X  (tg_gated_backward)
+ *
+ * X: M x K.  Wg, Wu: N x K, as a linear layer stores its weight (the two
+ * halves of one 2N x K matrix, or two matrices).  H, G, U, dH: M x N.  All are
+ * 16-bit floats of one type (options->type), row-major with row strides of
+ * their own, on any 2-byte boundary.  act: TG_ACT_RELU (max(g, 0); values that
+ * are not > 0, NaN among them, give +0 and slope 0), TG_ACT_SILU
+ * (g / (1 + exp(-g))) or TG_ACT_GELU (the tanh form,
+ * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))).
+ *
+ * Sums, activations and products are fp32; every result is rounded once to
+ * the 16-bit type (nearest even).  One kernel computes both projections, the
+ * activation and the product; with G and U given (both or neither) it stores
+ * them too, rounded to the 16-bit type, which is what the backward pass reads.
+ * The backward pass rounds dG and dU to the 16-bit type before the products.
+ * Results do not depend on timing: equal inputs give equal bits.
+ *
+ * Sizes: each in [0, 2^30].  M == 0 or N == 0: nothing is enqueued by the
+ * forward; a gradient that is a sum over nothing is set to +0.  K == 0 sets H
+ * (and G, U) to +0.  Bytes between a row's end and the next row are not
+ * written.  No result may overlap an input or another result.
+ *
+ * Workspace (256-byte aligned, overlapping nothing, free to reuse once the
+ * call's work on `stream` is done): the forward needs it only where TMA cannot
+ * describe an operand (a row stride or base off 16 bytes), for padded copies;
+ * the backward for dG and dU as well.  The size functions tell how much; with
+ * less, TG_ERR_INVALID_ARG.  Two calls whose work may overlap need two
+ * workspaces.
+ * ------------------------------------------------------------------------- */
+enum { TG_TYPE_F16 = 0, TG_TYPE_BF16 = 1 };
+enum { TG_ACT_RELU = 0, TG_ACT_SILU = 1, TG_ACT_GELU = 2 };
+
+/* A zero-initialised value (or NULL): fp16, ReLU, dense rows. */
+typedef struct tg_gated_options {
+    int32_t type;       /* TG_TYPE_F16 or TG_TYPE_BF16                            */
+    int32_t act;        /* TG_ACT_*                                              */
+    int64_t ldx;        /* elements between rows of X; 0 = dense, here and below  */
+    int64_t ldwg, ldwu; /* of Wg and Wu                                          */
+    int64_t ldh;        /* of H (backward: of dH)                                */
+    int64_t ldg, ldu;   /* of G and U                                            */
+    int64_t lddx, lddwg, lddwu; /* of the gradients (backward only)              */
+    int64_t reserved;   /* must be 0                                             */
+} tg_gated_options;
+
+TG_API tg_status tg_gated(const void *X, const void *Wg, const void *Wu, void *H, void *G, void *U, int64_t M,
+                          int64_t N, int64_t K, const tg_gated_options *options, void *stream, void *workspace,
+                          int64_t workspace_bytes);
+
+/* Workspace bytes tg_gated needs (usually 0), or -1 for invalid arguments.
+ * Host logic only. */
+TG_API int64_t tg_gated_workspace_size(const void *X, const void *Wg, const void *Wu, int64_t M, int64_t N, int64_t K,
+                                       const tg_gated_options *options);
+
+/* Any of dX, dWg and dWu may be NULL: it is not computed. */
+TG_API tg_status tg_gated_backward(const void *dH, const void *X, const void *Wg, const void *Wu, const void *G,
+                                   const void *U, void *dX, void *dWg, void *dWu, int64_t M, int64_t N, int64_t K,
+                                   const tg_gated_options *options, void *stream, void *workspace,
+                                   int64_t workspace_bytes);
+
+/* Workspace bytes tg_gated_backward needs for the gradients that are not
+ * NULL, or -1 for invalid arguments.  Host logic only. */
+TG_API int64_t tg_gated_backward_workspace_size(const void *X, const void *Wg, const void *Wu, const void *dX,
+                                                const void *dWg, const void *dWu, int64_t M, int64_t N, int64_t K,
+                                                const tg_gated_options *options);
+
+/* ---------------------------------------------------------------------------
+ * 8-bit integer products with a scale for each token and channel
+ *
+ * tg_quantize_rows_i8, for each row m of X (M x K, 16-bit floats of `type`, row
+ * stride ldx, any 2-byte boundary):
+ *   scale[m] = max_k |x(m,k)| / 127             (one IEEE fp32 division)
+ *   q(m,k)   = x(m,k) / scale[m] to the nearest integer, ties to even
+ * exactly, so |q| <= 127.  A row of zeros gives scale 0 and codes 0.  A row
+ * that holds an infinity or a NaN gives scale NaN and codes 0, so products
+ * with it are NaN in that row alone.  Q: M x K signed bytes, row stride ldq.
+ * It serves activations (rows are tokens) and weights (rows are channels).
+ *
+ * tg_gemm_i8:  C(m,n) = [relu]( (sum_k a(m,k) w(n,k)) * a_scale[m] * w_scale[n] + bias[n] )
+ * tg_gated_i8: H = act(G) * U with G and U so scaled from Wg and Wu (no bias)
+ *
+ * A: M x K and W: N x K signed bytes (any value, -128 included); rows start on
+ * 16-byte boundaries: a 16-byte aligned base and a row stride (lda, ldw; 0 =
+ * dense) that is a multiple of 16, whatever K is.  The sums are exact 32-bit
+ * integers (K <= 131071), rounded to fp32, multiplied by the row's and then
+ * the column's scale in fp32, rounded once to `type` after bias and ReLU.
+ * scales: fp32, 4-byte aligned.  bias: N values of `type`, or NULL.  C, H: M x N
+ * of `type`, row stride ldc (ldh), any 2-byte boundary.  Of tg_gated_options,
+ * tg_gated_i8 reads type (of H), act, ldx (of A), ldwg, ldwu and ldh.
+ * Sizes in [0, 2^30].  M == 0 or N == 0: nothing enqueued.  K == 0: the sums
+ * are 0.  No workspace; no result may overlap an input.
+ * Strides of 0 mean dense rows.  Errors: TG_ERR_INVALID_ARG as above,
+ * TG_ERR_UNSUPPORTED_DEVICE, TG_ERR_LAUNCH.
+ * ------------------------------------------------------------------------- */
+TG_API tg_status tg_quantize_rows_i8(const void *X, void *Q, float *scales, int64_t M, int64_t K, int64_t ldx,
+                                     int64_t ldq, int32_t type, void *stream);
+
+TG_API tg_status tg_gemm_i8(const void *A, const float *a_scale, const void *W, const float *w_scale, const void *bias,
+                            void *C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw, int64_t ldc,
+                            int32_t relu, int32_t type, void *stream);
+
+TG_API tg_status tg_gated_i8(const void *A, const float *a_scale, const void *Wg, const float *g_scale, const void *Wu,
+                             const float *u_scale, void *H, int64_t M, int64_t N, int64_t K,
+                             const tg_gated_options *options, void *stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,139 @@
+// ff_ops.cuh -- what the feed-forward kernels share: the 16-bit float and
+// 8-bit integer tcgen05 MMAs, the activations with their slopes, and the
+// rounding of fp32 results to either 16-bit type.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "ptx.cuh"
+
+namespace tg {
+
+// Operand kinds of the feed-forward kernels.  Both move 128 bytes of K per
+// k-block and 32 bytes of K per MMA, so they share every byte offset.
+enum { kFfF16 = 0, kFfI8 = 1 };
+
+// Activations of the gated block (the values of TG_ACT_*).
+enum { kActRelu = 0, kActSilu = 1, kActGelu = 2 };
+
+// D[tmem] (+)= A[smem desc] * B[smem desc] on a CTA pair: 16-bit floats into
+// fp32, or signed 8-bit integers into 32-bit integers.
+template <int KIND>
+__device__ __forceinline__ void umma_ff_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  if (KIND == kFfF16) {
+    umma_f16_ss_pair(d_tmem, a_desc, b_desc, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// The same on one CTA.
+template <int KIND>
+__device__ __forceinline__ void umma_ff(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (KIND == kFfF16) {
+    umma_f16_ss(d_tmem, a_desc, b_desc, idesc, accumulate);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  }
+}
+
+// Instruction descriptor: bits 4-5 D format (1 = f32, 2 = s32); bits 7-9 /
+// 10-12 A / B format (kind::f16: 0 = f16, 1 = bf16, the same for both;
+// kind::i8: 1 = signed); bit 15 / 16 A / B major-ness (0 = K-major, 1 =
+// MN-major, 16-bit operands only); bits 17-22 N >> 3; bits 24-28 M >> 4.
+inline uint32_t make_idesc_ff(int kind, bool bf16, int M, int N, bool a_mn_major, bool b_mn_major) {
+  const uint32_t d = kind == kFfI8 ? 2u : 1u;
+  const uint32_t f = kind == kFfI8 ? 1u : (bf16 ? 1u : 0u);
+  return (d << 4) | (f << 7) | (f << 10) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// ----------------------------------------------------------------------------
+// Activations, in fp32
+// ----------------------------------------------------------------------------
+// Both smooth activations are g * s(z) with the logistic function s: z = g
+// for silu, and for gelu (tanh form) z = 2 sqrt(2/pi) (g + 0.044715 g^3),
+// since (1 + tanh(y)) / 2 = s(2y).  exp(-z) overflows to +inf for z below
+// about -88, where s is 0 to within 3e-39.  The fast exponential and division
+// are good to a few parts in 2^22, far below half a step of a 16-bit result.
+constexpr float kGeluC1 = 1.5957691216057308f;   // 2 sqrt(2/pi)
+constexpr float kGeluC3 = 0.07135481282553557f;  // 2 sqrt(2/pi) 0.044715
+
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+
+template <int ACT>
+__device__ __forceinline__ float act_value(float g) {
+  if (ACT == kActRelu) return g > 0.0f ? g : 0.0f;
+  if (ACT == kActSilu) return g * logistic(g);
+  return g * logistic(g * fmaf(kGeluC3, g * g, kGeluC1));
+}
+
+// act(g) and its derivative: with p = s(z), act = g p and act' = p + g p (1 - p) z'.
+template <int ACT>
+__device__ __forceinline__ void act_value_slope(float g, float& value, float& slope) {
+  if (ACT == kActRelu) {
+    value = g > 0.0f ? g : 0.0f;
+    slope = g > 0.0f ? 1.0f : 0.0f;
+  } else {
+    const float g2 = g * g;
+    const float p = logistic(ACT == kActSilu ? g : g * fmaf(kGeluC3, g2, kGeluC1));
+    value = g * p;
+    const float dz = ACT == kActSilu ? 1.0f : fmaf(3.0f * kGeluC3, g2, kGeluC1);
+    // For gelu dz grows with g^2; where p is exactly 0 or 1 the term is 0.
+    const float q = p * (1.0f - p);
+    slope = q == 0.0f ? p : fmaf(value * (1.0f - p), dz, p);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// 16-bit results
+// ----------------------------------------------------------------------------
+// Two fp32 values rounded (nearest even) to fp16 or bf16 and packed, the
+// first in the low half.
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Two packed 16-bit values as fp32.
+__device__ __forceinline__ float2 unpack_16(uint32_t w, bool bf16) {
+  if (bf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+__device__ __forceinline__ float load_16(const unsigned short* p, bool bf16) {
+  const unsigned short v = __ldg(p);
+  return bf16 ? __uint_as_float(static_cast<uint32_t>(v) << 16) : __half2float(__ushort_as_half(v));
+}
+__device__ __forceinline__ unsigned short round_16(float x, bool bf16) {
+  return static_cast<unsigned short>((bf16 ? pack_bf16(x, 0.0f) : pack_f16(x, 0.0f)) & 0xffffu);
+}
+
+// N fp32 values of one row as packed 16-bit pairs.
+template <int N>
+__device__ __forceinline__ void pack_row(const float (&v)[N], uint32_t* h, bool bf16) {
+  if (bf16) {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) h[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) h[e] = pack_f16(v[2 * e], v[2 * e + 1]);
+  }
+}
+
+}  // namespace tg

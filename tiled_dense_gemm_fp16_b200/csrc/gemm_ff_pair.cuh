@@ -1,0 +1,467 @@
+// gemm_ff_pair.cuh -- the products of a feed-forward block on CTA pairs
+// (cta_group::2): one persistent tcgen05 kernel for
+//   * the gated forward  H = act(X Wg^T) * (X Wu^T), 16-bit or 8-bit operands,
+//     both projections, the activation and the product in one pass, G and U
+//     stored too on request (for the backward pass);
+//   * its gradients: dX = dG Wg + dU Wu as one K loop over both sources, and
+//     dWg = dG^T X, dWu = dU^T X as one grid over both results;
+//   * the 8-bit product C = (A W^T) sa sw + bias with an optional ReLU.
+//
+// The pipeline is that of the fp16 pair kernel: both CTAs load their half of a
+// 256 x BN tile by TMA into an mbarrier ring (128-byte swizzle, 128 bytes of K
+// per k-block), the even CTA's MMA thread issues 256 x 256 MMAs over both SMs'
+// shared memory, eight epilogue warps per CTA drain TMEM.
+//
+// Gated tiles: of every 256 accumulator columns each CTA supplies the B rows
+// of 128, and these are 64 rows of Wg followed by the same 64 rows of Wu.  So
+// one MMA computes both projections of 128 block columns, the same thread of
+// an epilogue warp reads G and U of an element, and neither leaves the SM.  A
+// 256 x BN accumulator gives 256 x BN / 2 values of H; per SM and k-block it
+// moves what the plain product moves.
+//
+// An epilogue warp first turns all its accumulator columns into packed 16-bit
+// results in registers, then frees the accumulator, then stores: TMA boxes
+// where rows of the result start on 16-byte boundaries, else through the same
+// staging boxes row by row, 64 bytes per store instruction.  Stored G and U
+// (twice the registers) leave during the drain.
+#pragma once
+
+#include "ff_ops.cuh"
+#include "gemm_tc_pair.cuh"
+
+namespace tg {
+
+struct FfMaps {
+  CUtensorMap a[2];  // sources along K (dX) or along the rows of the result (dWg, dWu)
+  CUtensorMap b[2];  // gate and up weights, or sources along K
+  CUtensorMap c[3];  // H, G, U; or the results of the two row sources
+};
+
+struct FfParams {
+  void* c[3];
+  int64_t ldc[3];
+  const float* row_scale;     // 8-bit: one per row of A
+  const float* col_scale[2];  // 8-bit: one per row of the (gate, up) weight
+  const void* bias;           // 16-bit values of the result's type, or nullptr
+  int M, N;                   // rows and columns of one result
+  int m_tiles, n_tiles, num_tiles;  // m_tiles over all row sources
+  int m_tiles_src;            // row tiles of one row source
+  int k_blocks, k_blocks_src; // k-blocks over all K sources, and of one
+  int group_m;
+  int a_mnmajor, b_kmajor;
+  int bf16;                   // type of the 16-bit results (and operands)
+  int act, relu;
+  int save;                   // gated: store G and U
+  int c_aligned[3];           // rows of the result start on 16-byte boundaries
+  int l2_hints;               // as TcParams
+  uint32_t idesc;
+  uint64_t wait_budget_ns;
+};
+
+template <int STAGES_, int BN_>
+struct FfPairCfg {
+  static constexpr int BM = 128;
+  static constexpr int PAIR_M = 256;
+  static constexpr int BN = BN_;             // accumulator columns per tile
+  static constexpr int SLABS = BN / 256;
+  static constexpr int STAGES = STAGES_;
+  static constexpr int MMA_WARP = 1;
+  static constexpr int EPI_WARP0 = 2;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int EPI_COLS = BN / 2;    // accumulator columns per epilogue warp
+  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+  static constexpr int K_BYTES = 128;        // bytes of K per k-block
+  static constexpr int A_BYTES = BM * K_BYTES;
+  static constexpr int B_BYTES = (BN / 2) * K_BYTES;
+  static constexpr int HALF_BYTES = 64 * K_BYTES;     // 64 rows (K-major) or one 64-column panel (MN-major)
+  static constexpr int B_SLAB_BYTES = 2 * HALF_BYTES;
+  static constexpr int NUM_ACC = (BN == 256) ? 2 : 1;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int C_BUF_BYTES = 32 * 64;         // one 32 x 32 box of 16-bit values
+  static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * C_BUF_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + C_STAGE_BYTES + BAR_BYTES;
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per CTA");
+  static_assert(NUM_ACC * BN <= TMEM_COLS, "TMEM columns");
+};
+
+__device__ __forceinline__ void ff_tile_coords(const FfParams& p, int t, int& m_blk, int& n_blk) {
+  const int group_tiles = p.group_m * p.n_tiles;
+  const int g = t / group_tiles;
+  const int first_m = g * p.group_m;
+  const int gm = min(p.m_tiles - first_m, p.group_m);
+  const int local = t - g * group_tiles;
+  m_blk = first_m + local % gm;
+  n_blk = local / gm;
+}
+
+// Scales of 16 consecutive columns (0 past N).
+__device__ __forceinline__ void load_scale16(const float* scale, int col, int N, float (&s)[16]) {
+  const float* src = scale + col;
+  if (col + 16 <= N && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(src) + q);
+      s[4 * q] = v.x;
+      s[4 * q + 1] = v.y;
+      s[4 * q + 2] = v.z;
+      s[4 * q + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = col + e < N ? __ldg(src + e) : 0.0f;
+  }
+}
+
+// 16 accumulator words as fp32: the fp32 sums themselves, or the 32-bit
+// integer sums (one rounding to fp32) times the row's and column's scale.
+template <int KIND>
+__device__ __forceinline__ void ff_values(const uint32_t (&r)[16], float row_scale, const float* col_scale, int col,
+                                          int N, float (&v)[16]) {
+  if (KIND == kFfF16) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(r[e]);
+  } else {
+    float s[16];
+    load_scale16(col_scale, col, N, s);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = __int2float_rn(static_cast<int>(r[e])) * row_scale * s[e];
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void gate_row(float (&g)[16], const float (&u)[16]) {
+#pragma unroll
+  for (int e = 0; e < 16; ++e) g[e] = act_value<ACT>(g[e]) * u[e];
+}
+
+// One 32 x 32 box of a result: lane = row, h = its 32 packed values.  `buf`
+// is one of the warp's two staging boxes (64-byte swizzle), used in turn.
+__device__ __forceinline__ void ff_store_box(const CUtensorMap* map, void* c, int64_t ldc, bool aligned, int M, int N,
+                                             int y0, int col0, const uint32_t* h, uint8_t* buf, int lane,
+                                             uint64_t policy) {
+  if (lane == 0) bulk_wait_group_read<1>();  // the box stored two turns ago has been read
+  __syncwarp();
+  const uint32_t row_addr = smem_u32(buf) + lane * 64;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(row_addr + ((q ^ ((lane >> 1) & 3)) << 4), h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+  if (aligned) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_2d_hint(map, buf, col0, y0, policy);
+      bulk_commit_group();
+    }
+  } else {
+    // Rows on any 2-byte boundary: lane = column, one row per store.
+    __syncwarp();
+    unsigned short* dst = static_cast<unsigned short*>(c) + static_cast<int64_t>(y0) * ldc + col0 + lane;
+    const int rows = min(32, M - y0);
+    const bool col_ok = col0 + lane < N;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      const unsigned short v = *reinterpret_cast<const unsigned short*>(
+          buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+      if (r < rows && col_ok) dst[static_cast<int64_t>(r) * ldc] = v;
+    }
+    if (lane == 0) bulk_commit_group();  // an empty group, so that the wait above counts boxes
+    __syncwarp();
+  }
+}
+
+template <int STAGES, int BN, int KIND, bool GATED>
+__global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
+    ff_pair_kernel(const __grid_constant__ FfMaps maps, const FfParams p) {
+  using Cfg = FfPairCfg<STAGES, BN>;
+  constexpr int K_ELEMS = KIND == kFfI8 ? 128 : 64;   // elements of K per k-block
+  constexpr int TILE_N = GATED ? BN / 2 : BN;         // result columns per tile
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_smem = smem;
+  uint8_t* b_smem = smem + Cfg::STAGES * Cfg::A_BYTES;
+  uint8_t* c_stage = smem + Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(c_stage + Cfg::C_STAGE_BYTES);
+  uint64_t* full_bar = bars;                              // used in the even CTA
+  uint64_t* empty_bar = bars + Cfg::STAGES;               // per CTA
+  uint64_t* acc_full_bar = bars + 2 * Cfg::STAGES;        // per CTA
+  uint64_t* acc_empty_bar = acc_full_bar + Cfg::NUM_ACC;  // used in the even CTA
+  uint64_t* mma_done_bar = acc_empty_bar + Cfg::NUM_ACC;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < Cfg::NUM_ACC; ++b) {
+      mbar_init(&acc_full_bar[b], 1);
+      mbar_init(&acc_empty_bar[b], 2 * Cfg::EPI_WARPS);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+    if (GATED) tma_prefetch_desc(&maps.b[1]);
+    if (p.c_aligned[0]) tma_prefetch_desc(&maps.c[0]);
+  }
+  if (warp == Cfg::MMA_WARP) {
+    tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+    tmem_relinquish_alloc_permit_pair();
+  }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote use
+  tcgen05_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    // Producer (both CTAs): this CTA's half of the A and B tiles.
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_parity[Cfg::STAGES];
+#pragma unroll
+      for (int s = 0; s < Cfg::STAGES; ++s) last_parity[s] = -1;
+      bool ok = true;
+      const uint64_t pol_a = (p.l2_hints & 1) ? l2_policy_evict_last() : l2_policy_evict_normal();
+      const uint64_t pol_b = (p.l2_hints & 2)   ? l2_policy_evict_last()
+                             : (p.l2_hints & 4) ? l2_policy_evict_first()
+                                                : l2_policy_evict_normal();
+      for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
+        int m_blk, n_blk;
+        ff_tile_coords(p, t, m_blk, n_blk);
+        const int row_src = m_blk >= p.m_tiles_src ? 1 : 0;
+        const int m0 = (m_blk - row_src * p.m_tiles_src) * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
+        const int n0 = n_blk * TILE_N + static_cast<int>(rank) * (GATED ? 64 : 128);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0x81)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_even = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (Cfg::A_BYTES + Cfg::B_BYTES));
+          const int k_src = kb >= p.k_blocks_src ? 1 : 0;
+          const int k0 = (kb - k_src * p.k_blocks_src) * K_ELEMS;
+          const CUtensorMap* ma = &maps.a[row_src | k_src];
+          uint8_t* adst = a_smem + stage * Cfg::A_BYTES;
+          uint8_t* bdst = b_smem + stage * Cfg::B_BYTES;
+          if (KIND == kFfF16 && p.a_mnmajor) {
+            // A stored K x M: this CTA's 128 rows as two 64 m x 64 k boxes.
+            tma_load_2d_pair_hint(adst, ma, full_even, m0, k0, pol_a);
+            tma_load_2d_pair_hint(adst + Cfg::HALF_BYTES, ma, full_even, m0 + 64, k0, pol_a);
+          } else {
+            tma_load_2d_pair_hint(adst, ma, full_even, k0, m0, pol_a);
+          }
+#pragma unroll
+          for (int j = 0; j < Cfg::SLABS; ++j) {
+            uint8_t* slab = bdst + j * Cfg::B_SLAB_BYTES;
+            if (GATED) {
+              // 64 rows of Wg, then the same 64 rows of Wu.
+              tma_load_2d_pair_hint(slab, &maps.b[0], full_even, k0, n0 + 128 * j, pol_b);
+              tma_load_2d_pair_hint(slab + Cfg::HALF_BYTES, &maps.b[1], full_even, k0, n0 + 128 * j, pol_b);
+            } else if (KIND == kFfI8 || p.b_kmajor) {
+              tma_load_2d_pair_hint(slab, &maps.b[k_src], full_even, k0, n0 + 256 * j, pol_b);
+            } else {
+              tma_load_2d_pair_hint(slab, &maps.b[k_src], full_even, n0 + 256 * j, k0, pol_b);
+              tma_load_2d_pair_hint(slab + Cfg::HALF_BYTES, &maps.b[k_src], full_even, n0 + 256 * j + 64, k0, pol_b);
+            }
+          }
+          last_parity[stage] = static_cast<int>(phase);
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // The even CTA's full barriers count both CTAs' bytes: once they have
+      // completed, every load of the pair has landed.
+      if (leader) {
+#pragma unroll 1
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+          if (last_parity[s] >= 0) {
+            volatile int no_abort = 0;
+            mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.wait_budget_ns, 0x82);
+          }
+        }
+      }
+    }
+  } else if (warp == Cfg::MMA_WARP) {
+    // MMA issuer (even CTA only).
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true;
+      const bool a_mn = KIND == kFfF16 && p.a_mnmajor != 0;
+      const bool b_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
+      for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters, ++local) {
+        const int acc = local % Cfg::NUM_ACC;
+        const uint32_t acc_phase = (local / Cfg::NUM_ACC) & 1;
+        if (!mbar_wait(&acc_empty_bar[acc], acc_phase ^ 1u, abort_flag, p.wait_budget_ns, 0x83)) break;
+        tcgen05_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + acc * Cfg::BN;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0x84)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after_sync();
+          const uint32_t a_addr = smem_u32(a_smem + stage * Cfg::A_BYTES);
+          const uint32_t b_addr = smem_u32(b_smem + stage * Cfg::B_BYTES);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
+            const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                        : make_sw128_desc(a_addr + k * 32, 16, 1024);
+#pragma unroll
+            for (int j = 0; j < Cfg::SLABS; ++j) {
+              const uint32_t slab_addr = b_addr + j * Cfg::B_SLAB_BYTES;
+              const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                          : make_sw128_desc(slab_addr + k * 32, 16, 1024);
+              umma_ff_pair<KIND>(d_tmem + 256 * j, adesc, bdesc, p.idesc, (kb | k) != 0 ? 1u : 0u);
+            }
+          }
+          umma_commit_pair_mc(&empty_bar[stage], 0x3);  // both CTAs may refill this stage
+          if (++stage == Cfg::STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
+      }
+      umma_commit_pair_mc(mma_done_bar, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0x85);
+    }
+    __syncwarp();
+  } else {
+    // Epilogue (both CTAs): warp w takes TMEM lanes 32 (w mod 4) .. + 31 and
+    // half `part` of the accumulator's columns.
+    const int quad = warp & 3;
+    const int part = (warp - Cfg::EPI_WARP0) >> 2;
+    constexpr int OUT = GATED ? Cfg::EPI_COLS / 2 : Cfg::EPI_COLS;  // result columns of this warp
+    uint8_t* wbuf = c_stage + (warp - Cfg::EPI_WARP0) * 2 * Cfg::C_BUF_BYTES;
+    const uint64_t pol = l2_policy_evict_first();
+    int local = 0;
+    int turn = 0;  // which staging box comes next
+    for (int t = cluster_id; t < p.num_tiles; t += num_clusters, ++local) {
+      int m_blk, n_blk;
+      ff_tile_coords(p, t, m_blk, n_blk);
+      const int row_src = m_blk >= p.m_tiles_src ? 1 : 0;
+      const int acc = local % Cfg::NUM_ACC;
+      const uint32_t acc_phase = (local / Cfg::NUM_ACC) & 1;
+      const int y0 =
+          (m_blk - row_src * p.m_tiles_src) * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM + quad * 32;
+      const int out0 = n_blk * TILE_N + part * OUT;
+      float row_scale = 0.0f;
+      if (KIND == kFfI8 && y0 + lane < p.M) row_scale = __ldg(p.row_scale + y0 + lane);
+      const bool ready = mbar_wait(&acc_full_bar[acc], acc_phase, abort_flag, p.wait_budget_ns, 0x86);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tcgen05_fence_after_sync();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::BN;
+      const bool rows_live = y0 < p.M;
+      uint32_t h[OUT / 2];
+#pragma unroll
+      for (int c = 0; c < OUT / 32; ++c) {
+        const int col0 = out0 + c * 32;
+        if (GATED) {
+          // Result column o of the tile: gate at accumulator column
+          // 128 (o / 64) + o mod 64, up 64 columns further.
+          const int o = part * OUT + c * 32;
+          const uint32_t gaddr = taddr + (o >> 6) * 128 + (o & 63);
+          const bool save = KIND == kFfF16 && p.save && rows_live && col0 < p.N;
+          uint32_t hg[16], hu[16];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t rg[16], ru[16];
+            tmem_ld_32x32b_x16(gaddr + b * 16, rg);
+            tmem_ld_32x32b_x16(gaddr + 64 + b * 16, ru);
+            tmem_ld_wait();
+            float g[16], u[16];
+            ff_values<KIND>(rg, row_scale, p.col_scale[0], col0 + b * 16, p.N, g);
+            ff_values<KIND>(ru, row_scale, p.col_scale[1], col0 + b * 16, p.N, u);
+            if (save) {
+              pack_row<16>(g, hg + b * 8, p.bf16 != 0);
+              pack_row<16>(u, hu + b * 8, p.bf16 != 0);
+            }
+            if (p.act == kActSilu)
+              gate_row<kActSilu>(g, u);
+            else if (p.act == kActGelu)
+              gate_row<kActGelu>(g, u);
+            else
+              gate_row<kActRelu>(g, u);
+            pack_row<16>(g, h + c * 16 + b * 8, p.bf16 != 0);
+          }
+          if (save) {
+            ff_store_box(&maps.c[1], p.c[1], p.ldc[1], p.c_aligned[1] != 0, p.M, p.N, y0, col0, hg,
+                         wbuf + (turn & 1) * Cfg::C_BUF_BYTES, lane, pol);
+            ff_store_box(&maps.c[2], p.c[2], p.ldc[2], p.c_aligned[2] != 0, p.M, p.N, y0, col0, hu,
+                         wbuf + ((turn + 1) & 1) * Cfg::C_BUF_BYTES, lane, pol);
+            turn += 2;
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(taddr + part * OUT + c * 32 + b * 16, r);
+            tmem_ld_wait();
+            const int col = col0 + b * 16;
+            float v[16];
+            ff_values<KIND>(r, row_scale, p.col_scale[0], col, p.N, v);
+            if (KIND == kFfI8) {
+              if (p.bias != nullptr) {
+                const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + col;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if (col + e < p.N) v[e] += load_16(b16 + e, p.bf16 != 0);
+              }
+              if (p.relu) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = v[e] > 0.0f ? v[e] : 0.0f;
+              }
+            }
+            pack_row<16>(v, h + c * 16 + b * 8, p.bf16 != 0);
+          }
+        }
+      }
+      tcgen05_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty_bar[acc]), 0));
+      if (rows_live) {
+        const int ci = GATED ? 0 : row_src;
+#pragma unroll
+        for (int c = 0; c < OUT / 32; ++c) {
+          const int col0 = out0 + c * 32;
+          if (col0 < p.N) {
+            ff_store_box(&maps.c[ci], p.c[ci], p.ldc[ci], p.c_aligned[ci] != 0, p.M, p.N, y0, col0, h + c * 16,
+                         wbuf + (turn & 1) * Cfg::C_BUF_BYTES, lane, pol);
+            ++turn;
+          }
+        }
+      }
+    }
+  }
+
+  if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait_group<0>();  // the results are written
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the pair is done with each other's shared memory and barriers
+  if (warp == Cfg::MMA_WARP) {
+    tcgen05_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace tg

@@ -1,0 +1,311 @@
+// gemm_ff_skinny.cuh -- the same products for few rows (M <= 256): a step is
+// bound by streaming the weights from HBM once, so the kernel computes the
+// transposed result (the weight's rows fill the 128-row MMA side, the padded M
+// is the MMA's N) and splits K over a cluster of S CTAs, as the fp16 small-M
+// kernel does.
+//   * Gated: a panel is 64 rows of Wg and the same 64 rows of Wu, so both
+//     projections of 64 block columns meet in one accumulator.
+//   * Plain: a panel is 128 rows of W (K-major), or, for dX = dG Wg + dU Wu,
+//     128 columns of Wg and then of Wu (stored K x N, MN-major) with the K
+//     loop over both sources.
+// Each CTA moves its partial (fp32, or 32-bit integers) to shared memory; after
+// a cluster barrier every CTA adds a share of the panel's outputs over the S
+// partials in rank order, so results do not depend on timing.
+#pragma once
+
+#include "ff_ops.cuh"
+#include "gemm_ff_pair.cuh"
+
+namespace tg {
+
+struct FfSkinnyParams {
+  void* c[3];                 // H, G, U; or the one result
+  int64_t ldc[3];
+  int c_aligned[3];           // rows of the result start on 8-byte boundaries
+  const float* row_scale;
+  const float* col_scale[2];
+  const void* bias;
+  int M, N;
+  int m_pad;                  // M rounded up to a multiple of 16
+  int k_blocks, k_blocks_src;
+  int splits, stages;
+  uint32_t a_stage_bytes;     // m_pad * 128
+  uint32_t tmem_cols;
+  uint32_t idesc;
+  int b_kmajor;
+  int bf16, act, relu, save;
+  uint64_t wait_budget_ns;
+};
+
+struct FfSkinnyCfg {
+  static constexpr int PANEL = 128;                    // weight rows per panel
+  static constexpr int W_STAGE_BYTES = PANEL * 128;    // 16 KiB
+  static constexpr int HALF_BYTES = W_STAGE_BYTES / 2;
+  static constexpr int EPI_WARP0 = 2;
+  static constexpr int THREADS = 192;
+  static constexpr int MAX_STAGES = 8;
+  static constexpr int BAR_BYTES = 256;
+  static int stage_bytes(int m_pad) { return W_STAGE_BYTES + m_pad * 128; }
+  static int smem_bytes(int m_pad, int stages) { return 1024 + stages * stage_bytes(m_pad) + BAR_BYTES; }
+};
+
+// Four results of one row, from column n on.
+__device__ __forceinline__ void ff_store4(void* c, int64_t ldc, bool aligned, int m, int n, int N, const float (&v)[4],
+                                          bool bf16) {
+  uint32_t w[2];
+  pack_row<4>(v, w, bf16);
+  unsigned short* dst = static_cast<unsigned short*>(c) + static_cast<int64_t>(m) * ldc + n;
+  if (aligned && n + 4 <= N) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (n + e < N) dst[e] = static_cast<unsigned short>(w[e >> 1] >> ((e & 1) * 16));
+  }
+}
+
+// The sum over the cluster's partials of four words at `off`, in rank order,
+// as fp32 (8-bit operands: the exact integer sum, then one rounding).
+template <int KIND>
+__device__ __forceinline__ void ff_cluster_sum4(uint32_t addr, int splits, float (&v)[4]) {
+  float4 s = ld_shared_cluster_f4(mapa_shared(addr, 0));
+  if (KIND == kFfF16) {
+    for (int q = 1; q < splits; ++q) {
+      const float4 x = ld_shared_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(q)));
+      s.x += x.x;
+      s.y += x.y;
+      s.z += x.z;
+      s.w += x.w;
+    }
+    v[0] = s.x;
+    v[1] = s.y;
+    v[2] = s.z;
+    v[3] = s.w;
+  } else {
+    int i[4] = {__float_as_int(s.x), __float_as_int(s.y), __float_as_int(s.z), __float_as_int(s.w)};
+    for (int q = 1; q < splits; ++q) {
+      const float4 x = ld_shared_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(q)));
+      i[0] += __float_as_int(x.x);
+      i[1] += __float_as_int(x.y);
+      i[2] += __float_as_int(x.z);
+      i[3] += __float_as_int(x.w);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __int2float_rn(i[e]);
+  }
+}
+
+__device__ __forceinline__ void ff_scale4(float (&v)[4], float row_scale, const float* col_scale, int n, int N) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = v[e] * row_scale * (n + e < N ? __ldg(col_scale + n + e) : 0.0f);
+}
+
+template <int KIND, bool GATED>
+__global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
+    ff_skinny_kernel(const __grid_constant__ FfMaps maps, const FfSkinnyParams p) {
+  using Cfg = FfSkinnyCfg;
+  constexpr int K_ELEMS = KIND == kFfI8 ? 128 : 64;
+  constexpr int OUT = GATED ? 64 : 128;  // result columns per panel
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* w_smem = smem;
+  uint8_t* a_smem = smem + p.stages * Cfg::W_STAGE_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * (Cfg::W_STAGE_BYTES + p.a_stage_bytes));
+  uint64_t* full_bar = bars;
+  uint64_t* empty_bar = bars + Cfg::MAX_STAGES;
+  uint64_t* acc_full_bar = bars + 2 * Cfg::MAX_STAGES;
+  uint64_t* mma_done_bar = acc_full_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  uint32_t* partial = reinterpret_cast<uint32_t*>(smem);  // [m_pad][128] words, reuses the ring
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int n0 = blockIdx.y * OUT;
+  const int kb_lo = static_cast<int>((static_cast<int64_t>(p.k_blocks) * rank) / p.splits);
+  const int kb_hi = static_cast<int>((static_cast<int64_t>(p.k_blocks) * (rank + 1)) / p.splits);
+  const int my_blocks = kb_hi - kb_lo;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(acc_full_bar, 1);
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&maps.a[0]);
+    tma_prefetch_desc(&maps.b[0]);
+    if (GATED) tma_prefetch_desc(&maps.b[1]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish_alloc_permit();
+  }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  tcgen05_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  grid_dependency_wait();
+  grid_launch_dependents();
+
+  if (warp == 0) {
+    // Producer: this CTA's K slice of the panel and of the activations.
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_parity[Cfg::MAX_STAGES];
+#pragma unroll
+      for (int s = 0; s < Cfg::MAX_STAGES; ++s) last_parity[s] = -1;
+      const uint32_t tx = Cfg::W_STAGE_BYTES + p.a_stage_bytes;
+      const uint64_t pol_w = l2_policy_evict_first();
+      const uint64_t pol_a = l2_policy_evict_last();
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0x91)) break;
+        mbar_arrive_expect_tx(&full_bar[stage], tx);
+        const int k_src = kb >= p.k_blocks_src ? 1 : 0;
+        const int k0 = (kb - k_src * p.k_blocks_src) * K_ELEMS;
+        uint8_t* wdst = w_smem + stage * Cfg::W_STAGE_BYTES;
+        if (GATED) {
+          tma_load_2d_hint(wdst, &maps.b[0], &full_bar[stage], k0, n0, pol_w);
+          tma_load_2d_hint(wdst + Cfg::HALF_BYTES, &maps.b[1], &full_bar[stage], k0, n0, pol_w);
+        } else if (KIND == kFfI8 || p.b_kmajor) {
+          tma_load_2d_hint(wdst, &maps.b[k_src], &full_bar[stage], k0, n0, pol_w);
+        } else {
+          tma_load_2d_hint(wdst, &maps.b[k_src], &full_bar[stage], n0, k0, pol_w);
+          tma_load_2d_hint(wdst + Cfg::HALF_BYTES, &maps.b[k_src], &full_bar[stage], n0 + 64, k0, pol_w);
+        }
+        tma_load_2d_hint(a_smem + stage * p.a_stage_bytes, &maps.a[k_src], &full_bar[stage], k0, 0, pol_a);
+        last_parity[stage] = static_cast<int>(phase);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      for (int s = 0; s < p.stages; ++s) {
+        if (last_parity[s] >= 0) {
+          volatile int no_abort = 0;
+          mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.wait_budget_ns, 0x92);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      const bool w_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
+      for (int i = 0; i < my_blocks; ++i) {
+        if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0x93)) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after_sync();
+        const uint32_t w_addr = smem_u32(w_smem + stage * Cfg::W_STAGE_BYTES);
+        const uint32_t a_addr = smem_u32(a_smem + stage * p.a_stage_bytes);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint64_t wdesc = w_mn ? make_sw128_desc(w_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                      : make_sw128_desc(w_addr + k * 32, 16, 1024);
+          umma_ff<KIND>(tmem_base, wdesc, make_sw128_desc(a_addr + k * 32, 16, 1024), p.idesc,
+                        (i | k) != 0 ? 1u : 0u);
+        }
+        umma_commit(&empty_bar[stage]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok && my_blocks > 0) umma_commit(acc_full_bar);
+      umma_commit(mma_done_bar);
+      volatile int no_abort = 0;
+      mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0x94);
+    }
+    __syncwarp();
+  } else {
+    // TMEM partial -> shared memory [m][panel row].
+    const int quad = warp & 3;
+    const int n_local = quad * 32 + lane;
+    bool ready = true;
+    if (my_blocks > 0) ready = mbar_wait(acc_full_bar, 0, abort_flag, p.wait_budget_ns, 0x95);
+    ready = __all_sync(0xffffffffu, ready);
+    if (ready) {
+      tcgen05_fence_after_sync();
+      for (int c = 0; c < p.m_pad / 16; ++c) {
+        uint32_t r[16];
+        if (my_blocks > 0) {
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c * 16, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) r[e] = 0u;  // empty K slice
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) partial[(c * 16 + e) * Cfg::PANEL + n_local] = r[e];
+      }
+    }
+    tcgen05_fence_before_sync();
+  }
+
+  __syncthreads();
+  cluster_sync();  // every partial of the cluster is in shared memory
+
+  if (warp >= Cfg::EPI_WARP0 && !*abort_flag) {
+    // Items are (m, 4-column group); CTA `rank` finishes its share.
+    const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
+    constexpr int GROUPS = OUT / 4;
+    const int items = p.M * GROUPS;
+    const int lo = static_cast<int>((static_cast<int64_t>(items) * rank) / p.splits);
+    const int hi = static_cast<int>((static_cast<int64_t>(items) * (rank + 1)) / p.splits);
+    const uint32_t part_addr = smem_u32(partial);
+    const bool bf16 = p.bf16 != 0;
+    for (int it = lo + e; it < hi; it += 128) {
+      const int m = it / GROUPS;
+      const int j = it - m * GROUPS;
+      const int n = n0 + 4 * j;
+      if (n >= p.N) continue;
+      const uint32_t off = part_addr + static_cast<uint32_t>((m * Cfg::PANEL + 4 * j) * 4);
+      float v[4];
+      ff_cluster_sum4<KIND>(off, p.splits, v);
+      const float row_scale = KIND == kFfI8 ? __ldg(p.row_scale + m) : 1.0f;
+      if (KIND == kFfI8) ff_scale4(v, row_scale, p.col_scale[0], n, p.N);
+      if (GATED) {
+        float u[4];
+        ff_cluster_sum4<KIND>(off + 64 * 4, p.splits, u);
+        if (KIND == kFfI8) ff_scale4(u, row_scale, p.col_scale[1], n, p.N);
+        if (KIND == kFfF16 && p.save) {
+          ff_store4(p.c[1], p.ldc[1], p.c_aligned[1] != 0, m, n, p.N, v, bf16);
+          ff_store4(p.c[2], p.ldc[2], p.c_aligned[2] != 0, m, n, p.N, u, bf16);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          v[q] = (p.act == kActSilu   ? act_value<kActSilu>(v[q])
+                  : p.act == kActGelu ? act_value<kActGelu>(v[q])
+                                      : act_value<kActRelu>(v[q])) *
+                 u[q];
+      } else if (KIND == kFfI8) {
+        if (p.bias != nullptr) {
+          const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + n;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (n + q < p.N) v[q] += load_16(b16 + q, bf16);
+        }
+        if (p.relu) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = v[q] > 0.0f ? v[q] : 0.0f;
+        }
+      }
+      ff_store4(p.c[0], p.ldc[0], p.c_aligned[0] != 0, m, n, p.N, v, bf16);
+    }
+  }
+
+  cluster_sync();  // peers are done reading this CTA's partial
+  if (warp == 1) {
+    tcgen05_fence_after_sync();
+    tmem_dealloc(tmem_base, p.tmem_cols);
+  }
+}
+
+}  // namespace tg

@@ -51,6 +51,7 @@ struct DeviceInfo {
   unsigned rc_attr = 0;       // one bit per residue-class kernel instance with its attribute set
   bool w4_attr = false;
   bool w4_decode_attr = false;
+  unsigned ff_attr = 0;       // one bit per feed-forward kernel instance with its attribute set
   void* static_ws = nullptr;  // device address of g_static_workspace on this device
 };
 
@@ -1503,6 +1504,8 @@ tg_status run_w4a16(const void* A, const void* Wq, const void* S, void* C, int64
 
 }  // namespace
 }  // namespace tg
+
+#include "ff_host.cuh"
 
 extern "C" {
 
