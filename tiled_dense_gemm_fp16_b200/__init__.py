@@ -27,19 +27,13 @@ from ._binding import (  # noqa: F401
     TYPE_F16,
     bmm_relu,
     device_status,
-    gated,
-    gated_backward,
     gated_backward_raw,
     gated_backward_workspace_size,
-    gated_block,
-    gated_i8,
     gated_i8_raw,
     gated_options,
     gated_raw,
     gated_workspace_size,
-    gemm_i8,
     gemm_i8_raw,
-    quantize_i8,
     quantize_rows_i8_raw,
     gemm_relu,
     gemm_relu_f16_ex_raw,
@@ -73,3 +67,15 @@ from ._binding import (  # noqa: F401
     workspace_size,
     workspace_size_ex,
 )
+
+# The feed-forward operators need torch at import; they load with their first use.
+_FEEDFORWARD = ("gated", "gated_backward", "gated_block", "gated_i8", "gemm_i8", "quantize_i8")
+
+
+def __getattr__(name):
+    if name in _FEEDFORWARD:
+        from . import feedforward
+        for n in _FEEDFORWARD:
+            globals()[n] = getattr(feedforward, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -571,9 +571,6 @@ def gemm_relu_w4a16(A, Wq, S, group, out=None, stream=None, workspace="auto"):
 # Gated feed-forward block and 8-bit integer products
 # ---------------------------------------------------------------------------
 
-_ACTS = {"relu": ACT_RELU, "silu": ACT_SILU, "gelu": ACT_GELU}
-
-
 def gated_options(type=TYPE_F16, act=ACT_RELU, ldx=0, ldwg=0, ldwu=0, ldh=0, ldg=0, ldu=0, lddx=0, lddwg=0, lddwu=0,
                   reserved=0) -> GatedOptions:
     """A tg_gated_options value (zeros mean fp16, ReLU and dense rows)."""
@@ -620,293 +617,3 @@ def gemm_i8_raw(A: int, a_scale: int, W: int, w_scale: int, bias: int, C: int, M
 def gated_i8_raw(A: int, a_scale: int, Wg: int, g_scale: int, Wu: int, u_scale: int, H: int, M: int, N: int, K: int,
                  opts: GatedOptions | None = None, stream: int = 0) -> int:
     return int(lib().tg_gated_i8(A, a_scale, Wg, g_scale, Wu, u_scale, H, M, N, K, _ref(opts), stream))
-
-
-def _type_code(dtype):
-    import torch
-    if dtype == torch.float16:
-        return TYPE_F16
-    if dtype == torch.bfloat16:
-        return TYPE_BF16
-    raise TypeError(f"expected torch.float16 or torch.bfloat16, got {dtype}")
-
-
-def _act_code(act):
-    try:
-        return _ACTS[act]
-    except KeyError:
-        raise ValueError(f"unknown activation {act!r}; one of {sorted(_ACTS)}") from None
-
-
-def _row_stride(t, name):
-    """Elements between the rows of a 2-D tensor whose columns are adjacent (0: dense or a single row)."""
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have adjacent columns (stride 1), got strides {t.stride()}")
-    if rows <= 1 or cols == 0:
-        return 0
-    if t.stride(0) < cols:
-        raise ValueError(f"{name} has overlapping rows: strides {t.stride()} for shape {tuple(t.shape)}")
-    return t.stride(0)
-
-
-def _matrix(t, name, shape, dtype, device):
-    """Check a 2-D operand; returns its row stride (0: dense)."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    return _row_stride(t, name)
-
-
-def _vector(t, name, n, dtype, device):
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.numel() != n or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be {n} contiguous values on {device}")
-    return t.data_ptr()
-
-
-def _flat(t, name):
-    """(..., K) as (rows, K), without a copy."""
-    if t.dim() < 1 or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor with at least one dimension")
-    if t.dim() == 2:
-        return t
-    rows = 1
-    for d in t.shape[:-1]:
-        rows *= d
-    try:
-        return t.view(rows, t.shape[-1])
-    except RuntimeError:
-        raise ValueError(f"{name}: the leading dimensions of shape {tuple(t.shape)} with strides {t.stride()} "
-                         "are not evenly spaced rows") from None
-
-
-def _on(device, stream, *tensors):
-    """Context in which a call runs and allocates: `stream`, or the device's current stream.
-
-    Tensors made on another stream are recorded on `stream`, so that their memory is not reused
-    before the call's work is done (making the streams wait for each other stays the caller's part)."""
-    import contextlib
-
-    import torch
-    if stream is None:
-        return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    if stream != torch.cuda.current_stream(device):
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
-    return torch.cuda.stream(stream)
-
-
-def _scratch(workspace, need, device):
-    """(pointer, bytes) of the workspace of a call that needs `need` bytes, and the tensor that holds it."""
-    import torch
-    if need < 0:
-        raise TGError(Status.INVALID_ARG, "workspace size")
-    if isinstance(workspace, str):
-        if workspace != "auto":
-            raise ValueError("workspace must be 'auto', None or a uint8 CUDA tensor")
-        if need == 0:
-            return 0, 0, None
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is None:
-        return 0, 0, None
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {device}")
-    return workspace.data_ptr(), workspace.numel(), workspace
-
-
-def _given(workspace):
-    return None if workspace is None or isinstance(workspace, str) else workspace
-
-
-def gated(x, w_gate, w_up, act="silu", out=None, save=False, stream=None, workspace="auto"):
-    """act(x @ w_gate^T) * (x @ w_up^T) for float16 or bfloat16 CUDA tensors: x (..., K), w_gate and
-    w_up (N, K) as linear layers store them (the halves of one (2N, K) weight do too).
-
-    ``act``: "silu", "gelu" (tanh form) or "relu".  Returns H (..., N); with ``save`` the tuple
-    (H, gate, up) with the two projections, which ``gated_backward`` takes.  ``out`` receives H.
-    Rows may have any stride; ``workspace`` (as for ``gemm_relu``) is needed only where a row stride or
-    base is off 16 bytes.  ``gated_block`` is the same under autograd.
-    """
-    import torch
-    x2 = _flat(x, "x")
-    M, K = x2.shape
-    dtype, device = x.dtype, x.device
-    code = _type_code(dtype)
-    if w_gate.dim() != 2:
-        raise ValueError(f"w_gate must be (N, K), got {tuple(w_gate.shape)}")
-    N = w_gate.shape[0]
-    opts = GatedOptions(code, _act_code(act), _row_stride(x2, "x"), _matrix(w_gate, "w_gate", (N, K), dtype, device),
-                        _matrix(w_up, "w_up", (N, K), dtype, device))
-    lead = x.shape[:-1]
-    out2 = None
-    if out is not None:
-        if tuple(out.shape) != (*lead, N):
-            raise ValueError(f"out must have shape {(*lead, N)}, got {tuple(out.shape)}")
-        out2 = _flat(out, "out")
-        opts.ldh = _matrix(out2, "out", (M, N), dtype, device)
-    with _on(device, stream, x, w_gate, w_up, out, _given(workspace)):
-        if out is None:
-            out = out2 = torch.empty((M, N), dtype=dtype, device=device)
-            if x.dim() != 2:
-                out = out2.view(*lead, N)
-        gate = up = None
-        if save:
-            gate, up = torch.empty((2, M, N), dtype=dtype, device=device)
-        ptrs = (x2.data_ptr(), w_gate.data_ptr(), w_up.data_ptr())
-        ws, ws_bytes, held = _scratch(workspace, gated_workspace_size(*ptrs, M, N, K, opts), device)
-        st = gated_raw(*ptrs, out2.data_ptr(), gate.data_ptr() if save else 0, up.data_ptr() if save else 0, M, N, K,
-                       opts, _stream_handle(device), ws, ws_bytes)
-    _check(st, "tg_gated")
-    return (out, gate.view(*lead, N), up.view(*lead, N)) if save else out
-
-
-def gated_backward(grad, x, w_gate, w_up, gate, up, act="silu", needs=(True, True, True), stream=None,
-                   workspace="auto"):
-    """Gradients of ``gated`` for grad = dH (..., N), with the projections that ``gated(..., save=True)``
-    returned: (dx, dw_gate, dw_up), None where ``needs`` is false.
-
-    ``workspace``: "auto" lets torch allocate the bytes for dG and dU; a uint8 CUDA tensor is used as
-    given (calls whose work may overlap need one each).
-    """
-    import torch
-    x2 = _flat(x, "x")
-    M, K = x2.shape
-    dtype, device = x.dtype, x.device
-    code = _type_code(dtype)
-    if w_gate.dim() != 2:
-        raise ValueError(f"w_gate must be (N, K), got {tuple(w_gate.shape)}")
-    N = w_gate.shape[0]
-    grad2, gate2, up2 = _flat(grad, "grad"), _flat(gate, "gate"), _flat(up, "up")
-    opts = GatedOptions(code, _act_code(act), _row_stride(x2, "x"), _matrix(w_gate, "w_gate", (N, K), dtype, device),
-                        _matrix(w_up, "w_up", (N, K), dtype, device), _matrix(grad2, "grad", (M, N), dtype, device),
-                        _matrix(gate2, "gate", (M, N), dtype, device), _matrix(up2, "up", (M, N), dtype, device))
-    need_x, need_g, need_u = needs
-    with _on(device, stream, grad, x, w_gate, w_up, gate, up, _given(workspace)):
-        dx = torch.empty((M, K), dtype=dtype, device=device) if need_x else None
-        dwg = torch.empty((N, K), dtype=dtype, device=device) if need_g else None
-        dwu = torch.empty((N, K), dtype=dtype, device=device) if need_u else None
-        grads = [t.data_ptr() if t is not None else 0 for t in (dx, dwg, dwu)]
-        ins = (x2.data_ptr(), w_gate.data_ptr(), w_up.data_ptr())
-        ws, ws_bytes, held = _scratch(workspace, gated_backward_workspace_size(*ins, *grads, M, N, K, opts), device)
-        st = gated_backward_raw(grad2.data_ptr(), *ins, gate2.data_ptr(), up2.data_ptr(), *grads, M, N, K, opts,
-                                _stream_handle(device), ws, ws_bytes)
-    _check(st, "tg_gated_backward")
-    return (dx.view(x.shape) if need_x else None), dwg, dwu
-
-
-def gated_block(x, w_gate, w_up, act="silu"):
-    """``gated`` under autograd: gradients reach x, w_gate and w_up (those that ask for one).
-
-    Runs on the current stream.  Without gradients to take, no projection is stored."""
-    from .autograd import gated_block as impl
-    return impl(x, w_gate, w_up, act)
-
-
-def quantize_i8(x, out=None, scales=None, stream=None):
-    """Rows of x (..., K), float16 or bfloat16, as 8-bit integers with one scale each: (codes, scales) with
-    codes (..., K) int8 and scales (...) float32, scale = max |x| / 127, codes = x / scale rounded to
-    nearest even.  Rows of codes that the call allocates start on 16-byte boundaries whatever K is, as
-    ``gemm_i8`` and ``gated_i8`` want them.  Serves activations (a row is a token) and weights (a row is
-    a channel).  Rows of zeros: scale 0.  Rows with an infinity or a NaN: scale NaN, codes 0."""
-    import torch
-    x2 = _flat(x, "x")
-    M, K = x2.shape
-    device, lead = x.device, x.shape[:-1]
-    code, ldx = _type_code(x.dtype), _row_stride(x2, "x")
-    out2 = None
-    if out is not None:
-        if out.shape != x.shape:
-            raise ValueError(f"out must have shape {tuple(x.shape)}, got {tuple(out.shape)}")
-        out2 = _flat(out, "out")
-        ldq = _matrix(out2, "out", (M, K), torch.int8, device)
-    if scales is not None:
-        _vector(scales, "scales", M, torch.float32, device)
-    with _on(device, stream, x, out, scales):
-        if out is None:
-            ldq = (K + 15) // 16 * 16
-            stored = torch.empty((M, ldq), dtype=torch.int8, device=device)
-            out2 = stored[:, :K] if ldq != K else stored
-            out = out2 if x.dim() == 2 else stored.view(*lead, ldq)[..., :K]
-        if scales is None:
-            scales = torch.empty(lead, dtype=torch.float32, device=device)
-        st = quantize_rows_i8_raw(x2.data_ptr(), out2.data_ptr(), scales.data_ptr(), M, K, ldx, ldq, code,
-                                  _stream_handle(device))
-    _check(st, "tg_quantize_rows_i8")
-    return out, scales
-
-
-def gemm_i8(a, a_scale, w, w_scale, bias=None, relu=False, dtype=None, out=None, stream=None):
-    """(a @ w^T) * a_scale * w_scale + bias, with an optional ReLU, for int8 CUDA tensors a (..., K) and
-    w (N, K) with a float32 scale for each of their rows; bias (N,) of the result's type.
-
-    Returns (..., N) of ``dtype`` (float16 unless given, or ``out``'s).  The integer sums are exact.
-    Rows of a and w must start on 16-byte boundaries (as those of ``quantize_i8`` do)."""
-    import torch
-    a2 = _flat(a, "a")
-    M, K = a2.shape
-    device, lead = a.device, a.shape[:-1]
-    if w.dim() != 2:
-        raise ValueError(f"w must be (N, K), got {tuple(w.shape)}")
-    N = w.shape[0]
-    lda, ldw = _matrix(a2, "a", (M, K), torch.int8, device), _matrix(w, "w", (N, K), torch.int8, device)
-    sa, sw = _vector(a_scale, "a_scale", M, torch.float32, device), _vector(w_scale, "w_scale", N, torch.float32, device)
-    out2, ldc, dtype = _result(out, dtype, lead, M, N, device)
-    code = _type_code(dtype)
-    b = _vector(bias, "bias", N, dtype, device) if bias is not None else 0
-    with _on(device, stream, a, a_scale, w, w_scale, bias, out):
-        if out is None:
-            out2 = torch.empty((M, N), dtype=dtype, device=device)
-            out = out2 if a.dim() == 2 else out2.view(*lead, N)
-        st = gemm_i8_raw(a2.data_ptr(), sa, w.data_ptr(), sw, b, out2.data_ptr(), M, N, K, lda, ldw, ldc, relu, code,
-                         _stream_handle(device))
-    _check(st, "tg_gemm_i8")
-    return out
-
-
-def _result(out, dtype, lead, M, N, device):
-    """(2-D view of `out` or None, its row stride, result type)."""
-    import torch
-    if out is None:
-        return None, 0, dtype if dtype is not None else torch.float16
-    if tuple(out.shape) != (*lead, N):
-        raise ValueError(f"out must have shape {(*lead, N)}, got {tuple(out.shape)}")
-    if dtype is None:
-        dtype = out.dtype
-    out2 = _flat(out, "out")
-    return out2, _matrix(out2, "out", (M, N), dtype, device), dtype
-
-
-def gated_i8(a, a_scale, w_gate, gate_scale, w_up, up_scale, act="silu", dtype=None, out=None, stream=None):
-    """``gated`` on 8-bit operands: a (..., K) int8 with a scale a row, w_gate and w_up (N, K) int8 with a
-    scale a row.  Returns (..., N) of ``dtype`` (float16 unless given, or ``out``'s).  Operands as for
-    ``gemm_i8``."""
-    import torch
-    a2 = _flat(a, "a")
-    M, K = a2.shape
-    device, lead = a.device, a.shape[:-1]
-    if w_gate.dim() != 2:
-        raise ValueError(f"w_gate must be (N, K), got {tuple(w_gate.shape)}")
-    N = w_gate.shape[0]
-    out2, ldh, dtype = _result(out, dtype, lead, M, N, device)
-    opts = GatedOptions(_type_code(dtype), _act_code(act), _matrix(a2, "a", (M, K), torch.int8, device),
-                        _matrix(w_gate, "w_gate", (N, K), torch.int8, device),
-                        _matrix(w_up, "w_up", (N, K), torch.int8, device), ldh)
-    sa = _vector(a_scale, "a_scale", M, torch.float32, device)
-    sg = _vector(gate_scale, "gate_scale", N, torch.float32, device)
-    su = _vector(up_scale, "up_scale", N, torch.float32, device)
-    with _on(device, stream, a, a_scale, w_gate, gate_scale, w_up, up_scale, out):
-        if out is None:
-            out2 = torch.empty((M, N), dtype=dtype, device=device)
-            out = out2 if a.dim() == 2 else out2.view(*lead, N)
-        st = gated_i8_raw(a2.data_ptr(), sa, w_gate.data_ptr(), sg, w_up.data_ptr(), su, out2.data_ptr(), M, N, K,
-                          opts, _stream_handle(device))
-    _check(st, "tg_gated_i8")
-    return out

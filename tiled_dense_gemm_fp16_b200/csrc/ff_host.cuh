@@ -554,6 +554,25 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
 // ---------------------------------------------------------------------------
 // 8-bit operands
 // ---------------------------------------------------------------------------
+template <int THREADS, int HELD>
+tg_status launch_quantize(const QuantizeParams& p, cudaStream_t stream, DeviceInfo* info) {
+  using Cfg = QuantizeCfg<THREADS, HELD>;
+  const int64_t blocks = (static_cast<int64_t>(p.M) + Cfg::ROWS - 1) / Cfg::ROWS;
+  const int64_t cap = static_cast<int64_t>(info->sm_count) * (2048 / Cfg::BLOCK / 2);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 1, 1);
+  cfg.blockDim = dim3(Cfg::BLOCK, 1, 1);
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 1);
+  if (cudaLaunchKernelEx(&cfg, quantize_rows_kernel<THREADS, HELD>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
 tg_status run_quantize(const void* X, void* Q, float* scales, int64_t M, int64_t K, int64_t ldx, int64_t ldq,
                        int32_t type, void* stream_ptr) {
   if (!ff_sizes_valid(M, 1, K) || !ff_type_valid(type) || ldx < 0 || ldq < 0) return TG_ERR_INVALID_ARG;
@@ -578,24 +597,11 @@ tg_status run_quantize(const void* X, void* Q, float* scales, int64_t M, int64_t
   p.K = static_cast<int>(K);
   p.vec = (x.rows_on(16) && q.rows_on(8)) ? 1 : 0;
   p.bf16 = type == TG_TYPE_BF16 ? 1 : 0;
-  // A warp holds 1024 values of a row in registers, a block 8192.
-  const bool warp_rows = K <= 32 * 8 * kQuantizeHeld;
-  const int64_t blocks = warp_rows ? (M + kQuantizeThreads / 32 - 1) / (kQuantizeThreads / 32) : M;
-  const int64_t cap = static_cast<int64_t>(info->sm_count) * 8;
-  cudaLaunchConfig_t cfg;
-  std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 1, 1);
-  cfg.blockDim = dim3(kQuantizeThreads, 1, 1);
-  cfg.stream = stream;
-  LaunchAttrs la;
-  la.fill(cfg, 1);
-  const cudaError_t e = warp_rows ? cudaLaunchKernelEx(&cfg, quantize_rows_kernel<32>, p)
-                                  : cudaLaunchKernelEx(&cfg, quantize_rows_kernel<kQuantizeThreads>, p);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return TG_ERR_LAUNCH;
-  }
-  return TG_OK;
+  // A warp holds rows of up to 1024 values, a block of 256 up to 8192.  With
+  // few long rows a block of 1024 shortens each thread's part.
+  if (K <= QuantizeCfg<32, 4>::HELD_VALUES) return launch_quantize<32, 4>(p, stream, info);
+  if (M <= info->sm_count) return launch_quantize<1024, 1>(p, stream, info);
+  return launch_quantize<256, 4>(p, stream, info);
 }
 
 // The 8-bit operands of a product: rows on 16-byte boundaries (TMA).

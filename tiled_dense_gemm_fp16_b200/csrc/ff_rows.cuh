@@ -88,11 +88,20 @@ __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const Gat
 // Row quantization
 // ----------------------------------------------------------------------------
 // scale = max |x| / 127 (one IEEE fp32 division), q = x / scale rounded to the
-// nearest integer, ties to even, exactly: the quotient is first estimated by a
-// product with 1 / scale, then settled by the remainder r = x - q scale, which
-// one fused multiply-add gives without error (|r| stays below scale and is a
-// multiple of the smaller of the last places of x and scale).  So codes do not
-// depend on how a division rounds.  |q| <= 127.
+// nearest integer, ties to even, exactly.  Two steps:
+//   * t = x * (1 / scale), off from the quotient by at most 127 * 2^-23; one
+//     fused multiply-add onto 1.5 * 2^23 leaves its nearest integer in the low
+//     mantissa bits, a second gives the distance of t from that integer;
+//   * where a distance comes within 2^-14 of a half (a few values in ten
+//     thousand), the chunk is settled by remainders: r = x - q scale, which
+//     one fused multiply-add gives without error (|r| stays below 2 scale and
+//     is a multiple of scale's last place).
+// So codes do not depend on how a division rounds.  |q| <= 127.
+//
+// Bound by memory: 2 bytes in and 1 out an element, each read once.  A row is
+// held in registers between its maximum and its codes (up to THREADS * 8 HELD
+// values; what a longer row has more is read again, from L2), and the next
+// row's loads are in flight meanwhile.
 struct QuantizeParams {
   const void* X;
   int8_t* Q;
@@ -103,10 +112,9 @@ struct QuantizeParams {
   int bf16;
 };
 
-constexpr int kQuantizeThreads = 256;
-constexpr int kQuantizeHeld = 4;  // chunks of 8 values a thread keeps in registers
+constexpr float kTwo64 = 18446744073709551616.0f;
 
-__device__ __forceinline__ int quantize_one(float x, float scale, float inv) {
+__device__ __forceinline__ int quantize_settled(float x, float scale, float inv) {
   float q = rintf(x * inv);
   const float r = fmaf(-q, scale, x);
   const float half = 0.5f * scale;
@@ -117,74 +125,106 @@ __device__ __forceinline__ int quantize_one(float x, float scale, float inv) {
   return static_cast<int>(q);
 }
 
-// Eight codes of one chunk, packed.
+// Eight codes of one chunk, packed.  `tiny`: scale is below 2^-64, where 1 /
+// scale could overflow; values and scale are multiplied by 2^64 first (exact),
+// and `inv` belongs to the product.
 __device__ __forceinline__ uint2 quantize8(const uint4& v, float scale, float inv, bool tiny, bool bf16) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t out[2] = {0u, 0u};
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  float x[8];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    float2 x = unpack_16(w[e], bf16);
-    float s = scale;
-    if (tiny) {  // both scaled by 2^64, exactly: 1 / scale would overflow
-      x.x *= 18446744073709551616.0f;
-      x.y *= 18446744073709551616.0f;
-      s *= 18446744073709551616.0f;
+    const float2 f = unpack_16(w[e], bf16);
+    x[2 * e] = f.x;
+    x[2 * e + 1] = f.y;
+  }
+  if (!tiny) {
+    uint32_t q[8];
+    float worst = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float f = fmaf(x[e], inv, kMagic);
+      worst = fmaxf(worst, fabsf(fmaf(x[e], inv, kMagic - f)));
+      q[e] = __float_as_uint(f);
     }
-    const int q0 = quantize_one(x.x, s, inv), q1 = quantize_one(x.y, s, inv);
-    out[e >> 1] |= (static_cast<uint32_t>(q0 & 0xff) | (static_cast<uint32_t>(q1 & 0xff) << 8)) << ((e & 1) * 16);
+    if (worst < 0.5f - 6.103515625e-5f)
+      return make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
+                        __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
+  }
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int q = quantize_settled(tiny ? x[e] * kTwo64 : x[e], tiny ? scale * kTwo64 : scale, inv);
+    out[e >> 2] |= static_cast<uint32_t>(q & 0xff) << ((e & 3) * 8);
   }
   return make_uint2(out[0], out[1]);
 }
 
-// THREADS threads per row: 32 (a warp; eight rows a block) or a whole block.
-template <int THREADS>
-__global__ void __launch_bounds__(kQuantizeThreads) quantize_rows_kernel(const QuantizeParams p) {
+// THREADS threads per row: a warp (several rows a block) or a whole block of
+// them.  HELD: 16-byte chunks a thread keeps.
+template <int THREADS, int HELD>
+struct QuantizeCfg {
+  static constexpr int BLOCK = THREADS < 256 ? 256 : THREADS;
+  static constexpr int ROWS = BLOCK / THREADS;
+  static constexpr int HELD_VALUES = THREADS * HELD * 8;
+};
+
+template <int THREADS, int HELD>
+__global__ void __launch_bounds__(QuantizeCfg<THREADS, HELD>::BLOCK) quantize_rows_kernel(const QuantizeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  __shared__ uint32_t warp_max[2][kQuantizeThreads / 32];
-  constexpr int ROWS = kQuantizeThreads / THREADS;
+  using Cfg = QuantizeCfg<THREADS, HELD>;
+  constexpr int WARPS = Cfg::BLOCK / 32;
+  __shared__ uint32_t warp_max[2][WARPS];
   const int t = threadIdx.x % THREADS;
   const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
   const int chunks = (p.K + 7) / 8;
+  const int64_t stride = static_cast<int64_t>(gridDim.x) * Cfg::ROWS;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * Cfg::ROWS + threadIdx.x / THREADS;
+  auto row_of = [&](int64_t r) { return static_cast<const unsigned short*>(p.X) + r * p.ldx; };
+  auto load = [&](int64_t r, uint4 (&held)[HELD]) {
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) {
+      const int c = t + i * THREADS;
+      held[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < p.M && c < chunks) held[i] = load8_16(row_of(r) + c * 8, p.K - c * 8, vec);
+    }
+  };
+  uint4 held[HELD], next[HELD];
+  load(row, held);
   int parity = 0;
-  for (int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / THREADS; row < p.M;
-       row += static_cast<int64_t>(gridDim.x) * ROWS, parity ^= 1) {
-    const unsigned short* src = static_cast<const unsigned short*>(p.X) + row * p.ldx;
-    uint4 held[kQuantizeHeld];
+  for (; row < p.M; row += stride, parity ^= 1) {
+    load(row + stride, next);
     // The maximum of the magnitudes' bits: fp16 and bf16 order as integers,
     // and infinities and NaN come out above every finite value.
     uint32_t best = 0u;
     auto take = [&](const uint4& v) {
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) best = __vmaxu2(best, w[e] & 0x7fff7fffu);
+      best = __vmaxu2(best, v.x & 0x7fff7fffu);
+      best = __vmaxu2(best, v.y & 0x7fff7fffu);
+      best = __vmaxu2(best, v.z & 0x7fff7fffu);
+      best = __vmaxu2(best, v.w & 0x7fff7fffu);
     };
 #pragma unroll
-    for (int i = 0; i < kQuantizeHeld; ++i) {
-      const int c = t + i * THREADS;
-      held[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (c < chunks) held[i] = load8_16(src + c * 8, p.K - c * 8, vec);
-    }
-#pragma unroll
-    for (int i = 0; i < kQuantizeHeld; ++i) take(held[i]);
-    for (int c = t + kQuantizeHeld * THREADS; c < chunks; c += THREADS) take(load8_16(src + c * 8, p.K - c * 8, vec));
+    for (int i = 0; i < HELD; ++i) take(held[i]);
+    for (int c = t + HELD * THREADS; c < chunks; c += THREADS) take(load8_16(row_of(row) + c * 8, p.K - c * 8, vec));
     best = max(best & 0xffffu, best >> 16);
     best = __reduce_max_sync(0xffffffffu, best);
     if (THREADS > 32) {
       if ((threadIdx.x & 31) == 0) warp_max[parity][threadIdx.x >> 5] = best;
-      __syncthreads();
-      best = warp_max[parity][threadIdx.x & 7];
-      best = __reduce_max_sync(0xffffffffu, best);
+      __syncthreads();  // the other half of warp_max serves the next row, so one barrier a row is enough
+      best = __reduce_max_sync(0xffffffffu, warp_max[parity][threadIdx.x & (WARPS - 1)]);
     }
-    const float amax = bf16 ? __uint_as_float(best << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(best)));
+    const float amax =
+        bf16 ? __uint_as_float(best << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(best)));
     const bool finite = best < (bf16 ? 0x7f80u : 0x7c00u);
     const float scale = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7fffffffu);
+    const bool live = finite && scale > 0.0f;
     const bool tiny = scale < 5.421010862427522e-20f;  // 2^-64
-    const float inv = finite && scale > 0.0f ? __fdiv_rn(1.0f, tiny ? scale * 18446744073709551616.0f : scale) : 0.0f;
+    const float inv = live ? __fdiv_rn(1.0f, tiny ? scale * kTwo64 : scale) : 0.0f;
     if (t == 0) p.scale[row] = scale;
     int8_t* dst = p.Q + row * p.ldq;
     auto put = [&](int c, const uint4& v) {
-      const uint2 q = (finite && scale > 0.0f) ? quantize8(v, scale, inv, tiny, bf16) : make_uint2(0u, 0u);
+      const uint2 q = live ? quantize8(v, scale, inv, tiny, bf16) : make_uint2(0u, 0u);
       const int n = p.K - c * 8;
       if (vec && n >= 8) {
         *reinterpret_cast<uint2*>(dst + c * 8) = q;
@@ -196,11 +236,13 @@ __global__ void __launch_bounds__(kQuantizeThreads) quantize_rows_kernel(const Q
       }
     };
 #pragma unroll
-    for (int i = 0; i < kQuantizeHeld; ++i) {
+    for (int i = 0; i < HELD; ++i) {
       const int c = t + i * THREADS;
       if (c < chunks) put(c, held[i]);
     }
-    for (int c = t + kQuantizeHeld * THREADS; c < chunks; c += THREADS) put(c, load8_16(src + c * 8, p.K - c * 8, vec));
+    for (int c = t + HELD * THREADS; c < chunks; c += THREADS) put(c, load8_16(row_of(row) + c * 8, p.K - c * 8, vec));
+#pragma unroll
+    for (int i = 0; i < HELD; ++i) held[i] = next[i];
   }
 }
 
