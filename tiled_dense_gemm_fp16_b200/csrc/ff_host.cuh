@@ -107,10 +107,10 @@ bool ff_set_smem(const void* kernel, unsigned& done, unsigned bit, int bytes) {
   return true;
 }
 
-template <int STAGES, int BN, int KIND, bool GATED>
+template <int STAGES, int BN, int EPI_WARPS, int KIND, bool GATED>
 tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo* info) {
-  using Cfg = FfPairCfg<STAGES, BN>;
-  auto kernel = ff_pair_kernel<STAGES, BN, KIND, GATED>;
+  using Cfg = FfPairCfg<STAGES, BN, EPI_WARPS>;
+  auto kernel = ff_pair_kernel<STAGES, BN, EPI_WARPS, KIND, GATED>;
   constexpr unsigned kBit = 1u << ((BN == 512 ? 1 : 0) + (KIND == kFfI8 ? 2 : 0) + (GATED ? 4 : 0));
   if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->ff_attr, kBit, Cfg::SMEM_BYTES)) return TG_ERR_LAUNCH;
   FfMaps maps;
@@ -146,7 +146,13 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
   p.k_blocks = p.k_blocks_src * f.k_sources;
   p.group_m = BN == 512 ? 16 : 12;
   if (tiles > INT_MAX - 65536 || static_cast<int64_t>(p.group_m) * p.n_tiles > INT_MAX) return TG_ERR_INVALID_ARG;
-  p.num_tiles = static_cast<int>(tiles);
+  const int pairs = info->sm_count / 2;
+  // Whole waves of whole tiles; what is left over, if it fits in one wave of
+  // half tiles, runs as those (half the time of a last wave of whole tiles).
+  const int rest = static_cast<int>(tiles % pairs);
+  const bool halves = Cfg::SLABS == 2 && 2 * rest <= pairs;
+  p.whole_tiles = static_cast<int>(halves ? tiles - rest : tiles);
+  p.num_tiles = static_cast<int>(halves ? tiles + rest : tiles);
   p.a_mnmajor = f.a_km ? 1 : 0;
   p.b_kmajor = f.b_kn ? 0 : 1;
   p.bf16 = f.bf16 ? 1 : 0;
@@ -156,7 +162,6 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
   p.l2_hints = BN == 512 ? 2 : 5;
   p.idesc = make_idesc_ff(KIND, f.bf16, Cfg::PAIR_M, 256, f.a_km, f.b_kn);
   p.wait_budget_ns = wait_budget(p.k_blocks);
-  const int pairs = info->sm_count / 2;
   const int clusters = p.num_tiles < pairs ? p.num_tiles : pairs;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
@@ -175,8 +180,19 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
 
 template <int KIND, bool GATED>
 tg_status launch_ff_pair(const FfProduct& f, int bn, cudaStream_t stream, DeviceInfo* info) {
-  return bn == 512 ? launch_ff_pair_cfg<4, 512, KIND, GATED>(f, stream, info)
-                   : launch_ff_pair_cfg<6, 256, KIND, GATED>(f, stream, info);
+  return bn == 512 ? launch_ff_pair_cfg<4, 512, 16, KIND, GATED>(f, stream, info)
+                   : launch_ff_pair_cfg<6, 256, 16, KIND, GATED>(f, stream, info);
+}
+
+// CTAs along K that share a panel of the small-M kernel: as many as fill the
+// device, up to 8.  With one CTA per SM a cluster of 8 leaves SMs of its GPC
+// unused (16 such clusters already take two waves: M = 256, N = K = 1024 gated
+// 23 us against 12 with clusters of 4), so 8 only for few panels.
+int ff_splits(int64_t panels, int k_blocks, bool two_per_sm, int sms) {
+  const int most = two_per_sm || panels <= 8 ? 8 : 4;
+  int64_t s = (two_per_sm ? 2 : 1) * sms / panels;
+  s = s < 1 ? 1 : (s > most ? most : s);
+  return static_cast<int>(s > k_blocks ? k_blocks : s);
 }
 
 template <int KIND, bool GATED>
@@ -224,9 +240,7 @@ tg_status launch_ff_skinny(const FfProduct& f, cudaStream_t stream, DeviceInfo* 
   p.wait_budget_ns = wait_budget(p.k_blocks);
   const int out = GATED ? 64 : 128;
   const int64_t panels = (f.N + out - 1) / out;
-  int splits = static_cast<int>((two_per_sm ? 2 : 1) * info->sm_count / panels);
-  splits = splits < 1 ? 1 : (splits > 8 ? 8 : splits);
-  if (splits > p.k_blocks) splits = p.k_blocks;
+  const int splits = ff_splits(panels, p.k_blocks, two_per_sm, info->sm_count);
   p.splits = splits;
   FfMaps maps;
   std::memset(&maps, 0, sizeof maps);
@@ -251,38 +265,60 @@ tg_status launch_ff_skinny(const FfProduct& f, cudaStream_t stream, DeviceInfo* 
   return TG_OK;
 }
 
-// Few rows take the split-K kernel under the rule of the fp16 product
-// (M <= 128, or M <= 256 with a large weight), when its grid can hold the
-// panels; products whose A is stored K x M never do.
-bool ff_skinny_route(const FfProduct& f) {
+// Few rows take the split-K kernel: M <= 128 always (two CTAs share an SM); for
+// 128 < M <= 256 where its estimated time is the lower one.  A k-block takes
+// its CTA 0.2 us and 0.3 us more at 256 rows, after about 6 us + M / 64 for
+// the launch and the reduction; on the pair kernel one takes 0.344 us, after 5
+// us.  Measured, us, split-K / pair, M = 256: gated fp16 1024 x 1024 10.4 /
+// 10.7, 4096 x 1024 13.4 / 10.9, 1024 x 4096 14.1 / 27.2, 8192 x 8192 69.6 /
+// 68.3, 16384 x 4096 77 / 61; dX of N = K = 8192 69 / 110; 8-bit 8192 x 8192 23 /
+// 28.  At M <= 128 it loses at most 1 us, where K is short (gated 8-bit 8192 x
+// 1024, M = 128: 10.2 / 9.0).  Products whose A is stored K x M never take it.
+bool ff_skinny_route(const FfProduct& f, int sms) {
   if (f.a_km || f.row_sources > 1 || f.M > kSkinnyMaxM) return false;
-  if ((f.N + 63) / 64 > 65535) return false;
-  const int64_t weight = f.N * f.K * f.weights();
-  return f.M <= 128 || weight >= (int64_t(1) << 23);
+  const int out = f.gated ? 64 : 128;
+  const int64_t panels = (f.N + out - 1) / out;
+  if (panels > 65535) return false;
+  if (f.M <= 128) return true;
+  const int64_t kb = (f.K + f.k_elems() - 1) / f.k_elems() * f.k_sources;
+  if (kb > INT_MAX) return false;
+  const int splits = ff_splits(panels, static_cast<int>(kb), false, sms);
+  const double rows = static_cast<double>(f.M);
+  const double split_k = 6.0 + rows / 64.0 +
+                         static_cast<double>((panels * splits + sms - 1) / sms) *
+                             static_cast<double>((kb + splits - 1) / splits) * (0.2 + 0.3 * rows / 256.0);
+  const int64_t tiles = (f.N * (f.gated ? 2 : 1) + 255) / 256, pairs = sms / 2;
+  return split_k < 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * static_cast<double>(kb) * 0.344;
 }
 
-// Accumulator width of the pair kernel: waves of tiles over the 74 pairs of a
-// device times the per-SM work of a tile, as for the fp16 product (the
-// 512-wide tile's epilogue is not hidden and costs about 384 elements of K;
-// the 256-wide tile moves more bytes per product, 0.88 of the rate).
-int ff_tile_width(const FfProduct& f) {
-  constexpr int64_t kPairs = 74;
+// Accumulator width of the pair kernel, by estimated time in units of one
+// accumulator column and 16-bit element of K on one of `pairs` SM pairs.  The
+// 256-wide tile hides its epilogue behind the next tile (two accumulators), but
+// fetches a third more operand bytes per product, which L2 cannot quite feed:
+// 0.93 of the rate.  The 512-wide tile's epilogue hides about half; the rest is
+// worth 160 elements of K (gated: half the results) or 256.  Its last wave may
+// be of half tiles.  Measured, us, 512 / 256: gated fp16 4096 x 8192 with K =
+// 4096 357 / 371, 2048 219 / 220, 1024 130 / 124; 8-bit product 4096 x 8192 with
+// K = 4096 119 / 109, 8192^3 375 / 390; dX of 8192 x 8192 x 4096 825 / 935.
+int ff_tile_width(const FfProduct& f, int64_t pairs) {
   const int64_t m_tiles = (f.M + 255) / 256 * f.row_sources;
   const int64_t cols = f.N * (f.gated ? 2 : 1);
   const double k = static_cast<double>(f.K * f.k_sources) * (f.kind == kFfI8 ? 0.5 : 1.0);
-  auto waves = [](int64_t tiles) { return static_cast<double>((tiles + kPairs - 1) / kPairs); };
-  const double t256 = waves(m_tiles * ((cols + 255) / 256)) * 256.0 * k / 0.88 + 256.0 * 384.0;
-  const double t512 = waves(m_tiles * ((cols + 511) / 512)) * 512.0 * (k + 384.0);
-  return t512 <= t256 ? 512 : 256;
+  const double drain = f.gated ? 160.0 : 256.0;
+  const int64_t tiles256 = m_tiles * ((cols + 255) / 256), tiles512 = m_tiles * ((cols + 511) / 512);
+  const double t256 = static_cast<double>((tiles256 + pairs - 1) / pairs) * k / 0.93 + drain;
+  const int64_t rest = tiles512 % pairs;
+  const double waves512 = 2.0 * static_cast<double>(tiles512 / pairs) + (rest == 0 ? 0.0 : 2 * rest <= pairs ? 1.0 : 2.0);
+  return waves512 * (k + drain) <= t256 ? 512 : 256;
 }
 
 tg_status launch_ff(const FfProduct& f, cudaStream_t stream, DeviceInfo* info) {
-  if (ff_skinny_route(f)) {
+  if (ff_skinny_route(f, info->sm_count)) {
     if (f.kind == kFfI8)
       return f.gated ? launch_ff_skinny<kFfI8, true>(f, stream, info) : launch_ff_skinny<kFfI8, false>(f, stream, info);
     return f.gated ? launch_ff_skinny<kFfF16, true>(f, stream, info) : launch_ff_skinny<kFfF16, false>(f, stream, info);
   }
-  const int bn = ff_tile_width(f);
+  const int bn = ff_tile_width(f, info->sm_count / 2);
   if (f.kind == kFfI8)
     return f.gated ? launch_ff_pair<kFfI8, true>(f, bn, stream, info) : launch_ff_pair<kFfI8, false>(f, bn, stream, info);
   return f.gated ? launch_ff_pair<kFfF16, true>(f, bn, stream, info) : launch_ff_pair<kFfF16, false>(f, bn, stream, info);

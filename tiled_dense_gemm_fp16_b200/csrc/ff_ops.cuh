@@ -17,6 +17,19 @@ enum { kFfF16 = 0, kFfI8 = 1 };
 // Activations of the gated block (the values of TG_ACT_*).
 enum { kActRelu = 0, kActSilu = 1, kActGelu = 2 };
 
+// Whether the phase with parity `parity` has completed, without waiting at all.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar_addr, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar_addr), "r"(parity)
+      : "memory");
+  return ok != 0u;
+}
+
 // D[tmem] (+)= A[smem desc] * B[smem desc] on a CTA pair: 16-bit floats into
 // fp32, or signed 8-bit integers into 32-bit integers.
 template <int KIND>
@@ -66,35 +79,90 @@ inline uint32_t make_idesc_ff(int kind, bool bf16, int M, int N, bool a_mn_major
 // ----------------------------------------------------------------------------
 // Both smooth activations are g * s(z) with the logistic function s: z = g
 // for silu, and for gelu (tanh form) z = 2 sqrt(2/pi) (g + 0.044715 g^3),
-// since (1 + tanh(y)) / 2 = s(2y).  exp(-z) overflows to +inf for z below
-// about -88, where s is 0 to within 3e-39.  The fast exponential and division
-// are good to a few parts in 2^22, far below half a step of a 16-bit result.
+// since (1 + tanh(y)) / 2 = s(2y).  s(z) = 1 / (1 + 2^(-z log2 e)), with -log2
+// e folded into the constants: one exponential and one reciprocal instruction,
+// each good to about 2^-22, far below half a step of a 16-bit result.  Below z
+// = -127 ln 2 the sum overflows towards +inf and s is 0 (less than 2^-126).
+constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluC1 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluC3 = 0.07135481282553557f;  // 2 sqrt(2/pi) 0.044715
 
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two fp32 operations per instruction (sm_100's packed pairs; each half
+// rounds as the single operation does).
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 same2(float a) { return make_float2(a, a); }
+
+// s(z) of the activation's z, for two values.
+template <int ACT>
+__device__ __forceinline__ float2 act_logistic2(float2 g) {
+  float2 t;  // -z log2 e
+  if (ACT == kActSilu)
+    t = mul2(g, same2(-kLog2E));
+  else
+    t = mul2(g, fma2(mul2(g, g), same2(-kLog2E * kGeluC3), same2(-kLog2E * kGeluC1)));
+  const float2 d = add2(make_float2(exp2_approx(t.x), exp2_approx(t.y)), same2(1.0f));
+  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+}
 
 template <int ACT>
-__device__ __forceinline__ float act_value(float g) {
-  if (ACT == kActRelu) return g > 0.0f ? g : 0.0f;
-  if (ACT == kActSilu) return g * logistic(g);
-  return g * logistic(g * fmaf(kGeluC3, g * g, kGeluC1));
+__device__ __forceinline__ float2 act_value2(float2 g) {
+  if (ACT == kActRelu) return make_float2(g.x > 0.0f ? g.x : 0.0f, g.y > 0.0f ? g.y : 0.0f);
+  return mul2(g, act_logistic2<ACT>(g));
 }
 
 // act(g) and its derivative: with p = s(z), act = g p and act' = p + g p (1 - p) z'.
 template <int ACT>
-__device__ __forceinline__ void act_value_slope(float g, float& value, float& slope) {
+__device__ __forceinline__ void act_value_slope2(float2 g, float2& value, float2& slope) {
   if (ACT == kActRelu) {
-    value = g > 0.0f ? g : 0.0f;
-    slope = g > 0.0f ? 1.0f : 0.0f;
+    value = act_value2<ACT>(g);
+    slope = make_float2(g.x > 0.0f ? 1.0f : 0.0f, g.y > 0.0f ? 1.0f : 0.0f);
+    return;
+  }
+  const float2 p = act_logistic2<ACT>(g);
+  value = mul2(g, p);
+  const float2 q = fma2(p, same2(-1.0f), same2(1.0f));
+  const float2 r = mul2(value, q);
+  if (ACT == kActSilu) {
+    slope = add2(p, r);
   } else {
-    const float g2 = g * g;
-    const float p = logistic(ACT == kActSilu ? g : g * fmaf(kGeluC3, g2, kGeluC1));
-    value = g * p;
-    const float dz = ACT == kActSilu ? 1.0f : fmaf(3.0f * kGeluC3, g2, kGeluC1);
-    // For gelu dz grows with g^2; where p is exactly 0 or 1 the term is 0.
-    const float q = p * (1.0f - p);
-    slope = q == 0.0f ? p : fmaf(value * (1.0f - p), dz, p);
+    slope = fma2(r, fma2(mul2(g, g), same2(3.0f * kGeluC3), same2(kGeluC1)), p);
+    // z' grows with g^2; where p is 0 or 1 its factor is 0, whatever g is.
+    if (r.x == 0.0f) slope.x = p.x;
+    if (r.y == 0.0f) slope.y = p.y;
   }
 }
 

@@ -55,13 +55,13 @@ __device__ __forceinline__ void gated_grad_rows(const GatedGradParams& p) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const float2 d = unpack_16(dw[q], bf16), g = unpack_16(gw[q], bf16), u = unpack_16(uw[q], bf16);
-      float a, s;
-      act_value_slope<ACT>(g.x, a, s);
-      dg[2 * q] = d.x * u.x * s;
-      du[2 * q] = d.x * a;
-      act_value_slope<ACT>(g.y, a, s);
-      dg[2 * q + 1] = d.y * u.y * s;
-      du[2 * q + 1] = d.y * a;
+      float2 a, s;
+      act_value_slope2<ACT>(g, a, s);
+      const float2 vg = mul2(mul2(d, u), s), vu = mul2(d, a);
+      dg[2 * q] = vg.x;
+      dg[2 * q + 1] = vg.y;
+      du[2 * q] = vu.x;
+      du[2 * q + 1] = vu.y;
     }
     uint32_t h[4];
     pack_row<8>(dg, h, bf16);

@@ -44,7 +44,9 @@ struct FfParams {
   const float* col_scale[2];  // 8-bit: one per row of the (gate, up) weight
   const void* bias;           // 16-bit values of the result's type, or nullptr
   int M, N;                   // rows and columns of one result
-  int m_tiles, n_tiles, num_tiles;  // m_tiles over all row sources
+  int m_tiles, n_tiles;       // m_tiles over all row sources
+  int num_tiles;              // tiles to walk: `whole_tiles` whole ones, then halves of the rest
+  int whole_tiles;
   int m_tiles_src;            // row tiles of one row source
   int k_blocks, k_blocks_src; // k-blocks over all K sources, and of one
   int group_m;
@@ -58,7 +60,7 @@ struct FfParams {
   uint64_t wait_budget_ns;
 };
 
-template <int STAGES_, int BN_>
+template <int STAGES_, int BN_, int EPI_WARPS_>
 struct FfPairCfg {
   static constexpr int BM = 128;
   static constexpr int PAIR_M = 256;
@@ -67,8 +69,8 @@ struct FfPairCfg {
   static constexpr int STAGES = STAGES_;
   static constexpr int MMA_WARP = 1;
   static constexpr int EPI_WARP0 = 2;
-  static constexpr int EPI_WARPS = 8;
-  static constexpr int EPI_COLS = BN / 2;    // accumulator columns per epilogue warp
+  static constexpr int EPI_WARPS = EPI_WARPS_;
+  static constexpr int EPI_COLS = 1024 / EPI_WARPS;    // accumulator columns of a slab per epilogue warp
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int K_BYTES = 128;        // bytes of K per k-block
   static constexpr int A_BYTES = BM * K_BYTES;
@@ -79,21 +81,44 @@ struct FfPairCfg {
   static constexpr int TMEM_COLS = 512;
   static constexpr int BAR_BYTES = 256;
   static constexpr int C_BUF_BYTES = 32 * 64;         // one 32 x 32 box of 16-bit values
-  static constexpr int C_STAGE_BYTES = EPI_WARPS * 2 * C_BUF_BYTES;
+  static constexpr int C_BUFS = 16 / EPI_WARPS;       // staging boxes per epilogue warp
+  static constexpr int C_STAGE_BYTES = EPI_WARPS * C_BUFS * C_BUF_BYTES;
   static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + C_STAGE_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per CTA");
   static_assert(NUM_ACC * BN <= TMEM_COLS, "TMEM columns");
 };
 
-__device__ __forceinline__ void ff_tile_coords(const FfParams& p, int t, int& m_blk, int& n_blk) {
+// Tile t of the walk: its place, and for a half tile (one slab of 256
+// accumulator columns) which half.
+struct FfTile {
+  int m_blk, n_blk;
+  int row_src;   // which source of rows, m_blk counted inside it
+  int half;      // 0 or 1 of a half tile
+  bool whole;
+};
+
+__device__ __forceinline__ FfTile ff_tile(const FfParams& p, int t) {
+  FfTile f;
+  f.whole = t < p.whole_tiles;
+  f.half = 0;
+  if (!f.whole) {
+    const int r = t - p.whole_tiles;
+    f.half = r & 1;
+    t = p.whole_tiles + (r >> 1);
+  }
   const int group_tiles = p.group_m * p.n_tiles;
   const int g = t / group_tiles;
   const int first_m = g * p.group_m;
   const int gm = min(p.m_tiles - first_m, p.group_m);
   const int local = t - g * group_tiles;
-  m_blk = first_m + local % gm;
-  n_blk = local / gm;
+  f.m_blk = first_m + local % gm;
+  f.n_blk = local / gm;
+  f.row_src = f.m_blk >= p.m_tiles_src ? 1 : 0;
+  f.m_blk -= f.row_src * p.m_tiles_src;
+  return f;
 }
+
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 
 // Scales of 16 consecutive columns (0 past N).
 __device__ __forceinline__ void load_scale16(const float* scale, int col, int N, float (&s)[16]) {
@@ -113,6 +138,27 @@ __device__ __forceinline__ void load_scale16(const float* scale, int col, int N,
   }
 }
 
+// Scales of tile t's rows and columns into L1: `row` is this lane's row inside
+// the tile, `col` its first column inside a slab.
+template <bool GATED, int TILE_N, int SLAB_N>
+__device__ __forceinline__ void ff_prefetch_scales(const FfParams& p, int t, int row, int col) {
+  if (t >= p.num_tiles) return;
+  const FfTile f = ff_tile(p, t);
+  if (f.m_blk * 256 + row < p.M) prefetch_l1(p.row_scale + f.m_blk * 256 + row);
+#pragma unroll
+  for (int c = 0; c < TILE_N; c += SLAB_N) {
+    if (c > 0 && !f.whole) break;
+#pragma unroll
+    for (int q = 0; q < SLAB_N / 4; q += 32) {
+      const int n = f.n_blk * TILE_N + f.half * SLAB_N + c + col + q;
+      if (n < p.N) {
+        prefetch_l1(p.col_scale[0] + n);
+        if (GATED) prefetch_l1(p.col_scale[1] + n);
+      }
+    }
+  }
+}
+
 // 16 accumulator words as fp32: the fp32 sums themselves, or the 32-bit
 // integer sums (one rounding to fp32) times the row's and column's scale.
 template <int KIND>
@@ -125,57 +171,110 @@ __device__ __forceinline__ void ff_values(const uint32_t (&r)[16], float row_sca
     float s[16];
     load_scale16(col_scale, col, N, s);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = __int2float_rn(static_cast<int>(r[e])) * row_scale * s[e];
+    for (int e = 0; e < 16; e += 2) {
+      const float2 x = make_float2(__int2float_rn(static_cast<int>(r[e])), __int2float_rn(static_cast<int>(r[e + 1])));
+      const float2 y = mul2(mul2(x, same2(row_scale)), make_float2(s[e], s[e + 1]));
+      v[e] = y.x;
+      v[e + 1] = y.y;
+    }
   }
 }
 
 template <int ACT>
 __device__ __forceinline__ void gate_row(float (&g)[16], const float (&u)[16]) {
 #pragma unroll
-  for (int e = 0; e < 16; ++e) g[e] = act_value<ACT>(g[e]) * u[e];
+  for (int e = 0; e < 16; e += 2) {
+    const float2 h = mul2(act_value2<ACT>(make_float2(g[e], g[e + 1])), make_float2(u[e], u[e + 1]));
+    g[e] = h.x;
+    g[e + 1] = h.y;
+  }
 }
 
-// One 32 x 32 box of a result: lane = row, h = its 32 packed values.  `buf`
-// is one of the warp's two staging boxes (64-byte swizzle), used in turn.
+// One 32 x 32 box of a result: lane = row, h = its 32 packed values, `buf` one
+// of the warp's BUFS staging boxes (64-byte swizzle), which take turns.  Rows
+// that start on 16-byte boundaries leave as one TMA box.  Else two rows leave
+// per store instruction, 4 bytes a lane: the rows are staged shifted so that
+// words start on 4-byte boundaries, which leaves the first and last value of a
+// row on an odd 2-byte boundary to single stores by the row's lane.
+template <int BUFS>
 __device__ __forceinline__ void ff_store_box(const CUtensorMap* map, void* c, int64_t ldc, bool aligned, int M, int N,
                                              int y0, int col0, const uint32_t* h, uint8_t* buf, int lane,
                                              uint64_t policy) {
-  if (lane == 0) bulk_wait_group_read<1>();  // the box stored two turns ago has been read
+  if (lane == 0) bulk_wait_group_read<BUFS - 1>();  // the last box stored from `buf` has been read
   __syncwarp();
   const uint32_t row_addr = smem_u32(buf) + lane * 64;
-#pragma unroll
-  for (int q = 0; q < 4; ++q)
-    st_shared_v4(row_addr + ((q ^ ((lane >> 1) & 3)) << 4), h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
   if (aligned) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      st_shared_v4(row_addr + ((q ^ ((lane >> 1) & 3)) << 4), h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       tma_store_2d_hint(map, buf, col0, y0, policy);
       bulk_commit_group();
     }
-  } else {
-    // Rows on any 2-byte boundary: lane = column, one row per store.
-    __syncwarp();
-    unsigned short* dst = static_cast<unsigned short*>(c) + static_cast<int64_t>(y0) * ldc + col0 + lane;
-    const int rows = min(32, M - y0);
+    return;
+  }
+  unsigned short* box = static_cast<unsigned short*>(c) + static_cast<int64_t>(y0) * ldc + col0;
+  const int rows = min(32, M - y0);
+  const bool whole = col0 + 32 <= N;
+  const uint32_t odd0 = (reinterpret_cast<uintptr_t>(box) >> 1) & 1u;  // row 0 starts on an odd 2-byte boundary
+  const uint32_t odd = whole ? (odd0 ^ (lane & static_cast<uint32_t>(ldc) & 1u)) : 0u;  // this lane's row
+  uint32_t w[17];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) w[e] = h[e];
+  w[16] = 0u;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(row_addr + ((q ^ ((lane >> 1) & 3)) << 4), __funnelshift_r(w[4 * q], w[4 * q + 1], odd * 16),
+                 __funnelshift_r(w[4 * q + 1], w[4 * q + 2], odd * 16),
+                 __funnelshift_r(w[4 * q + 2], w[4 * q + 3], odd * 16),
+                 __funnelshift_r(w[4 * q + 3], w[4 * q + 4], odd * 16));
+  __syncwarp();
+  if (whole) {
+    const int half = lane >> 4, j = lane & 15;  // row 2 i + half, word j
+    const uint32_t odd_r = odd0 ^ (static_cast<uint32_t>(half) & static_cast<uint32_t>(ldc) & 1u);
+    const bool word_ok = j + static_cast<int>(odd_r) < 16;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(box + half * ldc + 2 * j + odd_r);
+    const uint32_t src = smem_u32(buf) + half * 64 + (j & 3) * 4;
+    const int turns = rows == 32 ? 16 : (rows - half + 1) / 2;
+    if (word_ok) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (i < turns) {
+          uint32_t v;
+          asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(src + i * 128 + (((j >> 2) ^ (i & 3)) << 4)));
+          *dst = v;
+        }
+        dst += ldc;  // two rows of 2-byte values
+      }
+    }
+    if (odd && lane < rows) {
+      unsigned short* r = box + lane * ldc;
+      r[0] = static_cast<unsigned short>(h[0] & 0xffffu);
+      r[31] = static_cast<unsigned short>(h[15] >> 16);
+    }
+  } else {  // the last columns: lane = column, one row per store
+    unsigned short* dst = box + lane;
     const bool col_ok = col0 + lane < N;
-#pragma unroll 8
+#pragma unroll 4
     for (int r = 0; r < 32; ++r) {
       const unsigned short v = *reinterpret_cast<const unsigned short*>(
           buf + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
-      if (r < rows && col_ok) dst[static_cast<int64_t>(r) * ldc] = v;
+      if (r < rows && col_ok) dst[r * ldc] = v;
     }
-    if (lane == 0) bulk_commit_group();  // an empty group, so that the wait above counts boxes
-    __syncwarp();
   }
+  if (lane == 0) bulk_commit_group();  // an empty group, so that the wait above counts boxes
+  __syncwarp();
 }
 
-template <int STAGES, int BN, int KIND, bool GATED>
-__global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
+template <int STAGES, int BN, int EPI_WARPS, int KIND, bool GATED>
+__global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
     ff_pair_kernel(const __grid_constant__ FfMaps maps, const FfParams p) {
-  using Cfg = FfPairCfg<STAGES, BN>;
+  using Cfg = FfPairCfg<STAGES, BN, EPI_WARPS>;
   constexpr int K_ELEMS = KIND == kFfI8 ? 128 : 64;   // elements of K per k-block
-  constexpr int TILE_N = GATED ? BN / 2 : BN;         // result columns per tile
+  constexpr int SLAB_N = GATED ? 128 : 256;           // result columns per slab of 256 accumulator columns
+  constexpr int TILE_N = Cfg::SLABS * SLAB_N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* a_smem = smem;
@@ -185,8 +284,8 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
   uint64_t* full_bar = bars;                              // used in the even CTA
   uint64_t* empty_bar = bars + Cfg::STAGES;               // per CTA
   uint64_t* acc_full_bar = bars + 2 * Cfg::STAGES;        // per CTA
-  uint64_t* acc_empty_bar = acc_full_bar + Cfg::NUM_ACC;  // used in the even CTA
-  uint64_t* mma_done_bar = acc_empty_bar + Cfg::NUM_ACC;
+  uint64_t* acc_empty_bar = acc_full_bar + 2;             // used in the even CTA: one per slab of TMEM
+  uint64_t* mma_done_bar = acc_empty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -202,7 +301,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
-    for (int b = 0; b < Cfg::NUM_ACC; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full_bar[b], 1);
       mbar_init(&acc_empty_bar[b], 2 * Cfg::EPI_WARPS);
     }
@@ -240,18 +339,19 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
                              : (p.l2_hints & 4) ? l2_policy_evict_first()
                                                 : l2_policy_evict_normal();
       for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
-        int m_blk, n_blk;
-        ff_tile_coords(p, t, m_blk, n_blk);
-        const int row_src = m_blk >= p.m_tiles_src ? 1 : 0;
-        const int m0 = (m_blk - row_src * p.m_tiles_src) * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
-        const int n0 = n_blk * TILE_N + static_cast<int>(rank) * (GATED ? 64 : 128);
+        const FfTile f = ff_tile(p, t);
+        const int row_src = f.row_src;
+        const int slabs = f.whole ? Cfg::SLABS : 1;
+        const int m0 = f.m_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
+        const int n0 = f.n_blk * TILE_N + f.half * SLAB_N + static_cast<int>(rank) * (GATED ? 64 : 128);
+        const uint32_t tx = 2 * (Cfg::A_BYTES + slabs * Cfg::B_SLAB_BYTES);
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0x81)) {
             ok = false;
             break;
           }
           const uint32_t full_even = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (Cfg::A_BYTES + Cfg::B_BYTES));
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const int k_src = kb >= p.k_blocks_src ? 1 : 0;
           const int k0 = (kb - k_src * p.k_blocks_src) * K_ELEMS;
           const CUtensorMap* ma = &maps.a[row_src | k_src];
@@ -266,6 +366,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
           }
 #pragma unroll
           for (int j = 0; j < Cfg::SLABS; ++j) {
+            if (j >= slabs) break;
             uint8_t* slab = bdst + j * Cfg::B_SLAB_BYTES;
             if (GATED) {
               // 64 rows of Wg, then the same 64 rows of Wu.
@@ -306,37 +407,68 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
       bool ok = true;
       const bool a_mn = KIND == kFfF16 && p.a_mnmajor != 0;
       const bool b_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
+      // The four MMAs of one k-block and one slab.
+      auto issue = [&](int st, int j, uint32_t d_tmem, bool first) {
+        const uint32_t a_addr = smem_u32(a_smem + st * Cfg::A_BYTES);
+        const uint32_t slab_addr = smem_u32(b_smem + st * Cfg::B_BYTES) + j * Cfg::B_SLAB_BYTES;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
+          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                      : make_sw128_desc(a_addr + k * 32, 16, 1024);
+          const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                      : make_sw128_desc(slab_addr + k * 32, 16, 1024);
+          umma_ff_pair<KIND>(d_tmem + 256 * j, adesc, bdesc, p.idesc, (first && k == 0) ? 0u : 1u);
+        }
+      };
+      auto advance = [&](int& st, uint32_t& ph) {
+        if (++st == Cfg::STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
+      };
       for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters, ++local) {
+        const bool whole = t < p.whole_tiles;
         const int acc = local % Cfg::NUM_ACC;
         const uint32_t acc_phase = (local / Cfg::NUM_ACC) & 1;
         if (!mbar_wait(&acc_empty_bar[acc], acc_phase ^ 1u, abort_flag, p.wait_budget_ns, 0x83)) break;
         tcgen05_fence_after_sync();
         const uint32_t d_tmem = tmem_base + acc * Cfg::BN;
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
+        int kb = 0;
+        if (Cfg::SLABS == 2) {
+          // The epilogue frees slab 0 while it still drains slab 1: until that
+          // is free too, the k-blocks in the ring go into slab 0 alone, and
+          // catch up in slab 1 after.
+          const uint32_t second = smem_u32(&acc_empty_bar[1]);
+          int ahead = 0, st = stage;
+          uint32_t ph = phase;
+          while (whole && ahead < Cfg::STAGES && ahead < p.k_blocks && !mbar_test_wait(second, acc_phase ^ 1u)) {
+            if (!mbar_wait(&full_bar[st], ph, abort_flag, p.wait_budget_ns, 0x87)) {
+              ok = false;
+              break;
+            }
+            tcgen05_fence_after_sync();
+            issue(st, 0, d_tmem, ahead == 0);
+            ++ahead;
+            advance(st, ph);
+          }
+          if (!ok || !mbar_wait(&acc_empty_bar[1], acc_phase ^ 1u, abort_flag, p.wait_budget_ns, 0x88)) break;
+          tcgen05_fence_after_sync();
+          for (; kb < ahead; ++kb) {
+            issue(stage, 1, d_tmem, kb == 0);
+            umma_commit_pair_mc(&empty_bar[stage], 0x3);
+            advance(stage, phase);
+          }
+        }
+        for (; kb < p.k_blocks; ++kb) {
           if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0x84)) {
             ok = false;
             break;
           }
           tcgen05_fence_after_sync();
-          const uint32_t a_addr = smem_u32(a_smem + stage * Cfg::A_BYTES);
-          const uint32_t b_addr = smem_u32(b_smem + stage * Cfg::B_BYTES);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
-            const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
-                                        : make_sw128_desc(a_addr + k * 32, 16, 1024);
-#pragma unroll
-            for (int j = 0; j < Cfg::SLABS; ++j) {
-              const uint32_t slab_addr = b_addr + j * Cfg::B_SLAB_BYTES;
-              const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::HALF_BYTES, 1024)
-                                          : make_sw128_desc(slab_addr + k * 32, 16, 1024);
-              umma_ff_pair<KIND>(d_tmem + 256 * j, adesc, bdesc, p.idesc, (kb | k) != 0 ? 1u : 0u);
-            }
-          }
+          issue(stage, 0, d_tmem, kb == 0);
+          if (Cfg::SLABS == 2 && whole) issue(stage, 1, d_tmem, kb == 0);
           umma_commit_pair_mc(&empty_bar[stage], 0x3);  // both CTAs may refill this stage
-          if (++stage == Cfg::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          advance(stage, phase);
         }
         if (!ok) break;
         umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
@@ -348,106 +480,122 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN>::THREADS, 1)
     __syncwarp();
   } else {
     // Epilogue (both CTAs): warp w takes TMEM lanes 32 (w mod 4) .. + 31 and
-    // half `part` of the accumulator's columns.
+    // part `part` of every slab's columns.
     const int quad = warp & 3;
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
-    constexpr int OUT = GATED ? Cfg::EPI_COLS / 2 : Cfg::EPI_COLS;  // result columns of this warp
-    uint8_t* wbuf = c_stage + (warp - Cfg::EPI_WARP0) * 2 * Cfg::C_BUF_BYTES;
+    constexpr int OUT = GATED ? Cfg::EPI_COLS / 2 : Cfg::EPI_COLS;  // result columns of this warp per slab
+    uint8_t* wbuf = c_stage + (warp - Cfg::EPI_WARP0) * Cfg::C_BUFS * Cfg::C_BUF_BYTES;
     const uint64_t pol = l2_policy_evict_first();
+    const int row_in_tile = static_cast<int>(rank) * Cfg::BM + quad * 32;
     int local = 0;
     int turn = 0;  // which staging box comes next
+    if (KIND == kFfI8)
+      ff_prefetch_scales<GATED, TILE_N, SLAB_N>(p, cluster_id, row_in_tile + lane, part * OUT + lane);
     for (int t = cluster_id; t < p.num_tiles; t += num_clusters, ++local) {
-      int m_blk, n_blk;
-      ff_tile_coords(p, t, m_blk, n_blk);
-      const int row_src = m_blk >= p.m_tiles_src ? 1 : 0;
+      const FfTile f = ff_tile(p, t);
       const int acc = local % Cfg::NUM_ACC;
       const uint32_t acc_phase = (local / Cfg::NUM_ACC) & 1;
-      const int y0 =
-          (m_blk - row_src * p.m_tiles_src) * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM + quad * 32;
-      const int out0 = n_blk * TILE_N + part * OUT;
+      const int y0 = f.m_blk * Cfg::PAIR_M + row_in_tile;
+      const int out0 = f.n_blk * TILE_N + f.half * SLAB_N + part * OUT;
       float row_scale = 0.0f;
-      if (KIND == kFfI8 && y0 + lane < p.M) row_scale = __ldg(p.row_scale + y0 + lane);
+      if (KIND == kFfI8) {
+        if (y0 + lane < p.M) row_scale = __ldg(p.row_scale + y0 + lane);
+        // The next tile's scales come into L1 while this tile is finished.
+        ff_prefetch_scales<GATED, TILE_N, SLAB_N>(p, t + num_clusters, row_in_tile + lane, part * OUT + lane);
+      }
       const bool ready = mbar_wait(&acc_full_bar[acc], acc_phase, abort_flag, p.wait_budget_ns, 0x86);
       if (!__all_sync(0xffffffffu, ready)) break;
       tcgen05_fence_after_sync();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::BN;
       const bool rows_live = y0 < p.M;
-      uint32_t h[OUT / 2];
+      uint32_t h[Cfg::SLABS][OUT / 2];
 #pragma unroll
-      for (int c = 0; c < OUT / 32; ++c) {
-        const int col0 = out0 + c * 32;
-        if (GATED) {
-          // Result column o of the tile: gate at accumulator column
-          // 128 (o / 64) + o mod 64, up 64 columns further.
-          const int o = part * OUT + c * 32;
-          const uint32_t gaddr = taddr + (o >> 6) * 128 + (o & 63);
-          const bool save = KIND == kFfF16 && p.save && rows_live && col0 < p.N;
-          uint32_t hg[16], hu[16];
+      for (int s = 0; s < Cfg::SLABS; ++s) {
+        if (s == 0 || f.whole) {
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint32_t rg[16], ru[16];
-            tmem_ld_32x32b_x16(gaddr + b * 16, rg);
-            tmem_ld_32x32b_x16(gaddr + 64 + b * 16, ru);
-            tmem_ld_wait();
-            float g[16], u[16];
-            ff_values<KIND>(rg, row_scale, p.col_scale[0], col0 + b * 16, p.N, g);
-            ff_values<KIND>(ru, row_scale, p.col_scale[1], col0 + b * 16, p.N, u);
-            if (save) {
-              pack_row<16>(g, hg + b * 8, p.bf16 != 0);
-              pack_row<16>(u, hu + b * 8, p.bf16 != 0);
-            }
-            if (p.act == kActSilu)
-              gate_row<kActSilu>(g, u);
-            else if (p.act == kActGelu)
-              gate_row<kActGelu>(g, u);
-            else
-              gate_row<kActRelu>(g, u);
-            pack_row<16>(g, h + c * 16 + b * 8, p.bf16 != 0);
-          }
-          if (save) {
-            ff_store_box(&maps.c[1], p.c[1], p.ldc[1], p.c_aligned[1] != 0, p.M, p.N, y0, col0, hg,
-                         wbuf + (turn & 1) * Cfg::C_BUF_BYTES, lane, pol);
-            ff_store_box(&maps.c[2], p.c[2], p.ldc[2], p.c_aligned[2] != 0, p.M, p.N, y0, col0, hu,
-                         wbuf + ((turn + 1) & 1) * Cfg::C_BUF_BYTES, lane, pol);
-            turn += 2;
-          }
-        } else {
+          for (int c = 0; c < OUT / 32; ++c) {
+            const int col0 = out0 + s * SLAB_N + c * 32;
+            if (GATED) {
+              // Result column o of the slab: gate at accumulator column
+              // 128 (o / 64) + o mod 64, up 64 columns further.
+              const int o = part * OUT + c * 32;
+              const uint32_t gaddr = taddr + s * 256 + (o >> 6) * 128 + (o & 63);
+              const bool save = KIND == kFfF16 && p.save && rows_live && col0 < p.N;
+              uint32_t hg[16], hu[16];
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(taddr + part * OUT + c * 32 + b * 16, r);
-            tmem_ld_wait();
-            const int col = col0 + b * 16;
-            float v[16];
-            ff_values<KIND>(r, row_scale, p.col_scale[0], col, p.N, v);
-            if (KIND == kFfI8) {
-              if (p.bias != nullptr) {
-                const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + col;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (col + e < p.N) v[e] += load_16(b16 + e, p.bf16 != 0);
+              for (int b = 0; b < 2; ++b) {
+                uint32_t rg[16], ru[16];
+                tmem_ld_32x32b_x16(gaddr + b * 16, rg);
+                tmem_ld_32x32b_x16(gaddr + 64 + b * 16, ru);
+                tmem_ld_wait();
+                float g[16], u[16];
+                ff_values<KIND>(rg, row_scale, p.col_scale[0], col0 + b * 16, p.N, g);
+                ff_values<KIND>(ru, row_scale, p.col_scale[1], col0 + b * 16, p.N, u);
+                if (save) {
+                  pack_row<16>(g, hg + b * 8, p.bf16 != 0);
+                  pack_row<16>(u, hu + b * 8, p.bf16 != 0);
+                }
+                if (p.act == kActSilu)
+                  gate_row<kActSilu>(g, u);
+                else if (p.act == kActGelu)
+                  gate_row<kActGelu>(g, u);
+                else
+                  gate_row<kActRelu>(g, u);
+                pack_row<16>(g, h[s] + c * 16 + b * 8, p.bf16 != 0);
               }
-              if (p.relu) {
+              if (save) {
+                ff_store_box<Cfg::C_BUFS>(&maps.c[1], p.c[1], p.ldc[1], p.c_aligned[1] != 0, p.M, p.N, y0, col0, hg,
+                                          wbuf + (turn % Cfg::C_BUFS) * Cfg::C_BUF_BYTES, lane, pol);
+                ff_store_box<Cfg::C_BUFS>(&maps.c[2], p.c[2], p.ldc[2], p.c_aligned[2] != 0, p.M, p.N, y0, col0, hu,
+                                          wbuf + ((turn + 1) % Cfg::C_BUFS) * Cfg::C_BUF_BYTES, lane, pol);
+                turn += 2;
+              }
+            } else {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) v[e] = v[e] > 0.0f ? v[e] : 0.0f;
+              for (int b = 0; b < 2; ++b) {
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(taddr + s * 256 + part * OUT + c * 32 + b * 16, r);
+                tmem_ld_wait();
+                const int col = col0 + b * 16;
+                float v[16];
+                ff_values<KIND>(r, row_scale, p.col_scale[0], col, p.N, v);
+                if (KIND == kFfI8) {
+                  if (p.bias != nullptr) {
+                    const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + col;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                      if (col + e < p.N) v[e] += load_16(b16 + e, p.bf16 != 0);
+                  }
+                  if (p.relu) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = v[e] > 0.0f ? v[e] : 0.0f;
+                  }
+                }
+                pack_row<16>(v, h[s] + c * 16 + b * 8, p.bf16 != 0);
               }
             }
-            pack_row<16>(v, h + c * 16 + b * 8, p.bf16 != 0);
           }
         }
+        tcgen05_fence_before_sync();
+        __syncwarp();
+        // Relaxed: the arrival orders only the TMEM reads, which are complete
+        // (wait::ld) and fenced; a release would also wait for the stores of
+        // the tile before.
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_empty_bar[acc + s]), 0));
       }
-      tcgen05_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty_bar[acc]), 0));
       if (rows_live) {
-        const int ci = GATED ? 0 : row_src;
+        const int ci = GATED ? 0 : f.row_src;
 #pragma unroll
-        for (int c = 0; c < OUT / 32; ++c) {
-          const int col0 = out0 + c * 32;
-          if (col0 < p.N) {
-            ff_store_box(&maps.c[ci], p.c[ci], p.ldc[ci], p.c_aligned[ci] != 0, p.M, p.N, y0, col0, h + c * 16,
-                         wbuf + (turn & 1) * Cfg::C_BUF_BYTES, lane, pol);
-            ++turn;
+        for (int s = 0; s < Cfg::SLABS; ++s) {
+          if (s > 0 && !f.whole) break;
+#pragma unroll
+          for (int c = 0; c < OUT / 32; ++c) {
+            const int col0 = out0 + s * SLAB_N + c * 32;
+            if (col0 < p.N) {
+              ff_store_box<Cfg::C_BUFS>(&maps.c[ci], p.c[ci], p.ldc[ci], p.c_aligned[ci] != 0, p.M, p.N, y0, col0,
+                                        h[s] + c * 16, wbuf + (turn % Cfg::C_BUFS) * Cfg::C_BUF_BYTES, lane, pol);
+              ++turn;
+            }
           }
         }
       }

@@ -64,31 +64,44 @@ __device__ __forceinline__ void ff_store4(void* c, int64_t ldc, bool aligned, in
   }
 }
 
-// The sum over the cluster's partials of four words at `off`, in rank order,
-// as fp32 (8-bit operands: the exact integer sum, then one rounding).
+// The cluster's partials of four words at `addr`: every remote read is issued
+// before the first sum (read one after the other, 8 of them cost 4 us at M =
+// 128).
+__device__ __forceinline__ void ff_cluster_read(uint32_t addr, int splits, float4 (&x)[8]) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    if (q < splits) x[q] = ld_shared_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(q)));
+}
+
+// Their sum in rank order, as fp32 (8-bit operands: the exact integer sum,
+// then one rounding).
 template <int KIND>
-__device__ __forceinline__ void ff_cluster_sum4(uint32_t addr, int splits, float (&v)[4]) {
-  float4 s = ld_shared_cluster_f4(mapa_shared(addr, 0));
+__device__ __forceinline__ void ff_cluster_sum(const float4 (&x)[8], int splits, float (&v)[4]) {
   if (KIND == kFfF16) {
-    for (int q = 1; q < splits; ++q) {
-      const float4 x = ld_shared_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(q)));
-      s.x += x.x;
-      s.y += x.y;
-      s.z += x.z;
-      s.w += x.w;
+    float4 s = x[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+      if (q < splits) {
+        s.x += x[q].x;
+        s.y += x[q].y;
+        s.z += x[q].z;
+        s.w += x[q].w;
+      }
     }
     v[0] = s.x;
     v[1] = s.y;
     v[2] = s.z;
     v[3] = s.w;
   } else {
-    int i[4] = {__float_as_int(s.x), __float_as_int(s.y), __float_as_int(s.z), __float_as_int(s.w)};
-    for (int q = 1; q < splits; ++q) {
-      const float4 x = ld_shared_cluster_f4(mapa_shared(addr, static_cast<uint32_t>(q)));
-      i[0] += __float_as_int(x.x);
-      i[1] += __float_as_int(x.y);
-      i[2] += __float_as_int(x.z);
-      i[3] += __float_as_int(x.w);
+    int i[4] = {__float_as_int(x[0].x), __float_as_int(x[0].y), __float_as_int(x[0].z), __float_as_int(x[0].w)};
+#pragma unroll
+    for (int q = 1; q < 8; ++q) {
+      if (q < splits) {
+        i[0] += __float_as_int(x[q].x);
+        i[1] += __float_as_int(x[q].y);
+        i[2] += __float_as_int(x[q].z);
+        i[3] += __float_as_int(x[q].w);
+      }
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = __int2float_rn(i[e]);
@@ -252,39 +265,45 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
   __syncthreads();
   cluster_sync();  // every partial of the cluster is in shared memory
 
-  if (warp >= Cfg::EPI_WARP0 && !*abort_flag) {
+  if (!*abort_flag) {
     // Items are (m, 4-column group); CTA `rank` finishes its share.
-    const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
+    const int e = threadIdx.x;
     constexpr int GROUPS = OUT / 4;
     const int items = p.M * GROUPS;
     const int lo = static_cast<int>((static_cast<int64_t>(items) * rank) / p.splits);
     const int hi = static_cast<int>((static_cast<int64_t>(items) * (rank + 1)) / p.splits);
     const uint32_t part_addr = smem_u32(partial);
     const bool bf16 = p.bf16 != 0;
-    for (int it = lo + e; it < hi; it += 128) {
+    for (int it = lo + e; it < hi; it += Cfg::THREADS) {
       const int m = it / GROUPS;
       const int j = it - m * GROUPS;
       const int n = n0 + 4 * j;
       if (n >= p.N) continue;
       const uint32_t off = part_addr + static_cast<uint32_t>((m * Cfg::PANEL + 4 * j) * 4);
+      float4 xv[8], xu[8];
+      ff_cluster_read(off, p.splits, xv);
+      if (GATED) ff_cluster_read(off + 64 * 4, p.splits, xu);
       float v[4];
-      ff_cluster_sum4<KIND>(off, p.splits, v);
+      ff_cluster_sum<KIND>(xv, p.splits, v);
       const float row_scale = KIND == kFfI8 ? __ldg(p.row_scale + m) : 1.0f;
       if (KIND == kFfI8) ff_scale4(v, row_scale, p.col_scale[0], n, p.N);
       if (GATED) {
         float u[4];
-        ff_cluster_sum4<KIND>(off + 64 * 4, p.splits, u);
+        ff_cluster_sum<KIND>(xu, p.splits, u);
         if (KIND == kFfI8) ff_scale4(u, row_scale, p.col_scale[1], n, p.N);
         if (KIND == kFfF16 && p.save) {
           ff_store4(p.c[1], p.ldc[1], p.c_aligned[1] != 0, m, n, p.N, v, bf16);
           ff_store4(p.c[2], p.ldc[2], p.c_aligned[2] != 0, m, n, p.N, u, bf16);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          v[q] = (p.act == kActSilu   ? act_value<kActSilu>(v[q])
-                  : p.act == kActGelu ? act_value<kActGelu>(v[q])
-                                      : act_value<kActRelu>(v[q])) *
-                 u[q];
+        for (int q = 0; q < 4; q += 2) {
+          const float2 g = make_float2(v[q], v[q + 1]);
+          const float2 a = p.act == kActSilu   ? act_value2<kActSilu>(g)
+                           : p.act == kActGelu ? act_value2<kActGelu>(g)
+                                               : act_value2<kActRelu>(g);
+          v[q] = a.x * u[q];
+          v[q + 1] = a.y * u[q + 1];
+        }
       } else if (KIND == kFfI8) {
         if (p.bias != nullptr) {
           const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + n;
