@@ -349,16 +349,46 @@ int64_t ff_copy_bytes(const FfMat& m) {
   return (m.bytes() == 0 || m.rows_on(16)) ? 0 : up256(2 * m.rows * round_up(m.cols, 8));
 }
 
-// Replace `m` by its padded copy at `ws`, if it needs one; advances `ws`.
-tg_status ff_make_copy(FfMat& m, uint8_t*& ws, cudaStream_t stream, DeviceInfo* info) {
-  const int64_t bytes = ff_copy_bytes(m);
-  if (bytes == 0) return TG_OK;
-  const int64_t ld = round_up(m.cols, 8);
-  const tg_status st = launch_pad(m.p, m.ld, ws, m.rows, m.cols, ld, stream, info);
-  if (st != TG_OK) return st;
-  m.p = ws;
-  m.ld = ld;
-  ws += bytes;
+// Replace those of `mats` that need one by their padded copies at `ws`, made by
+// one launch; advances `ws`.
+tg_status ff_make_copies(FfMat* const* mats, int count, uint8_t*& ws, cudaStream_t stream, DeviceInfo* info) {
+  PadSetParams p;
+  std::memset(&p, 0, sizeof p);
+  int n = 0;
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    FfMat& m = *mats[i];
+    const int64_t bytes = ff_copy_bytes(m);
+    if (bytes == 0) continue;
+    const int64_t ld = round_up(m.cols, 8);
+    RepackParams& r = p.m[n++];
+    r.src = static_cast<const __half*>(m.p);
+    r.dst = reinterpret_cast<__half*>(ws);
+    r.src_ld = m.ld;
+    r.rows = static_cast<int>(m.rows);
+    r.cols = static_cast<int>(m.cols);
+    r.cols_pad = static_cast<int>(ld);
+    r.chunks = m.rows * (ld / 8);
+    most = r.chunks > most ? r.chunks : most;
+    m.p = ws;
+    m.ld = ld;
+    ws += bytes;
+  }
+  if (n == 0) return TG_OK;
+  int64_t blocks = (most + 256 * 4 - 1) / (256 * 4);
+  const int64_t cap = static_cast<int64_t>(info->sm_count) * 8;
+  blocks = blocks > cap ? cap : blocks;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(n), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 1);
+  if (cudaLaunchKernelEx(&cfg, pad_set_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
   return TG_OK;
 }
 
@@ -430,8 +460,8 @@ tg_status run_gated(GatedArgs& a, void* stream_ptr, void* ws_ptr, int64_t ws_byt
     return TG_OK;
   }
   uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
-  for (FfMat* m : {&a.x, &a.wg, &a.wu})
-    if ((st = ff_make_copy(*m, ws, stream, info)) != TG_OK) return st;
+  FfMat* const operands[3] = {&a.x, &a.wg, &a.wu};
+  if ((st = ff_make_copies(operands, 3, ws, stream, info)) != TG_OK) return st;
   FfProduct f;
   f.gated = true;
   f.save = save;
@@ -546,8 +576,15 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
       return TG_ERR_LAUNCH;
     }
   }
+  FfMat* operands[3];
+  int n_operands = 0;
+  if (a.dwg.p || a.dwu.p) operands[n_operands++] = &a.f.x;
+  if (a.dx.p) {
+    operands[n_operands++] = &a.f.wg;
+    operands[n_operands++] = &a.f.wu;
+  }
+  if ((st = ff_make_copies(operands, n_operands, ws, stream, info)) != TG_OK) return st;
   if (a.dwg.p || a.dwu.p) {
-    if ((st = ff_make_copy(a.f.x, ws, stream, info)) != TG_OK) return st;
     FfProduct f;  // dW = dG^T X: rows of the result are columns of dG
     f.a_km = true;
     f.b_kn = true;
@@ -568,8 +605,6 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
     if ((st = launch_ff(f, stream, info)) != TG_OK) return st;
   }
   if (a.dx.p) {
-    for (FfMat* m : {&a.f.wg, &a.f.wu})
-      if ((st = ff_make_copy(*m, ws, stream, info)) != TG_OK) return st;
     FfProduct f;  // dX = dG Wg + dU Wu
     f.b_kn = true;
     f.bf16 = gp.bf16 != 0;
@@ -591,10 +626,10 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
 // 8-bit operands
 // ---------------------------------------------------------------------------
 template <int THREADS, int HELD>
-tg_status launch_quantize(const QuantizeParams& p, cudaStream_t stream, DeviceInfo* info) {
+tg_status launch_quantize(const QuantizeParams& p, bool bf16, bool vec, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = QuantizeCfg<THREADS, HELD>;
   const int64_t blocks = (static_cast<int64_t>(p.M) + Cfg::ROWS - 1) / Cfg::ROWS;
-  const int64_t cap = static_cast<int64_t>(info->sm_count) * (2048 / Cfg::BLOCK / 2);
+  const int64_t cap = static_cast<int64_t>(info->sm_count) * Cfg::BLOCKS_PER_SM;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks < cap ? blocks : cap), 1, 1);
@@ -602,7 +637,9 @@ tg_status launch_quantize(const QuantizeParams& p, cudaStream_t stream, DeviceIn
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, 1);
-  if (cudaLaunchKernelEx(&cfg, quantize_rows_kernel<THREADS, HELD>, p) != cudaSuccess) {
+  auto kernel = bf16 ? (vec ? quantize_rows_kernel<THREADS, HELD, true, true> : quantize_rows_kernel<THREADS, HELD, true, false>)
+                     : (vec ? quantize_rows_kernel<THREADS, HELD, false, true> : quantize_rows_kernel<THREADS, HELD, false, false>);
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
     cudaGetLastError();
     return TG_ERR_LAUNCH;
   }
@@ -631,13 +668,20 @@ tg_status run_quantize(const void* X, void* Q, float* scales, int64_t M, int64_t
   p.ldq = q.ld;
   p.M = static_cast<int>(M);
   p.K = static_cast<int>(K);
-  p.vec = (x.rows_on(16) && q.rows_on(8)) ? 1 : 0;
-  p.bf16 = type == TG_TYPE_BF16 ? 1 : 0;
-  // A warp holds rows of up to 1024 values, a block of 256 up to 8192.  With
-  // few long rows a block of 1024 shortens each thread's part.
-  if (K <= QuantizeCfg<32, 4>::HELD_VALUES) return launch_quantize<32, 4>(p, stream, info);
-  if (M <= info->sm_count) return launch_quantize<1024, 1>(p, stream, info);
-  return launch_quantize<256, 4>(p, stream, info);
+  p.vec_out = q.rows_on(8) ? 1 : 0;
+  const bool vec = x.rows_on(16);
+  const bool bf16 = type == TG_TYPE_BF16;
+  // Threads per row: the fewest that hold the row, at four chunks each, so that
+  // many rows are in flight per SM.  Measured at 8192 rows, us: K = 2048 with 64
+  // / 256 threads 12.1 / 21.8, K = 4096 with 128 / 256 21.0 / 27.9.  With fewer
+  // rows than SMs a block of 1024, one chunk each, shortens a long row's path
+  // (16 x 8192: 2.2 us).
+  if (K <= QuantizeCfg<32, 4>::HELD_VALUES) return launch_quantize<32, 4>(p, bf16, vec, stream, info);
+  if (M <= info->sm_count) return launch_quantize<1024, 1>(p, bf16, vec, stream, info);
+  if (K <= QuantizeCfg<64, 4>::HELD_VALUES) return launch_quantize<64, 4>(p, bf16, vec, stream, info);
+  if (K <= QuantizeCfg<128, 4>::HELD_VALUES) return launch_quantize<128, 4>(p, bf16, vec, stream, info);
+  if (K <= QuantizeCfg<256, 4>::HELD_VALUES) return launch_quantize<256, 4>(p, bf16, vec, stream, info);
+  return launch_quantize<512, 4>(p, bf16, vec, stream, info);
 }
 
 // The 8-bit operands of a product: rows on 16-byte boundaries (TMA).

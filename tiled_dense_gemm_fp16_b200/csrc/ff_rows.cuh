@@ -4,6 +4,8 @@
 #pragma once
 
 #include "ff_ops.cuh"
+#include "gemm_tc.cuh"
+#include "repack.cuh"
 
 namespace tg {
 
@@ -29,13 +31,29 @@ struct GatedGradParams {
 
 constexpr int kGatedGradThreads = 256;
 
-__device__ __forceinline__ uint4 load8_16(const unsigned short* p, int n, bool vec) {
-  if (vec && n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
+// The first n (up to 8) 16-bit values at p, zeros after them.  vec: p is on a
+// 16-byte boundary.  Else two aligned 16-byte loads cover 8 values on any
+// 2-byte boundary and are shifted into place, if both lie inside the matrix
+// [lo, hi); what is left is read value by value.
+__device__ __forceinline__ uint4 load8_16(const unsigned short* p, int n, bool vec, const void* lo, const void* hi) {
+  if (n >= 8) {
+    if (vec) return __ldg(reinterpret_cast<const uint4*>(p));
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), block = at & ~uintptr_t(15);
+    if (block >= reinterpret_cast<uintptr_t>(lo) && block + 32 <= reinterpret_cast<uintptr_t>(hi)) {
+      const uint4* q = reinterpret_cast<const uint4*>(block);
+      return edge_realign(__ldg(q), __ldg(q + 1), static_cast<uint32_t>(at - block));
+    }
+  }
   uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (e < n) w[e >> 1] |= static_cast<uint32_t>(__ldg(p + e)) << ((e & 1) * 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// End of a matrix of `rows` rows of `cols` 16-bit values.
+__device__ __forceinline__ const unsigned short* end_16(const void* p, int64_t rows, int64_t ld, int cols) {
+  return static_cast<const unsigned short*>(p) + (rows - 1) * ld + cols;
 }
 
 template <int ACT>
@@ -44,11 +62,14 @@ __device__ __forceinline__ void gated_grad_rows(const GatedGradParams& p) {
   const int col = (blockIdx.x * kGatedGradThreads + threadIdx.x) * 8;
   if (col >= p.N) return;
   const int n = p.N - col;
+  const void* end_d = end_16(p.dH, p.M, p.ld_dh, p.N);
+  const void* end_g = end_16(p.G, p.M, p.ld_g, p.N);
+  const void* end_u = end_16(p.U, p.M, p.ld_u, p.N);
   for (int row = blockIdx.y; row < p.M; row += gridDim.y) {
     const int64_t r = row;
-    const uint4 d4 = load8_16(static_cast<const unsigned short*>(p.dH) + r * p.ld_dh + col, n, vec);
-    const uint4 g4 = load8_16(static_cast<const unsigned short*>(p.G) + r * p.ld_g + col, n, vec);
-    const uint4 u4 = load8_16(static_cast<const unsigned short*>(p.U) + r * p.ld_u + col, n, vec);
+    const uint4 d4 = load8_16(static_cast<const unsigned short*>(p.dH) + r * p.ld_dh + col, n, vec, p.dH, end_d);
+    const uint4 g4 = load8_16(static_cast<const unsigned short*>(p.G) + r * p.ld_g + col, n, vec, p.G, end_g);
+    const uint4 u4 = load8_16(static_cast<const unsigned short*>(p.U) + r * p.ld_u + col, n, vec, p.U, end_u);
     const uint32_t dw[4] = {d4.x, d4.y, d4.z, d4.w}, gw[4] = {g4.x, g4.y, g4.z, g4.w},
                    uw[4] = {u4.x, u4.y, u4.z, u4.w};
     float dg[8], du[8];
@@ -88,28 +109,34 @@ __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const Gat
 // Row quantization
 // ----------------------------------------------------------------------------
 // scale = max |x| / 127 (one IEEE fp32 division), q = x / scale rounded to the
-// nearest integer, ties to even, exactly.  Two steps:
-//   * t = x * (1 / scale), off from the quotient by at most 127 * 2^-23; one
-//     fused multiply-add onto 1.5 * 2^23 leaves its nearest integer in the low
-//     mantissa bits, a second gives the distance of t from that integer;
-//   * where a distance comes within 2^-14 of a half (a few values in ten
-//     thousand), the chunk is settled by remainders: r = x - q scale, which
-//     one fused multiply-add gives without error (|r| stays below 2 scale and
-//     is a multiple of scale's last place).
-// So codes do not depend on how a division rounds.  |q| <= 127.
+// nearest integer, ties to even, exactly.  One fused multiply-add of x * inv
+// onto 1.5 * 2^23 leaves the nearest integer in the low mantissa bits; what
+// makes it exact is inv, 1 / scale rounded in the direction that ties need:
+//   * x and max |x| = A are integers below 2^11 times powers of two, so 127 x /
+//     A either is a half-integer exactly (a rational tie) or stays away from
+//     every half-integer by 1 / (2 * 127 * 2047) of itself or more, 1.9e-6.
+//     Scale and inv are off by 2^-24 and 2^-23, 1.8e-7: only rational ties
+//     are in doubt;
+//   * at a rational tie x / scale is off the tie to the side that scale's
+//     rounding sends it: away from zero where scale < A / 127, so inv is
+//     rounded up there, and down where scale > A / 127;
+//   * where scale = A / 127 exactly, ties are true ones: inv is exact if scale
+//     is a power of two, and the row is settled by remainders otherwise (8 of
+//     1024 fp16 maxima; no bf16 one), as are rows with scale below 2^-64, whose
+//     rounding may be coarser.
+// |q| <= 127.
 //
 // Bound by memory: 2 bytes in and 1 out an element, each read once.  A row is
 // held in registers between its maximum and its codes (up to THREADS * 8 HELD
-// values; what a longer row has more is read again, from L2), and the next
-// row's loads are in flight meanwhile.
+// values; what a longer row has more is read again, from L2).  Enough rows are
+// in flight per SM to cover the memory's latency.
 struct QuantizeParams {
   const void* X;
   int8_t* Q;
   float* scale;
   int64_t ldx, ldq;
   int M, K;
-  int vec;  // rows of X start on 16-byte boundaries, rows of Q on 8-byte ones
-  int bf16;
+  int vec_out;  // rows of Q start on 8-byte boundaries
 };
 
 constexpr float kTwo64 = 18446744073709551616.0f;
@@ -125,76 +152,74 @@ __device__ __forceinline__ int quantize_settled(float x, float scale, float inv)
   return static_cast<int>(q);
 }
 
-// Eight codes of one chunk, packed.  `tiny`: scale is below 2^-64, where 1 /
-// scale could overflow; values and scale are multiplied by 2^64 first (exact),
-// and `inv` belongs to the product.
-__device__ __forceinline__ uint2 quantize8(const uint4& v, float scale, float inv, bool tiny, bool bf16) {
+// Eight codes of one chunk, packed, each settled by its remainder.  `tiny`:
+// scale is below 2^-64, where 1 / scale could overflow; values and scale are
+// multiplied by 2^64 first (exact), and `inv` belongs to the product.  Out of
+// line: it is rarely called, and its registers would cost the others warps.
+template <bool BF16>
+__device__ __noinline__ uint2 quantize8_settled(uint4 v, float scale, float inv, bool tiny) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  float x[8];
+  uint32_t out[2] = {0u, 0u};
+  const float up = tiny ? kTwo64 : 1.0f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const float2 f = unpack_16(w[e], bf16);
-    x[2 * e] = f.x;
-    x[2 * e + 1] = f.y;
-  }
-  if (!tiny) {
-    uint32_t q[8];
-    float worst = 0.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float f = fmaf(x[e], inv, kMagic);
-      worst = fmaxf(worst, fabsf(fmaf(x[e], inv, kMagic - f)));
-      q[e] = __float_as_uint(f);
-    }
-    if (worst < 0.5f - 6.103515625e-5f)
-      return make_uint2(__byte_perm(__byte_perm(q[0], q[1], 0x0040), __byte_perm(q[2], q[3], 0x0040), 0x5410),
-                        __byte_perm(__byte_perm(q[4], q[5], 0x0040), __byte_perm(q[6], q[7], 0x0040), 0x5410));
-  }
-  uint32_t out[2] = {0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int q = quantize_settled(tiny ? x[e] * kTwo64 : x[e], tiny ? scale * kTwo64 : scale, inv);
-    out[e >> 2] |= static_cast<uint32_t>(q & 0xff) << ((e & 3) * 8);
+    const float2 x = unpack_16(w[e], BF16);
+    const int q0 = quantize_settled(x.x * up, scale * up, inv), q1 = quantize_settled(x.y * up, scale * up, inv);
+    out[e >> 1] |= (static_cast<uint32_t>(q0 & 0xff) | (static_cast<uint32_t>(q1 & 0xff) << 8)) << ((e & 1) * 16);
   }
   return make_uint2(out[0], out[1]);
 }
 
+// Eight codes of one chunk, packed.
+template <bool BF16>
+__device__ __forceinline__ uint2 quantize8(const uint4& v, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
+  uint32_t half[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = fma2(unpack_16(w[e], BF16), same2(inv), same2(kMagic));
+    half[e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040);
+  }
+  return make_uint2(__byte_perm(half[0], half[1], 0x5410), __byte_perm(half[2], half[3], 0x5410));
+}
+
 // THREADS threads per row: a warp (several rows a block) or a whole block of
-// them.  HELD: 16-byte chunks a thread keeps.
+// them.  HELD: 16-byte chunks a thread keeps.  VEC: rows of X start on 16-byte
+// boundaries.
 template <int THREADS, int HELD>
 struct QuantizeCfg {
-  static constexpr int BLOCK = THREADS < 256 ? 256 : THREADS;
+  static constexpr int BLOCK = THREADS == 32 ? 256 : THREADS;
   static constexpr int ROWS = BLOCK / THREADS;
   static constexpr int HELD_VALUES = THREADS * HELD * 8;
+  static constexpr int BLOCKS_PER_SM = 1536 / BLOCK;
 };
 
-template <int THREADS, int HELD>
-__global__ void __launch_bounds__(QuantizeCfg<THREADS, HELD>::BLOCK) quantize_rows_kernel(const QuantizeParams p) {
+template <int THREADS, int HELD, bool BF16, bool VEC>
+__global__ void __launch_bounds__(QuantizeCfg<THREADS, HELD>::BLOCK,
+                                  QuantizeCfg<THREADS, HELD>::BLOCKS_PER_SM) quantize_rows_kernel(const QuantizeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   using Cfg = QuantizeCfg<THREADS, HELD>;
   constexpr int WARPS = Cfg::BLOCK / 32;
+  constexpr int STEP = THREADS * 8;  // values between a thread's chunks
   __shared__ uint32_t warp_max[2][WARPS];
-  const int t = threadIdx.x % THREADS;
-  const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
-  const int chunks = (p.K + 7) / 8;
+  const int first = (threadIdx.x % THREADS) * 8;  // this thread's chunks start at first + i STEP
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * Cfg::ROWS + threadIdx.x / THREADS;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * Cfg::ROWS;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * Cfg::ROWS + threadIdx.x / THREADS;
-  auto row_of = [&](int64_t r) { return static_cast<const unsigned short*>(p.X) + r * p.ldx; };
-  auto load = [&](int64_t r, uint4 (&held)[HELD]) {
+  const unsigned short* src = static_cast<const unsigned short*>(p.X) + row0 * p.ldx + first;
+  int8_t* dst = p.Q + row0 * p.ldq + first;
+  const void* end = end_16(p.X, p.M, p.ldx, p.K);
+  const bool vec_out = p.vec_out != 0;
+  int parity = 0;
+  for (int64_t row = row0; row < p.M; row += stride, parity ^= 1) {
+    uint4 held[HELD];
 #pragma unroll
     for (int i = 0; i < HELD; ++i) {
-      const int c = t + i * THREADS;
+      const int n = p.K - first - i * STEP;
       held[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < p.M && c < chunks) held[i] = load8_16(row_of(r) + c * 8, p.K - c * 8, vec);
+      if (n > 0) held[i] = load8_16(src + i * STEP, n, VEC, p.X, end);
     }
-  };
-  uint4 held[HELD], next[HELD];
-  load(row, held);
-  int parity = 0;
-  for (; row < p.M; row += stride, parity ^= 1) {
-    load(row + stride, next);
     // The maximum of the magnitudes' bits: fp16 and bf16 order as integers,
     // and infinities and NaN come out above every finite value.
     uint32_t best = 0u;
@@ -206,7 +231,7 @@ __global__ void __launch_bounds__(QuantizeCfg<THREADS, HELD>::BLOCK) quantize_ro
     };
 #pragma unroll
     for (int i = 0; i < HELD; ++i) take(held[i]);
-    for (int c = t + HELD * THREADS; c < chunks; c += THREADS) take(load8_16(row_of(row) + c * 8, p.K - c * 8, vec));
+    for (int c = HELD * STEP; c < p.K - first; c += STEP) take(load8_16(src + c, p.K - first - c, VEC, p.X, end));
     best = max(best & 0xffffu, best >> 16);
     best = __reduce_max_sync(0xffffffffu, best);
     if (THREADS > 32) {
@@ -215,34 +240,36 @@ __global__ void __launch_bounds__(QuantizeCfg<THREADS, HELD>::BLOCK) quantize_ro
       best = __reduce_max_sync(0xffffffffu, warp_max[parity][threadIdx.x & (WARPS - 1)]);
     }
     const float amax =
-        bf16 ? __uint_as_float(best << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(best)));
-    const bool finite = best < (bf16 ? 0x7f80u : 0x7c00u);
+        BF16 ? __uint_as_float(best << 16) : __half2float(__ushort_as_half(static_cast<unsigned short>(best)));
+    const bool finite = best < (BF16 ? 0x7f80u : 0x7c00u);
     const float scale = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7fffffffu);
     const bool live = finite && scale > 0.0f;
     const bool tiny = scale < 5.421010862427522e-20f;  // 2^-64
-    const float inv = live ? __fdiv_rn(1.0f, tiny ? scale * kTwo64 : scale) : 0.0f;
-    if (t == 0) p.scale[row] = scale;
-    int8_t* dst = p.Q + row * p.ldq;
+    const float off = fmaf(-scale, 127.0f, amax);      // exact: the sign of A / 127 - scale
+    const bool settle = tiny || (off == 0.0f && (__float_as_uint(scale) & 0x7fffffu) != 0u);
+    const float base = tiny ? scale * kTwo64 : scale;
+    const float inv = !live ? 0.0f : off > 0.0f ? __fdiv_ru(1.0f, base) : __fdiv_rd(1.0f, base);
+    if (first == 0) p.scale[row] = scale;
     auto put = [&](int c, const uint4& v) {
-      const uint2 q = live ? quantize8(v, scale, inv, tiny, bf16) : make_uint2(0u, 0u);
-      const int n = p.K - c * 8;
-      if (vec && n >= 8) {
-        *reinterpret_cast<uint2*>(dst + c * 8) = q;
+      const uint2 q = !live ? make_uint2(0u, 0u)
+                      : settle ? quantize8_settled<BF16>(v, scale, inv, tiny)
+                               : quantize8<BF16>(v, inv);
+      const int n = p.K - first - c;
+      if (vec_out && n >= 8) {
+        *reinterpret_cast<uint2*>(dst + c) = q;
       } else {
         const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (e < n) dst[c * 8 + e] = static_cast<int8_t>(w[e >> 2] >> ((e & 3) * 8));
+          if (e < n) dst[c + e] = static_cast<int8_t>(w[e >> 2] >> ((e & 3) * 8));
       }
     };
 #pragma unroll
-    for (int i = 0; i < HELD; ++i) {
-      const int c = t + i * THREADS;
-      if (c < chunks) put(c, held[i]);
-    }
-    for (int c = t + HELD * THREADS; c < chunks; c += THREADS) put(c, load8_16(row_of(row) + c * 8, p.K - c * 8, vec));
-#pragma unroll
-    for (int i = 0; i < HELD; ++i) held[i] = next[i];
+    for (int i = 0; i < HELD; ++i)
+      if (p.K - first > i * STEP) put(i * STEP, held[i]);
+    for (int c = HELD * STEP; c < p.K - first; c += STEP) put(c, load8_16(src + c, p.K - first - c, VEC, p.X, end));
+    src += stride * p.ldx;
+    dst += stride * p.ldq;
   }
 }
 
@@ -268,6 +295,23 @@ __global__ void __launch_bounds__(256) bias_fill_kernel(const BiasFillParams p) 
     if (p.relu) v = v > 0.0f ? v : 0.0f;
     static_cast<unsigned short*>(p.C)[m * p.ldc + n] = round_16(v, p.bf16 != 0);
   }
+}
+
+// ----------------------------------------------------------------------------
+// Padded copies of up to three operands that TMA cannot describe, in one launch
+// ----------------------------------------------------------------------------
+struct PadSetParams {
+  RepackParams m[3];  // blockIdx.y picks one
+};
+
+__global__ void __launch_bounds__(256) pad_set_kernel(const __grid_constant__ PadSetParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const RepackParams& m = p.m[blockIdx.y];
+  if (m.chunks < (int64_t(1) << 31))
+    pad_rows_body<uint32_t>(m);
+  else
+    pad_rows_body<int64_t>(m);
 }
 
 }  // namespace tg
