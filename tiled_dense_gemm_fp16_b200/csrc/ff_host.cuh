@@ -369,13 +369,13 @@ tg_status ff_make_copies(FfMat* const* mats, int count, uint8_t*& ws, cudaStream
     r.cols = static_cast<int>(m.cols);
     r.cols_pad = static_cast<int>(ld);
     r.chunks = m.rows * (ld / 8);
-    most = r.chunks > most ? r.chunks : most;
+    most = m.rows > most ? m.rows : most;
     m.p = ws;
     m.ld = ld;
     ws += bytes;
   }
   if (n == 0) return TG_OK;
-  int64_t blocks = (most + 256 * 4 - 1) / (256 * 4);
+  int64_t blocks = (most + 7) / 8;  // eight warps, a row each
   const int64_t cap = static_cast<int64_t>(info->sm_count) * 8;
   blocks = blocks > cap ? cap : blocks;
   cudaLaunchConfig_t cfg;
