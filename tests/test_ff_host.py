@@ -193,3 +193,44 @@ def test_python_refusals():
         tg.gemm_i8(x.to(torch.int8), x, w, w)
     with pytest.raises(ValueError, match="CUDA"):
         tg.gated_i8(x.to(torch.int8), x, w, w, w, w)
+
+
+# ---------------------------------------------------------------------------
+# The 64-bit forms that the GPU tests compare with
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu"])
+def test_reference_gradients_against_differences(act):
+    import numpy as np
+
+    import ff_ref as ref
+    rng = np.random.default_rng(3)
+    M, N, K = 5, 4, 6
+    x, wg, wu, dh = (rng.standard_normal(s) for s in ((M, K), (N, K), (N, K), (M, N)))
+    g, u = x @ wg.T, x @ wu.T
+    assert np.abs(g).min() > 1e-4  # relu: no kink within a step
+    grads, _ = ref.gated_backward(dh, x, wg, wu, g, u, act, "f16")
+
+    def loss(*args):
+        return float((ref.gated(*args, act, "f16")[0][0] * dh).sum())
+
+    for i, (t, grad) in enumerate(zip((x, wg, wu), grads)):
+        for at in np.ndindex(*t.shape):
+            ends = []
+            for d in (1e-5, -1e-5):
+                args = [x.copy(), wg.copy(), wu.copy()]
+                args[i][at] += d
+                ends.append(loss(*args))
+            assert abs((ends[0] - ends[1]) / 2e-5 - grad[at]) <= 1e-7 * (1 + abs(grad[at])), (i, at)
+
+
+def test_reference_quantization():
+    import numpy as np
+
+    import ff_ref as ref
+    x = np.array([[127.0, 0.5, 1.5, -2.5, -63.5], [0.0] * 5, [1.0, np.inf, 0, 0, 0], [-4.0, 1.0, 2.0, 0.0157, -0.0158]])
+    q, s = ref.quantize(x)
+    assert s[0] == 1.0 and list(q[0]) == [127, 0, 2, -2, -64]      # ties to even
+    assert s[1] == 0.0 and not q[1].any()
+    assert np.isnan(s[2]) and not q[2].any()
+    assert list(q[3]) == [-127, 32, 64, 0, -1]                     # 0.0157 / (4 / 127) = 0.498..., 0.0158: 0.502

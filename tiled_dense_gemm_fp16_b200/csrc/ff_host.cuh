@@ -184,24 +184,105 @@ tg_status launch_ff_pair(const FfProduct& f, int bn, cudaStream_t stream, Device
                    : launch_ff_pair_cfg<6, 256, 16, KIND, GATED>(f, stream, info);
 }
 
-// CTAs along K that share a panel of the small-M kernel: as many as fill the
-// device, up to 8.  With one CTA per SM a cluster of 8 leaves SMs of its GPC
-// unused (16 such clusters already take two waves: M = 256, N = K = 1024 gated
-// 23 us against 12 with clusters of 4), so 8 only for few panels.
-int ff_splits(int64_t panels, int k_blocks, bool two_per_sm, int sms) {
-  const int most = two_per_sm || panels <= 8 ? 8 : 4;
-  int64_t s = (two_per_sm ? 2 : 1) * sms / panels;
-  s = s < 1 ? 1 : (s > most ? most : s);
-  return static_cast<int>(s > k_blocks ? k_blocks : s);
+// ---------------------------------------------------------------------------
+// Small-M kernel
+// ---------------------------------------------------------------------------
+using FfSkinnyKernel = void (*)(FfMaps, FfSkinnyParams);
+
+int ff_skinny_index(const FfProduct& f) { return (f.kind == kFfI8 ? 1 : 0) + (f.gated ? 2 : 0); }
+
+FfSkinnyKernel ff_skinny_kernel_of(const FfProduct& f) {
+  if (f.kind == kFfI8) return f.gated ? ff_skinny_kernel<kFfI8, true> : ff_skinny_kernel<kFfI8, false>;
+  return f.gated ? ff_skinny_kernel<kFfF16, true> : ff_skinny_kernel<kFfF16, false>;
 }
 
-template <int KIND, bool GATED>
-tg_status launch_ff_skinny(const FfProduct& f, cudaStream_t stream, DeviceInfo* info) {
+struct FfSkinnyPlan {
+  int m_pad, stages, smem, k_blocks, splits;
+  int64_t panels, waves;
+};
+
+// Clusters of `splits` CTAs that fit on the device with one CTA per SM, asked
+// of the runtime once per number of splits (for the largest launch, whose
+// shared memory allows one): GPCs hold different numbers of SMs, so there is no
+// formula (a B200 gave 148, 74, 45, 33, 26, 22, 15, 15 for 1 .. 8).
+int ff_resident_clusters(const FfProduct& f, int splits, DeviceInfo* info) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  short& known = info->ff_clusters[splits];
+  if (known == 0) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(splits), 1024, 1);
+    cfg.blockDim = dim3(FfSkinnyCfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(FfSkinnyCfg::MAX_SMEM);
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(splits);
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, ff_skinny_kernel_of(f), &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = info->sm_count / splits > 0 ? info->sm_count / splits : 1;
+    }
+    known = static_cast<short>(n > 32767 ? 32767 : n);
+  }
+  return known;
+}
+
+// The plan of a product of at most 256 rows, or false if the kernel cannot
+// take it.  Splits of K, by estimated time in us: at most as many as give every
+// SM two CTAs (one where two do not fit).  A k-block takes 0.59 with one CTA per
+// SM and 0.72 with two (the stream from memory), a wave 1.5 for its start, a
+// second CTA per SM 1.5 + M / 40 more for the partials both have to move and
+// add.  Measured, us, gated fp16 N = K = 2048 with 4 / 8 splits: M = 128 9.4 /
+// 12.2, M = 1 6.0 / 6.0; 4096 with 2 / 4: M = 128 19.4 / 16.8; 8-bit 5120 at M =
+// 128 with 4 in one wave / 7 that do not quite fit: 13 / 21.
+bool ff_skinny_plan(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* out) {
   using Cfg = FfSkinnyCfg;
-  constexpr int kMaxSmem = 1024 + 220 * 1024 + Cfg::BAR_BYTES;
-  auto kernel = ff_skinny_kernel<KIND, GATED>;
-  constexpr unsigned kBit = 1u << (8 + (KIND == kFfI8 ? 1 : 0) + (GATED ? 2 : 0));
-  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->ff_attr, kBit, kMaxSmem)) return TG_ERR_LAUNCH;
+  if (!ff_set_smem(reinterpret_cast<const void*>(ff_skinny_kernel_of(f)), info->ff_attr, 1u << (8 + ff_skinny_index(f)),
+                   Cfg::MAX_SMEM))
+    return false;
+  FfSkinnyPlan pl;
+  pl.m_pad = static_cast<int>((f.M + 15) / 16 * 16);
+  const int64_t kb = (f.K + f.k_elems() - 1) / f.k_elems() * f.k_sources;
+  const int cols = f.gated ? 64 : 128;
+  pl.panels = (f.N + cols - 1) / cols;
+  if (kb > INT_MAX || pl.panels > 65535) return false;
+  pl.k_blocks = static_cast<int>(kb);
+  // Two CTAs per SM while a ring stays within 112 KiB; at m_pad <= 32 three
+  // stages of 64 KiB stream best.
+  const int budget = (pl.m_pad <= 32 ? 64 : (pl.m_pad <= 128 ? 112 : 220)) * 1024;
+  const int stage_bytes = Cfg::stage_bytes(pl.m_pad);
+  pl.stages = budget / stage_bytes;
+  pl.stages = pl.stages > Cfg::MAX_STAGES ? Cfg::MAX_STAGES : pl.stages;
+  // The partial [m_pad][128] reuses the ring after the main loop.
+  if (pl.stages < 2 || pl.stages * stage_bytes < pl.m_pad * Cfg::PANEL * 4) return false;
+  pl.smem = Cfg::smem_bytes(pl.m_pad, pl.stages);
+  double best = 0.0;
+  pl.splits = 0;
+  const int per_sm = pl.m_pad <= 128 ? 2 : 1;
+  const int64_t slots = per_sm * info->sm_count;
+  const int64_t most = pl.panels >= slots ? 1 : slots / pl.panels;
+  for (int s = 1; s <= 8 && s <= most && s <= pl.k_blocks; ++s) {
+    const int64_t resident = per_sm * ff_resident_clusters(f, s, info);
+    const int64_t waves = (pl.panels + resident - 1) / resident;
+    const bool second = pl.panels > ff_resident_clusters(f, s, info);
+    const double cost = static_cast<double>(waves) * ((pl.k_blocks + s - 1) / s * (second ? 0.72 : 0.59) + 1.5) +
+                        (second ? 1.5 + pl.m_pad / 40.0 : 0.0) + 0.05 * s;
+    if (pl.splits == 0 || cost < best) {
+      best = cost;
+      pl.splits = s;
+      pl.waves = waves;
+    }
+  }
+  *out = pl;
+  return true;
+}
+
+tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStream_t stream) {
+  using Cfg = FfSkinnyCfg;
   const int ke = f.k_elems();
   FfSkinnyParams p;
   std::memset(&p, 0, sizeof p);
@@ -216,49 +297,44 @@ tg_status launch_ff_skinny(const FfProduct& f, cudaStream_t stream, DeviceInfo* 
   p.bias = f.bias;
   p.M = static_cast<int>(f.M);
   p.N = static_cast<int>(f.N);
-  p.m_pad = static_cast<int>((f.M + 15) / 16 * 16);
-  p.k_blocks_src = static_cast<int>((f.K + ke - 1) / ke);
-  p.k_blocks = p.k_blocks_src * f.k_sources;
-  const bool two_per_sm = p.m_pad <= 128;
-  const int budget = (p.m_pad <= 32 ? 64 : (two_per_sm ? 112 : 220)) * 1024;
-  const int stage_bytes = Cfg::stage_bytes(p.m_pad);
-  int stages = budget / stage_bytes;
-  stages = stages > Cfg::MAX_STAGES ? Cfg::MAX_STAGES : stages;
-  // The partial [m_pad][128] reuses the ring after the main loop.
-  if (stages < 2 || stages * stage_bytes < p.m_pad * Cfg::PANEL * 4) return TG_ERR_INTERNAL;
-  p.stages = stages;
+  p.m_pad = pl.m_pad;
+  p.k_blocks_src = pl.k_blocks / f.k_sources;
+  p.k_blocks = pl.k_blocks;
+  p.stages = pl.stages;
+  p.splits = pl.splits;
   p.a_stage_bytes = static_cast<uint32_t>(p.m_pad * 128);
   uint32_t cols = 32;
   while (cols < static_cast<uint32_t>(p.m_pad)) cols <<= 1;
   p.tmem_cols = cols;
-  p.idesc = make_idesc_ff(KIND, f.bf16, Cfg::PANEL, p.m_pad, f.b_kn, false);
+  p.idesc = make_idesc_ff(f.kind, f.bf16, Cfg::PANEL, p.m_pad, f.b_kn, false);
   p.b_kmajor = f.b_kn ? 0 : 1;
   p.bf16 = f.bf16 ? 1 : 0;
   p.act = f.act;
   p.relu = f.relu;
   p.save = f.save ? 1 : 0;
+  // Four k-blocks ahead where a CTA streams 16 or more of two weights (32 of
+  // one).  Measured back to back, us, without / with: gated 64 x 8192 x 8192 49.2
+  // / 46.7, 8-bit gated 64 x 8192 x 4096 17.1 / 15.9; 8-bit 16 x 8192 x 8192 (16
+  // of one weight) 14.7 / 15.2.
+  p.prefetch_kb = p.k_blocks / p.splits >= (f.gated ? 16 : 32) ? 4 : 0;
   p.wait_budget_ns = wait_budget(p.k_blocks);
-  const int out = GATED ? 64 : 128;
-  const int64_t panels = (f.N + out - 1) / out;
-  const int splits = ff_splits(panels, p.k_blocks, two_per_sm, info->sm_count);
-  p.splits = splits;
   FfMaps maps;
   std::memset(&maps, 0, sizeof maps);
   for (int i = 0; i < f.k_sources; ++i)
     if (!ff_encode(&maps.a[i], f.a[i], ke, p.m_pad, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   for (int i = 0; i < f.weights(); ++i)
-    if (!ff_encode(&maps.b[i], f.b[i], f.b_kn ? 64 : ke, f.b_kn || GATED ? 64 : Cfg::PANEL,
+    if (!ff_encode(&maps.b[i], f.b[i], f.b_kn ? 64 : ke, f.b_kn || f.gated ? 64 : Cfg::PANEL,
                    CU_TENSOR_MAP_SWIZZLE_128B))
       return TG_ERR_LAUNCH;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>(splits), static_cast<unsigned>(panels), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.splits), static_cast<unsigned>(pl.panels), 1);
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(p.m_pad, stages));
+  cfg.dynamicSmemBytes = static_cast<size_t>(pl.smem);
   cfg.stream = stream;
   LaunchAttrs la;
-  la.fill(cfg, static_cast<unsigned>(splits));
-  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) {
+  la.fill(cfg, static_cast<unsigned>(pl.splits));
+  if (cudaLaunchKernelEx(&cfg, ff_skinny_kernel_of(f), maps, p) != cudaSuccess) {
     cudaGetLastError();
     return TG_ERR_LAUNCH;
   }
@@ -274,21 +350,16 @@ tg_status launch_ff_skinny(const FfProduct& f, cudaStream_t stream, DeviceInfo* 
 // 68.3, 16384 x 4096 77 / 61; dX of N = K = 8192 69 / 110; 8-bit 8192 x 8192 23 /
 // 28.  At M <= 128 it loses at most 1 us, where K is short (gated 8-bit 8192 x
 // 1024, M = 128: 10.2 / 9.0).  Products whose A is stored K x M never take it.
-bool ff_skinny_route(const FfProduct& f, int sms) {
-  if (f.a_km || f.row_sources > 1 || f.M > kSkinnyMaxM) return false;
-  const int out = f.gated ? 64 : 128;
-  const int64_t panels = (f.N + out - 1) / out;
-  if (panels > 65535) return false;
+bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
+  if (f.a_km || f.row_sources > 1 || f.M > kSkinnyMaxM || !ff_skinny_plan(f, info, plan)) return false;
   if (f.M <= 128) return true;
-  const int64_t kb = (f.K + f.k_elems() - 1) / f.k_elems() * f.k_sources;
-  if (kb > INT_MAX) return false;
-  const int splits = ff_splits(panels, static_cast<int>(kb), false, sms);
   const double rows = static_cast<double>(f.M);
   const double split_k = 6.0 + rows / 64.0 +
-                         static_cast<double>((panels * splits + sms - 1) / sms) *
-                             static_cast<double>((kb + splits - 1) / splits) * (0.2 + 0.3 * rows / 256.0);
-  const int64_t tiles = (f.N * (f.gated ? 2 : 1) + 255) / 256, pairs = sms / 2;
-  return split_k < 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * static_cast<double>(kb) * 0.344;
+                         static_cast<double>(plan->waves) *
+                             static_cast<double>((plan->k_blocks + plan->splits - 1) / plan->splits) *
+                             (0.2 + 0.3 * rows / 256.0);
+  const int64_t tiles = (f.N * (f.gated ? 2 : 1) + 255) / 256, pairs = info->sm_count / 2;
+  return split_k < 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * static_cast<double>(plan->k_blocks) * 0.344;
 }
 
 // Accumulator width of the pair kernel, by estimated time in units of one
@@ -313,11 +384,8 @@ int ff_tile_width(const FfProduct& f, int64_t pairs) {
 }
 
 tg_status launch_ff(const FfProduct& f, cudaStream_t stream, DeviceInfo* info) {
-  if (ff_skinny_route(f, info->sm_count)) {
-    if (f.kind == kFfI8)
-      return f.gated ? launch_ff_skinny<kFfI8, true>(f, stream, info) : launch_ff_skinny<kFfI8, false>(f, stream, info);
-    return f.gated ? launch_ff_skinny<kFfF16, true>(f, stream, info) : launch_ff_skinny<kFfF16, false>(f, stream, info);
-  }
+  FfSkinnyPlan plan;
+  if (ff_skinny_route(f, info, &plan)) return launch_ff_skinny(f, plan, stream);
   const int bn = ff_tile_width(f, info->sm_count / 2);
   if (f.kind == kFfI8)
     return f.gated ? launch_ff_pair<kFfI8, true>(f, bn, stream, info) : launch_ff_pair<kFfI8, false>(f, bn, stream, info);

@@ -34,6 +34,7 @@ struct FfSkinnyParams {
   uint32_t idesc;
   int b_kmajor;
   int bf16, act, relu, save;
+  int prefetch_kb;            // k-blocks of the weight brought into L2 ahead of the previous kernel's end
   uint64_t wait_budget_ns;
 };
 
@@ -45,6 +46,7 @@ struct FfSkinnyCfg {
   static constexpr int THREADS = 192;
   static constexpr int MAX_STAGES = 8;
   static constexpr int BAR_BYTES = 256;
+  static constexpr int MAX_SMEM = 1024 + 220 * 1024 + BAR_BYTES;
   static int stage_bytes(int m_pad) { return W_STAGE_BYTES + m_pad * 128; }
   static int smem_bytes(int m_pad, int stages) { return 1024 + stages * stage_bytes(m_pad) + BAR_BYTES; }
 };
@@ -156,6 +158,26 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish_alloc_permit();
+  }
+  if (threadIdx.x == 0) {
+    // The weight's first boxes come into L2 while the previous kernel on the
+    // stream still drains.  That is a hint, which reads nothing into this
+    // kernel: should that kernel write the weight, its stores update the same
+    // L2 lines before the loads below, which wait for it.
+    const int ahead = min(kb_hi, kb_lo + p.prefetch_kb);
+    for (int kb = kb_lo; kb < ahead; ++kb) {
+      const int k_src = kb >= p.k_blocks_src ? 1 : 0;
+      const int k0 = (kb - k_src * p.k_blocks_src) * K_ELEMS;
+      if (GATED) {
+        tma_prefetch_l2_2d(&maps.b[0], k0, n0);
+        tma_prefetch_l2_2d(&maps.b[1], k0, n0);
+      } else if (KIND == kFfI8 || p.b_kmajor) {
+        tma_prefetch_l2_2d(&maps.b[k_src], k0, n0);
+      } else {
+        tma_prefetch_l2_2d(&maps.b[k_src], n0, k0);
+        tma_prefetch_l2_2d(&maps.b[k_src], n0 + 64, k0);
+      }
+    }
   }
   tcgen05_fence_before_sync();
   __syncthreads();

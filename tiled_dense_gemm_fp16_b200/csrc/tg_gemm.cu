@@ -52,6 +52,7 @@ struct DeviceInfo {
   bool w4_attr = false;
   bool w4_decode_attr = false;
   unsigned ff_attr = 0;       // one bit per feed-forward kernel instance with its attribute set
+  short ff_clusters[9] = {};  // clusters of 1 .. 8 CTAs, one per SM, that fit on the device (0: not asked yet)
   void* static_ws = nullptr;  // device address of g_static_workspace on this device
 };
 
