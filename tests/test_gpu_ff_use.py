@@ -442,3 +442,59 @@ def test_refusals():
             call()
             pytest.fail(f"case {i} was taken")
     _ok()
+
+
+def test_one_dimension():
+    """A single row without a row dimension."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, wg, wu, dh = _randn(1, (40,), "f16"), _randn(2, (24, 40), "f16"), _randn(3, (24, 40), "f16"), _randn(4, (24,), "f16")
+    h, g, u = tg.gated(x, wg, wu, save=True)
+    dx, dwg, dwu = tg.gated_backward(dh, x, wg, wu, g, u)
+    q, s = tg.quantize_i8(x)
+    qw, sw = tg.quantize_i8(wg)
+    y = tg.gemm_i8(q, s, qw, sw)
+    z = tg.gated_i8(q, s, qw, sw, qw, sw)
+    _ok()
+    assert h.shape == g.shape == u.shape == y.shape == z.shape == (24,) and dx.shape == q.shape == (40,) and s.shape == ()
+    two = tg.gated(x[None], wg, wu, save=True)
+    assert all(torch.equal(a, b[0]) for a, b in zip((h, g, u), two))
+    grads = tg.gated_backward(dh[None], x[None], wg, wu, two[1], two[2])
+    assert torch.equal(dx, grads[0][0]) and torch.equal(dwg, grads[1]) and torch.equal(dwu, grads[2])
+    q2, s2 = tg.quantize_i8(x[None])
+    assert torch.equal(q, q2[0]) and s == s2[0] and torch.equal(y, tg.gemm_i8(q2, s2, qw, sw)[0])
+
+
+FIRST_CALL = """
+import torch
+x, w, dh = (torch.randn(s, device="cuda").half() for s in ((20, 40), (24, 40), (20, 24)))
+a = torch.randint(-127, 128, (200, 48), device="cuda", dtype=torch.int8)
+s = torch.rand(200, device="cuda")
+torch.cuda.synchronize()
+import tiled_dense_gemm_fp16_b200 as tg
+graph = torch.cuda.CUDAGraph()
+
+def run():
+    h, g, u = tg.gated(x, w, w, save=True)
+    q, qs = tg.quantize_i8(x)
+    return (h, *tg.gated_backward(dh, x, w, w, g, u), q, qs, tg.gemm_i8(a, s, a, s), tg.gated_i8(a, s, a, s, a, s))
+
+with torch.cuda.graph(graph):
+    out = run()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(p, q) for p, q in zip(out, run()))
+assert tg.device_status()[0] == tg.Status.OK
+del graph
+print("same")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: nothing they set up is refused during a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
