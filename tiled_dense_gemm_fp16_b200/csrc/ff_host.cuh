@@ -111,7 +111,7 @@ template <int STAGES, int BN, int EPI_WARPS, int KIND, bool GATED>
 tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = FfPairCfg<STAGES, BN, EPI_WARPS>;
   auto kernel = ff_pair_kernel<STAGES, BN, EPI_WARPS, KIND, GATED>;
-  constexpr unsigned kBit = 1u << ((BN == 512 ? 1 : 0) + (KIND == kFfI8 ? 2 : 0) + (GATED ? 4 : 0));
+  constexpr unsigned kBit = 1u << (BN / 256 + (KIND == kFfI8 ? 3 : 0) + (GATED ? 6 : 0));
   if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->ff_attr, kBit, Cfg::SMEM_BYTES)) return TG_ERR_LAUNCH;
   FfMaps maps;
   std::memset(&maps, 0, sizeof maps);
@@ -123,7 +123,7 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
     if (!ff_encode(&maps.a[i], f.a[i], f.a_km ? 64 : ke, f.a_km ? 64 : Cfg::BM, CU_TENSOR_MAP_SWIZZLE_128B))
       return TG_ERR_LAUNCH;
   for (int i = 0; i < f.weights(); ++i)
-    if (!ff_encode(&maps.b[i], f.b[i], f.b_kn ? 64 : ke, f.b_kn || GATED ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_128B))
+    if (!ff_encode(&maps.b[i], f.b[i], f.b_kn ? 64 : ke, f.b_kn ? 64 : (GATED ? Cfg::B_ROWS / 2 : Cfg::B_ROWS), CU_TENSOR_MAP_SWIZZLE_128B))
       return TG_ERR_LAUNCH;
   for (int i = 0; i < f.results(); ++i) {
     p.c[i] = const_cast<void*>(f.c[i].p);
@@ -160,7 +160,7 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
   p.relu = f.relu;
   p.save = f.save ? 1 : 0;
   p.l2_hints = BN == 512 ? 2 : 5;
-  p.idesc = make_idesc_ff(KIND, f.bf16, Cfg::PAIR_M, 256, f.a_km, f.b_kn);
+  p.idesc = make_idesc_ff(KIND, f.bf16, Cfg::PAIR_M, Cfg::SLAB, f.a_km, f.b_kn);
   p.wait_budget_ns = wait_budget(p.k_blocks);
   const int clusters = p.num_tiles < pairs ? p.num_tiles : pairs;
   cudaLaunchConfig_t cfg;
@@ -180,8 +180,11 @@ tg_status launch_ff_pair_cfg(const FfProduct& f, cudaStream_t stream, DeviceInfo
 
 template <int KIND, bool GATED>
 tg_status launch_ff_pair(const FfProduct& f, int bn, cudaStream_t stream, DeviceInfo* info) {
-  return bn == 512 ? launch_ff_pair_cfg<4, 512, 16, KIND, GATED>(f, stream, info)
-                   : launch_ff_pair_cfg<6, 256, 16, KIND, GATED>(f, stream, info);
+  switch (bn) {
+    case 512: return launch_ff_pair_cfg<4, 512, 16, KIND, GATED>(f, stream, info);
+    case 256: return launch_ff_pair_cfg<6, 256, 16, KIND, GATED>(f, stream, info);
+    default: return launch_ff_pair_cfg<8, 128, 8, KIND, GATED>(f, stream, info);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -241,7 +244,7 @@ int ff_resident_clusters(const FfProduct& f, int splits, DeviceInfo* info) {
 // 128 with 4 in one wave / 7 that do not quite fit: 13 / 21.
 bool ff_skinny_plan(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* out) {
   using Cfg = FfSkinnyCfg;
-  if (!ff_set_smem(reinterpret_cast<const void*>(ff_skinny_kernel_of(f)), info->ff_attr, 1u << (8 + ff_skinny_index(f)),
+  if (!ff_set_smem(reinterpret_cast<const void*>(ff_skinny_kernel_of(f)), info->ff_attr, 1u << (12 + ff_skinny_index(f)),
                    Cfg::MAX_SMEM))
     return false;
   FfSkinnyPlan pl;
@@ -344,12 +347,13 @@ tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStrea
 // Few rows take the split-K kernel: M <= 128 always (two CTAs share an SM); for
 // 128 < M <= 256 where its estimated time is the lower one.  A k-block takes
 // its CTA 0.2 us and 0.3 us more at 256 rows, after about 6 us + M / 64 for
-// the launch and the reduction; on the pair kernel one takes 0.344 us, after 5
-// us.  Measured, us, split-K / pair, M = 256: gated fp16 1024 x 1024 10.4 /
-// 10.7, 4096 x 1024 13.4 / 10.9, 1024 x 4096 14.1 / 27.2, 8192 x 8192 69.6 /
-// 68.3, 16384 x 4096 77 / 61; dX of N = K = 8192 69 / 110; 8-bit 8192 x 8192 23 /
-// 28.  At M <= 128 it loses at most 1 us, where K is short (gated 8-bit 8192 x
-// 1024, M = 128: 10.2 / 9.0).  Products whose A is stored K x M never take it.
+// the launch and the reduction; on the pair kernel one takes 0.30 us after 4 us
+// with 128-wide tiles (few columns), 0.344 after 5 with wider ones.  Measured,
+// us, split-K / pair, M = 256: gated fp16 1024 x 1024 10.4 / 8.8, 4096 x 1024
+// 13.4 / 9.8, 1024 x 4096 13.7 / 23.4, 8192 x 8192 69.6 / 68.3, 16384 x 4096 77 /
+// 61; dX of N = K = 8192 69 / 110; 8-bit 8192 x 8192 23 / 28.  At M <= 128 it
+// loses at most 2 us, where K is short (gated 8-bit 4096 x 1024, M = 128: 8.7 /
+// 7.3).  Products whose A is stored K x M never take it.
 bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
   if (f.a_km || f.row_sources > 1 || f.M > kSkinnyMaxM || !ff_skinny_plan(f, info, plan)) return false;
   if (f.M <= 128) return true;
@@ -359,7 +363,9 @@ bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
                              static_cast<double>((plan->k_blocks + plan->splits - 1) / plan->splits) *
                              (0.2 + 0.3 * rows / 256.0);
   const int64_t tiles = (f.N * (f.gated ? 2 : 1) + 255) / 256, pairs = info->sm_count / 2;
-  return split_k < 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * static_cast<double>(plan->k_blocks) * 0.344;
+  const double kb = static_cast<double>(plan->k_blocks);
+  return split_k < (2 * tiles <= pairs ? 4.0 + kb * 0.30
+                                       : 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * kb * 0.344);
 }
 
 // Accumulator width of the pair kernel, by estimated time in units of one
@@ -371,12 +377,17 @@ bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
 // be of half tiles.  Measured, us, 512 / 256: gated fp16 4096 x 8192 with K =
 // 4096 357 / 371, 2048 219 / 220, 1024 130 / 124; 8-bit product 4096 x 8192 with
 // K = 4096 119 / 109, 8192^3 375 / 390; dX of 8192 x 8192 x 4096 825 / 935.
+// Where all 128-wide tiles find a pair at once, they take half the time of
+// 256-wide ones a k-block (us, 128 / 256: gated fp16 500 x 700 x 600 8.3 / 10, 129
+// x 1000 x 264 stored 6.4 / 8.1; 8-bit 1000^3 7.3 / 10); in several waves they
+// gain nothing (3001 x 5003 x 1021 with a last wave of them 59.7 / 58.3).
 int ff_tile_width(const FfProduct& f, int64_t pairs) {
   const int64_t m_tiles = (f.M + 255) / 256 * f.row_sources;
   const int64_t cols = f.N * (f.gated ? 2 : 1);
   const double k = static_cast<double>(f.K * f.k_sources) * (f.kind == kFfI8 ? 0.5 : 1.0);
   const double drain = f.gated ? 160.0 : 256.0;
   const int64_t tiles256 = m_tiles * ((cols + 255) / 256), tiles512 = m_tiles * ((cols + 511) / 512);
+  if (2 * tiles256 <= pairs) return 128;
   const double t256 = static_cast<double>((tiles256 + pairs - 1) / pairs) * k / 0.93 + drain;
   const int64_t rest = tiles512 % pairs;
   const double waves512 = 2.0 * static_cast<double>(tiles512 / pairs) + (rest == 0 ? 0.0 : 2 * rest <= pairs ? 1.0 : 2.0);

@@ -10,7 +10,7 @@
 // The pipeline is that of the fp16 pair kernel: both CTAs load their half of a
 // 256 x BN tile by TMA into an mbarrier ring (128-byte swizzle, 128 bytes of K
 // per k-block), the even CTA's MMA thread issues 256 x 256 MMAs over both SMs'
-// shared memory, eight epilogue warps per CTA drain TMEM.
+// shared memory, the epilogue warps of both CTAs drain TMEM.
 //
 // Gated tiles: of every 256 accumulator columns each CTA supplies the B rows
 // of 128, and these are 64 rows of Wg followed by the same 64 rows of Wu.  So
@@ -64,28 +64,32 @@ template <int STAGES_, int BN_, int EPI_WARPS_>
 struct FfPairCfg {
   static constexpr int BM = 128;
   static constexpr int PAIR_M = 256;
-  static constexpr int BN = BN_;             // accumulator columns per tile
-  static constexpr int SLABS = BN / 256;
+  static constexpr int BN = BN_;                       // accumulator columns per tile
+  static constexpr int SLAB = BN < 256 ? BN : 256;     // of one MMA
+  static constexpr int SLABS = BN / SLAB;
+  static constexpr int B_ROWS = SLAB / 2;              // rows of B a CTA loads per slab
   static constexpr int STAGES = STAGES_;
   static constexpr int MMA_WARP = 1;
   static constexpr int EPI_WARP0 = 2;
   static constexpr int EPI_WARPS = EPI_WARPS_;
-  static constexpr int EPI_COLS = 1024 / EPI_WARPS;    // accumulator columns of a slab per epilogue warp
+  static constexpr int EPI_COLS = SLAB * 4 / EPI_WARPS;  // accumulator columns of a slab per epilogue warp
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
-  static constexpr int K_BYTES = 128;        // bytes of K per k-block
+  static constexpr int K_BYTES = 128;                  // bytes of K per k-block
   static constexpr int A_BYTES = BM * K_BYTES;
-  static constexpr int B_BYTES = (BN / 2) * K_BYTES;
-  static constexpr int HALF_BYTES = 64 * K_BYTES;     // 64 rows (K-major) or one 64-column panel (MN-major)
-  static constexpr int B_SLAB_BYTES = 2 * HALF_BYTES;
-  static constexpr int NUM_ACC = (BN == 256) ? 2 : 1;
+  static constexpr int B_SLAB_BYTES = B_ROWS * K_BYTES;
+  static constexpr int B_BYTES = SLABS * B_SLAB_BYTES;
+  static constexpr int PANEL_BYTES = 64 * K_BYTES;     // one 64-column panel of an MN-major operand
+  static constexpr int NUM_ACC = SLABS == 1 ? 2 : 1;
   static constexpr int TMEM_COLS = 512;
   static constexpr int BAR_BYTES = 256;
-  static constexpr int C_BUF_BYTES = 32 * 64;         // one 32 x 32 box of 16-bit values
-  static constexpr int C_BUFS = 16 / EPI_WARPS;       // staging boxes per epilogue warp
+  static constexpr int C_BUF_BYTES = 32 * 64;          // one 32 x 32 box of 16-bit values
+  static constexpr int C_BUFS = 16 / EPI_WARPS;        // staging boxes per epilogue warp
   static constexpr int C_STAGE_BYTES = EPI_WARPS * C_BUFS * C_BUF_BYTES;
   static constexpr int SMEM_BYTES = 1024 + STAGES * (A_BYTES + B_BYTES) + C_STAGE_BYTES + BAR_BYTES;
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per CTA");
+  static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(NUM_ACC * BN <= TMEM_COLS, "TMEM columns");
+  static_assert(EPI_COLS % 64 == 0, "a warp finishes whole boxes of 32 result columns");
 };
 
 // Tile t of the walk: its place, and for a half tile (one slab of 256
@@ -140,7 +144,7 @@ __device__ __forceinline__ void load_scale16(const float* scale, int col, int N,
 
 // Scales of tile t's rows and columns into L1: `row` is this lane's row inside
 // the tile, `col` its first column inside a slab.
-template <bool GATED, int TILE_N, int SLAB_N>
+template <bool GATED, int TILE_N, int SLAB_N, int OUT>
 __device__ __forceinline__ void ff_prefetch_scales(const FfParams& p, int t, int row, int col) {
   if (t >= p.num_tiles) return;
   const FfTile f = ff_tile(p, t);
@@ -149,7 +153,7 @@ __device__ __forceinline__ void ff_prefetch_scales(const FfParams& p, int t, int
   for (int c = 0; c < TILE_N; c += SLAB_N) {
     if (c > 0 && !f.whole) break;
 #pragma unroll
-    for (int q = 0; q < SLAB_N / 4; q += 32) {
+    for (int q = 0; q < OUT; q += 32) {
       const int n = f.n_blk * TILE_N + f.half * SLAB_N + c + col + q;
       if (n < p.N) {
         prefetch_l1(p.col_scale[0] + n);
@@ -273,7 +277,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
     ff_pair_kernel(const __grid_constant__ FfMaps maps, const FfParams p) {
   using Cfg = FfPairCfg<STAGES, BN, EPI_WARPS>;
   constexpr int K_ELEMS = KIND == kFfI8 ? 128 : 64;   // elements of K per k-block
-  constexpr int SLAB_N = GATED ? 128 : 256;           // result columns per slab of 256 accumulator columns
+  constexpr int SLAB_N = GATED ? Cfg::SLAB / 2 : Cfg::SLAB;  // result columns per slab
   constexpr int TILE_N = Cfg::SLABS * SLAB_N;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
         const int row_src = f.row_src;
         const int slabs = f.whole ? Cfg::SLABS : 1;
         const int m0 = f.m_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
-        const int n0 = f.n_blk * TILE_N + f.half * SLAB_N + static_cast<int>(rank) * (GATED ? 64 : 128);
+        const int n0 = f.n_blk * TILE_N + f.half * SLAB_N + static_cast<int>(rank) * (GATED ? Cfg::B_ROWS / 2 : Cfg::B_ROWS);
         const uint32_t tx = 2 * (Cfg::A_BYTES + slabs * Cfg::B_SLAB_BYTES);
         for (int kb = 0; kb < p.k_blocks; ++kb) {
           if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0x81)) {
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
           if (KIND == kFfF16 && p.a_mnmajor) {
             // A stored K x M: this CTA's 128 rows as two 64 m x 64 k boxes.
             tma_load_2d_pair_hint(adst, ma, full_even, m0, k0, pol_a);
-            tma_load_2d_pair_hint(adst + Cfg::HALF_BYTES, ma, full_even, m0 + 64, k0, pol_a);
+            tma_load_2d_pair_hint(adst + Cfg::PANEL_BYTES, ma, full_even, m0 + 64, k0, pol_a);
           } else {
             tma_load_2d_pair_hint(adst, ma, full_even, k0, m0, pol_a);
           }
@@ -368,15 +372,17 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
           for (int j = 0; j < Cfg::SLABS; ++j) {
             if (j >= slabs) break;
             uint8_t* slab = bdst + j * Cfg::B_SLAB_BYTES;
+            const int n = n0 + SLAB_N * j;
             if (GATED) {
-              // 64 rows of Wg, then the same 64 rows of Wu.
-              tma_load_2d_pair_hint(slab, &maps.b[0], full_even, k0, n0 + 128 * j, pol_b);
-              tma_load_2d_pair_hint(slab + Cfg::HALF_BYTES, &maps.b[1], full_even, k0, n0 + 128 * j, pol_b);
+              // Half of the slab's rows of Wg, then the same rows of Wu.
+              tma_load_2d_pair_hint(slab, &maps.b[0], full_even, k0, n, pol_b);
+              tma_load_2d_pair_hint(slab + Cfg::B_SLAB_BYTES / 2, &maps.b[1], full_even, k0, n, pol_b);
             } else if (KIND == kFfI8 || p.b_kmajor) {
-              tma_load_2d_pair_hint(slab, &maps.b[k_src], full_even, k0, n0 + 256 * j, pol_b);
+              tma_load_2d_pair_hint(slab, &maps.b[k_src], full_even, k0, n, pol_b);
             } else {
-              tma_load_2d_pair_hint(slab, &maps.b[k_src], full_even, n0 + 256 * j, k0, pol_b);
-              tma_load_2d_pair_hint(slab + Cfg::HALF_BYTES, &maps.b[k_src], full_even, n0 + 256 * j + 64, k0, pol_b);
+#pragma unroll
+              for (int q = 0; q < Cfg::B_ROWS / 64; ++q)
+                tma_load_2d_pair_hint(slab + q * Cfg::PANEL_BYTES, &maps.b[k_src], full_even, n + 64 * q, k0, pol_b);
             }
           }
           last_parity[stage] = static_cast<int>(phase);
@@ -413,11 +419,11 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
         const uint32_t slab_addr = smem_u32(b_smem + st * Cfg::B_BYTES) + j * Cfg::B_SLAB_BYTES;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
-          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::PANEL_BYTES, 1024)
                                       : make_sw128_desc(a_addr + k * 32, 16, 1024);
-          const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+          const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::PANEL_BYTES, 1024)
                                       : make_sw128_desc(slab_addr + k * 32, 16, 1024);
-          umma_ff_pair<KIND>(d_tmem + 256 * j, adesc, bdesc, p.idesc, (first && k == 0) ? 0u : 1u);
+          umma_ff_pair<KIND>(d_tmem + Cfg::SLAB * j, adesc, bdesc, p.idesc, (first && k == 0) ? 0u : 1u);
         }
       };
       auto advance = [&](int& st, uint32_t& ph) {
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
     int local = 0;
     int turn = 0;  // which staging box comes next
     if (KIND == kFfI8)
-      ff_prefetch_scales<GATED, TILE_N, SLAB_N>(p, cluster_id, row_in_tile + lane, part * OUT + lane);
+      ff_prefetch_scales<GATED, TILE_N, SLAB_N, OUT>(p, cluster_id, row_in_tile + lane, part * OUT + lane);
     for (int t = cluster_id; t < p.num_tiles; t += num_clusters, ++local) {
       const FfTile f = ff_tile(p, t);
       const int acc = local % Cfg::NUM_ACC;
@@ -501,7 +507,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
       if (KIND == kFfI8) {
         if (y0 + lane < p.M) row_scale = __ldg(p.row_scale + y0 + lane);
         // The next tile's scales come into L1 while this tile is finished.
-        ff_prefetch_scales<GATED, TILE_N, SLAB_N>(p, t + num_clusters, row_in_tile + lane, part * OUT + lane);
+        ff_prefetch_scales<GATED, TILE_N, SLAB_N, OUT>(p, t + num_clusters, row_in_tile + lane, part * OUT + lane);
       }
       const bool ready = mbar_wait(&acc_full_bar[acc], acc_phase, abort_flag, p.wait_budget_ns, 0x86);
       if (!__all_sync(0xffffffffu, ready)) break;
@@ -516,17 +522,19 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
           for (int c = 0; c < OUT / 32; ++c) {
             const int col0 = out0 + s * SLAB_N + c * 32;
             if (GATED) {
-              // Result column o of the slab: gate at accumulator column
-              // 128 (o / 64) + o mod 64, up 64 columns further.
+              // Result column o of the slab: with W = B_ROWS / 2 (64, or 32 in
+              // the narrow tile) its gate is accumulator column 2 W (o / W) +
+              // o mod W, its up value W columns further.
+              constexpr int W = Cfg::B_ROWS / 2;
               const int o = part * OUT + c * 32;
-              const uint32_t gaddr = taddr + s * 256 + (o >> 6) * 128 + (o & 63);
+              const uint32_t gaddr = taddr + s * Cfg::SLAB + (o / W) * (2 * W) + o % W;
               const bool save = KIND == kFfF16 && p.save && rows_live && col0 < p.N;
               uint32_t hg[16], hu[16];
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 uint32_t rg[16], ru[16];
                 tmem_ld_32x32b_x16(gaddr + b * 16, rg);
-                tmem_ld_32x32b_x16(gaddr + 64 + b * 16, ru);
+                tmem_ld_32x32b_x16(gaddr + W + b * 16, ru);
                 tmem_ld_wait();
                 float g[16], u[16];
                 ff_values<KIND>(rg, row_scale, p.col_scale[0], col0 + b * 16, p.N, g);
@@ -554,7 +562,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 uint32_t r[16];
-                tmem_ld_32x32b_x16(taddr + s * 256 + part * OUT + c * 32 + b * 16, r);
+                tmem_ld_32x32b_x16(taddr + s * Cfg::SLAB + part * OUT + c * 32 + b * 16, r);
                 tmem_ld_wait();
                 const int col = col0 + b * 16;
                 float v[16];
