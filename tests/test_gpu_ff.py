@@ -379,3 +379,33 @@ def test_gated_i8(M, N, K, act, dt):
     u, du = ref.i8_product(host[0], host[1], host[4], host[5])
     outs, tols = ref.gate(g, u, dg, du, act, dt)
     ref.check(ref.f64(got), outs[0], tols[0], "H")
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,pad,off", [(300, 700, 0, 1), (300, 700, 1, 0), (300, 701, 0, 0), (290, 1025, 1, 1), (257, 95, 2, 3),
+                                         (130, 64, 1, 0), (1000, 5003, 0, 0), (20, 77, 3, 1)])
+def test_i8_results_on_any_boundary(M, N, pad, off, gated):
+    """Rows of the result on every 2-byte boundary; bytes around and between them stay."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    K = 48
+    a, sa = _codes(M, M, K)
+    w, sw = _codes(N + 1, N, K)
+    u, su = _codes(N + 2, N, K)
+    frame, c = _framed(M, N, N + pad, off, torch.bfloat16)
+    if gated:
+        got = tg.gated_i8(a, sa, w, sw, u, su, act="relu", out=c)
+    else:
+        got = tg.gemm_i8(a, sa, w, sw, out=c)
+    _ok()
+    assert got is c
+    host = [t.cpu().numpy() for t in (a, sa, w, sw, u, su)]
+    g, dg = ref.i8_product(*host[:4])
+    if gated:
+        v, dv = ref.i8_product(host[0], host[1], host[4], host[5])
+        outs, tols = ref.gate(g, v, dg, dv, "relu", "bf16")
+        g, tol = outs[0], tols[0]
+    else:
+        tol = dg + ref.round_error(g, "bf16")
+    ref.check(ref.f64(c), g, tol, "C")
+    _guards_ok(frame, c, N + pad, off)
