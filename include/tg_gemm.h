@@ -447,10 +447,13 @@ TG_API tg_status tg_dequant_w4_f16(const void *Wq, const void *scales, void *W, 
  * the 16-bit type (nearest even).  One kernel computes both projections, the
  * activation and the product; with G and U given (both or neither) it stores
  * them too, rounded to the 16-bit type, which is what the backward pass reads.
- * The backward pass rounds dG and dU to the 16-bit type before the products.
+ * The backward pass rounds dG and dU to the 16-bit type before the products; a
+ * gate whose slope is 0 gives dG = 0 whatever U is, and a stored G that
+ * overflowed to an infinity acts as the limit does.
  * Results do not depend on timing: equal inputs give equal bits.
  *
- * Sizes: each in [0, 2^30].  M == 0 or N == 0: nothing is enqueued by the
+ * Sizes: each in [0, 2^30]; matrices of up to 2^50 elements with the gaps
+ * between their rows, row strides up to 2^38.  M == 0 or N == 0: nothing is enqueued by the
  * forward; a gradient that is a sum over nothing is set to +0.  K == 0 sets H
  * (and G, U) to +0.  Bytes between a row's end and the next row are not
  * written.  No result may overlap an input or another result.
@@ -521,8 +524,9 @@ TG_API int64_t tg_gated_backward_workspace_size(const void *X, const void *Wg, c
  * scales: fp32, 4-byte aligned.  bias: N values of `type`, or NULL.  C, H: M x N
  * of `type`, row stride ldc (ldh), any 2-byte boundary.  Of tg_gated_options,
  * tg_gated_i8 reads type (of H), act, ldx (of A), ldwg, ldwu and ldh.
- * Sizes in [0, 2^30].  M == 0 or N == 0: nothing enqueued.  K == 0: the sums
- * are 0.  No workspace; no result may overlap an input.
+ * Sizes and strides as for tg_gated.  M == 0 or N == 0: nothing enqueued.  K ==
+ * 0: the sums are 0.  [relu] maps every value that is not > 0, NaN among them,
+ * to +0.  No workspace; no result may overlap an input.
  * Strides of 0 mean dense rows.  Errors: TG_ERR_INVALID_ARG as above,
  * TG_ERR_UNSUPPORTED_DEVICE, TG_ERR_LAUNCH.
  * ------------------------------------------------------------------------- */

@@ -55,6 +55,16 @@ def test_sizes(sizes):
     assert tg.gated_backward_workspace_size(*P[:6], *sizes) == -1
 
 
+def test_spans_stay_countable():
+    """Sizes or strides whose byte counts would leave 64 bits are refused, not computed with."""
+    big = 1 << 30
+    assert tg.gated_workspace_size(*P[:3], big, big, 8) == -1 and tg.gated_workspace_size(*P[:3], big, 8, big) == -1
+    assert tg.gated_backward_workspace_size(*P[:6], 8, big, big) == -1
+    assert tg.gated_workspace_size(*P[:3], big, 1 << 20, 8) == 0
+    assert gated(big, 8, 8, tg.gated_options(ldx=1 << 38)) == BAD and gated(big, 8, 8, tg.gated_options(ldh=1 << 38)) == BAD
+    assert gemm_i8(big, 8, 16, lda=1 << 38) == BAD and quantize(big, 8, ldx=1 << 38) == BAD and quantize(big, 8, ldq=1 << 38) == BAD
+
+
 def test_k_of_the_integer_sums():
     assert gemm_i8(K=131072) == BAD and gated_i8(K=131072) == BAD
     if not _gpu():

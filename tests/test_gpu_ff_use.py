@@ -498,3 +498,139 @@ def test_first_calls_inside_a_capture():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     done = subprocess.run([sys.executable, "-c", FIRST_CALL], cwd=root, capture_output=True, text=True, timeout=300)
     assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
+
+
+def test_far_gates_in_the_gradient():
+    """Gates past the type's range, stored as infinities, give the limits' gradients; a closed gate gives 0 whatever U is."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    inf = float("inf")
+    g = torch.tensor([[-inf, inf, -60000.0, 60000.0, -inf, 0.0, -200.0, 300.0]] * 3, device="cuda").half()
+    u = torch.tensor([[2.0, 3.0, inf, 4.0, inf, 1.0, -inf, 5.0]] * 3, device="cuda").half()
+    dh = torch.full((3, 8), 0.5, device="cuda").half()
+    x, w = torch.eye(3, 8, device="cuda").half(), torch.eye(8, device="cuda").half()
+    half = {"silu": 0.5, "gelu": 0.5, "relu": 0.0}
+    for act in ("silu", "gelu", "relu"):
+        dx, dwg, dwu = tg.gated_backward(dh, x, w, torch.zeros_like(w), g, u, act=act)
+        _ok()
+        want_dg = torch.tensor([0.0, 1.5, 0.0, 2.0, 0.0, 0.5 * half[act], 0.0, 2.5])
+        assert torch.equal(dwg[:, 0].float().cpu(), want_dg), act           # x is the identity: dWg holds dG
+        # dU of the infinite gate is an infinity, and dWu's sum holds it times the identity's zeros.
+        want_du = torch.tensor([0.0, float("nan"), 0.0, 30000.0, 0.0, 0.0, 0.0, 150.0])
+        assert torch.equal(dwu[:, 0].float().cpu().nan_to_num(-1), want_du.nan_to_num(-1)), act
+
+
+def test_gaps_between_rows_are_not_read():
+    """NaN between the rows of every operand reaches no result."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    M, N, K = 70, 72, 40
+
+    def spaced(t):
+        wide = torch.full((t.shape[0], t.shape[1] + 24), float("nan"), dtype=t.dtype, device="cuda")
+        wide[:, :t.shape[1]] = t
+        return wide[:, :t.shape[1]]
+
+    for m in (M, 400):
+        x, wg, wu, dh = (_randn(i, s, "bf16") for i, s in enumerate(((m, K), (N, K), (N, K), (m, N))))
+        want = tg.gated(x, wg, wu, save=True)
+        got = tg.gated(spaced(x), spaced(wg), spaced(wu), save=True)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        want_g = tg.gated_backward(dh, x, wg, wu, *want[1:])
+        got_g = tg.gated_backward(spaced(dh), spaced(x), spaced(wg), spaced(wu), spaced(want[1]), spaced(want[2]))
+        assert all(torch.equal(a, b) for a, b in zip(want_g, got_g))
+        assert all(torch.equal(a, b) for a, b in zip(tg.quantize_i8(x), tg.quantize_i8(spaced(x))))
+    _ok()
+
+
+def test_one_weight_twice():
+    """The same leaf as gate and up: its gradient is the sum of both."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, w, dh = _randn(1, (50, 40), "bf16"), _randn(2, (24, 40), "bf16", 0.2).requires_grad_(), _randn(3, (50, 24), "bf16")
+    tg.gated_block(x, w, w).backward(dh)
+    _ok()
+    d = w.detach()
+    _, g, u = tg.gated(x, d, d, save=True)
+    _, dwg, dwu = tg.gated_backward(dh, x, d, d, g, u)
+    assert torch.equal(w.grad, dwg + dwu)
+
+
+def test_another_current_device(monkeypatch):
+    """A call whose tensors are not on the current device runs on theirs (seen through the device it asks for)."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    from tiled_dense_gemm_fp16_b200 import feedforward
+    x, w = _randn(1, (5, 40), "f16"), _randn(2, (24, 40), "f16")
+    want = tg.gated(x, w, w)
+    answers = iter([7, 0])
+    entered = []
+    real = torch.cuda.device
+    monkeypatch.setattr(feedforward, "_current_device", lambda: next(answers))
+    monkeypatch.setattr(torch.cuda, "device", lambda index: entered.append(index) or real(index))
+    assert torch.equal(tg.gated(x, w, w), want) and entered == [0]
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 1), (2, 1, 1), (1, 2, 3), (129, 1, 1), (300, 1, 2), (2, 3, 100000), (260, 8, 70000),
+                                   (1, 4300001, 8), (2000003, 9, 8), (300, 600000, 8)])
+def test_smallest_and_longest(M, N, K):
+    """One element, one row, very long sums, more panels than a grid holds, very many rows or columns."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    dt = "bf16"
+    x, wg, wu = _randn(1, (M, K), dt), _randn(2, (N, K), dt, K ** -0.5), _randn(3, (N, K), dt, K ** -0.5)
+    h, g, u = tg.gated(x, wg, wu, save=True)
+    dh = _randn(4, (M, N), dt)
+    dx, dwg, dwu = tg.gated_backward(dh, x, wg, wu, g, u)
+    q, s = tg.quantize_i8(x)
+    (qg, sg), (qu, su) = tg.quantize_i8(wg), tg.quantize_i8(wu)
+    h8, c8 = tg.gated_i8(q, s, qg, sg, qu, su), tg.gemm_i8(q, s, qg, sg)
+    _ok()
+    ri, ci, ki = (torch.from_numpy(_some(n, n)).cuda() for n in (M, N, K))
+    outs, tols = ref.gated(ref.f64(x[ri]), ref.f64(wg[ci]), ref.f64(wu[ci]), "silu", dt)
+    for t, o, tol in zip((h, g, u), outs, tols):
+        ref.check(ref.f64(t[ri][:, ci]), o, tol, "gated")
+    args = [ref.f64(t) for t in (dh[ri], x[ri][:, ki], wg[:, ki], wu[:, ki], g[ri], u[ri])]
+    outs, tols = ref.gated_backward(*args, "silu", dt)
+    ref.check(ref.f64(dx[ri][:, ki]), outs[0], tols[0], "dX")
+    args = [ref.f64(t) for t in (dh[:, ci], x[:, ki], wg[ci][:, ki], wu[ci][:, ki], g[:, ci], u[:, ci])]
+    outs, tols = ref.gated_backward(*args, "silu", dt)
+    ref.check(ref.f64(dwg[ci][:, ki]), outs[1], tols[1], "dWg")
+    ref.check(ref.f64(dwu[ci][:, ki]), outs[2], tols[2], "dWu")
+    want_q, want_s = ref.quantize(ref.f64(x[ri]))
+    assert np.array_equal(q[ri].cpu().numpy(), want_q) and np.array_equal(s[ri].cpu().numpy(), want_s)
+    c, err = ref.i8_product(want_q, want_s, qg[ci].cpu().numpy(), sg[ci].cpu().numpy())
+    v, verr = ref.i8_product(want_q, want_s, qu[ci].cpu().numpy(), su[ci].cpu().numpy())
+    ref.check(ref.f64(c8[ri][:, ci]), c, err + ref.round_error(c, "f16"), "C")
+    outs, tols = ref.gate(c, v, err, verr, "silu", "f16")
+    ref.check(ref.f64(h8[ri][:, ci]), outs[0], tols[0], "H")
+
+
+def test_two_host_threads():
+    """Calls from two host threads, each on a stream of its own."""
+    import threading
+
+    import torch
+    pairs = [_all_operators(seed=1), _all_operators(seed=50, M=301)]
+    want = [run() for _, run in pairs]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got[i] = pairs[i][1]()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    _ok()
+    assert not errors
+    for w, g in zip(want, got):
+        assert all(torch.equal(a, b) for a, b in zip(w, g))

@@ -11,6 +11,7 @@ namespace tg {
 namespace {
 
 constexpr int64_t kFfMaxSize = int64_t(1) << 30;    // M, N, K: tile coordinates stay in 32 bits
+constexpr int64_t kFfMaxSpan = int64_t(1) << 50;    // elements of a matrix, gaps included: byte counts stay in 64 bits
 constexpr int64_t kFfMaxStride = int64_t(1) << 38;  // elements: byte strides stay below TMA's 2^40
 constexpr int64_t kFfMaxKI8 = 131071;               // 2^31 / 128^2: a sum of products of two codes stays in 32 bits
 
@@ -20,14 +21,16 @@ struct FfMat {
   int64_t rows, cols, ld;
   int elem;
 
-  int64_t bytes() const { return (rows > 0 && cols > 0) ? elem * ((rows - 1) * ld + cols) : 0; }
+  bool empty() const { return rows == 0 || cols == 0; }
+  int64_t bytes() const { return empty() ? 0 : elem * ((rows - 1) * ld + cols); }  // of a valid matrix
   bool rows_on(int align) const {  // every row starts on a multiple of `align` bytes
     return (reinterpret_cast<uintptr_t>(p) % align) == 0 && (ld * elem) % align == 0;
   }
   // Pointer, alignment and stride of a matrix that is read or written.
   bool valid() const {
-    if (bytes() == 0) return true;
-    return p != nullptr && (reinterpret_cast<uintptr_t>(p) % elem) == 0 && ld >= cols && ld <= kFfMaxStride;
+    if (empty()) return true;
+    return p != nullptr && (reinterpret_cast<uintptr_t>(p) % elem) == 0 && ld >= cols && ld <= kFfMaxStride &&
+           rows <= kFfMaxSpan / ld;
   }
   bool overlaps(const FfMat& o) const { return ranges_overlap(p, bytes(), o.p, o.bytes()); }
 };
@@ -43,7 +46,8 @@ FfMat mat8(const void* p, int64_t rows, int64_t cols, int64_t ld) { return ff_ma
 FfMat vec32(const void* p, int64_t n) { return FfMat{p, n > 0 ? 1 : 0, n, n, 4}; }
 
 bool ff_sizes_valid(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 0 && K >= 0 && M <= kFfMaxSize && N <= kFfMaxSize && K <= kFfMaxSize;
+  return M >= 0 && N >= 0 && K >= 0 && M <= kFfMaxSize && N <= kFfMaxSize && K <= kFfMaxSize &&
+         M * N <= kFfMaxSpan && N * K <= kFfMaxSpan && M * K <= kFfMaxSpan;
 }
 bool ff_type_valid(int32_t t) { return t == TG_TYPE_F16 || t == TG_TYPE_BF16; }
 bool ff_act_valid(int32_t a) { return a == TG_ACT_RELU || a == TG_ACT_SILU || a == TG_ACT_GELU; }
@@ -425,7 +429,7 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 // Bytes of the padded copy of a 16-bit operand that TMA cannot describe (rows
 // rounded up to 8 elements), or 0.
 int64_t ff_copy_bytes(const FfMat& m) {
-  return (m.bytes() == 0 || m.rows_on(16)) ? 0 : up256(2 * m.rows * round_up(m.cols, 8));
+  return (m.empty() || m.rows_on(16)) ? 0 : up256(2 * m.rows * round_up(m.cols, 8));
 }
 
 // Replace those of `mats` that need one by their padded copies at `ws`, made by
@@ -764,7 +768,7 @@ tg_status run_quantize(const void* X, void* Q, float* scales, int64_t M, int64_t
 }
 
 // The 8-bit operands of a product: rows on 16-byte boundaries (TMA).
-bool ff_i8_operand(const FfMat& m) { return m.valid() && (m.bytes() == 0 || m.rows_on(16)); }
+bool ff_i8_operand(const FfMat& m) { return m.valid() && (m.empty() || m.rows_on(16)); }
 
 tg_status run_gemm_i8(const void* A, const float* a_scale, const void* W, const float* w_scale, const void* bias,
                       void* C, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldw, int64_t ldc, int32_t relu,

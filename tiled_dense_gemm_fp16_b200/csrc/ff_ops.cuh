@@ -161,14 +161,13 @@ __device__ __forceinline__ void act_value_slope2(float2 g, float2& value, float2
   value = mul2(g, p);
   const float2 q = fma2(p, same2(-1.0f), same2(1.0f));
   const float2 r = mul2(value, q);
-  if (ACT == kActSilu) {
-    slope = add2(p, r);
-  } else {
-    slope = fma2(r, fma2(mul2(g, g), same2(3.0f * kGeluC3), same2(kGeluC1)), p);
-    // z' grows with g^2; where p is 0 or 1 its factor is 0, whatever g is.
-    if (r.x == 0.0f) slope.x = p.x;
-    if (r.y == 0.0f) slope.y = p.y;
-  }
+  slope = ACT == kActSilu ? add2(p, r) : fma2(r, fma2(mul2(g, g), same2(3.0f * kGeluC3), same2(kGeluC1)), p);
+  // Far gates: where p is 0 so is everything, and where it is 1 the slope is,
+  // though g (an infinity, when the stored value overflowed) or z' is not finite.
+  if (p.x == 0.0f) value.x = slope.x = 0.0f;
+  if (p.y == 0.0f) value.y = slope.y = 0.0f;
+  if (q.x == 0.0f) slope.x = 1.0f;
+  if (q.y == 0.0f) slope.y = 1.0f;
 }
 
 // ----------------------------------------------------------------------------

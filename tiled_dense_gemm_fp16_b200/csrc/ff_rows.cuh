@@ -79,8 +79,8 @@ __device__ __forceinline__ void gated_grad_rows(const GatedGradParams& p) {
       float2 a, s;
       act_value_slope2<ACT>(g, a, s);
       const float2 vg = mul2(mul2(d, u), s), vu = mul2(d, a);
-      dg[2 * q] = vg.x;
-      dg[2 * q + 1] = vg.y;
+      dg[2 * q] = s.x == 0.0f ? 0.0f : vg.x;  // a closed gate, whatever U is
+      dg[2 * q + 1] = s.y == 0.0f ? 0.0f : vg.y;
       du[2 * q] = vu.x;
       du[2 * q + 1] = vu.y;
     }
