@@ -3,6 +3,8 @@ launched: without a GPU a call that passes every check ends in UNSUPPORTED_DEVIC
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -186,6 +188,37 @@ def test_valid_calls_reach_the_device():
     assert gated_i8() == want and quantize() == want and quantize(type=tg.TYPE_BF16, ldx=11, ldq=9) == want
     need = tg.gated_workspace_size(*P[:3], 100, 41, 33)
     assert gated(100, 41, 33, ws=P[9], ws_bytes=need) == want
+
+
+def test_compiled_refusals():
+    """The compiled calls raise and go on raising (in a process of their own: two C++ runtimes in one process
+    end it at the third exception), and keep no reference to what they refused."""
+    pytest.importorskip("torch")
+    code = """
+import sys, torch
+from tiled_dense_gemm_fp16_b200 import feedforward
+calls, x = feedforward._calls, torch.zeros(4, 16)
+def refused(error, f, *args):
+    try:
+        f(*args)
+    except error:
+        return
+    raise SystemExit(f"{f.__name__} took its arguments")
+before = sys.getrefcount(x)
+for i in range(100):
+    refused(ValueError, calls.gated, x, x, x, "silu", None, False, "auto")
+    refused(TypeError, calls.gated, None, x, x, "silu", None, False, "auto")
+    refused(TypeError, calls.gated, x, x, x)
+    refused(ValueError, calls.gated_backward, x, x, x, x, x, x, "silu", True, True, True, "auto")
+    refused(TypeError, calls.gated_backward, x, 0, x, x, x, x, "silu", True, True, True, "auto")
+    refused(ValueError, calls.quantize_i8, x, None, None)
+    refused(ValueError, calls.gemm_i8, x, x, x, x, None, False, None, None)
+    refused(ValueError, calls.gated_i8, x, x, x, x, x, x, "silu", None, None)
+assert sys.getrefcount(x) == before
+print("done")
+"""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip() == "done", p.stderr[-2000:]
 
 
 def test_python_refusals():

@@ -556,21 +556,6 @@ def test_one_weight_twice():
     assert torch.equal(w.grad, dwg + dwu)
 
 
-def test_another_current_device(monkeypatch):
-    """A call whose tensors are not on the current device runs on theirs (seen through the device it asks for)."""
-    import torch
-    import tiled_dense_gemm_fp16_b200 as tg
-    from tiled_dense_gemm_fp16_b200 import feedforward
-    x, w = _randn(1, (5, 40), "f16"), _randn(2, (24, 40), "f16")
-    want = tg.gated(x, w, w)
-    answers = iter([7, 0])
-    entered = []
-    real = torch.cuda.device
-    monkeypatch.setattr(feedforward, "_current_device", lambda: next(answers))
-    monkeypatch.setattr(torch.cuda, "device", lambda index: entered.append(index) or real(index))
-    assert torch.equal(tg.gated(x, w, w), want) and entered == [0]
-
-
 @pytest.mark.parametrize("M,N,K", [(1, 1, 1), (2, 1, 1), (1, 2, 3), (129, 1, 1), (300, 1, 2), (2, 3, 100000), (260, 8, 70000),
                                    (1, 4300001, 8), (2000003, 9, 8), (300, 600000, 8)])
 def test_smallest_and_longest(M, N, K):

@@ -14,6 +14,7 @@ import threading
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libtg_gemm.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
 
 
 class Status(enum.IntEnum):

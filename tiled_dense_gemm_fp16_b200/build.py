@@ -1,9 +1,12 @@
-"""Build the in-tree shared library ``libtg_gemm.so`` for sm_100a with nvcc.
+"""Build the in-tree shared library ``libtg_gemm.so`` for sm_100a with nvcc, and the
+CPython module ``_calls.so`` that marshals torch tensors to its feed-forward calls.
 
 Run ``python -m tiled_dense_gemm_fp16_b200.build`` (or call ``build()``).
-The library is built in the package directory so that it travels with the
-source tree; cudart is linked statically and the driver's tensor-map encoder
-is looked up at run time, so the library needs no other CUDA library at load.
+Both are built in the package directory so that they travel with the source
+tree; the library links cudart statically and looks the driver's tensor-map
+encoder up at run time, so it needs no other CUDA library at load.  The module
+links to torch and to the library beside it; without torch only the library is
+built.
 """
 from __future__ import annotations
 
@@ -16,6 +19,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB_PATH = os.path.join(HERE, "libtg_gemm.so")
+CALLS_PATH = os.path.join(HERE, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "torch_calls.cpp")
 SOURCES = [os.path.join(CSRC, "tg_gemm.cu")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
@@ -38,15 +43,48 @@ def _deps():
     return deps
 
 
-def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+def _older(target, deps) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIB_PATH)
-    return any(os.path.getmtime(d) > t for d in _deps())
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in deps)
+
+
+def is_stale() -> bool:
+    return _older(LIB_PATH, _deps())
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str | None:
+    """The torch module (None without torch).  Needs the library to link to."""
+    import importlib.util
+    import sysconfig
+    if importlib.util.find_spec("torch") is None:
+        return None
+    if not force and not _older(CALLS_PATH, [CALLS_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")]):
+        return CALLS_PATH
+    import torch
+    torch_dir = os.path.dirname(torch.__file__)
+    cuda_dir = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
+                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(cuda_dir, "include")]
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    # nvcc's host compiler, not $CXX: one that links its own C++ runtime statically leaves two of them in the
+    # process, and an exception that torch's code throws through the module ends it.
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in includes),
+           CALLS_SOURCE, "-o", tmp, f"-L{HERE}", "-l:libtg_gemm.so", f"-L{os.path.join(torch_dir, 'lib')}", "-lc10",
+           "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(tmp, CALLS_PATH)
+    return CALLS_PATH
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and not is_stale():
+        build_calls(False, verbose)
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [_nvcc(), *ARCH, *NVCC_FLAGS, *extra_flags, *SOURCES, "-o", tmp]
@@ -55,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB_PATH)
+    build_calls(force, verbose)
     return LIB_PATH
 
 
