@@ -409,3 +409,141 @@ def test_i8_results_on_any_boundary(M, N, pad, off, gated):
         tol = dg + ref.round_error(g, "bf16")
     ref.check(ref.f64(c), g, tol, "C")
     _guards_ok(frame, c, N + pad, off)
+
+
+# ---------------------------------------------------------------------------
+# Few tiles and long sums: K split over a cluster, in blocks of rows
+# ---------------------------------------------------------------------------
+
+# Blocks that end inside their rows, panels that end inside their columns, K that ends inside a k-block; sums over
+# the columns of X (forward), of G and U (dX) and over the rows (dWg, dWu).
+LONG = [(129, 64, 1536), (131, 70, 1501), (300, 136, 2104), (640, 40, 3001), (700, 1040, 72), (515, 1501, 129),
+        (1500, 89, 93), (2050, 200, 136), (2304, 320, 64), (4099, 65, 7)]
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("M,N,K", LONG)
+def test_gated_long_sums(M, N, K, dt):
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, wg, wu = _gated_inputs(M, N, K, dt, seed=M + N + K)
+    dh = _rng_tensor(9, (M, N), dt, 0.5)
+    h, g, u = tg.gated(x, wg, wu, act="gelu", save=True)
+    again = tg.gated(x, wg, wu, act="gelu")
+    grads = tg.gated_backward(dh, x, wg, wu, g, u, act="gelu")
+    _ok()
+    outs, tols = ref.gated(ref.f64(x), ref.f64(wg), ref.f64(wu), "gelu", dt)
+    for name, t, o, tol in zip("HGU", (h, g, u), outs, tols):
+        ref.check(ref.f64(t), o, tol, name)
+    assert np.array_equal(ref.f64(h), ref.f64(again))
+    outs, tols = ref.gated_backward(*(ref.f64(t) for t in (dh, x, wg, wu, g, u)), "gelu", dt)
+    for name, t, o, tol in zip(("dX", "dWg", "dWu"), grads, outs, tols):
+        ref.check(ref.f64(t), o, tol, name)
+
+
+@pytest.mark.parametrize("needs", [(False, True, False), (False, False, True), (True, False, True)])
+def test_gated_backward_long_sums_needs(needs):
+    """One weight's gradient alone is the same as beside the other's, whatever K is split into."""
+    import tiled_dense_gemm_fp16_b200 as tg
+    M, N, K = 2050, 200, 136
+    x, wg, wu = _gated_inputs(M, N, K, "f16", seed=5)
+    dh = _rng_tensor(6, (M, N), "f16")
+    _, g, u = tg.gated(x, wg, wu, save=True)
+    part = tg.gated_backward(dh, x, wg, wu, g, u, needs=needs)
+    again = tg.gated_backward(dh, x, wg, wu, g, u, needs=needs)
+    _ok()
+    outs, tols = ref.gated_backward(*(ref.f64(t) for t in (dh, x, wg, wu, g, u)), "silu", "f16")
+    for n, p, a, o, tol in zip(needs, part, again, outs, tols):
+        assert (p is not None) == n
+        if n:
+            ref.check(ref.f64(p), o, tol, "gradient")
+            assert np.array_equal(ref.f64(p), ref.f64(a))
+
+
+@pytest.mark.parametrize("M,N,K,pad", [(300, 72, 1537, 1), (1301, 72, 65, 3), (259, 1101, 40, 0)])
+def test_long_sums_on_any_boundary(M, N, K, pad):
+    """Results with gaps between their rows, on every 2-byte boundary; bytes around and between the rows stay."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    dt = torch.float16
+    x, wg, wu = _gated_inputs(M, N, K, "f16", seed=K)
+    dh = _rng_tensor(8, (M, N), "f16")
+    frames = [_framed(M, N, N + pad, pad, dt) for _ in range(3)]
+    outs = [_framed(*s, s[1] + pad, pad, dt) for s in ((M, K), (N, K), (N, K))]
+    opts = tg.gated_options(act=tg.ACT_GELU, ldh=N + pad, ldg=N + pad, ldu=N + pad)
+    stream = torch.cuda.current_stream().cuda_stream
+    px, pg, pu = (t.data_ptr() for t in (x, wg, wu))
+    ptr = [f[1].data_ptr() for f in frames]
+    need = tg.gated_workspace_size(px, pg, pu, M, N, K, opts)
+    ws = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    assert tg.gated_raw(px, pg, pu, *ptr, M, N, K, opts, stream, ws.data_ptr(), need) == tg.Status.OK
+    opts = tg.gated_options(act=tg.ACT_GELU, ldg=N + pad, ldu=N + pad, lddx=K + pad, lddwg=K + pad, lddwu=K + pad)
+    optr = [o[1].data_ptr() for o in outs]
+    need = tg.gated_backward_workspace_size(px, pg, pu, *optr, M, N, K, opts)
+    buf = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    st = tg.gated_backward_raw(dh.data_ptr(), px, pg, pu, ptr[1], ptr[2], *optr, M, N, K, opts, stream, buf.data_ptr(), need)
+    assert st == tg.Status.OK
+    _ok()
+    assert torch.all(buf[need:] == 0x5A)
+    want, tols = ref.gated(ref.f64(x), ref.f64(wg), ref.f64(wu), "gelu", "f16")
+    for name, f, w, tol in zip("HGU", frames, want, tols):
+        ref.check(ref.f64(f[1]), w, tol, name)
+        _guards_ok(f[0], f[1], N + pad, pad)
+    want, tols = ref.gated_backward(*(ref.f64(t) for t in (dh, x, wg, wu, frames[1][1], frames[2][1])), "gelu", "f16")
+    for name, o, w, tol in zip(("dX", "dWg", "dWu"), outs, want, tols):
+        ref.check(ref.f64(o[1]), w, tol, name)
+        _guards_ok(o[0], o[1], K + pad, pad)
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,K", [(129, 64, 4096), (300, 520, 2064), (600, 71, 3333), (131, 700, 2500), (2000, 130, 4000)])
+def test_i8_long_sums(M, N, K, gated):
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    a, sa = _codes(M, M, K)
+    w, sw = _codes(N + 1, N, K)
+    u, su = _codes(N + 2, N, K)
+    b = _rng_tensor(3, (N,), "bf16")
+    host = [t.cpu().numpy() for t in (a, sa, w, sw, u, su)]
+    c, err = ref.i8_product(*host[:4])
+    if gated:
+        got = tg.gated_i8(a, sa, w, sw, u, su, act="silu", dtype=torch.bfloat16)
+        v, dv = ref.i8_product(*host[:2], *host[4:])
+        outs, tols = ref.gate(c, v, err, dv, "silu", "bf16")
+        c, tol = outs[0], tols[0]
+    else:
+        got = tg.gemm_i8(a, sa, w, sw, bias=b, relu=True, dtype=torch.bfloat16)
+        c = c + ref.f64(b)
+        err = err + np.abs(c) * 2.0 ** -24
+        c = np.maximum(c, 0)
+        tol = err + ref.round_error(c, "bf16")
+    _ok()
+    ref.check(ref.f64(got), c, tol, "C")
+
+
+def test_long_sums_keep_rows_apart():
+    """A row with an infinity or a NaN reaches its own row of H and of dX, and no other; a column of G does so in dWg."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    M, N, K = 260, 72, 1536
+    x, wg, wu = _gated_inputs(M, N, K, "f16", seed=1)
+    clean = tg.gated(x, wg, wu, act="relu")
+    x[127, 3], x[259, K - 1] = float("nan"), float("inf")
+    got = tg.gated(x, wg, wu, act="relu")
+    _ok()
+    rows = torch.ones(M, dtype=torch.bool, device="cuda")
+    rows[127] = rows[259] = False
+    assert torch.equal(got[rows], clean[rows])
+    assert torch.isnan(got[127]).all()
+    M, N, K = 2100, 130, 72
+    x, wg, wu = _gated_inputs(M, N, K, "f16", seed=2)
+    dh = _rng_tensor(3, (M, N), "f16")
+    _, g, u = tg.gated(x, wg, wu, act="silu", save=True)
+    dx0, dwg0, dwu0 = tg.gated_backward(dh, x, wg, wu, g, u)
+    dh[2099, 63] = float("nan")
+    dx, dwg, dwu = tg.gated_backward(dh, x, wg, wu, g, u)
+    _ok()
+    assert torch.equal(dx[:2099], dx0[:2099]) and torch.isnan(dx[2099]).all()
+    cols = torch.ones(N, dtype=torch.bool, device="cuda")
+    cols[63] = False
+    for got, want in ((dwg, dwg0), (dwu, dwu0)):
+        assert torch.equal(got[cols], want[cols]) and torch.isnan(got[63]).all()

@@ -204,8 +204,9 @@ FfSkinnyKernel ff_skinny_kernel_of(const FfProduct& f) {
 }
 
 struct FfSkinnyPlan {
-  int m_pad, stages, smem, k_blocks, splits;
+  int m_pad, m_blocks, a_bytes, stages, smem, k_blocks, splits;
   int64_t panels, waves;
+  double us;  // estimated time
 };
 
 // Clusters of `splits` CTAs that fit on the device with one CTA per SM, asked
@@ -238,21 +239,32 @@ int ff_resident_clusters(const FfProduct& f, int splits, DeviceInfo* info) {
   return known;
 }
 
-// The plan of a product of at most 256 rows, or false if the kernel cannot
-// take it.  Splits of K, by estimated time in us: at most as many as give every
-// SM two CTAs (one where two do not fit).  A k-block takes 0.59 with one CTA per
-// SM and 0.72 with two (the stream from memory), a wave 1.5 for its start, a
-// second CTA per SM 1.5 + M / 40 more for the partials both have to move and
-// add.  Measured, us, gated fp16 N = K = 2048 with 4 / 8 splits: M = 128 9.4 /
-// 12.2, M = 1 6.0 / 6.0; 4096 with 2 / 4: M = 128 19.4 / 16.8; 8-bit 5120 at M =
-// 128 with 4 in one wave / 7 that do not quite fit: 13 / 21.
-bool ff_skinny_plan(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* out) {
+// The plan of a product in blocks of at most `block_rows` rows, or false if the
+// kernel cannot take it.  Splits of K, by estimated time in us: at most as many
+// as give every SM two CTAs (one where two do not fit).  One block of rows: a
+// k-block takes 0.59 with one CTA per SM and 0.72 with two (the weight's stream
+// from memory), a wave 1.5 for its start, a second CTA per SM 1.5 + M / 40 more
+// for the partials both have to move and add.  Measured, us, gated fp16 N = K =
+// 2048 with 4 / 8 splits: M = 128 9.4 / 12.2, M = 1 6.0 / 6.0; 4096 with 2 / 4: M
+// = 128 19.4 / 16.8; 8-bit 5120 at M = 128 with 4 in one wave / 7 that do not
+// quite fit: 13 / 21.  Several blocks read the operands from L2: 0.31 with one
+// CTA per SM, 0.44 with two, for blocks of 128 rows (a CTA takes in 32 KiB), 0.11
+// more with rows stored K x M, and 2 for a second CTA; in between where some SMs
+// have two (dX of 152 x 3344 x 896: 16 clusters of 8, one more than fit alone,
+// 12.7, of 6 14.2).  Measured, gated fp16
+// 1024 x 1024 x 8192 with 1 / 2 splits 44 / 35, 512 x 1024 x 2048 11.7 with 2.
+bool ff_skinny_plan(const FfProduct& f, int block_rows, DeviceInfo* info, FfSkinnyPlan* out) {
   using Cfg = FfSkinnyCfg;
   if (!ff_set_smem(reinterpret_cast<const void*>(ff_skinny_kernel_of(f)), info->ff_attr, 1u << (12 + ff_skinny_index(f)),
                    Cfg::MAX_SMEM))
     return false;
   FfSkinnyPlan pl;
-  pl.m_pad = static_cast<int>((f.M + 15) / 16 * 16);
+  const int64_t m_blocks = (f.M + block_rows - 1) / block_rows;
+  if (m_blocks * f.row_sources > 65535) return false;
+  pl.m_blocks = static_cast<int>(m_blocks);
+  const int unit = f.a_km ? 64 : 16;  // rows stored K x M come in whole panels
+  pl.m_pad = static_cast<int>(((f.M + m_blocks - 1) / m_blocks + unit - 1) / unit * unit);
+  pl.a_bytes = Cfg::a_bytes(pl.m_pad, f.a_km);
   const int64_t kb = (f.K + f.k_elems() - 1) / f.k_elems() * f.k_sources;
   const int cols = f.gated ? 64 : 128;
   pl.panels = (f.N + cols - 1) / cols;
@@ -261,29 +273,41 @@ bool ff_skinny_plan(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* out) {
   // Two CTAs per SM while a ring stays within 112 KiB; at m_pad <= 32 three
   // stages of 64 KiB stream best.
   const int budget = (pl.m_pad <= 32 ? 64 : (pl.m_pad <= 128 ? 112 : 220)) * 1024;
-  const int stage_bytes = Cfg::stage_bytes(pl.m_pad);
+  const int stage_bytes = Cfg::W_STAGE_BYTES + pl.a_bytes;
   pl.stages = budget / stage_bytes;
   pl.stages = pl.stages > Cfg::MAX_STAGES ? Cfg::MAX_STAGES : pl.stages;
   // The partial [m_pad][128] reuses the ring after the main loop.
   if (pl.stages < 2 || pl.stages * stage_bytes < pl.m_pad * Cfg::PANEL * 4) return false;
-  pl.smem = Cfg::smem_bytes(pl.m_pad, pl.stages);
+  pl.smem = Cfg::smem_bytes(pl.a_bytes, pl.stages);
   double best = 0.0;
   pl.splits = 0;
   const int per_sm = pl.m_pad <= 128 ? 2 : 1;
   const int64_t slots = per_sm * info->sm_count;
-  const int64_t most = pl.panels >= slots ? 1 : slots / pl.panels;
+  const int64_t tiles = pl.panels * pl.m_blocks * f.row_sources;
+  const int64_t most = tiles >= slots ? 1 : slots / tiles;
+  const bool from_l2 = f.a_km || pl.m_blocks > 1;
   for (int s = 1; s <= 8 && s <= most && s <= pl.k_blocks; ++s) {
     const int64_t resident = per_sm * ff_resident_clusters(f, s, info);
-    const int64_t waves = (pl.panels + resident - 1) / resident;
-    const bool second = pl.panels > ff_resident_clusters(f, s, info);
-    const double cost = static_cast<double>(waves) * ((pl.k_blocks + s - 1) / s * (second ? 0.72 : 0.59) + 1.5) +
-                        (second ? 1.5 + pl.m_pad / 40.0 : 0.0) + 0.05 * s;
+    const int64_t waves = (tiles + resident - 1) / resident;
+    const double alone = static_cast<double>(ff_resident_clusters(f, s, info));
+    const bool second = static_cast<double>(tiles) > alone;
+    double per_block = second ? 0.72 : 0.59, share = second ? 1.5 + pl.m_pad / 40.0 : 0.0;
+    if (from_l2) {
+      const double part = !second ? 0.0 : tiles < 2 * alone ? tiles / alone - 1.0 : 1.0;  // SMs with two
+      per_block = (0.31 + 0.13 * part + (f.a_km ? 0.11 : 0.0)) * (128 + pl.m_pad) / 256.0;
+      share = 2.0 * part;
+    }
+    const double cost = static_cast<double>(waves) * ((pl.k_blocks + s - 1) / s * per_block + 1.5) + share + 0.05 * s;
     if (pl.splits == 0 || cost < best) {
       best = cost;
       pl.splits = s;
       pl.waves = waves;
     }
   }
+  const double rows = static_cast<double>(f.M);
+  pl.us = from_l2 ? best + 5.0
+                  : 6.0 + rows / 64.0 + static_cast<double>(pl.waves) * ((pl.k_blocks + pl.splits - 1) / pl.splits) *
+                                            (0.2 + 0.3 * rows / 256.0);
   *out = pl;
   return true;
 }
@@ -305,15 +329,17 @@ tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStrea
   p.M = static_cast<int>(f.M);
   p.N = static_cast<int>(f.N);
   p.m_pad = pl.m_pad;
+  p.m_blocks = pl.m_blocks;
   p.k_blocks_src = pl.k_blocks / f.k_sources;
   p.k_blocks = pl.k_blocks;
   p.stages = pl.stages;
   p.splits = pl.splits;
-  p.a_stage_bytes = static_cast<uint32_t>(p.m_pad * 128);
+  p.a_stage_bytes = static_cast<uint32_t>(pl.a_bytes);
   uint32_t cols = 32;
   while (cols < static_cast<uint32_t>(p.m_pad)) cols <<= 1;
   p.tmem_cols = cols;
-  p.idesc = make_idesc_ff(f.kind, f.bf16, Cfg::PANEL, p.m_pad, f.b_kn, false);
+  p.idesc = make_idesc_ff(f.kind, f.bf16, Cfg::PANEL, p.m_pad, f.b_kn, f.a_km);
+  p.a_mnmajor = f.a_km ? 1 : 0;
   p.b_kmajor = f.b_kn ? 0 : 1;
   p.bf16 = f.bf16 ? 1 : 0;
   p.act = f.act;
@@ -327,15 +353,18 @@ tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStrea
   p.wait_budget_ns = wait_budget(p.k_blocks);
   FfMaps maps;
   std::memset(&maps, 0, sizeof maps);
-  for (int i = 0; i < f.k_sources; ++i)
-    if (!ff_encode(&maps.a[i], f.a[i], ke, p.m_pad, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
+  const int a_sources = f.k_sources > f.row_sources ? f.k_sources : f.row_sources;
+  for (int i = 0; i < a_sources; ++i)
+    if (!ff_encode(&maps.a[i], f.a[i], f.a_km ? 64 : ke, f.a_km ? 64 : p.m_pad, CU_TENSOR_MAP_SWIZZLE_128B))
+      return TG_ERR_LAUNCH;
   for (int i = 0; i < f.weights(); ++i)
     if (!ff_encode(&maps.b[i], f.b[i], f.b_kn ? 64 : ke, f.b_kn || f.gated ? 64 : Cfg::PANEL,
                    CU_TENSOR_MAP_SWIZZLE_128B))
       return TG_ERR_LAUNCH;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>(pl.splits), static_cast<unsigned>(pl.panels), 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(pl.splits), static_cast<unsigned>(pl.panels),
+                     static_cast<unsigned>(pl.m_blocks * f.row_sources));
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
   cfg.dynamicSmemBytes = static_cast<size_t>(pl.smem);
   cfg.stream = stream;
@@ -348,28 +377,34 @@ tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStrea
   return TG_OK;
 }
 
-// Few rows take the split-K kernel: M <= 128 always (two CTAs share an SM); for
-// 128 < M <= 256 where its estimated time is the lower one.  A k-block takes
-// its CTA 0.2 us and 0.3 us more at 256 rows, after about 6 us + M / 64 for
-// the launch and the reduction; on the pair kernel one takes 0.30 us after 4 us
-// with 128-wide tiles (few columns), 0.344 after 5 with wider ones.  Measured,
-// us, split-K / pair, M = 256: gated fp16 1024 x 1024 10.4 / 8.8, 4096 x 1024
-// 13.4 / 9.8, 1024 x 4096 13.7 / 23.4, 8192 x 8192 69.6 / 68.3, 16384 x 4096 77 /
-// 61; dX of N = K = 8192 69 / 110; 8-bit 8192 x 8192 23 / 28.  At M <= 128 it
-// loses at most 2 us, where K is short (gated 8-bit 4096 x 1024, M = 128: 8.7 /
-// 7.3).  Products whose A is stored K x M never take it.
+// Few rows take the split-K kernel: M <= 128 always (two CTAs share an SM), where
+// it loses at most 2 us to the pair kernel, with short K (gated 8-bit 4096 x 1024,
+// M = 128: 8.7 / 7.3).  So do products with few tiles and long K, in blocks of at
+// most 128 rows: where the pair kernel would take 128-wide tiles it leaves SMs
+// idle, and each of those that work is held up by its own loads.  Up to 256 rows
+// of a weight of 64 panels or more are one block (its second reading costs more
+// than the longer reduction: dX of 160 x 8192 x 8192 56 in one block, 62 in two;
+// gated 256 x 1024 x 4096, 16 panels, 13.3 and 11.5).  Both by estimated time: a
+// k-block takes the pair kernel 0.30 us with 128-wide tiles, 0.27 with 8-bit
+// operands, 0.35 with one stored K-first, after 3.7 (8-bit 5), and 0.344 after 5
+// with wider ones.  Measured, us, split-K / pair: gated fp16 512 x 512 with K =
+// 512, 1024, 2048 7.0 / 6.0, 7.6 / 8.4, 9.0 / 13.3; 1024 x 1024 with K = 8192 35 /
+// 44; dX of 1024 x 4096 x 256 19.5 / 49; dWg and dWu (with dG and dU before) of
+// 8192 x 512 x 512 26 / 51, of 512 x 512 x 512 8.9 / 7.7; 8-bit 512 x 512 x 2048
+// 7.5 / 9.1, 256 x 8192 x 8192 26 / 28.
 bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
-  if (f.a_km || f.row_sources > 1 || f.M > kSkinnyMaxM || !ff_skinny_plan(f, info, plan)) return false;
-  if (f.M <= 128) return true;
-  const double rows = static_cast<double>(f.M);
-  const double split_k = 6.0 + rows / 64.0 +
-                         static_cast<double>(plan->waves) *
-                             static_cast<double>((plan->k_blocks + plan->splits - 1) / plan->splits) *
-                             (0.2 + 0.3 * rows / 256.0);
-  const int64_t tiles = (f.N * (f.gated ? 2 : 1) + 255) / 256, pairs = info->sm_count / 2;
+  const int64_t pairs = info->sm_count / 2, cols = f.N * (f.gated ? 2 : 1);
+  const int64_t tiles = (f.M + 255) / 256 * f.row_sources * ((cols + 255) / 256);
+  const bool few_rows = f.M <= 128 && !f.a_km, narrow = 2 * tiles <= pairs;
+  const bool one_block = f.M <= kSkinnyMaxM && !f.a_km && cols > 63 * FfSkinnyCfg::PANEL;
+  if (!few_rows && !one_block && !narrow) return false;
+  if (!ff_skinny_plan(f, one_block ? kSkinnyMaxM : 128, info, plan)) return false;
+  if (few_rows) return true;
   const double kb = static_cast<double>(plan->k_blocks);
-  return split_k < (2 * tiles <= pairs ? 4.0 + kb * 0.30
-                                       : 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * kb * 0.344);
+  const double pair = !narrow                ? 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * kb * 0.344
+                      : f.kind == kFfI8      ? 5.0 + kb * 0.27
+                                             : 3.7 + kb * (f.b_kn ? 0.35 : 0.30);
+  return plan->us < pair;
 }
 
 // Accumulator width of the pair kernel, by estimated time in units of one
@@ -643,9 +678,18 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
   gp.bf16 = a.f.type == TG_TYPE_BF16 ? 1 : 0;
   gp.act = a.f.act;
   {
-    const int64_t bx = (N + 8 * kGatedGradThreads - 1) / (8 * kGatedGradThreads);
+    // A block takes several rows where they are short: dG and dU of 4442 x 89
+    // take 11.3 us with a row a block, 6.9 so.
+    using Kernel = void (*)(GatedGradParams);
+    static const Kernel kernels[] = {gated_grad_kernel<1>, gated_grad_kernel<2>,  gated_grad_kernel<4>,
+                                     gated_grad_kernel<8>, gated_grad_kernel<16>, gated_grad_kernel<32>};
+    const int64_t chunks = (N + 7) / 8;
+    int log_rows = 0;
+    while (log_rows < 5 && chunks <= (kGatedGradThreads >> (log_rows + 1))) ++log_rows;
+    const int tx = kGatedGradThreads >> log_rows;
+    const int64_t bx = (chunks + tx - 1) / tx, row_blocks = (M + (1 << log_rows) - 1) >> log_rows;
     int64_t by = (static_cast<int64_t>(info->sm_count) * 8 * 4 + bx - 1) / bx;
-    by = by < 1 ? 1 : (by > M ? M : by);
+    by = by < 1 ? 1 : (by > row_blocks ? row_blocks : by);
     if (by > 65535) by = 65535;
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof cfg);
@@ -654,7 +698,7 @@ tg_status run_gated_grad(GatedGradArgs& a, void* stream_ptr, void* ws_ptr, int64
     cfg.stream = stream;
     LaunchAttrs la;
     la.fill(cfg, 1);
-    if (cudaLaunchKernelEx(&cfg, gated_grad_kernel, gp) != cudaSuccess) {
+    if (cudaLaunchKernelEx(&cfg, kernels[log_rows], gp) != cudaSuccess) {
       cudaGetLastError();
       return TG_ERR_LAUNCH;
     }

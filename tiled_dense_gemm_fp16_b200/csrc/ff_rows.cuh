@@ -56,16 +56,17 @@ __device__ __forceinline__ const unsigned short* end_16(const void* p, int64_t r
   return static_cast<const unsigned short*>(p) + (rows - 1) * ld + cols;
 }
 
-template <int ACT>
+template <int ACT, int ROWS>
 __device__ __forceinline__ void gated_grad_rows(const GatedGradParams& p) {
+  constexpr int TX = kGatedGradThreads / ROWS;  // threads per row, 8 columns each
   const bool bf16 = p.bf16 != 0, vec = p.vec != 0;
-  const int col = (blockIdx.x * kGatedGradThreads + threadIdx.x) * 8;
+  const int col = (blockIdx.x * TX + threadIdx.x % TX) * 8;
   if (col >= p.N) return;
   const int n = p.N - col;
   const void* end_d = end_16(p.dH, p.M, p.ld_dh, p.N);
   const void* end_g = end_16(p.G, p.M, p.ld_g, p.N);
   const void* end_u = end_16(p.U, p.M, p.ld_u, p.N);
-  for (int row = blockIdx.y; row < p.M; row += gridDim.y) {
+  for (int row = blockIdx.y * ROWS + threadIdx.x / TX; row < p.M; row += gridDim.y * ROWS) {
     const int64_t r = row;
     const uint4 d4 = load8_16(static_cast<const unsigned short*>(p.dH) + r * p.ld_dh + col, n, vec, p.dH, end_d);
     const uint4 g4 = load8_16(static_cast<const unsigned short*>(p.G) + r * p.ld_g + col, n, vec, p.G, end_g);
@@ -94,15 +95,17 @@ __device__ __forceinline__ void gated_grad_rows(const GatedGradParams& p) {
   }
 }
 
+// ROWS rows a block at a time, so that short rows leave no thread idle.
+template <int ROWS>
 __global__ void __launch_bounds__(kGatedGradThreads) gated_grad_kernel(const GatedGradParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   if (p.act == kActSilu)
-    gated_grad_rows<kActSilu>(p);
+    gated_grad_rows<kActSilu, ROWS>(p);
   else if (p.act == kActGelu)
-    gated_grad_rows<kActGelu>(p);
+    gated_grad_rows<kActGelu, ROWS>(p);
   else
-    gated_grad_rows<kActRelu>(p);
+    gated_grad_rows<kActRelu, ROWS>(p);
 }
 
 // ----------------------------------------------------------------------------

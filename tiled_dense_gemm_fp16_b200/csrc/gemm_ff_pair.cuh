@@ -142,7 +142,27 @@ __device__ __forceinline__ void load_scale16(const float* scale, int col, int N,
   }
 }
 
-// Scales of tile t's rows and columns into L1: `row` is this lane's row inside
+// 16 consecutive 16-bit values from `src` on, for columns from `col` on (0 past N).
+__device__ __forceinline__ void load_bias16(const unsigned short* src, int col, int N, bool bf16, float (&v)[16]) {
+  if (col + 16 <= N && (reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + q);
+      const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = unpack_16(h[e], bf16);
+        v[8 * q + 2 * e] = x.x;
+        v[8 * q + 2 * e + 1] = x.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = col + e < N ? load_16(src + e, bf16) : 0.0f;
+  }
+}
+
+// Scales (and bias) of tile t's rows and columns into L1: `row` is this lane's row inside
 // the tile, `col` its first column inside a slab.
 template <bool GATED, int TILE_N, int SLAB_N, int OUT>
 __device__ __forceinline__ void ff_prefetch_scales(const FfParams& p, int t, int row, int col) {
@@ -158,6 +178,7 @@ __device__ __forceinline__ void ff_prefetch_scales(const FfParams& p, int t, int
       if (n < p.N) {
         prefetch_l1(p.col_scale[0] + n);
         if (GATED) prefetch_l1(p.col_scale[1] + n);
+        if (!GATED && p.bias != nullptr) prefetch_l1(static_cast<const unsigned short*>(p.bias) + n);
       }
     }
   }
@@ -569,10 +590,10 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
                 ff_values<KIND>(r, row_scale, p.col_scale[0], col, p.N, v);
                 if (KIND == kFfI8) {
                   if (p.bias != nullptr) {
-                    const unsigned short* b16 = static_cast<const unsigned short*>(p.bias) + col;
+                    float bias[16];
+                    load_bias16(static_cast<const unsigned short*>(p.bias) + col, col, p.N, p.bf16 != 0, bias);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                      if (col + e < p.N) v[e] += load_16(b16 + e, p.bf16 != 0);
+                    for (int e = 0; e < 16; ++e) v[e] += bias[e];
                   }
                   if (p.relu) {
 #pragma unroll

@@ -1,13 +1,20 @@
-// gemm_ff_skinny.cuh -- the same products for few rows (M <= 256): a step is
-// bound by streaming the weights from HBM once, so the kernel computes the
-// transposed result (the weight's rows fill the 128-row MMA side, the padded M
-// is the MMA's N) and splits K over a cluster of S CTAs, as the fp16 small-M
-// kernel does.
+// gemm_ff_skinny.cuh -- the same products where whole tiles would leave most SMs
+// idle: few rows (M <= 256), bound by streaming the weights from HBM once, or
+// few tiles and a long K (dWg and dWu of a narrow block: K is the tokens).  The
+// kernel computes the transposed result (the weight's rows fill the 128-row MMA
+// side, a block of up to 256 rows is the MMA's N) and splits K over a cluster
+// of S CTAs, as the fp16 small-M kernel does.  With few tiles a kernel is held
+// up by what one SM can load, about 50 bytes a clock, so its time goes down with
+// the number of SMs until the cluster's reduction (about 3 us) is what is left:
+// dWg and dWu of 8192 x 256 x 256 (with dG and dU before) take 50 us on 8 CTA
+// pairs, 19 on 64 CTAs.
 //   * Gated: a panel is 64 rows of Wg and the same 64 rows of Wu, so both
 //     projections of 64 block columns meet in one accumulator.
 //   * Plain: a panel is 128 rows of W (K-major), or, for dX = dG Wg + dU Wu,
 //     128 columns of Wg and then of Wu (stored K x N, MN-major) with the K
 //     loop over both sources.
+//   * dWg and dWu: a panel is 128 columns of X, the rows are columns of dG and
+//     then of dU (both stored K x M, MN-major, in panels of 64 rows).
 // Each CTA moves its partial (fp32, or 32-bit integers) to shared memory; after
 // a cluster barrier every CTA adds a share of the panel's outputs over the S
 // partials in rank order, so results do not depend on timing.
@@ -19,20 +26,21 @@
 namespace tg {
 
 struct FfSkinnyParams {
-  void* c[3];                 // H, G, U; or the one result
+  void* c[3];                 // H, G, U; or the results of the row sources
   int64_t ldc[3];
   int c_aligned[3];           // rows of the result start on 8-byte boundaries
   const float* row_scale;
   const float* col_scale[2];
   const void* bias;
   int M, N;
-  int m_pad;                  // M rounded up to a multiple of 16
+  int m_pad;                  // rows of a block, a multiple of 16
+  int m_blocks;               // blocks of rows of one row source
   int k_blocks, k_blocks_src;
   int splits, stages;
-  uint32_t a_stage_bytes;     // m_pad * 128
+  uint32_t a_stage_bytes;     // of the activations: m_pad * 128, or whole 64-row panels if stored K x M
   uint32_t tmem_cols;
   uint32_t idesc;
-  int b_kmajor;
+  int a_mnmajor, b_kmajor;
   int bf16, act, relu, save;
   int prefetch_kb;            // k-blocks of the weight brought into L2 ahead of the previous kernel's end
   uint64_t wait_budget_ns;
@@ -47,8 +55,8 @@ struct FfSkinnyCfg {
   static constexpr int MAX_STAGES = 8;
   static constexpr int BAR_BYTES = 256;
   static constexpr int MAX_SMEM = 1024 + 220 * 1024 + BAR_BYTES;
-  static int stage_bytes(int m_pad) { return W_STAGE_BYTES + m_pad * 128; }
-  static int smem_bytes(int m_pad, int stages) { return 1024 + stages * stage_bytes(m_pad) + BAR_BYTES; }
+  static int a_bytes(int m_pad, bool a_km) { return a_km ? (m_pad + 63) / 64 * HALF_BYTES : m_pad * 128; }
+  static int smem_bytes(int a_bytes, int stages) { return 1024 + stages * (W_STAGE_BYTES + a_bytes) + BAR_BYTES; }
 };
 
 // Four results of one row, from column n on.
@@ -138,6 +146,8 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
   const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int n0 = blockIdx.y * OUT;
+  const int row_src = KIND == kFfF16 && !GATED && static_cast<int>(blockIdx.z) >= p.m_blocks ? 1 : 0;
+  const int m0 = (static_cast<int>(blockIdx.z) - row_src * p.m_blocks) * p.m_pad;
   const int kb_lo = static_cast<int>((static_cast<int64_t>(p.k_blocks) * rank) / p.splits);
   const int kb_hi = static_cast<int>((static_cast<int64_t>(p.k_blocks) * (rank + 1)) / p.splits);
   const int my_blocks = kb_hi - kb_lo;
@@ -212,7 +222,13 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
           tma_load_2d_hint(wdst, &maps.b[k_src], &full_bar[stage], n0, k0, pol_w);
           tma_load_2d_hint(wdst + Cfg::HALF_BYTES, &maps.b[k_src], &full_bar[stage], n0 + 64, k0, pol_w);
         }
-        tma_load_2d_hint(a_smem + stage * p.a_stage_bytes, &maps.a[k_src], &full_bar[stage], k0, 0, pol_a);
+        uint8_t* adst = a_smem + stage * p.a_stage_bytes;
+        if (KIND == kFfF16 && !GATED && p.a_mnmajor) {
+          for (uint32_t b = 0; b < p.a_stage_bytes; b += Cfg::HALF_BYTES)  // panels of 64 rows
+            tma_load_2d_hint(adst + b, &maps.a[row_src], &full_bar[stage], m0 + static_cast<int>(b >> 7), k0, pol_a);
+        } else {
+          tma_load_2d_hint(adst, &maps.a[k_src], &full_bar[stage], k0, m0, pol_a);
+        }
         last_parity[stage] = static_cast<int>(phase);
         if (++stage == p.stages) {
           stage = 0;
@@ -232,6 +248,7 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       const bool w_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
+      const bool a_mn = KIND == kFfF16 && !GATED && p.a_mnmajor != 0;
       for (int i = 0; i < my_blocks; ++i) {
         if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0x93)) {
           ok = false;
@@ -244,8 +261,9 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
         for (int k = 0; k < 4; ++k) {
           const uint64_t wdesc = w_mn ? make_sw128_desc(w_addr + k * 2048, Cfg::HALF_BYTES, 1024)
                                       : make_sw128_desc(w_addr + k * 32, 16, 1024);
-          umma_ff<KIND>(tmem_base, wdesc, make_sw128_desc(a_addr + k * 32, 16, 1024), p.idesc,
-                        (i | k) != 0 ? 1u : 0u);
+          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
+                                      : make_sw128_desc(a_addr + k * 32, 16, 1024);
+          umma_ff<KIND>(tmem_base, wdesc, adesc, p.idesc, (i | k) != 0 ? 1u : 0u);
         }
         umma_commit(&empty_bar[stage]);
         if (++stage == p.stages) {
@@ -291,17 +309,22 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
     // Items are (m, 4-column group); CTA `rank` finishes its share.
     const int e = threadIdx.x;
     constexpr int GROUPS = OUT / 4;
-    const int items = p.M * GROUPS;
+    const int rows = min(p.m_pad, p.M - m0);
+    const int items = rows * GROUPS;
     const int lo = static_cast<int>((static_cast<int64_t>(items) * rank) / p.splits);
     const int hi = static_cast<int>((static_cast<int64_t>(items) * (rank + 1)) / p.splits);
     const uint32_t part_addr = smem_u32(partial);
     const bool bf16 = p.bf16 != 0;
+    void* const c0 = row_src ? p.c[1] : p.c[0];
+    const int64_t ldc0 = row_src ? p.ldc[1] : p.ldc[0];
+    const bool aligned0 = (row_src ? p.c_aligned[1] : p.c_aligned[0]) != 0;
     for (int it = lo + e; it < hi; it += Cfg::THREADS) {
-      const int m = it / GROUPS;
-      const int j = it - m * GROUPS;
+      const int y = it / GROUPS;
+      const int j = it - y * GROUPS;
+      const int m = m0 + y;
       const int n = n0 + 4 * j;
       if (n >= p.N) continue;
-      const uint32_t off = part_addr + static_cast<uint32_t>((m * Cfg::PANEL + 4 * j) * 4);
+      const uint32_t off = part_addr + static_cast<uint32_t>((y * Cfg::PANEL + 4 * j) * 4);
       float4 xv[8], xu[8];
       ff_cluster_read(off, p.splits, xv);
       if (GATED) ff_cluster_read(off + 64 * 4, p.splits, xu);
@@ -338,7 +361,7 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
           for (int q = 0; q < 4; ++q) v[q] = v[q] > 0.0f ? v[q] : 0.0f;
         }
       }
-      ff_store4(p.c[0], p.ldc[0], p.c_aligned[0] != 0, m, n, p.N, v, bf16);
+      ff_store4(c0, ldc0, aligned0, m, n, p.N, v, bf16);
     }
   }
 
