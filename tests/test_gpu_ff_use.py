@@ -619,3 +619,29 @@ def test_two_host_threads():
     assert not errors
     for w, g in zip(want, got):
         assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
+def test_results_given_count_as_written():
+    """A given result that another operator saved for its backward pass: that pass refuses the changed values."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, w = (torch.randn((n, 64), device="cuda").half() for n in (4, 32))
+    out = torch.ones((4, 32), dtype=torch.float16, device="cuda")
+    leaf = torch.ones((4, 32), dtype=torch.float16, device="cuda", requires_grad=True)
+    loss = (leaf * out).sum()
+    assert tg.gated(x, w, w, out=out) is out
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    codes, scales = torch.empty((4, 64), dtype=torch.int8, device="cuda"), torch.empty(4, device="cuda")
+    before = codes._version, scales._version
+    q, s = tg.quantize_i8(x, out=codes, scales=scales)
+    assert q is codes and s is scales and codes._version > before[0] and scales._version > before[1]
+    qw, sw = tg.quantize_i8(w)
+    before = out._version
+    tg.gemm_i8(q, s, qw, sw, out=out)
+    tg.gated_i8(q, s, qw, sw, qw, sw, out=out)
+    assert out._version == before + 2
+    with torch.inference_mode():
+        mine = torch.empty((4, 32), dtype=torch.float16, device="cuda")
+    assert tg.gated(x, w, w, out=mine) is mine
+    _ok()

@@ -194,6 +194,13 @@ PyObject* new_ref(PyObject* o) {
   return o;
 }
 
+// The caller's tensor as a result: its version counts up, so that a backward pass that saved its old values says so.
+PyObject* written(PyObject* o) {
+  const at::Tensor& t = THPVariable_Unpack(o);
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+  return new_ref(o);
+}
+
 // (a, b, c), taking over the references.
 template <typename... Items>
 PyObject* tuple_of(Items... items) {
@@ -243,7 +250,7 @@ PyObject* gated(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return tg_gated(px, pg, pu, out.data_ptr(), save ? gate.data_ptr() : nullptr, save ? up.data_ptr() : nullptr, M, N,
                     K, &o, stream_of(device), ws.ptr, ws.bytes);
   });
-  PyObject* result = given ? new_ref(args[4]) : THPVariable_Wrap(out);
+  PyObject* result = given ? written(args[4]) : THPVariable_Wrap(out);
   return save ? tuple_of(result, THPVariable_Wrap(gate), THPVariable_Wrap(up)) : result;
   END_HANDLE_TH_ERRORS
 }
@@ -311,7 +318,7 @@ PyObject* quantize_i8(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return tg_quantize_rows_i8(x.data_ptr(), q.data_ptr(), static_cast<float*>(s.data_ptr()), r.rows, r.cols, r.ld,
                                ldq, type, stream_of(device));
   });
-  return tuple_of(given_q ? new_ref(args[1]) : THPVariable_Wrap(q), given_s ? new_ref(args[2]) : THPVariable_Wrap(s));
+  return tuple_of(given_q ? written(args[1]) : THPVariable_Wrap(q), given_s ? written(args[2]) : THPVariable_Wrap(s));
   END_HANDLE_TH_ERRORS
 }
 
@@ -349,7 +356,7 @@ PyObject* gemm_i8(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return tg_gemm_i8(a.data_ptr(), static_cast<const float*>(psa), w.data_ptr(), static_cast<const float*>(psw), bias,
                       out.data_ptr(), M, N, K, ar.ld, ldw, ldc, relu, code, stream_of(device));
   });
-  return given ? new_ref(args[7]) : THPVariable_Wrap(out);
+  return given ? written(args[7]) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
@@ -382,7 +389,7 @@ PyObject* gated_i8(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
     return tg_gated_i8(a.data_ptr(), psa, wg.data_ptr(), psg, wu.data_ptr(), psu, out.data_ptr(), M, N, K, &o,
                        stream_of(device));
   });
-  return given ? new_ref(args[8]) : THPVariable_Wrap(out);
+  return given ? written(args[8]) : THPVariable_Wrap(out);
   END_HANDLE_TH_ERRORS
 }
 
