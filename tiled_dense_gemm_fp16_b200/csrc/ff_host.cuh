@@ -385,8 +385,8 @@ tg_status launch_ff_skinny(const FfProduct& f, const FfSkinnyPlan& pl, cudaStrea
 // of a weight of 64 panels or more are one block (its second reading costs more
 // than the longer reduction: dX of 160 x 8192 x 8192 56 in one block, 62 in two;
 // gated 256 x 1024 x 4096, 16 panels, 13.3 and 11.5).  Both by estimated time: a
-// k-block takes the pair kernel 0.30 us with 128-wide tiles, 0.27 with 8-bit
-// operands, 0.35 with one stored K-first, after 3.7 (8-bit 5), and 0.344 after 5
+// k-block takes the pair kernel 0.28 us with 128-wide tiles, 0.27 with 8-bit
+// operands, 0.33 with one stored K-first, after 3.7 (8-bit 5), and 0.344 after 5
 // with wider ones.  Measured, us, split-K / pair: gated fp16 512 x 512 with K =
 // 512, 1024, 2048 7.0 / 6.0, 7.6 / 8.4, 9.0 / 13.3; 1024 x 1024 with K = 8192 35 /
 // 44; dX of 1024 x 4096 x 256 19.5 / 49; dWg and dWu (with dG and dU before) of
@@ -403,7 +403,7 @@ bool ff_skinny_route(const FfProduct& f, DeviceInfo* info, FfSkinnyPlan* plan) {
   const double kb = static_cast<double>(plan->k_blocks);
   const double pair = !narrow                ? 5.0 + static_cast<double>((tiles + pairs - 1) / pairs) * kb * 0.344
                       : f.kind == kFfI8      ? 5.0 + kb * 0.27
-                                             : 3.7 + kb * (f.b_kn ? 0.35 : 0.30);
+                                             : 3.7 + kb * (f.b_kn ? 0.33 : 0.28);
   return plan->us < pair;
 }
 

@@ -363,6 +363,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
       const uint64_t pol_b = (p.l2_hints & 2)   ? l2_policy_evict_last()
                              : (p.l2_hints & 4) ? l2_policy_evict_first()
                                                 : l2_policy_evict_normal();
+      const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
       for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
         const FfTile f = ff_tile(p, t);
         const int row_src = f.row_src;
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
             ok = false;
             break;
           }
-          const uint32_t full_even = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          const uint32_t full_even = full_even0 + stage * 8;
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const int k_src = kb >= p.k_blocks_src ? 1 : 0;
           const int k0 = (kb - k_src * p.k_blocks_src) * K_ELEMS;
@@ -434,18 +435,22 @@ __global__ void __launch_bounds__(FfPairCfg<STAGES, BN, EPI_WARPS>::THREADS, 1)
       bool ok = true;
       const bool a_mn = KIND == kFfF16 && p.a_mnmajor != 0;
       const bool b_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
-      // The four MMAs of one k-block and one slab.
+      // Descriptors of stage 0 and their steps in units of 16 bytes: one
+      // addition per descriptor and MMA (shared memory ends below 2^18, so the
+      // address field takes no carry).  This thread's instructions bound the
+      // 128-wide tile: a k-block takes 0.28 us (0.30 with descriptors built
+      // anew for each MMA), of which the loads of a stage are not felt.
+      const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), a_mn ? Cfg::PANEL_BYTES : 16, 1024);
+      const uint64_t b_desc0 = make_sw128_desc(smem_u32(b_smem), b_mn ? Cfg::PANEL_BYTES : 16, 1024);
+      const uint32_t a_step = a_mn ? 2048 / 16 : 32 / 16, b_step = b_mn ? 2048 / 16 : 32 / 16;
+      // The four MMAs of one k-block and one slab, 32 bytes of K each.
       auto issue = [&](int st, int j, uint32_t d_tmem, bool first) {
-        const uint32_t a_addr = smem_u32(a_smem + st * Cfg::A_BYTES);
-        const uint32_t slab_addr = smem_u32(b_smem + st * Cfg::B_BYTES) + j * Cfg::B_SLAB_BYTES;
+        const uint64_t a_desc = a_desc0 + st * (Cfg::A_BYTES / 16);
+        const uint64_t b_desc = b_desc0 + st * (Cfg::B_BYTES / 16) + j * (Cfg::B_SLAB_BYTES / 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // 32 bytes of K each
-          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::PANEL_BYTES, 1024)
-                                      : make_sw128_desc(a_addr + k * 32, 16, 1024);
-          const uint64_t bdesc = b_mn ? make_sw128_desc(slab_addr + k * 2048, Cfg::PANEL_BYTES, 1024)
-                                      : make_sw128_desc(slab_addr + k * 32, 16, 1024);
-          umma_ff_pair<KIND>(d_tmem + Cfg::SLAB * j, adesc, bdesc, p.idesc, (first && k == 0) ? 0u : 1u);
-        }
+        for (int k = 0; k < 4; ++k)
+          umma_ff_pair<KIND>(d_tmem + Cfg::SLAB * j, a_desc + k * a_step, b_desc + k * b_step, p.idesc,
+                             (first && k == 0) ? 0u : 1u);
       };
       auto advance = [&](int& st, uint32_t& ph) {
         if (++st == Cfg::STAGES) {

@@ -249,22 +249,21 @@ __global__ void __launch_bounds__(FfSkinnyCfg::THREADS, 1)
       bool ok = true;
       const bool w_mn = KIND == kFfF16 && !GATED && p.b_kmajor == 0;
       const bool a_mn = KIND == kFfF16 && !GATED && p.a_mnmajor != 0;
+      // As in the pair kernel: one addition per descriptor and MMA.
+      const uint64_t w_desc0 = make_sw128_desc(smem_u32(w_smem), w_mn ? Cfg::HALF_BYTES : 16, 1024);
+      const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), a_mn ? Cfg::HALF_BYTES : 16, 1024);
+      const uint32_t w_step = w_mn ? 2048 / 16 : 32 / 16, a_step = a_mn ? 2048 / 16 : 32 / 16;
       for (int i = 0; i < my_blocks; ++i) {
         if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0x93)) {
           ok = false;
           break;
         }
         tcgen05_fence_after_sync();
-        const uint32_t w_addr = smem_u32(w_smem + stage * Cfg::W_STAGE_BYTES);
-        const uint32_t a_addr = smem_u32(a_smem + stage * p.a_stage_bytes);
+        const uint64_t w_desc = w_desc0 + stage * (Cfg::W_STAGE_BYTES / 16);
+        const uint64_t a_desc = a_desc0 + stage * (p.a_stage_bytes / 16);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint64_t wdesc = w_mn ? make_sw128_desc(w_addr + k * 2048, Cfg::HALF_BYTES, 1024)
-                                      : make_sw128_desc(w_addr + k * 32, 16, 1024);
-          const uint64_t adesc = a_mn ? make_sw128_desc(a_addr + k * 2048, Cfg::HALF_BYTES, 1024)
-                                      : make_sw128_desc(a_addr + k * 32, 16, 1024);
-          umma_ff<KIND>(tmem_base, wdesc, adesc, p.idesc, (i | k) != 0 ? 1u : 0u);
-        }
+        for (int k = 0; k < 4; ++k)
+          umma_ff<KIND>(tmem_base, w_desc + k * w_step, a_desc + k * a_step, p.idesc, (i | k) != 0 ? 1u : 0u);
         umma_commit(&empty_bar[stage]);
         if (++stage == p.stages) {
           stage = 0;
