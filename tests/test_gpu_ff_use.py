@@ -283,11 +283,11 @@ def test_autograd_shapes_of_gradients():
 # Streams, graphs, repeats
 # ---------------------------------------------------------------------------
 
-def _all_operators(seed=1, M=150):
+def _all_operators(seed=1, M=150, N=131, K=265):
     """Calls of every operator on fixed inputs, as (inputs, function of a stream -> outputs)."""
     import torch
     import tiled_dense_gemm_fp16_b200 as tg
-    K, N, dt = 265, 131, "f16"  # odd: padded copies and unaligned results too
+    dt = "f16"  # odd sizes: padded copies and unaligned results too
     x, wg, wu, dh = (_randn(seed + i, s, dt, sc) for i, (s, sc) in
                      enumerate((((M, K), 1.0), ((N, K), 0.06), ((N, K), 0.06), ((M, N), 0.1))))
     qg, sg = tg.quantize_i8(wg)
@@ -370,6 +370,34 @@ def test_graphs():
         assert all(torch.equal(a, b) for a, b in zip(want2, out2))
     _ok()
     del g1, g2
+
+
+def test_long_sums_in_streams_and_graphs():
+    """Products whose K is split over clusters: two streams at once, one captured, repeated."""
+    import torch
+    (x, dh), run_a = _all_operators(seed=1, M=300, N=136, K=2104)
+    (y, _), run_b = _all_operators(seed=50, M=2050, N=200, K=133)
+    want_a, want_b = run_a(), run_b()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [(run_a(stream=s1), run_b(stream=s2)) for _ in range(10)]
+    torch.cuda.synchronize()
+    for a, b in got:
+        assert all(torch.equal(p, q) for p, q in zip(want_a, a)) and all(torch.equal(p, q) for p, q in zip(want_b, b))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out_a, out_b = run_a(), run_b()
+    for seed in (7, 8):
+        x.copy_(_randn(seed, x.shape, "f16"))
+        dh.copy_(_randn(seed + 10, dh.shape, "f16", 0.1))
+        y.copy_(_randn(seed + 20, y.shape, "f16"))
+        want_a, want_b = run_a(), run_b()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(want_a, out_a))
+        assert all(torch.equal(p, q) for p, q in zip(want_b, out_b))
+    _ok()
+    del graph
 
 
 def test_given_workspace():
