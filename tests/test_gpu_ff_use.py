@@ -673,3 +673,28 @@ def test_results_given_count_as_written():
         mine = torch.empty((4, 32), dtype=torch.float16, device="cuda")
     assert tg.gated(x, w, w, out=mine) is mine
     _ok()
+
+
+def test_another_device():
+    """Tensors of a device that is not the current one: the call runs there, on that device's stream."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    if torch.cuda.device_count() < 2:
+        pytest.skip("needs two GPUs")
+    x, wg, wu, dh = (_randn(i, s, "f16", 0.1) for i, s in enumerate(((40, 72), (24, 72), (24, 72), (40, 24))))
+
+    def run(*ts):
+        h, g, u = tg.gated(*ts[:3], save=True)
+        q, s = tg.quantize_i8(ts[0])
+        qw, sw = tg.quantize_i8(ts[1])
+        return (h, g, u, *tg.gated_backward(ts[3], *ts[:3], g, u), q, s, tg.gemm_i8(q, s, qw, sw),
+                tg.gated_i8(q, s, qw, sw, qw, sw))
+
+    want = run(x, wg, wu, dh)
+    with torch.cuda.device(0):
+        got = run(*(t.to("cuda:1") for t in (x, wg, wu, dh)))
+        assert torch.cuda.current_device() == 0
+    torch.cuda.synchronize(1)
+    assert all(b.device.index == 1 and torch.equal(a, b.to(a.device)) for a, b in zip(want, got))
+    with pytest.raises(ValueError):
+        tg.gated(x, wg.to("cuda:1"), wu)
