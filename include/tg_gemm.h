@@ -447,9 +447,12 @@ TG_API tg_status tg_dequant_w4_f16(const void *Wq, const void *scales, void *W, 
  * the 16-bit type (nearest even).  One kernel computes both projections, the
  * activation and the product; with G and U given (both or neither) it stores
  * them too, rounded to the 16-bit type, which is what the backward pass reads.
- * The backward pass rounds dG and dU to the 16-bit type before the products; a
- * gate whose slope is 0 gives dG = 0 whatever U is, and a stored G that
- * overflowed to an infinity acts as the limit does.
+ * The backward pass rounds dG and dU to the 16-bit type before the products.  A
+ * gate whose slope is 0 gives dG = 0 * dH whatever U is.  G and U that overflowed
+ * when they were stored are infinities to it: the slope is the limit's, a dH of 0
+ * gives dG = dU = 0, and any other dH gives an infinite dU (G = +inf) or dG (U
+ * infinite), which makes the rows of the gradients that sum it infinite or NaN,
+ * though H itself, which is not computed from the stored values, may be finite.
  * Results do not depend on timing: equal inputs give equal bits.
  *
  * Sizes: each in [0, 2^30]; matrices of up to 2^50 elements with the gaps
