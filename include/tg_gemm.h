@@ -443,7 +443,8 @@ TG_API tg_status tg_dequant_w4_f16(const void *Wq, const void *scales, void *W, 
  * (g / (1 + exp(-g))) or TG_ACT_GELU (the tanh form,
  * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))).
  *
- * Sums, activations and products are fp32; every result is rounded once to
+ * Sums, activations and products are fp32 (a logistic value below 2^-134 is 0:
+ * g < -92.9 for SiLU); every result is rounded once to
  * the 16-bit type (nearest even).  One kernel computes both projections, the
  * activation and the product; with G and U given (both or neither) it stores
  * them too, rounded to the 16-bit type, which is what the backward pass reads.

@@ -63,3 +63,60 @@ def test_closed_gates_hide_no_gradient(act, dt):
     _, dg, du = _row_gradients(dh, closed, u, act, dt)
     assert np.isnan(dg[:3]).all() and np.isnan(du[:3]).all(), (dg, du)
     assert not any(dg[3:]) and not any(du[3:]), (dg, du)
+
+
+# ---------------------------------------------------------------------------
+# Far gates: logistic values down to fp32's last normal reciprocals
+# ---------------------------------------------------------------------------
+
+# silu's logistic value falls to 2^-128 at g = -88.7, gelu's at g = -10.06: bf16 results times a large U are far from zero.
+FAR = {"silu": [-60.0, -80.0, -86.5, -87.0, -87.5, -88.0, -88.5, -40.0], "gelu": [-8.0, -9.0, -9.5, -9.75, -10.0, -10.0625, -5.0, -7.0]}
+# The exponent z log2 e, up to 128, carries at most 3.5 roundings of 2^-24 relative (gelu: the square, the constants, the
+# polynomial, and half a one of the last step): 3.5 * 2^-24 * 128 ln 2 = 2^-15.7 relative to the logistic value.
+FAR_ERROR = 2.0 ** -15
+
+
+@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_far_gates(act, M):
+    """H, dWg and dWu where the gate's logistic value is next to fp32's end but what it multiplies is large."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x = torch.zeros((M, 8), dtype=torch.bfloat16, device="cuda")
+    x[:, 0] = 1
+    wg, wu = torch.zeros((2, 8, 8), dtype=torch.bfloat16, device="cuda")
+    wg[:, 0] = torch.tensor(FAR[act], device="cuda")
+    wu[:, 0] = 2.0 ** 90
+    h, g, u = tg.gated(x, wg, wu, act=act, save=True)
+    dh = torch.zeros((M, 8), dtype=torch.bfloat16, device="cuda")
+    dh[1] = 2.0 ** 20
+    dx, dwg, dwu = tg.gated_backward(dh, x, wg, wu, g, u, act=act)
+    _ok()
+    g64, u64 = ref.f64(g), ref.f64(u)
+    assert np.array_equal(g64[0], np.array(FAR[act])) and np.all(u64 == 2.0 ** 90)
+    a, s = ref.act(g64, act)
+    tol = FAR_ERROR + ref.HALF["bf16"]
+    ref.check(ref.f64(h), a * u64, tol * np.abs(a * u64), "H")
+    # The slope p + g p (1 - p) z' loses up to the size of its larger term.
+    p = np.abs(a / g64)
+    dg, du = ref.f64(dh) * u64 * s, ref.f64(dh) * a
+    err_g = np.abs(ref.f64(dh) * u64) * (np.abs(s) + 2 * p) * FAR_ERROR + ref.HALF["bf16"] * np.abs(dg)
+    ref.check(ref.f64(dwg)[:, 0], dg[1], 1.01 * err_g[1] + ref.round_error(dg[1], "bf16"), "dWg")
+    ref.check(ref.f64(dwu)[:, 0], du[1], (tol + 2 * ref.HALF["bf16"]) * np.abs(du[1]) + ref.TINY["bf16"], "dWu")
+
+
+@pytest.mark.parametrize("M", [2, 300])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_far_gates_i8(act, M):
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    a = torch.zeros((M, 16), dtype=torch.int8, device="cuda")
+    a[:, 0] = 1
+    wg, wu = torch.zeros((2, 8, 16), dtype=torch.int8, device="cuda")
+    wg[:, 0], wu[:, 0] = -1, 1
+    sa, sg = torch.ones(M, device="cuda"), -torch.tensor(FAR[act], device="cuda")
+    su = torch.full((8,), 2.0 ** 90, device="cuda")
+    h = tg.gated_i8(a, sa, wg, sg, wu, su, act=act, dtype=torch.bfloat16)
+    _ok()
+    want = np.broadcast_to(ref.act(np.array(FAR[act]), act)[0] * 2.0 ** 90, (M, 8))
+    ref.check(ref.f64(h), want, (FAR_ERROR + ref.HALF["bf16"]) * np.abs(want), "H")

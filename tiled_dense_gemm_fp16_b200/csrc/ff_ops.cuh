@@ -79,10 +79,13 @@ inline uint32_t make_idesc_ff(int kind, bool bf16, int M, int N, bool a_mn_major
 // ----------------------------------------------------------------------------
 // Both smooth activations are g * s(z) with the logistic function s: z = g
 // for silu, and for gelu (tanh form) z = 2 sqrt(2/pi) (g + 0.044715 g^3),
-// since (1 + tanh(y)) / 2 = s(2y).  s(z) = 1 / (1 + 2^(-z log2 e)), with -log2
-// e folded into the constants: one exponential and one reciprocal instruction,
-// each good to about 2^-22, far below half a step of a 16-bit result.  Below z
-// = -127 ln 2 the sum overflows towards +inf and s is 0 (less than 2^-126).
+// since (1 + tanh(y)) / 2 = s(2y).  s(z) = 2^-8 / (2^-8 + 2^(-8 - z log2 e)), with
+// -log2 e folded into the constants: one exponential and one reciprocal
+// instruction, each good to about 2^-22.  (Far from 0 the exponent's own rounding
+// adds up to 2^-15.)  Both are far below half a step of a 16-bit result.  The
+// reciprocal instruction gives subnormal results as 0; the factors of 2^-8 keep
+// it out of them down to s = 2^-134, a subnormal with 15 bits (in bf16, a far
+// gate times a large U is not 0).  Below that (z < -92.9) s is 0.
 constexpr float kLog2E = 1.4426950408889634f;
 constexpr float kGeluC1 = 1.5957691216057308f;   // 2 sqrt(2/pi)
 constexpr float kGeluC3 = 0.07135481282553557f;  // 2 sqrt(2/pi) 0.044715
@@ -134,13 +137,13 @@ __device__ __forceinline__ float2 same2(float a) { return make_float2(a, a); }
 // s(z) of the activation's z, for two values.
 template <int ACT>
 __device__ __forceinline__ float2 act_logistic2(float2 g) {
-  float2 t;  // -z log2 e
+  float2 t;  // -8 - z log2 e
   if (ACT == kActSilu)
-    t = mul2(g, same2(-kLog2E));
+    t = fma2(g, same2(-kLog2E), same2(-8.0f));
   else
-    t = mul2(g, fma2(mul2(g, g), same2(-kLog2E * kGeluC3), same2(-kLog2E * kGeluC1)));
-  const float2 d = add2(make_float2(exp2_approx(t.x), exp2_approx(t.y)), same2(1.0f));
-  return make_float2(rcp_approx(d.x), rcp_approx(d.y));
+    t = fma2(g, fma2(mul2(g, g), same2(-kLog2E * kGeluC3), same2(-kLog2E * kGeluC1)), same2(-8.0f));
+  const float2 d = add2(make_float2(exp2_approx(t.x), exp2_approx(t.y)), same2(0.00390625f));
+  return mul2(make_float2(rcp_approx(d.x), rcp_approx(d.y)), same2(0.00390625f));
 }
 
 template <int ACT>
