@@ -460,7 +460,9 @@ TG_API tg_status tg_dequant_w4_f16(const void *Wq, const void *scales, void *W, 
  * between their rows, row strides up to 2^38.  M == 0 or N == 0: nothing is enqueued by the
  * forward; a gradient that is a sum over nothing is set to +0.  K == 0 sets H
  * (and G, U) to +0.  Bytes between a row's end and the next row are not
- * written.  No result may overlap an input or another result.
+ * written.  No result may overlap an input or another result; rows in the gaps
+ * between the rows of a matrix of the same pitch do not (column ranges of one
+ * wider buffer: G and U side by side, H beside X).
  *
  * Workspace (256-byte aligned, overlapping nothing, free to reuse once the
  * call's work on `stream` is done): the forward needs it only where TMA cannot

@@ -120,3 +120,77 @@ def test_far_gates_i8(act, M):
     _ok()
     want = np.broadcast_to(ref.act(np.array(FAR[act]), act)[0] * 2.0 ** 90, (M, 8))
     ref.check(ref.f64(h), want, (FAR_ERROR + ref.HALF["bf16"]) * np.abs(want), "H")
+
+
+# ---------------------------------------------------------------------------
+# Results in the gaps between the rows of other matrices
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M,N,K", [(20, 136, 72), (20, 41, 33), (300, 136, 72), (300, 261, 129), (700, 264, 130)])
+def test_results_beside_inputs(M, N, K):
+    """X, H, G and U as column ranges of one buffer, and dX, dWg and dWu beside X, Wg and Wu: equal to results of their
+    own, the inputs unchanged."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    wide = K + 3 * N
+    buf = _randn(1, (M, wide), "f16")
+    weights = _randn(2, (N, 4 * K), "f16", K ** -0.5)  # Wg, dWg, Wu, dWu
+    dx_wide = torch.zeros((M, 2 * K), dtype=torch.float16, device="cuda")
+    x, h, g, u = buf[:, :K], *(buf[:, K + i * N:K + (i + 1) * N] for i in range(3))
+    wg, dwg, wu, dwu = (weights[:, i * K:(i + 1) * K] for i in range(4))
+    keep = [t.clone() for t in (x, wg, wu)]
+    dh = _randn(3, (M, N), "f16", 0.1)
+    want = tg.gated(x, wg, wu, act="gelu", save=True)
+    want_grads = tg.gated_backward(dh, x, wg, wu, *want[1:], act="gelu")
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+
+    opts = tg.gated_options(act=tg.ACT_GELU, ldx=wide, ldwg=4 * K, ldwu=4 * K, ldh=wide, ldg=wide, ldu=wide)
+    ptr = [t.data_ptr() for t in (x, wg, wu, h, g, u)]
+    assert tg.gated_raw(*ptr, M, N, K, opts, stream, ws.data_ptr(), ws.numel()) == tg.Status.OK
+    _ok()
+    for name, got, t in zip("HGU", (h, g, u), want):
+        assert torch.equal(got, t), name
+
+    # dX beside a copy of X with the same pitch.
+    x2, dx = dx_wide[:, :K], dx_wide[:, K:]
+    x2.copy_(keep[0])
+    opts = tg.gated_options(act=tg.ACT_GELU, ldx=2 * K, ldwg=4 * K, ldwu=4 * K, ldg=wide, ldu=wide, lddx=2 * K, lddwg=4 * K,
+                            lddwu=4 * K)
+    ptr = [t.data_ptr() for t in (dh, x2, wg, wu, g, u, dx, dwg, dwu)]
+    assert tg.gated_backward_raw(*ptr, M, N, K, opts, stream, ws.data_ptr(), ws.numel()) == tg.Status.OK
+    _ok()
+    for name, got, t in zip(("dX", "dWg", "dWu"), (dx, dwg, dwu), want_grads):
+        assert torch.equal(got, t), name
+    assert all(torch.equal(a, b) for a, b in zip((x, wg, wu), keep)) and torch.equal(x2, keep[0])
+
+
+def test_out_beside_x():
+    """The torch call with H beside X in one buffer."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    for M in (5, 300):
+        buf = _randn(1, (M, 72 + 40), "bf16")
+        w = _randn(2, (40, 72), "bf16", 0.1)
+        want = tg.gated(buf[:, :72].contiguous(), w, w)
+        got = tg.gated(buf[:, :72], w, w, out=buf[:, 72:])
+        _ok()
+        assert torch.equal(got, want) and torch.equal(buf[:, 72:], want)
+
+
+@pytest.mark.parametrize("M,K", [(9, 64), (200, 1000), (3, 20000), (400, 8200)])
+def test_codes_beside_values(M, K):
+    """Codes in the gaps between the rows they are made from."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    for shift in (0, 1):  # rows of X on 16-byte boundaries or off them
+        pitch = (3 * K + 2 * shift + 15) // 16 * 16 + 2 * shift
+        buf = torch.zeros(M * pitch + 64, dtype=torch.int8, device="cuda")
+        x = buf[2 * shift:].view(torch.float16).as_strided((M, K), (pitch // 2, 1), shift)
+        q = buf.as_strided((M, K), (pitch, 1), 2 * K + 2 * shift)
+        src = _randn(K, (M, K), "f16")
+        x.copy_(src)
+        want = tg.quantize_i8(src)
+        got = tg.quantize_i8(x, out=q)
+        _ok()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(x, src)

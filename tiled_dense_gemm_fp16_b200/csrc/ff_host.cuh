@@ -32,7 +32,17 @@ struct FfMat {
     return p != nullptr && (reinterpret_cast<uintptr_t>(p) % elem) == 0 && ld >= cols && ld <= kFfMaxStride &&
            rows <= kFfMaxSpan / ld;
   }
-  bool overlaps(const FfMat& o) const { return ranges_overlap(p, bytes(), o.p, o.bytes()); }
+  // Any byte of both.  Where their ranges meet, rows of one may still lie in the
+  // gaps between the other's (column ranges of one wider buffer): both repeat
+  // with the same pitch, and their columns are disjoint within it.
+  bool overlaps(const FfMat& o) const {
+    if (!ranges_overlap(p, bytes(), o.p, o.bytes())) return false;
+    const int64_t mine = ld * elem, other = o.ld * o.elem, pitch = rows > 1 ? mine : other;
+    if ((rows > 1 && o.rows > 1 && mine != other) || (rows <= 1 && o.rows <= 1)) return true;
+    int64_t at = (reinterpret_cast<intptr_t>(o.p) - reinterpret_cast<intptr_t>(p)) % pitch;
+    at = at < 0 ? at + pitch : at;
+    return at < cols * elem || at + o.cols * o.elem > pitch;
+  }
 };
 
 // The caller's matrix; ld 0 means dense rows.  A single row has no stride, so
