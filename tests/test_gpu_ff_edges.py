@@ -194,3 +194,29 @@ def test_codes_beside_values(M, K):
         got = tg.quantize_i8(x, out=q)
         _ok()
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(x, src)
+
+
+# ---------------------------------------------------------------------------
+# Blocks of every height of the small-M kernel
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [15, 32, 47, 64, 79, 81, 96, 112, 113, 128, 144, 190, 192, 240, 288])
+def test_heights_of_row_blocks(M):
+    """One block of 16 to 128 rows, and blocks of 64 to 96: rings of every size, K long enough to go round them."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    N, K, dt = 136, 2600, "bf16"
+    x, wg, wu = _randn(M, (M, K), dt), _randn(2, (N, K), dt, K ** -0.5), _randn(3, (N, K), dt, K ** -0.5)
+    got = tg.gated(x, wg, wu, save=True)
+    (q, s), (qg, sg), (qu, su) = (tg.quantize_i8(t) for t in (x, wg, wu))
+    c8, h8 = tg.gemm_i8(q, s, qg, sg, dtype=torch.bfloat16), tg.gated_i8(q, s, qg, sg, qu, su, dtype=torch.bfloat16)
+    _ok()
+    outs, tols = ref.gated(ref.f64(x), ref.f64(wg), ref.f64(wu), "silu", dt)
+    for name, t, o, tol in zip("HGU", got, outs, tols):
+        ref.check(ref.f64(t), o, tol, name)
+    rows = (q.cpu().numpy(), s.cpu().numpy())
+    g, dg = ref.i8_product(*rows, qg.cpu().numpy(), sg.cpu().numpy())
+    u, du = ref.i8_product(*rows, qu.cpu().numpy(), su.cpu().numpy())
+    ref.check(ref.f64(c8), g, dg + ref.round_error(g, dt), "C")
+    outs, tols = ref.gate(g, u, dg, du, "silu", dt)
+    ref.check(ref.f64(h8), outs[0], tols[0], "H, 8-bit")

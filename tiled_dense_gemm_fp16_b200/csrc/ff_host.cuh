@@ -280,18 +280,14 @@ bool ff_skinny_plan(const FfProduct& f, int block_rows, DeviceInfo* info, FfSkin
   pl.panels = (f.N + cols - 1) / cols;
   if (kb > INT_MAX || pl.panels > 65535) return false;
   pl.k_blocks = static_cast<int>(kb);
-  // Two CTAs per SM while a ring stays within 112 KiB; at m_pad <= 32 three
-  // stages of 64 KiB stream best.
-  const int budget = (pl.m_pad <= 32 ? 64 : (pl.m_pad <= 128 ? 112 : 220)) * 1024;
   const int stage_bytes = Cfg::W_STAGE_BYTES + pl.a_bytes;
-  pl.stages = budget / stage_bytes;
-  pl.stages = pl.stages > Cfg::MAX_STAGES ? Cfg::MAX_STAGES : pl.stages;
+  pl.stages = Cfg::stages(pl.m_pad, f.a_km);
   // The partial [m_pad][128] reuses the ring after the main loop.
   if (pl.stages < 2 || pl.stages * stage_bytes < pl.m_pad * Cfg::PANEL * 4) return false;
   pl.smem = Cfg::smem_bytes(pl.a_bytes, pl.stages);
   double best = 0.0;
   pl.splits = 0;
-  const int per_sm = pl.m_pad <= 128 ? 2 : 1;
+  const int per_sm = Cfg::ctas_per_sm(pl.m_pad);
   const int64_t slots = per_sm * info->sm_count;
   const int64_t tiles = pl.panels * pl.m_blocks * f.row_sources;
   const int64_t most = tiles >= slots ? 1 : slots / tiles;

@@ -55,8 +55,25 @@ struct FfSkinnyCfg {
   static constexpr int MAX_STAGES = 8;
   static constexpr int BAR_BYTES = 256;
   static constexpr int MAX_SMEM = 1024 + 220 * 1024 + BAR_BYTES;
-  static int a_bytes(int m_pad, bool a_km) { return a_km ? (m_pad + 63) / 64 * HALF_BYTES : m_pad * 128; }
-  static int smem_bytes(int a_bytes, int stages) { return 1024 + stages * (W_STAGE_BYTES + a_bytes) + BAR_BYTES; }
+  static constexpr int SM_SMEM = 228 * 1024;           // of one SM
+  static constexpr int CTA_RESERVED = 1024;            // of it, taken by the system for each resident CTA
+  static constexpr int a_bytes(int m_pad, bool a_km) { return a_km ? (m_pad + 63) / 64 * HALF_BYTES : m_pad * 128; }
+  static constexpr int smem_bytes(int a_bytes, int stages) {
+    return 1024 + stages * (W_STAGE_BYTES + a_bytes) + BAR_BYTES;
+  }
+  // CTAs that share an SM with blocks of m_pad rows, and the most stages a CTA's
+  // ring can have so that they do: at m_pad = 96 three, since two rings of four
+  // pass the SM's shared memory by 512 bytes (with four, one CTA an SM, gated
+  // fp16 96 x 8192 x 8192 takes 64 us; so 51).  At m_pad <= 32 three stages
+  // of up to 20 KiB stream best.
+  static constexpr int ctas_per_sm(int m_pad) { return m_pad <= 128 ? 2 : 1; }
+  static constexpr int stages(int m_pad, bool a_km) {
+    const int share = SM_SMEM / ctas_per_sm(m_pad) - CTA_RESERVED;
+    const int most = share < MAX_SMEM ? share : MAX_SMEM;
+    const int budget = m_pad <= 32 ? 64 * 1024 : most - smem_bytes(0, 0);
+    const int n = budget / (W_STAGE_BYTES + a_bytes(m_pad, a_km));
+    return n > MAX_STAGES ? MAX_STAGES : n;
+  }
 };
 
 // Four results of one row, from column n on.
