@@ -220,3 +220,80 @@ def test_heights_of_row_blocks(M):
     ref.check(ref.f64(c8), g, dg + ref.round_error(g, dt), "C")
     outs, tols = ref.gate(g, u, dg, du, "silu", dt)
     ref.check(ref.f64(h8), outs[0], tols[0], "H, 8-bit")
+
+
+# ---------------------------------------------------------------------------
+# gated_block inside other machinery of torch
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [40, 300])
+def test_captured_training_step(M):
+    """Forward and backward of gated_block captured after a warm-up on a side stream, replayed on new inputs."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    N, K, dt = 131, 72, "bf16"
+    x, dh = _randn(1, (M, K), dt).requires_grad_(), _randn(4, (M, N), dt, 0.5)
+    wg, wu = (_randn(i, (N, K), dt, 0.1).requires_grad_() for i in (2, 3))
+    leaves = (x, wg, wu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            tg.gated_block(*leaves).backward(dh)
+            for t in leaves:
+                t.grad = None
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        h = tg.gated_block(*leaves)
+        h.backward(dh)
+    for seed in (7, 8):
+        with torch.no_grad():
+            x.copy_(_randn(seed, (M, K), dt))
+            wu.copy_(_randn(seed + 1, (N, K), dt, 0.1))
+        dh.copy_(_randn(seed + 2, (M, N), dt, 0.5))
+        for t in leaves:
+            t.grad.fill_(NAN)  # a replay writes the gradients, it does not add to them
+        graph.replay()
+        _ok()
+        plain = [t.detach() for t in leaves]
+        want_h, g, u = tg.gated(*plain, save=True)
+        want = tg.gated_backward(dh, *plain, g, u)
+        _ok()
+        assert torch.equal(h, want_h) and all(torch.equal(t.grad, w) for t, w in zip(leaves, want))
+    del graph
+
+
+def test_checkpointed_and_compiled():
+    """Recomputed in the backward pass, and between the parts of a compiled function: the same values."""
+    import torch
+    from torch.utils.checkpoint import checkpoint
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, w = _randn(1, (40, 72), "f16"), _randn(2, (24, 72), "f16", 0.1).requires_grad_()
+
+    def loss(a):
+        return (tg.gated_block(a, w, w) * 2).float().sum()
+
+    loss(x).backward()
+    want, w.grad = w.grad, None
+    for form in (lambda: checkpoint(loss, x, use_reentrant=False), lambda: torch.compile(loss, backend="eager")(x)):
+        form().backward()
+        _ok()
+        assert torch.equal(w.grad, want)
+        w.grad = None
+
+
+def test_transforms_are_refused():
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, w = _randn(1, (40, 72), "f16"), _randn(2, (24, 72), "f16", 0.1)
+    for call in (lambda: torch.func.vmap(lambda a: tg.gated_block(a, w, w))(x[None].expand(2, 40, 72)),
+                 lambda: torch.func.grad(lambda a: tg.gated_block(a, w, w).float().sum())(x),
+                 lambda: torch.func.jvp(lambda a: tg.gated_block(a, w, w), (x,), (x,))):
+        with pytest.raises(RuntimeError):
+            call()
+    w.requires_grad_()
+    first = torch.autograd.grad(tg.gated_block(x, w, w).float().sum(), w, create_graph=True)[0]
+    with pytest.raises(RuntimeError):
+        first.float().sum().backward()
+    _ok()

@@ -10,6 +10,7 @@ from __future__ import annotations
 import os
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _binding
@@ -55,8 +56,8 @@ def gated(x, w_gate, w_up, act="silu", out=None, save=False, stream=None, worksp
     (H, gate, up) with the two projections, which ``gated_backward`` takes (their rows may have gaps).
     ``out`` receives H.  Rows may have any stride; ``workspace`` ("auto", None or a uint8 CUDA tensor) is
     needed only where a row stride or base is off 16 bytes.  Runs on ``stream``, or the current one; what
-    the call allocates belongs to that stream.  Nothing is recorded for autograd: ``gated_block`` is the
-    differentiable form.
+    the call allocates belongs to that stream.  Nothing is recorded for autograd, in reverse or forward mode:
+    ``gated_block`` is the differentiable form.
     """
     if stream is None:
         return _calls.gated(x, w_gate, w_up, act, out, save, workspace)
@@ -150,7 +151,12 @@ class GatedBlock(torch.autograd.Function):
 def gated_block(x, w_gate, w_up, act="silu"):
     """``gated`` under autograd: gradients reach x, w_gate and w_up (those that ask for one).
 
-    Runs on the current stream.  Without a gradient to take, neither projection is stored."""
+    Runs on the current stream.  Without a gradient to take, neither projection is stored.  Reverse mode, once:
+    second derivatives, forward mode (dual tensors) and the transforms of ``torch.func`` are refused.  Under
+    ``torch.compile`` the call runs as it is, between compiled parts.  To capture a training step into a CUDA
+    graph, let go of every earlier autograd graph of the same leaves first, as torch asks for any operator."""
+    if any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w_gate, w_up)):
+        raise NotImplementedError("gated_block has no forward-mode derivative")
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
         return GatedBlock.apply(x, w_gate, w_up, act)
     return gated(_rows(x), _rows(w_gate), _rows(w_up), act=act)
