@@ -297,3 +297,17 @@ def test_transforms_are_refused():
     with pytest.raises(RuntimeError):
         first.float().sum().backward()
     _ok()
+
+
+def test_negated_views_under_autograd():
+    """Values and gradients that are negated views count with their sign."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    x, w, dh = _randn(1, (40, 72), "f16"), _randn(2, (24, 72), "f16", 0.1).requires_grad_(), _randn(3, (40, 24), "f16")
+    h = tg.gated_block(torch._neg_view(x), w, w)
+    h.backward(torch._neg_view(dh))
+    got, w.grad = w.grad, None
+    want = tg.gated_block(-x, w, w)
+    want.backward(-dh)
+    _ok()
+    assert torch.equal(h, want) and torch.equal(got, w.grad)

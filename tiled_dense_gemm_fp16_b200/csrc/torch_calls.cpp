@@ -38,7 +38,10 @@ void check_status(int status, const char* what) {
 
 const at::Tensor& tensor_of(PyObject* o, const char* name) {
   TORCH_CHECK_TYPE(THPVariable_Check(o), name, " must be a tensor");
-  return THPVariable_Unpack(o);
+  const at::Tensor& t = THPVariable_Unpack(o);
+  // A view whose values are the negatives of its memory (the imaginary part of a conjugate).
+  TORCH_CHECK_VALUE(!t.is_neg(), name, " is a negated view; pass its resolve_neg()");
+  return t;
 }
 
 const at::Tensor& cuda_tensor(PyObject* o, const char* name) {

@@ -118,7 +118,10 @@ def gated_i8(a, a_scale, w_gate, gate_scale, w_up, up_scale, act="silu", dtype=N
 # ---------------------------------------------------------------------------
 
 def _rows(t):
-    """t, or a dense copy where its rows are not evenly spaced with adjacent columns (an expanded gradient)."""
+    """t, or a dense copy where its rows are not evenly spaced with adjacent columns (an expanded gradient) or its
+    values are the negatives of its memory."""
+    if t.is_neg():
+        return t.resolve_neg().contiguous()
     if t.is_contiguous():
         return t
     if t.dim() >= 2 and t.numel() and (t.shape[-1] == 1 or t.stride(-1) == 1):
