@@ -396,6 +396,17 @@ PyObject* gated_i8(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// has_tangent(tensors...): whether any is a dual tensor of forward-mode differentiation.
+PyObject* has_tangent(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  for (Py_ssize_t i = 0; i < nargs; ++i) {
+    TORCH_CHECK_TYPE(THPVariable_Check(args[i]), "expected tensors");
+    if (THPVariable_Unpack(args[i])._fw_grad(/*level=*/0).defined()) Py_RETURN_TRUE;
+  }
+  Py_RETURN_FALSE;
+  END_HANDLE_TH_ERRORS
+}
+
 // set_error(class): what a status that is not TG_OK is raised as.
 PyObject* set_error(PyObject*, PyObject* error) {
   Py_INCREF(error);
@@ -414,6 +425,7 @@ PyMethodDef g_methods[] = {
     {"quantize_i8", fast(quantize_i8), METH_FASTCALL, nullptr},
     {"gemm_i8", fast(gemm_i8), METH_FASTCALL, nullptr},
     {"gated_i8", fast(gated_i8), METH_FASTCALL, nullptr},
+    {"has_tangent", fast(has_tangent), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -10,7 +10,6 @@ from __future__ import annotations
 import os
 
 import torch
-from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from . import _binding
@@ -158,7 +157,7 @@ def gated_block(x, w_gate, w_up, act="silu"):
     second derivatives, forward mode (dual tensors) and the transforms of ``torch.func`` are refused.  Under
     ``torch.compile`` the call runs as it is, between compiled parts.  To capture a training step into a CUDA
     graph, let go of every earlier autograd graph of the same leaves first, as torch asks for any operator."""
-    if any(forward_ad.unpack_dual(t).tangent is not None for t in (x, w_gate, w_up)):
+    if _calls.has_tangent(x, w_gate, w_up):
         raise NotImplementedError("gated_block has no forward-mode derivative")
     if torch.is_grad_enabled() and (x.requires_grad or w_gate.requires_grad or w_up.requires_grad):
         return GatedBlock.apply(x, w_gate, w_up, act)
