@@ -1,4 +1,8 @@
 """The torch side of the feed-forward calls: what it refuses before any device is needed."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -41,3 +45,40 @@ def test_negated_views_are_refused():
         tg.gated(x, w, w)
     with pytest.raises(ValueError, match="negated view"):
         calls.gemm_i8(q, s, q, s, None, False, None, None)
+
+
+# ---------------------------------------------------------------------------
+# The compiled module and what it was built for
+# ---------------------------------------------------------------------------
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def test_a_module_for_another_torch_is_stale(monkeypatch):
+    from tiled_dense_gemm_fp16_b200 import build, feedforward
+    if not build.calls_stale():
+        assert feedforward._calls.key == build._calls_key() and feedforward._calls.target == build.calls_target()
+    here, command = build.calls_target(), build._calls_command
+    assert torch.__version__ in here
+    for other in (here.replace(torch.__version__, "0.0"), here.replace("Python c", "Python d"), here + "x"):
+        with monkeypatch.context() as m:
+            m.setattr(build, "calls_target", lambda: other)
+            assert build.calls_stale()
+    with monkeypatch.context() as m:
+        m.setattr(build, "_calls_command", lambda out: [*command(out), "-O3"])
+        assert build.calls_stale()
+
+
+def test_a_module_for_another_torch_is_not_loaded():
+    code = """
+import tiled_dense_gemm_fp16_b200 as tg
+from tiled_dense_gemm_fp16_b200 import build
+build.calls_target = lambda: "torch 0.0"
+try:
+    tg.gated
+except ImportError as e:
+    assert "torch 0.0" in str(e) and "build" in str(e)
+    print("refused")
+"""
+    p = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0 and p.stdout.strip() == "refused", p.stderr[-2000:]

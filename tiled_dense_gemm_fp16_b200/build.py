@@ -54,27 +54,57 @@ def is_stale() -> bool:
     return _older(LIB_PATH, _deps())
 
 
-def build_calls(force: bool = False, verbose: bool = False) -> str | None:
-    """The torch module (None without torch).  Needs the library to link to."""
-    import importlib.util
+def calls_target() -> str:
+    """What the compiled torch module is good for: it reads torch's objects by their layout and Python's by their ABI."""
     import sysconfig
-    if importlib.util.find_spec("torch") is None:
-        return None
-    if not force and not _older(CALLS_PATH, [CALLS_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")]):
-        return CALLS_PATH
+
+    import torch
+    return (f"torch {torch.__version__}, C++11 ABI {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, "
+            f"Python {sysconfig.get_config_var('SOABI')}")
+
+
+def _calls_command(out: str) -> list[str]:
+    import sysconfig
+
     import torch
     torch_dir = os.path.dirname(torch.__file__)
     cuda_dir = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [os.path.join(ROOT, "include"), os.path.join(torch_dir, "include"),
                 os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
                 sysconfig.get_paths()["include"], os.path.join(cuda_dir, "include")]
-    tmp = CALLS_PATH + f".tmp{os.getpid()}"
     # nvcc's host compiler, not $CXX: one that links its own C++ runtime statically leaves two of them in the
     # process, and an exception that torch's code throws through the module ends it.
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in includes),
-           CALLS_SOURCE, "-o", tmp, f"-L{HERE}", "-l:libtg_gemm.so", f"-L{os.path.join(torch_dir, 'lib')}", "-lc10",
-           "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{d}" for d in includes),
+            CALLS_SOURCE, "-o", out, f"-L{HERE}", "-l:libtg_gemm.so", f"-L{os.path.join(torch_dir, 'lib')}", "-lc10",
+            "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-Wl,-rpath,$ORIGIN"]
+
+
+def _calls_key() -> str:
+    """Target and build command of the module, which it carries as text."""
+    import hashlib
+    command = hashlib.sha256(" ".join(_calls_command("")).encode()).hexdigest()[:16]
+    return f"{calls_target()}; built by {command}"
+
+
+def calls_stale() -> bool:
+    """Whether the module is missing, older than its sources, or built for another torch or Python or by another command."""
+    if _older(CALLS_PATH, [CALLS_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")]):
+        return True
+    with open(CALLS_PATH, "rb") as f:
+        return _calls_key().encode() + b"\0" not in f.read()
+
+
+def build_calls(force: bool = False, verbose: bool = False) -> str | None:
+    """The torch module (None without torch).  Needs the library to link to."""
+    import importlib.util
+    if importlib.util.find_spec("torch") is None:
+        return None
+    if not force and not calls_stale():
+        return CALLS_PATH
+    tmp = CALLS_PATH + f".tmp{os.getpid()}"
+    cmd = _calls_command(tmp)
+    cmd += [f'-DTG_CALLS_TARGET="{calls_target()}"', f'-DTG_CALLS_KEY="{_calls_key()}"']
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.run(cmd, check=True)

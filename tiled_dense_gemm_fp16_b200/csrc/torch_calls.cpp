@@ -435,4 +435,13 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the fee
 
 }  // namespace
 
-extern "C" __attribute__((visibility("default"))) PyObject* PyInit__calls(void) { return PyModule_Create(&g_module); }
+// `target` is what the module was built for; `key` also names the command that built it.
+extern "C" __attribute__((visibility("default"))) PyObject* PyInit__calls(void) {
+  PyObject* m = PyModule_Create(&g_module);
+  if (m && (PyModule_AddStringConstant(m, "target", TG_CALLS_TARGET) < 0 ||
+            PyModule_AddStringConstant(m, "key", TG_CALLS_KEY) < 0)) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

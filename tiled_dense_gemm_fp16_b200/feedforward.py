@@ -12,7 +12,7 @@ import os
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _binding
+from . import _binding, build
 
 if not os.path.exists(_binding.CALLS_PATH):
     raise ImportError(f"{_binding.CALLS_PATH} is not built; run `python -m tiled_dense_gemm_fp16_b200.build` "
@@ -21,6 +21,9 @@ _binding.lib()  # the C library first: _calls links to it
 
 from . import _calls  # noqa: E402
 
+if _calls.target != build.calls_target():
+    raise ImportError(f"{_binding.CALLS_PATH} was built for {_calls.target}, this is {build.calls_target()}; run "
+                      "`python -m tiled_dense_gemm_fp16_b200.build`")
 _calls.set_error(_binding.TGError)
 
 
