@@ -90,6 +90,12 @@ struct FfPairCfg {
   static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(NUM_ACC * BN <= TMEM_COLS, "TMEM columns");
   static_assert(EPI_COLS % 64 == 0, "a warp finishes whole boxes of 32 result columns");
+  // Every address that TMA, the MMAs and the barriers get is the base (on 1024)
+  // plus a sum of these.
+  static_assert(A_BYTES % 1024 == 0 && PANEL_BYTES % 1024 == 0 && B_SLAB_BYTES % 2048 == 0,
+                "operand tiles, and the gate and up halves of a slab, start on the swizzle's 1024 bytes");
+  static_assert(C_BUF_BYTES % 512 == 0, "staging boxes start on their swizzle's 512 bytes");
+  static_assert((STAGES * (A_BYTES + B_BYTES) + C_STAGE_BYTES) % 512 == 0, "barriers on 8 bytes");
 };
 
 // Tile t of the walk: its place, and for a half tile (one slab of 256

@@ -61,6 +61,7 @@ struct FfSkinnyCfg {
   static constexpr int smem_bytes(int a_bytes, int stages) {
     return 1024 + stages * (W_STAGE_BYTES + a_bytes) + BAR_BYTES;
   }
+  static_assert(HALF_BYTES % 1024 == 0 && (16 * 128) % 1024 == 0, "halves and blocks start on the swizzle's 1024 bytes");
   // CTAs that share an SM with blocks of m_pad rows, and the most stages a CTA's
   // ring can have so that they do: at m_pad = 96 three, since two rings of four
   // pass the SM's shared memory by 512 bytes (with four, one CTA an SM, gated
