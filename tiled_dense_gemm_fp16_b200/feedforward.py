@@ -56,7 +56,7 @@ def gated(x, w_gate, w_up, act="silu", out=None, save=False, stream=None, worksp
 
     ``act``: "silu", "gelu" (tanh form) or "relu".  Returns H (..., N); with ``save`` the tuple
     (H, gate, up) with the two projections, which ``gated_backward`` takes (their rows may have gaps).
-    ``out`` receives H.  Rows may have any stride; ``workspace`` ("auto", None or a uint8 CUDA tensor) is
+    ``out`` receives H (also beside x in one wider buffer).  Rows may have any stride; ``workspace`` ("auto", None or a uint8 CUDA tensor) is
     needed only where a row stride or base is off 16 bytes.  Runs on ``stream``, or the current one; what
     the call allocates belongs to that stream.  Nothing is recorded for autograd, in reverse or forward mode:
     ``gated_block`` is the differentiable form.
@@ -72,6 +72,7 @@ def gated_backward(grad, x, w_gate, w_up, gate, up, act="silu", needs=(True, Tru
     """Gradients of ``gated`` for grad = dH (..., N), with the projections that ``gated(..., save=True)``
     returned: (dx, dw_gate, dw_up), None where ``needs`` is false.
 
+    gate and up, and dG and dU between the two steps, are of the operands' 16-bit type; sums are 32-bit.
     ``workspace``: "auto" lets torch allocate the bytes for dG and dU; a uint8 CUDA tensor is used as
     given (calls whose work may overlap need one each).
     """
