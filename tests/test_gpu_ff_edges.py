@@ -311,3 +311,42 @@ def test_negated_views_under_autograd():
     want.backward(-dh)
     _ok()
     assert torch.equal(h, want) and torch.equal(got, w.grad)
+
+
+@pytest.mark.parametrize("M", [20, 128, 300, 2000])
+@pytest.mark.parametrize("N,ld", [(41, 48), (129, 136), (263, 264), (7, 8)])
+def test_bytes_behind_rows_on_16_byte_boundaries(M, N, ld):
+    """Rows that start on 16-byte boundaries and end inside one: the bytes up to the next row stay."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    K, guard = 96, 0x5A5A
+    x, wg, wu = _randn(1, (M, K), "f16"), _randn(2, (N, K), "f16", 0.1), _randn(3, (N, K), "f16", 0.1)
+    dh = _randn(4, (M, N), "f16", 0.5)
+
+    def framed(rows, cols, pitch):
+        whole = torch.full((rows, pitch), guard, dtype=torch.int16, device="cuda")
+        return whole, whole.view(torch.float16)[:, :cols]
+
+    stream = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    results = [framed(M, N, ld) for _ in range(3)]
+    opts = tg.gated_options(act=tg.ACT_SILU, ldh=ld, ldg=ld, ldu=ld)
+    ptr = [t.data_ptr() for t in (x, wg, wu, *(r[1] for r in results))]
+    assert tg.gated_raw(*ptr, M, N, K, opts, stream, ws.data_ptr(), ws.numel()) == tg.Status.OK
+    grads = [framed(rows, K - 1, K) for rows in (M, N, N)]  # of a block that is K - 1 wide
+    opts = tg.gated_options(act=tg.ACT_SILU, ldx=K, ldwg=K, ldwu=K, ldg=ld, ldu=ld, lddx=K, lddwg=K, lddwu=K)
+    ptr = [t.data_ptr() for t in (dh, x, wg, wu, *(r[1] for r in results[1:]), *(r[1] for r in grads))]
+    assert tg.gated_backward_raw(*ptr, M, N, K - 1, opts, stream, ws.data_ptr(), ws.numel()) == tg.Status.OK
+    (q, s), (qw, sw) = tg.quantize_i8(x), tg.quantize_i8(wg)
+    products = [framed(M, N, ld) for _ in range(2)]
+    tg.gemm_i8(q, s, qw, sw, out=products[0][1])
+    tg.gated_i8(q, s, qw, sw, qw, sw, out=products[1][1])
+    _ok()
+    for (whole, view), cols in [(r, N) for r in (*results, *products)] + [(r, K - 1) for r in grads]:
+        assert torch.all(whole[:, cols:] == guard)
+    want = tg.gated(x, wg, wu, save=True)
+    assert all(torch.equal(r[1], w) for r, w in zip(results, want))
+    xk, gk, uk = (t[:, :K - 1].contiguous() for t in (x, wg, wu))
+    for r, w in zip(grads, tg.gated_backward(dh, xk, gk, uk, *want[1:])):
+        assert torch.equal(r[1], w)
+    assert torch.equal(products[0][1], tg.gemm_i8(q, s, qw, sw)) and torch.equal(products[1][1], tg.gated_i8(q, s, qw, sw, qw, sw))

@@ -54,7 +54,7 @@ struct FfParams {
   int bf16;                   // type of the 16-bit results (and operands)
   int act, relu;
   int save;                   // gated: store G and U
-  int c_aligned[3];           // rows of the result start on 16-byte boundaries
+  int c_aligned[3];           // rows of the result start on 16-byte boundaries (they may end inside 16 bytes)
   int l2_hints;               // as TcParams
   uint32_t idesc;
   uint64_t wait_budget_ns;
@@ -223,7 +223,9 @@ __device__ __forceinline__ void gate_row(float (&g)[16], const float (&u)[16]) {
 
 // One 32 x 32 box of a result: lane = row, h = its 32 packed values, `buf` one
 // of the warp's BUFS staging boxes (64-byte swizzle), which take turns.  Rows
-// that start on 16-byte boundaries leave as one TMA box.  Else two rows leave
+// that start on 16-byte boundaries leave as one TMA box, but for a box in which
+// they end inside 16 bytes: TMA clips a store to whole 16-byte pieces (measured:
+// N = 41 in rows of 48 writes zeros up to column 47).  Else two rows leave
 // per store instruction, 4 bytes a lane: the rows are staged shifted so that
 // words start on 4-byte boundaries, which leaves the first and last value of a
 // row on an odd 2-byte boundary to single stores by the row's lane.
@@ -234,7 +236,7 @@ __device__ __forceinline__ void ff_store_box(const CUtensorMap* map, void* c, in
   if (lane == 0) bulk_wait_group_read<BUFS - 1>();  // the last box stored from `buf` has been read
   __syncwarp();
   const uint32_t row_addr = smem_u32(buf) + lane * 64;
-  if (aligned) {
+  if (aligned && (col0 + 32 <= N || (N & 7) == 0)) {
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       st_shared_v4(row_addr + ((q ^ ((lane >> 1) & 3)) << 4), h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);

@@ -56,10 +56,10 @@ def gated(x, w_gate, w_up, act="silu", out=None, save=False, stream=None, worksp
 
     ``act``: "silu", "gelu" (tanh form) or "relu".  Returns H (..., N); with ``save`` the tuple
     (H, gate, up) with the two projections, which ``gated_backward`` takes (their rows may have gaps).
-    ``out`` receives H (also beside x in one wider buffer).  Rows may have any stride; ``workspace`` ("auto", None or a uint8 CUDA tensor) is
-    needed only where a row stride or base is off 16 bytes.  Runs on ``stream``, or the current one; what
-    the call allocates belongs to that stream.  Nothing is recorded for autograd, in reverse or forward mode:
-    ``gated_block`` is the differentiable form.
+    ``out`` receives H (it may lie beside x in one wider buffer).  Rows may have any stride; ``workspace``
+    ("auto", None or a uint8 CUDA tensor) is needed only where a row stride or base is off 16 bytes.  Runs on
+    ``stream``, or the current one; what the call allocates belongs to that stream.  Nothing is recorded for
+    autograd, in reverse or forward mode: ``gated_block`` is the differentiable form.
     """
     if stream is None:
         return _calls.gated(x, w_gate, w_up, act, out, save, workspace)
