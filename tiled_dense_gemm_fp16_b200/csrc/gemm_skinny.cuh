@@ -40,7 +40,7 @@ struct SkinnyParams {
   uint32_t tmem_cols;     // power of two >= max(32, m_pad)
   uint32_t idesc;
   int prefetch_kb;        // > 0: also prefetch into L2 the B boxes this many k-blocks ahead
-  int c_aligned;          // 1: rows of C start on 8-byte boundaries (4-value stores)
+  int c_aligned;          // 1: rows of C start and end on 8-byte boundaries (4-value stores)
   uint64_t wait_budget_ns;
 };
 

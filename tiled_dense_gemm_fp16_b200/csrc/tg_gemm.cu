@@ -125,7 +125,7 @@ struct Operands {
   int64_t ldc;
   const void* bias;
   int64_t M, N, K;
-  bool c_aligned;  // every row of C starts on a 16-byte boundary
+  bool c_aligned;  // C is written in whole 16-byte pieces
 };
 
 // ---------------------------------------------------------------------------
@@ -322,6 +322,12 @@ int64_t rc_b_copy_bytes(const Problem& p) {
 bool c_rows_aligned(const Problem& p) {
   return (reinterpret_cast<uintptr_t>(p.C) & 15u) == 0 && p.ldc % 8 == 0 && (p.batch == 1 || p.sc % 8 == 0);
 }
+
+// Whether the kernels may write C in whole 16-byte pieces (vectors, or TMA
+// boxes, whose stores TMA clips to such pieces): rows that start on 16-byte
+// boundaries and end on one too, else up to 7 values behind every row would be
+// written.
+bool c_pieces_whole(const Problem& p) { return c_rows_aligned(p) && p.N % 8 == 0; }
 
 // The small-M kernel (A stored M x K) for M <= 128, where two CTAs share an
 // SM and the split-K partials are small; for 128 < M <= 256 only when B is
@@ -729,7 +735,7 @@ tg_status launch_skinny(const Operands& o, cudaStream_t stream, DeviceInfo* info
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N);
   p.K = static_cast<int>(K);
-  p.c_aligned = (reinterpret_cast<uintptr_t>(o.C) % 8 == 0 && o.ldc % 4 == 0) ? 1 : 0;
+  p.c_aligned = (reinterpret_cast<uintptr_t>(o.C) % 8 == 0 && o.ldc % 4 == 0 && N % 4 == 0) ? 1 : 0;  // whole pieces
   p.m_pad = static_cast<int>((M + 15) / 16 * 16);
   p.k_blocks = static_cast<int>((K + Cfg::BK - 1) / Cfg::BK);
   // Two CTAs per SM fit while the ring stays within ~112 KiB (M_pad <= 128).
@@ -1063,7 +1069,7 @@ tg_status run(const Problem& p, void* stream_ptr, int path, void* ws, int64_t ws
                p.M,
                p.N,
                p.K,
-               c_rows_aligned(p)};
+               c_pieces_whole(p)};
     if (path == TG_PATH_ZERO) {
       st = launch_k_zero(o, stream, info);
     } else if (path == TG_PATH_RC && rc_b_bytes > 0) {
