@@ -710,6 +710,21 @@ tg_status launch_tc_pair(const Operands& o, cudaStream_t stream, DeviceInfo* inf
   }
 }
 
+// Ring of a small-M CTA that shares its SM with another, in KiB.  With 112, four
+// stages at M_pad = 96 fill it to the last byte, and two such CTAs with the 1 KiB
+// that the system takes for each pass the SM's 228 KiB by 512 bytes; the ring
+// depths of all other heights are the same.
+constexpr int kSkinnySharedKb = 111;
+constexpr bool skinny_ctas_fit() {
+  for (int m_pad = 16; m_pad <= 128; m_pad += 16) {
+    const int stage = SkinnyCfg::B_STAGE_BYTES + m_pad * 128;
+    const int n = kSkinnySharedKb * 1024 / stage;
+    if (2 * (1024 + (n < 8 ? n : 8) * stage + SkinnyCfg::BAR_BYTES + 1024) > 228 * 1024) return false;
+  }
+  return true;
+}
+static_assert(skinny_ctas_fit(), "two small-M CTAs share an SM");
+
 // Small-M path: grid (S, P) with clusters of S CTAs along K.
 tg_status launch_skinny(const Operands& o, cudaStream_t stream, DeviceInfo* info) {
   const int64_t M = o.M, N = o.N, K = o.K;
@@ -738,11 +753,11 @@ tg_status launch_skinny(const Operands& o, cudaStream_t stream, DeviceInfo* info
   p.c_aligned = (reinterpret_cast<uintptr_t>(o.C) % 8 == 0 && o.ldc % 4 == 0 && N % 4 == 0) ? 1 : 0;  // whole pieces
   p.m_pad = static_cast<int>((M + 15) / 16 * 16);
   p.k_blocks = static_cast<int>((K + Cfg::BK - 1) / Cfg::BK);
-  // Two CTAs per SM fit while the ring stays within ~112 KiB (M_pad <= 128).
+  // Two CTAs per SM fit while the ring stays within kSkinnySharedKb (M_pad <= 128).
   const bool two_per_sm = p.m_pad <= 128;
-  // Measured: M_pad <= 32 streams best with a 3-stage ring, larger M_pad
-  // with ~112 KiB (4 stages at M_pad = 64).
-  int budget_kb = tune_int("TG_TUNE_SKINNY_SMEM_KB", p.m_pad <= 32 ? 64 : (two_per_sm ? 112 : 220));
+  // Measured: M_pad <= 32 streams best with a 3-stage ring, larger M_pad with
+  // all that fits (4 stages at M_pad = 64).
+  int budget_kb = tune_int("TG_TUNE_SKINNY_SMEM_KB", p.m_pad <= 32 ? 64 : (two_per_sm ? kSkinnySharedKb : 220));
   budget_kb = budget_kb < 32 ? 32 : (budget_kb > 220 ? 220 : budget_kb);
   const int budget = budget_kb * 1024;
   const int stage_bytes = Cfg::stage_bytes(p.m_pad);
