@@ -69,6 +69,18 @@ def test_a_module_for_another_torch_is_stale(monkeypatch):
         assert build.calls_stale()
 
 
+def test_a_built_module_needs_no_compiler(monkeypatch):
+    from tiled_dense_gemm_fp16_b200 import build
+    stale = build.calls_stale()
+
+    def missing():
+        raise RuntimeError("nvcc not found")
+    monkeypatch.setattr(build, "_nvcc", missing)
+    assert stale or not build.calls_stale()
+    monkeypatch.setattr(build, "calls_target", lambda: "torch 0.0")
+    assert build.calls_stale()
+
+
 def test_a_module_for_another_torch_is_not_loaded():
     code = """
 import tiled_dense_gemm_fp16_b200 as tg

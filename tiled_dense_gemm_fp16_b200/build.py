@@ -91,8 +91,12 @@ def calls_stale() -> bool:
     """Whether the module is missing, older than its sources, or built for another torch or Python or by another command."""
     if _older(CALLS_PATH, [CALLS_SOURCE, os.path.join(ROOT, "include", "tg_gemm.h")]):
         return True
+    try:
+        key = _calls_key() + "\0"
+    except RuntimeError:  # no nvcc, so none to build it again with: what it was built for still counts
+        key = calls_target() + "\0"
     with open(CALLS_PATH, "rb") as f:
-        return _calls_key().encode() + b"\0" not in f.read()
+        return key.encode() not in f.read()
 
 
 def build_calls(force: bool = False, verbose: bool = False) -> str | None:
