@@ -547,6 +547,107 @@ TG_API tg_status tg_gated_i8(const void *A, const float *a_scale, const void *Wg
                              const float *u_scale, void *H, int64_t M, int64_t N, int64_t K,
                              const tg_gated_options *options, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Products grouped by expert
+ *
+ * The rows of X lie group by group: group g owns rows [ends[g-1], ends[g]) (from
+ * row 0 for g = 0) and has a weight W_g of its own:
+ *
+ *   Y[r]  = W_g X[r]                                  (tg_grouped)
+ *   dX[r] = W_g^T dY[r],  dW_g = sum_{r in g} dY[r] X[r]^T   (tg_grouped_backward)
+ *
+ * X, dX: M x K.  W, dW: G stacked N x K matrices, as linear layers store them.
+ * Y, dY: M x N.  All are 16-bit floats of one type (options->type), row-major with
+ * row strides of their own, on any 2-byte boundary.  ends: G 32-bit integers in
+ * DEVICE memory, not decreasing, at most M: groups may be empty, and rows behind
+ * the last end belong to no group.  They are read by the kernels, never by the
+ * host, so a captured graph may be replayed with other groups.  Values that
+ * break the rule give wrong rows, but no access outside a matrix.
+ *
+ * Rows that belong to no group are left alone in Y and dX, or set to +0 with
+ * options->rest = 1; nothing in them reaches a result.  dW_g of an empty group is +0.  Sums are
+ * fp32, each result is rounded once (nearest even).  Results do not depend on
+ * timing: equal inputs give equal bits.  Rows of X may be NaN or infinite without
+ * effect on other rows, and rows of one group on other groups.
+ *
+ * Sizes: 0 <= G <= 1024, the others and the strides as for tg_gated.  M == 0: Y and dX
+ * are empty, dW is +0.  N == 0 or K == 0: a result that is a sum over nothing is
+ * set to +0.  No result may overlap an input or another result (as for tg_gated).
+ * Workspace (256-byte aligned): only where TMA cannot describe an operand (a row
+ * stride, a distance between weights or a base off 16 bytes), for padded copies;
+ * weights that are copied must be evenly spaced rows (stride_w = N * ldw).
+ * ------------------------------------------------------------------------- */
+/* A zero-initialised value (or NULL): fp16, dense rows, rows without a group left alone. */
+typedef struct tg_grouped_options {
+    int32_t type;        /* TG_TYPE_F16 or TG_TYPE_BF16                               */
+    int32_t rest;        /* 1: rows without a group are set to +0 in Y, dX            */
+    int64_t ldx, ldw, ldy; /* elements between rows of X, of one W, of Y (backward: of dY); 0 = dense */
+    int64_t stride_w;    /* elements between W_g and W_{g+1}; 0 = N * ldw             */
+    int64_t lddx, lddw;  /* of the gradients                                          */
+    int64_t stride_dw;   /* 0 = N * lddw; at least (N - 1) * lddw + K                 */
+    int64_t reserved;    /* must be 0                                                 */
+} tg_grouped_options;
+
+TG_API tg_status tg_grouped(const void *X, const void *W, const int32_t *ends, void *Y, int32_t groups, int64_t M,
+                            int64_t N, int64_t K, const tg_grouped_options *options, void *stream, void *workspace,
+                            int64_t workspace_bytes);
+
+/* Workspace bytes tg_grouped needs (usually 0), or -1 for invalid arguments.
+ * Host logic only. */
+TG_API int64_t tg_grouped_workspace_size(const void *X, const void *W, int32_t groups, int64_t M, int64_t N, int64_t K,
+                                         const tg_grouped_options *options);
+
+/* dX or dW may be NULL: it is not computed. */
+TG_API tg_status tg_grouped_backward(const void *dY, const void *X, const void *W, const int32_t *ends, void *dX,
+                                     void *dW, int32_t groups, int64_t M, int64_t N, int64_t K,
+                                     const tg_grouped_options *options, void *stream, void *workspace,
+                                     int64_t workspace_bytes);
+
+/* Workspace bytes tg_grouped_backward needs for the gradients that are not NULL,
+ * or -1 for invalid arguments.  Host logic only. */
+TG_API int64_t tg_grouped_backward_workspace_size(const void *dY, const void *X, const void *W, const void *dX,
+                                                  const void *dW, int32_t groups, int64_t M, int64_t N, int64_t K,
+                                                  const tg_grouped_options *options);
+
+/* ---------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection
+ *
+ *   Y[r] = W X[r] + scale[a] B_a (A_a X[r]) + bias,  a = index[r]
+ *
+ * X: M x K, W: N x K, Y: M x N, as for tg_gated.  A: `adapters` stacked rank x K
+ * matrices, B: as many N x rank ones.  index: M 32-bit integers in DEVICE memory;
+ * a row whose value is outside [0, adapters) (-1, say) has no adapter and gets W X[r] + bias.
+ * Rows of one adapter may lie anywhere; next to each other they are faster.
+ * scale: one fp32 value for each adapter, or NULL (1).  bias: N values of the type, or NULL.
+ *
+ * Sums are fp32.  scale[a] A_a X[r] is rounded to the 16-bit type before it meets
+ * B_a (the tensor cores read it so), the sum of all terms once more.  Each row's result
+ * depends on its own values and its own adapter only: infinities and NaN in other
+ * rows or other adapters do not reach it.  Equal inputs give equal bits.
+ *
+ * rank is a multiple of 8, at most 512, or 0 (no adapters); rows of A and B, and their matrices,
+ * start on 16-byte boundaries; X, W and Y may lie on any 2-byte boundary.  Sizes as
+ * for tg_gated, 0 <= adapters <= 2^20.  M == 0 or N == 0: nothing is enqueued.  K == 0: every
+ * row is the bias, or +0.  Y may overlap no input.  Workspace (256-byte aligned):
+ * the inner products of M x rank, and padded copies as for tg_gated.
+ * ------------------------------------------------------------------------- */
+typedef struct tg_lora_options {
+    int32_t type;          /* TG_TYPE_F16 or TG_TYPE_BF16                        */
+    int32_t reserved;      /* must be 0                                          */
+    int64_t ldx, ldw, ldy; /* elements between rows; 0 = dense, here and below   */
+    int64_t lda, stride_a; /* of A: between rows (0 = K) and matrices (0 = rank * lda)   */
+    int64_t ldb, stride_b; /* of B: between rows (0 = rank) and matrices (0 = N * ldb)   */
+} tg_lora_options;
+
+TG_API tg_status tg_lora(const void *X, const void *W, const void *A, const void *B, const float *scale,
+                         const int32_t *index, const void *bias, void *Y, int64_t M, int64_t N, int64_t K,
+                         int64_t rank, int64_t adapters, const tg_lora_options *options, void *stream,
+                         void *workspace, int64_t workspace_bytes);
+
+/* Workspace bytes tg_lora needs, or -1 for invalid arguments.  Host logic only. */
+TG_API int64_t tg_lora_workspace_size(const void *X, const void *W, int64_t M, int64_t N, int64_t K, int64_t rank,
+                                      int64_t adapters, const tg_lora_options *options);
+
 #ifdef __cplusplus
 }
 #endif

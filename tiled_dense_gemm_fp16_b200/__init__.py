@@ -18,6 +18,8 @@ from ._binding import (  # noqa: F401
     FP8_E5M2,
     GatedOptions,
     GemmOptions,
+    GroupedOptions,
+    LoraOptions,
     LIB_PATH,
     STATIC_WORKSPACE_BYTES,
     Path,
@@ -34,6 +36,14 @@ from ._binding import (  # noqa: F401
     gated_raw,
     gated_workspace_size,
     gemm_i8_raw,
+    grouped_backward_raw,
+    grouped_backward_workspace_size,
+    grouped_options,
+    grouped_raw,
+    grouped_workspace_size,
+    lora_options,
+    lora_raw,
+    lora_workspace_size,
     quantize_rows_i8_raw,
     gemm_relu,
     gemm_relu_f16_ex_raw,
@@ -68,8 +78,9 @@ from ._binding import (  # noqa: F401
     workspace_size_ex,
 )
 
-# The feed-forward operators need torch at import; they load with their first use.
+# The feed-forward operators, the grouped products and the adapters need torch at import; they load with their first use.
 _FEEDFORWARD = ("gated", "gated_backward", "gated_block", "gated_i8", "gemm_i8", "quantize_i8")
+_EXPERTS = ("grouped", "grouped_backward", "grouped_linear", "lora")
 
 
 def __getattr__(name):
@@ -77,5 +88,10 @@ def __getattr__(name):
         from . import feedforward
         for n in _FEEDFORWARD:
             globals()[n] = getattr(feedforward, n)
+        return globals()[name]
+    if name in _EXPERTS:
+        from . import experts
+        for n in _EXPERTS:
+            globals()[n] = getattr(experts, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

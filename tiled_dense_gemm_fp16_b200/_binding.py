@@ -90,6 +90,37 @@ class GatedOptions(ctypes.Structure):
     ]
 
 
+class GroupedOptions(ctypes.Structure):
+    """Mirror of tg_grouped_options (include/tg_gemm.h)."""
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("rest", ctypes.c_int32),
+        ("ldx", ctypes.c_int64),
+        ("ldw", ctypes.c_int64),
+        ("ldy", ctypes.c_int64),
+        ("stride_w", ctypes.c_int64),
+        ("lddx", ctypes.c_int64),
+        ("lddw", ctypes.c_int64),
+        ("stride_dw", ctypes.c_int64),
+        ("reserved", ctypes.c_int64),
+    ]
+
+
+class LoraOptions(ctypes.Structure):
+    """Mirror of tg_lora_options (include/tg_gemm.h)."""
+    _fields_ = [
+        ("type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("ldx", ctypes.c_int64),
+        ("ldw", ctypes.c_int64),
+        ("ldy", ctypes.c_int64),
+        ("lda", ctypes.c_int64),
+        ("stride_a", ctypes.c_int64),
+        ("ldb", ctypes.c_int64),
+        ("stride_b", ctypes.c_int64),
+    ]
+
+
 EXPORTS = (
     "tg_gemm_relu_f16_ex",
     "tg_workspace_size_ex",
@@ -123,6 +154,12 @@ EXPORTS = (
     "tg_quantize_rows_i8",
     "tg_gemm_i8",
     "tg_gated_i8",
+    "tg_grouped",
+    "tg_grouped_workspace_size",
+    "tg_grouped_backward",
+    "tg_grouped_backward_workspace_size",
+    "tg_lora",
+    "tg_lora_workspace_size",
 )
 
 _lib = None
@@ -200,6 +237,19 @@ def _bind(lib):
     lib.tg_gemm_i8.restype = i32
     lib.tg_gated_i8.argtypes = [vp] * 7 + [i64, i64, i64, gop, vp]
     lib.tg_gated_i8.restype = i32
+    grp, lop = ctypes.POINTER(GroupedOptions), ctypes.POINTER(LoraOptions)
+    lib.tg_grouped.argtypes = [vp] * 4 + [i32, i64, i64, i64, grp, vp, vp, i64]
+    lib.tg_grouped.restype = i32
+    lib.tg_grouped_workspace_size.argtypes = [vp] * 2 + [i32, i64, i64, i64, grp]
+    lib.tg_grouped_workspace_size.restype = i64
+    lib.tg_grouped_backward.argtypes = [vp] * 6 + [i32, i64, i64, i64, grp, vp, vp, i64]
+    lib.tg_grouped_backward.restype = i32
+    lib.tg_grouped_backward_workspace_size.argtypes = [vp] * 5 + [i32, i64, i64, i64, grp]
+    lib.tg_grouped_backward_workspace_size.restype = i64
+    lib.tg_lora.argtypes = [vp] * 8 + [i64] * 5 + [lop, vp, vp, i64]
+    lib.tg_lora.restype = i32
+    lib.tg_lora_workspace_size.argtypes = [vp] * 2 + [i64] * 5 + [lop]
+    lib.tg_lora_workspace_size.restype = i64
     return lib
 
 
@@ -618,3 +668,53 @@ def gemm_i8_raw(A: int, a_scale: int, W: int, w_scale: int, bias: int, C: int, M
 def gated_i8_raw(A: int, a_scale: int, Wg: int, g_scale: int, Wu: int, u_scale: int, H: int, M: int, N: int, K: int,
                  opts: GatedOptions | None = None, stream: int = 0) -> int:
     return int(lib().tg_gated_i8(A, a_scale, Wg, g_scale, Wu, u_scale, H, M, N, K, _ref(opts), stream))
+
+
+# ---------------------------------------------------------------------------
+# Products grouped by expert, and low-rank adapters
+# ---------------------------------------------------------------------------
+
+def grouped_options(type=TYPE_F16, rest=0, ldx=0, ldw=0, ldy=0, stride_w=0, lddx=0, lddw=0, stride_dw=0,
+                    reserved=0) -> GroupedOptions:
+    """A tg_grouped_options value (zeros mean fp16, dense rows, rows without a group left alone)."""
+    return GroupedOptions(int(type), int(rest), ldx, ldw, ldy, stride_w, lddx, lddw, stride_dw, reserved)
+
+
+def lora_options(type=TYPE_F16, reserved=0, ldx=0, ldw=0, ldy=0, lda=0, stride_a=0, ldb=0, stride_b=0) -> LoraOptions:
+    """A tg_lora_options value (zeros mean fp16 and dense rows)."""
+    return LoraOptions(int(type), reserved, ldx, ldw, ldy, lda, stride_a, ldb, stride_b)
+
+
+def grouped_raw(X: int, W: int, ends: int, Y: int, groups: int, M: int, N: int, K: int,
+                opts: GroupedOptions | None = None, stream: int = 0, ws: int = 0, ws_bytes: int = 0) -> int:
+    """tg_grouped on raw device pointers; returns the tg_status value."""
+    return int(lib().tg_grouped(X, W, ends, Y, groups, M, N, K, _ref(opts), stream, ws, ws_bytes))
+
+
+def grouped_workspace_size(X: int, W: int, groups: int, M: int, N: int, K: int,
+                           opts: GroupedOptions | None = None) -> int:
+    return int(lib().tg_grouped_workspace_size(X, W, groups, M, N, K, _ref(opts)))
+
+
+def grouped_backward_raw(dY: int, X: int, W: int, ends: int, dX: int, dW: int, groups: int, M: int, N: int, K: int,
+                         opts: GroupedOptions | None = None, stream: int = 0, ws: int = 0, ws_bytes: int = 0) -> int:
+    """tg_grouped_backward on raw device pointers; returns the tg_status value."""
+    return int(lib().tg_grouped_backward(dY, X, W, ends, dX, dW, groups, M, N, K, _ref(opts), stream, ws, ws_bytes))
+
+
+def grouped_backward_workspace_size(dY: int, X: int, W: int, dX: int, dW: int, groups: int, M: int, N: int, K: int,
+                                    opts: GroupedOptions | None = None) -> int:
+    return int(lib().tg_grouped_backward_workspace_size(dY, X, W, dX, dW, groups, M, N, K, _ref(opts)))
+
+
+def lora_raw(X: int, W: int, A: int, B: int, scale: int, index: int, bias: int, Y: int, M: int, N: int, K: int,
+             rank: int, adapters: int, opts: LoraOptions | None = None, stream: int = 0, ws: int = 0,
+             ws_bytes: int = 0) -> int:
+    """tg_lora on raw device pointers; returns the tg_status value."""
+    return int(lib().tg_lora(X, W, A, B, scale, index, bias, Y, M, N, K, rank, adapters, _ref(opts), stream, ws,
+                             ws_bytes))
+
+
+def lora_workspace_size(X: int, W: int, M: int, N: int, K: int, rank: int, adapters: int,
+                        opts: LoraOptions | None = None) -> int:
+    return int(lib().tg_lora_workspace_size(X, W, M, N, K, rank, adapters, _ref(opts)))

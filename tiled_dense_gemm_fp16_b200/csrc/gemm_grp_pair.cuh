@@ -1,0 +1,446 @@
+// gemm_grp_pair.cuh -- products whose rows pick their weight, on CTA pairs
+// (cta_group::2), persistent:
+//   * grouped:  Y[r] = W_g X[r] (W_g stored N x K, read K-major), or its gradient
+//     dX[r] = W_g^T dY[r] (the same weight read MN-major);
+//   * adapters: Y[r] = W X[r] + B_a T[r] + bias with T[r] = s_a A_a X[r] of the row's
+//     adapter a (made by the kernel of lora_shrink.cuh).
+//
+// A tile is 256 rows of a weight (128 a CTA) by up to 256 tokens: the even
+// CTA's MMA thread issues 256 x width instructions over both SMs' shared memory,
+// with the width of the tile at hand (a multiple of 32).  Two accumulators of
+// 256 columns, so that the epilogue of a tile hides behind the next one.  The
+// result leaves transposed: a lane of TMEM is a column of Y, so a warp stages
+// 32 x 32 boxes with a row per token.
+//
+// Adapters: each 32 tokens that share one get its product from the tensor cores,
+// as further k-blocks into their own 32 columns of the accumulator, so that no
+// adapter's values meet another request's rows, not even times zero.  Tokens of
+// several adapters within 32 (decoding requests beside each other, the ends of
+// prompts) get theirs in the epilogue, in fp32.
+#pragma once
+
+#include "grp_ops.cuh"
+
+namespace tg {
+
+struct GrpMaps {
+  CUtensorMap w;     // the weights: boxes of 64 x 128, or 64 x 64 where read MN-major
+  CUtensorMap x[4];  // tokens: boxes of 64 columns and 16, 32, 64, 128 rows
+  CUtensorMap lb;    // adapters' B: boxes of 64 x 128
+  CUtensorMap lt;    // T: boxes of 64 columns and 16 rows
+};
+
+// The adapters' part of a call.
+struct LoraParams {
+  const int* index;           // adapter of each token; outside [0, adapters): none
+  const int* kind;            // of each 32 tokens: their adapter, kLoraNone or kLoraMixed
+  const void* t;              // T: M x rank, 16-bit
+  const void* b;              // adapters' B
+  const void* bias;           // N values, or nullptr
+  int64_t ldb, stride_b;      // elements between rows and between adapters
+  int rank, adapters;         // no adapters: only W's product and the bias
+};
+enum { kLoraNone = -1, kLoraMixed = -2 };
+
+struct GrpParams {
+  void* c;
+  int64_t ldc;
+  const int* ends;            // device; nullptr: one group of all rows
+  int M, groups;
+  int out, red;               // columns of the result, length of the sums
+  int col_tiles, super;
+  int k_blocks;
+  int w_mn;                   // the weight is read MN-major (dX)
+  int rest;                   // rows behind the last group get zeros
+  int vec;                    // rows of the result start on 16-byte boundaries
+  int bf16;
+  uint32_t idesc;             // without N
+  uint64_t wait_budget_ns;
+  LoraParams lora;
+};
+
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_global_s32(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// Runs of 32-token groups of a tile that share an adapter, in order.
+struct LoraRun {
+  int first, count, adapter;
+};
+__device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraRun& run) {
+  int i = run.first + run.count;
+  int r = kLoraNone;
+  while (i < groups && (r = ld_global_s32(kind + i)) < 0) ++i;
+  if (i >= groups) return false;
+  run.first = i;
+  run.adapter = r;
+  while (++i < groups && ld_global_s32(kind + i) == r) {
+  }
+  run.count = i - run.first;
+  return true;
+}
+
+// sum_j B_a[n][j] T[m][j] in fp32, for one column and one token.
+__device__ __forceinline__ float lora_dot(const unsigned short* b, const unsigned short* t, int rank, bool bf16) {
+  float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll 2
+  for (int j = 0; j < rank; j += 8) {
+    const uint4 x = __ldg(reinterpret_cast<const uint4*>(b + j));
+    const uint4 y = ld_global_v4(t + j);
+    s = fma2(unpack_16(x.x, bf16), unpack_16(y.x, bf16), s);
+    s = fma2(unpack_16(x.y, bf16), unpack_16(y.y, bf16), s);
+    s = fma2(unpack_16(x.z, bf16), unpack_16(y.z, bf16), s);
+    s = fma2(unpack_16(x.w, bf16), unpack_16(y.w, bf16), s);
+  }
+  return s.x + s.y;
+}
+
+struct GrpPairCfg {
+  static constexpr int STAGES = 6;
+  static constexpr int BM = 128;                   // weight rows of a CTA
+  static constexpr int PAIR_M = 256;
+  static constexpr int TOKENS = 256;               // most of a tile
+  static constexpr int UNIT = 32;                  // its width is a multiple of
+  static constexpr int A_BYTES = BM * 128;
+  static constexpr int B_BYTES = TOKENS / 2 * 128;
+  static constexpr int PANEL_BYTES = 64 * 128;
+  static constexpr int MMA_WARP = 1;
+  static constexpr int EPI_WARP0 = 2;
+  static constexpr int EPI_WARPS = 8;
+  static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
+  static constexpr int TMEM_COLS = 512;
+  static constexpr int STAGING = EPI_WARPS * kGrpBoxBytes;
+  static constexpr int BAR_BYTES = 256;
+  static constexpr int FIXED_SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + STAGING + BAR_BYTES;
+  static constexpr int smem_bytes(int groups) { return FIXED_SMEM + grp_plan_bytes(groups); }
+  static_assert(FIXED_SMEM + (kGrpMaxGroups + 2) * 8 <= 232448, "dynamic shared memory per CTA");
+  static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
+  static_assert(A_BYTES % 1024 == 0 && PANEL_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && UNIT / 2 * 128 % 1024 == 0,
+                "operand tiles, and the pieces of rows they are loaded in, start on the swizzle's 1024 bytes");
+};
+
+// `rows` rows of tokens (a multiple of 16, at most 128) as the boxes of its binary digits.
+template <typename Load>
+__device__ __forceinline__ void grp_token_boxes(int rows, Load&& load) {
+  int at = 0;
+#pragma unroll
+  for (int b = 3; b >= 0; --b) {
+    const int box = 16 << b;
+    if (rows & box) {
+      load(b, at);
+      at += box;
+    }
+  }
+}
+
+template <bool LORA>
+__global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
+    grp_pair_kernel(const __grid_constant__ GrpMaps maps, const GrpParams p) {
+  using Cfg = GrpPairCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* a_smem = smem;
+  uint8_t* b_smem = smem + Cfg::STAGES * Cfg::A_BYTES;
+  uint8_t* staging = smem + Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING);
+  uint64_t* full_bar = bars;                        // used in the even CTA
+  uint64_t* empty_bar = bars + Cfg::STAGES;         // per CTA
+  uint64_t* acc_full_bar = bars + 2 * Cfg::STAGES;  // per CTA
+  uint64_t* acc_empty_bar = acc_full_bar + 2;       // used in the even CTA
+  uint64_t* mma_done_bar = acc_empty_bar + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  GrpPlan plan;
+  plan.lo = reinterpret_cast<int*>(staging + Cfg::STAGING + Cfg::BAR_BYTES);
+  plan.first = plan.lo + p.groups + 2;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster_id = blockIdx.x >> 1;
+  const int num_clusters = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < Cfg::STAGES; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full_bar[b], 1);
+      mbar_init(&acc_empty_bar[b], 2 * Cfg::EPI_WARPS);
+    }
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&maps.w);
+    tma_prefetch_desc(&maps.x[3]);
+  }
+  if (warp == Cfg::MMA_WARP) {
+    tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+    tmem_relinquish_alloc_permit_pair();
+  }
+  // Adapters: the kernel before this one on the stream makes T.  It waited for
+  // what came before it and then let this one start, so X, W, index and the
+  // workspace's copies are there already; only T and kind are waited for, by
+  // the threads that read them.
+  const bool early = LORA && p.lora.adapters > 0;
+  if (!early) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+  }
+  if (warp == Cfg::EPI_WARP0)
+    grp_make_plan(plan, p.ends, p.groups, p.M, Cfg::TOKENS, p.col_tiles, p.rest != 0, lane);
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote use
+  tcgen05_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const int num_tiles = plan.first[p.groups + 1];
+
+  if (warp == 0) {
+    // Producer (both CTAs): this CTA's half of the weight's rows and of the tokens.
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int last_parity[Cfg::STAGES];
+#pragma unroll
+      for (int s = 0; s < Cfg::STAGES; ++s) last_parity[s] = -1;
+      bool ok = true, waited = false;
+      const uint64_t pol = l2_policy_evict_normal();
+      const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
+      GrpWalk walk;
+      auto next = [&]() {
+        last_parity[stage] = static_cast<int>(phase);
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+        if (f.g == p.groups) break;  // zeros from here on
+        const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+        const int rows = width / 2;
+        const int tok = f.tok0 + static_cast<int>(rank) * rows;
+        const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
+        const uint32_t tx = 2 * (Cfg::A_BYTES + rows * 128);
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full = full_even0 + stage * 8;
+          if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
+          const int k0 = kb * 64;
+          uint8_t* adst = a_smem + stage * Cfg::A_BYTES;
+          uint8_t* bdst = b_smem + stage * Cfg::B_BYTES;
+          if (p.w_mn) {
+            tma_load_3d_pair_hint(adst, &maps.w, full, n0, k0, f.g, pol);
+            tma_load_3d_pair_hint(adst + Cfg::PANEL_BYTES, &maps.w, full, n0 + 64, k0, f.g, pol);
+          } else {
+            tma_load_3d_pair_hint(adst, &maps.w, full, k0, n0, f.g, pol);
+          }
+          grp_token_boxes(rows, [&](int b, int at) {
+            tma_load_2d_pair_hint(bdst + at * 128, &maps.x[b], full, k0, tok + at, pol);
+          });
+          next();
+        }
+        if (early && ok) {
+          if (!waited) grid_dependency_wait();
+          waited = true;
+          LoraRun run{0, 0, 0};
+          while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
+            for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
+              if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
+                ok = false;
+                break;
+              }
+              const uint32_t full = full_even0 + stage * 8;
+              if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (Cfg::A_BYTES + run.count * 2048));
+              tma_load_3d_pair_hint(a_smem + stage * Cfg::A_BYTES, &maps.lb, full, j0, n0, run.adapter, pol);
+              // 16 of each 32 tokens, where an MMA of 32 columns wants them.
+              for (int i = 0; i < run.count; ++i)
+                tma_load_2d_pair_hint(b_smem + stage * Cfg::B_BYTES + i * 2048, &maps.lt, full, j0,
+                                      f.tok0 + (run.first + i) * 32 + static_cast<int>(rank) * 16, pol);
+              next();
+            }
+          }
+        }
+      }
+      // The even CTA's full barriers count both CTAs' bytes: once they have
+      // completed, every load of the pair has landed.
+      if (leader) {
+#pragma unroll 1
+        for (int s = 0; s < Cfg::STAGES; ++s) {
+          if (last_parity[s] >= 0) {
+            volatile int no_abort = 0;
+            mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.wait_budget_ns, 0xa2);
+          }
+        }
+      }
+    }
+  } else if (warp == Cfg::MMA_WARP) {
+    // MMA issuer (even CTA only).
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int local = 0;
+      bool ok = true, waited = false;
+      // Descriptors of stage 0 and their steps in units of 16 bytes.
+      const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), p.w_mn ? Cfg::PANEL_BYTES : 16, 1024);
+      const uint64_t lb_desc0 = make_sw128_desc(smem_u32(a_smem), 16, 1024);
+      const uint64_t b_desc0 = make_sw128_desc(smem_u32(b_smem), 16, 1024);
+      const uint32_t a_step = p.w_mn ? 2048 / 16 : 32 / 16;
+      GrpWalk walk;
+      auto next = [&]() {
+        umma_commit_pair_mc(&empty_bar[stage], 0x3);  // both CTAs may refill this stage
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      };
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++local) {
+        const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+        if (f.g == p.groups) break;
+        const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+        const uint32_t idesc = p.idesc | static_cast<uint32_t>(width >> 3) << 17;
+        const int acc = local & 1;
+        if (!mbar_wait(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xa3)) break;
+        tcgen05_fence_after_sync();
+        const uint32_t d_tmem = tmem_base + acc * Cfg::TOKENS;
+        for (int kb = 0; kb < p.k_blocks; ++kb) {
+          if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
+            ok = false;
+            break;
+          }
+          tcgen05_fence_after_sync();
+          const uint64_t a_desc = a_desc0 + stage * (Cfg::A_BYTES / 16), b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f16_ss_pair(d_tmem, a_desc + k * a_step, b_desc + k * 2, idesc, (kb | k) != 0 ? 1u : 0u);
+          next();
+        }
+        if (early && ok) {
+          if (!waited) grid_dependency_wait();
+          waited = true;
+          const uint32_t idesc32 = p.idesc | (32u >> 3) << 17;
+          LoraRun run{0, 0, 0};
+          while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
+            for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
+              if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
+                ok = false;
+                break;
+              }
+              tcgen05_fence_after_sync();
+              const int steps = (min(p.lora.rank - j0, 64) + 15) / 16;
+              const uint64_t a_desc = lb_desc0 + stage * (Cfg::A_BYTES / 16);
+              for (int i = 0; i < run.count; ++i) {
+                const uint64_t b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16) + i * (2048 / 16);
+                for (int k = 0; k < steps; ++k)
+                  umma_f16_ss_pair(d_tmem + (run.first + i) * 32, a_desc + k * 2, b_desc + k * 2, idesc32, 1u);
+              }
+              next();
+            }
+          }
+        }
+        if (!ok) break;
+        umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
+      }
+      umma_commit_pair_mc(mma_done_bar, 0x1);
+      volatile int no_abort = 0;
+      mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0xa5);
+    }
+    __syncwarp();
+  } else {
+    // Epilogue (both CTAs): warp w takes TMEM lanes 32 (w mod 4) .. + 31, which
+    // are columns of the result, and every other 32 tokens.
+    if (early) {
+      grid_dependency_wait();
+      grid_launch_dependents();
+    }
+    const int quad = warp & 3;
+    const int part = (warp - Cfg::EPI_WARP0) >> 2;
+    uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
+    const bool bf16 = p.bf16 != 0;
+    GrpWalk walk;
+    int local = 0;
+    for (int t = cluster_id; t < num_tiles; t += num_clusters) {
+      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+      const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM + quad * 32;
+      const bool zero = f.g == p.groups;
+      const int acc = local & 1;
+      if (!zero) {
+        const bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.wait_budget_ns, 0xa6);
+        if (!__all_sync(0xffffffffu, ready)) break;
+        tcgen05_fence_after_sync();
+      }
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::TOKENS;
+      const int boxes = (f.cnt + 31) / 32;
+      for (int b = part; b < boxes && n0 < p.out; b += Cfg::EPI_WARPS / 4) {
+        uint32_t r[32];
+        if (!zero) {
+          tmem_ld_32x32b_x32(taddr + b * 32, r);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) r[e] = 0u;
+        }
+        const int rows = min(32, f.cnt - b * 32);
+        if (LORA) {
+          const int n = n0 + lane;
+          if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
+            const int m0 = f.tok0 + b * 32;
+            const int mine = lane < rows ? __ldg(p.lora.index + m0 + lane) : -1;
+            const unsigned short* brow = static_cast<const unsigned short*>(p.lora.b) + n * p.lora.ldb;
+            const unsigned short* trow = static_cast<const unsigned short*>(p.lora.t) + static_cast<int64_t>(m0) * p.lora.rank;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const int a = __shfl_sync(0xffffffffu, mine, e);
+              if (a >= 0 && a < p.lora.adapters && n < p.out)
+                r[e] = __float_as_uint(__uint_as_float(r[e]) +
+                                       lora_dot(brow + a * p.lora.stride_b, trow + e * p.lora.rank, p.lora.rank, bf16));
+            }
+          }
+          if (p.lora.bias != nullptr && n < p.out) {
+            const float bias = load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + bias);
+          }
+        }
+        __syncwarp();  // the box before has left
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
+              round_16(__uint_as_float(r[e]), bf16);
+        __syncwarp();
+        grp_store_box(static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32) * p.ldc + n0, p.ldc, rows,
+                      min(32, p.out - n0), p.vec != 0, box, lane);
+      }
+      if (!zero) {
+        tcgen05_fence_before_sync();
+        __syncwarp();
+        // Relaxed, as in the feed-forward pair kernel: it orders only TMEM reads.
+        if (lane == 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_empty_bar[acc]), 0));
+        ++local;
+      }
+    }
+  }
+
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // the pair is done with each other's shared memory and barriers
+  if (warp == Cfg::MMA_WARP) {
+    tcgen05_fence_after_sync();
+    tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+  }
+}
+
+}  // namespace tg

@@ -1,0 +1,643 @@
+// grp_host.cuh -- argument checks, kernel choice and launches of the grouped
+// products, their gradients and the low-rank adapters.  Included by tg_gemm.cu
+// after ff_host.cuh, whose helpers it uses.
+#pragma once
+
+#include "gemm_grp_narrow.cuh"
+#include "gemm_grp_pair.cuh"
+#include "gemm_grp_wgrad.cuh"
+#include "lora_shrink.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int64_t kLoraMaxRank = 512;
+constexpr int64_t kLoraMaxAdapters = int64_t(1) << 20;
+
+// `mats` matrices of 16-bit values, `stride` elements apart.
+struct GrpStack {
+  FfMat m;  // the first
+  int64_t mats, stride;
+
+  bool empty() const { return mats == 0 || m.empty(); }
+  // First to last byte, of a valid stack.
+  FfMat span() const {
+    if (empty()) return FfMat{m.p, 0, 0, 1, 2};
+    const int64_t n = (mats - 1) * stride + (m.rows - 1) * m.ld + m.cols;
+    return FfMat{m.p, 1, n, n, 2};
+  }
+  bool valid(bool written) const {
+    if (empty()) return true;
+    if (!m.valid() || m.rows > kFfMaxSpan / m.ld) return false;
+    if (mats == 1) return true;
+    const int64_t least = written ? (m.rows - 1) * m.ld + m.cols : m.cols;
+    return stride >= least && stride <= kFfMaxStride && mats <= kFfMaxSpan / stride;
+  }
+  bool on16() const { return m.rows_on(16) && (mats == 1 || (stride * 2) % 16 == 0); }
+  bool even_rows() const { return mats <= 1 || stride == m.rows * m.ld; }
+  // All rows as one matrix, for a stack of evenly spaced rows.
+  FfMat rows() const { return FfMat{m.p, mats * m.rows, m.cols, m.ld, 2}; }
+};
+
+GrpStack grp_stack(const void* p, int64_t mats, int64_t rows, int64_t cols, int64_t ld, int64_t stride) {
+  GrpStack s;
+  s.m = FfMat{p, rows, cols, ld ? ld : cols, 2};
+  s.mats = mats;
+  s.stride = stride;
+  if (stride == 0) s.stride = rows <= kFfMaxSize && s.m.ld <= kFfMaxSpan / (rows + 1) ? rows * s.m.ld : 0;
+  return s;
+}
+
+// Bytes of the padded copy of a stack that TMA cannot describe, 0 where it can, -1 where it cannot be copied.
+int64_t grp_copy_bytes(const GrpStack& s) {
+  if (s.empty() || s.on16()) return 0;
+  if (!s.even_rows() || s.mats * s.m.rows > INT_MAX) return -1;
+  return up256(2 * s.mats * s.m.rows * round_up(s.m.cols, 8));
+}
+
+// The copies of x and w (either may be null) that a product needs, in one launch; advances `ws`.
+tg_status grp_make_copies(FfMat* x, FfMat* y, GrpStack* w, uint8_t*& ws, cudaStream_t stream, DeviceInfo* info) {
+  FfMat rows{nullptr, 0, 0, 1, 2};
+  FfMat* mats[3];
+  int n = 0;
+  if (x) mats[n++] = x;
+  if (y) mats[n++] = y;
+  const bool copy_w = w && !w->empty() && !w->on16();
+  if (copy_w) {
+    rows = w->rows();
+    mats[n++] = &rows;
+  }
+  const tg_status st = ff_make_copies(mats, n, ws, stream, info);
+  if (copy_w) {
+    w->m.p = rows.p;
+    w->m.ld = rows.ld;
+    w->stride = w->m.rows * rows.ld;
+  }
+  return st;
+}
+
+bool grp_encode3(CUtensorMap* map, const GrpStack& s, int box_cols, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const int64_t stride = s.mats == 1 ? round_up(s.m.rows * s.m.ld, 8) : s.stride;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(s.m.cols), static_cast<cuuint64_t>(s.m.rows),
+                        static_cast<cuuint64_t>(s.mats)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(s.m.ld) * 2, static_cast<cuuint64_t>(stride) * 2};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estride[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(s.m.p), dims, strides, box, estride,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// One product whose rows pick their weight: c[r] = w_g a[r], or w_g^T a[r].
+struct GrpProduct {
+  FfMat a, c;
+  GrpStack w;
+  const int32_t* ends = nullptr;  // nullptr: one group of all rows
+  int groups = 1;
+  int64_t out = 0, red = 0;
+  bool transposed = false, rest = false, bf16 = false;
+  bool lora = false;
+  LoraParams l;
+  GrpStack lb;  // with adapters
+  FfMat t;
+};
+
+bool grp_fill(const GrpProduct& f, GrpMaps& maps, GrpParams& p, int weight_rows) {
+  std::memset(&maps, 0, sizeof maps);
+  std::memset(&p, 0, sizeof p);
+  if (!grp_encode3(&maps.w, f.w, 64, f.transposed ? 64 : 128)) return false;
+  for (int i = 0; i < 4; ++i)
+    if (!ff_encode(&maps.x[i], f.a, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
+  if (f.lora) {
+    p.lora = f.l;
+    if (f.l.adapters > 0 && (!grp_encode3(&maps.lb, f.lb, 64, 128) ||
+                             !ff_encode(&maps.lt, f.t, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return false;
+  }
+  p.c = const_cast<void*>(f.c.p);
+  p.ldc = f.c.ld;
+  p.ends = f.ends;
+  p.M = static_cast<int>(f.a.rows);
+  p.groups = f.groups;
+  p.out = static_cast<int>(f.out);
+  p.red = static_cast<int>(f.red);
+  p.col_tiles = static_cast<int>((f.out + weight_rows - 1) / weight_rows);
+  p.k_blocks = static_cast<int>((f.red + 63) / 64);
+  p.w_mn = f.transposed ? 1 : 0;
+  p.rest = f.rest ? 1 : 0;
+  p.bf16 = f.bf16 ? 1 : 0;
+  p.wait_budget_ns = wait_budget(p.k_blocks);
+  return true;
+}
+
+// Whether the walk's numbers of tiles, and its groups of `super` tiles, stay in 32 bits.
+bool grp_countable(const GrpParams& p, int64_t most) {
+  const int64_t tiles = (static_cast<int64_t>(p.M) + most - 1) / most + p.groups + 1;
+  return tiles * p.col_tiles <= INT_MAX - 65536 && static_cast<int64_t>(p.super) * p.col_tiles <= INT_MAX;
+}
+
+tg_status launch_grp_pair(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
+  using Cfg = GrpPairCfg;
+  auto kernel = f.lora ? grp_pair_kernel<true> : grp_pair_kernel<false>;
+  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, f.lora ? 2u : 1u, Cfg::smem_bytes(kGrpMaxGroups)))
+    return TG_ERR_LAUNCH;
+  GrpMaps maps;
+  GrpParams p;
+  if (!grp_fill(f, maps, p, Cfg::PAIR_M)) return TG_ERR_LAUNCH;
+  p.vec = f.c.rows_on(16) ? 1 : 0;
+  p.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PAIR_M, 0, f.transposed, false);
+  p.super = tune_int("TG_TUNE_GRP_SUPER", 8);
+  if (!grp_countable(p, Cfg::TOKENS)) return TG_ERR_INVALID_ARG;
+  const int64_t most = ((f.a.rows + Cfg::TOKENS - 1) / Cfg::TOKENS + f.groups) * p.col_tiles;
+  const int64_t pairs = info->sm_count / 2, clusters = most < pairs ? most : pairs;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(f.groups));
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 2);
+  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
+// Clusters of `splits` CTAs, one an SM, that fit on the device (see ff_resident_clusters).
+int grp_resident_clusters(int splits, DeviceInfo* info) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  short& known = info->grp_clusters[splits];
+  if (known == 0) {
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof cfg);
+    cfg.gridDim = dim3(static_cast<unsigned>(splits) * 1024, 1, 1);
+    cfg.blockDim = dim3(GrpNarrowCfg::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(GrpNarrowCfg::smem_bytes(128, GrpNarrowCfg::stages(128, 1), 1));
+    LaunchAttrs la;
+    la.fill(cfg, static_cast<unsigned>(splits));
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, grp_narrow_kernel<false>, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = info->sm_count / splits > 0 ? info->sm_count / splits : 1;
+    }
+    known = static_cast<short>(n > 32767 ? 32767 : n);
+  }
+  return known;
+}
+
+tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream, DeviceInfo* info) {
+  using Cfg = GrpNarrowCfg;
+  auto kernel = f.lora ? grp_narrow_kernel<true> : grp_narrow_kernel<false>;
+  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, f.lora ? 8u : 4u, 232448)) return TG_ERR_LAUNCH;
+  if (f.lora && !ff_set_smem(reinterpret_cast<const void*>(grp_narrow_kernel<false>), info->grp_attr, 4u, 232448))
+    return TG_ERR_LAUNCH;  // the one that grp_resident_clusters asks about
+  GrpMaps maps;
+  GrpNarrowParams p;
+  std::memset(&p, 0, sizeof p);
+  if (!grp_fill(f, maps, p.g, Cfg::PANEL)) return TG_ERR_LAUNCH;
+  p.g.vec = f.c.rows_on(8) ? 1 : 0;
+  p.g.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PANEL, 0, f.transposed, false);
+  p.g.super = 8;
+  if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
+  p.tokens = tokens;
+  p.stages = Cfg::stages(tokens, f.groups);
+  uint32_t cols = 32;
+  while (cols < static_cast<uint32_t>(2 * tokens)) cols <<= 1;
+  p.tmem_cols = cols;
+  int splits = tune_int("TG_TUNE_GRP_SPLITS", 4);
+  if (splits > p.g.k_blocks) splits = p.g.k_blocks;
+  p.splits = splits;
+  const int64_t most = ((f.a.rows + tokens - 1) / tokens + f.groups) * p.g.col_tiles;
+  const int64_t fit = grp_resident_clusters(splits, info), clusters = most < fit ? most : fit;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(splits * clusters), 1, 1);
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(tokens, p.stages, f.groups));
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, static_cast<unsigned>(splits));
+  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
+// Few rows a group take the narrow kernel, and so do products whose tiles would
+// leave half the pairs without one.
+tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
+  const int64_t rows = f.a.rows, live = rows < f.groups ? rows : f.groups;  // groups that can have rows
+  const int64_t each = (rows + live - 1) / live;
+  const int64_t tiles = ((rows + 255) / 256 > live ? (rows + 255) / 256 : live) * ((f.out + 255) / 256);
+  const bool narrow = tune_int("TG_TUNE_GRP_NARROW", each <= 64 || 4 * tiles <= info->sm_count ? 1 : 0) != 0;
+  if (!narrow) return launch_grp_pair(f, stream, info);
+  // Twice the even share, so that a group with more is one tile as a rule.
+  int tokens = 16;
+  while (tokens < 128 && tokens < (live > 1 ? 2 * each : each)) tokens <<= 1;
+  return launch_grp_narrow(f, tokens, stream, info);
+}
+
+// A result that is a sum over nothing: +0 in the rows of the groups, or in all with `rest`.
+struct GrpZeroParams {
+  unsigned short* c;
+  int64_t ldc;
+  const int* ends;
+  int groups, M, cols, rest;
+};
+
+__global__ void __launch_bounds__(256) grp_zero_kernel(const GrpZeroParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int rows = p.rest ? p.M : grp_end(p.ends, p.groups - 1, p.M);
+  const int64_t items = static_cast<int64_t>(rows) * p.cols;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < items;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+    const int64_t m = i / p.cols;
+    p.c[m * p.ldc + (i - m * p.cols)] = 0;
+  }
+}
+
+tg_status grp_zero(const FfMat& c, const int32_t* ends, int groups, bool rest, cudaStream_t stream, DeviceInfo* info) {
+  if (c.empty() || (groups == 0 && !rest)) return TG_OK;
+  if (rest) return ff_zero(c, stream);
+  const GrpZeroParams p{static_cast<unsigned short*>(const_cast<void*>(c.p)), c.ld, ends, groups,
+                        static_cast<int>(c.rows), static_cast<int>(c.cols), rest ? 1 : 0};
+  return launch_simple(grp_zero_kernel, p, c.rows * c.cols, 1, stream, info);
+}
+
+// ---------------------------------------------------------------------------
+// Grouped products
+// ---------------------------------------------------------------------------
+struct GroupedArgs {
+  FfMat x, y, dx;  // y is dY in the backward pass
+  GrpStack w, dw;
+  int groups;
+  int64_t M, N, K;
+  bool bf16, rest;
+};
+
+bool grouped_args(GroupedArgs& a, const void* X, const void* W, const void* Y, const void* dX, const void* dW, int32_t G,
+                  int64_t M, int64_t N, int64_t K, const tg_grouped_options* opt) {
+  tg_grouped_options o;
+  std::memset(&o, 0, sizeof o);
+  if (opt) o = *opt;
+  if (o.reserved != 0 || !ff_type_valid(o.type) || (o.rest != 0 && o.rest != 1) || !ff_sizes_valid(M, N, K) || G < 0 ||
+      G > kGrpMaxGroups || G * N > kFfMaxSpan / (K > 0 ? K : 1))
+    return false;
+  if (o.ldx < 0 || o.ldw < 0 || o.ldy < 0 || o.stride_w < 0 || o.lddx < 0 || o.lddw < 0 || o.stride_dw < 0) return false;
+  a.x = mat16(X, M, K, o.ldx);
+  a.y = mat16(Y, M, N, o.ldy);
+  a.dx = mat16(dX, M, K, o.lddx);
+  a.w = grp_stack(W, G, N, K, o.ldw, o.stride_w);
+  a.dw = grp_stack(dW, G, N, K, o.lddw, o.stride_dw);
+  a.groups = G;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.bf16 = o.type == TG_TYPE_BF16;
+  a.rest = o.rest != 0;
+  return true;
+}
+
+int64_t grouped_workspace(const GroupedArgs& a) {
+  if (a.M == 0 || a.N == 0 || a.K == 0 || a.groups == 0) return 0;
+  const int64_t w = grp_copy_bytes(a.w);
+  return w < 0 ? -1 : ff_copy_bytes(a.x) + w;
+}
+
+tg_status run_grouped(GroupedArgs& a, const int32_t* ends, void* stream_ptr, void* ws_ptr, int64_t ws_bytes) {
+  if (a.M == 0 || a.N == 0) return TG_OK;
+  const FfMat e = vec32(ends, a.groups);
+  const int64_t need = grouped_workspace(a);
+  if (!a.x.valid() || !a.w.valid(false) || !a.y.valid() || !e.valid() || need < 0) return TG_ERR_INVALID_ARG;
+  const FfMat in[4] = {a.x, a.w.span(), e, a.y};
+  if (!ff_disjoint(in, 3, &a.y, 1) || !ff_workspace_valid(ws_ptr, ws_bytes, need, in, 4)) return TG_ERR_INVALID_ARG;
+  int dev = 0;
+  DeviceInfo* info = nullptr;
+  tg_status st = current_device(dev, info);
+  if (st != TG_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (a.K == 0 || a.groups == 0) return grp_zero(a.y, ends, a.groups, a.rest, stream, info);
+  uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
+  if ((st = grp_make_copies(&a.x, nullptr, &a.w, ws, stream, info)) != TG_OK) return st;
+  GrpProduct f;
+  f.a = a.x;
+  f.c = a.y;
+  f.w = a.w;
+  f.ends = ends;
+  f.groups = a.groups;
+  f.out = a.N;
+  f.red = a.K;
+  f.rest = a.rest;
+  f.bf16 = a.bf16;
+  return launch_grp(f, stream, info);
+}
+
+int64_t grouped_grad_workspace(const GroupedArgs& a) {
+  if (a.M == 0 || a.N == 0 || a.K == 0 || a.groups == 0) return 0;
+  int64_t need = ff_copy_bytes(a.y);
+  if (a.dx.p) {
+    const int64_t w = grp_copy_bytes(a.w);
+    if (w < 0) return -1;
+    need += w;
+  }
+  return a.dw.m.p ? need + ff_copy_bytes(a.x) : need;
+}
+
+tg_status launch_grp_wgrad(const GroupedArgs& a, const int32_t* ends, cudaStream_t stream, DeviceInfo* info) {
+  using Cfg = GrpWgradCfg;
+  if (!ff_set_smem(reinterpret_cast<const void*>(grp_wgrad_kernel), info->grp_attr, 16u, Cfg::smem_bytes(kGrpMaxGroups)))
+    return TG_ERR_LAUNCH;
+  GrpWgradMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  if (!ff_encode(&maps.d, a.y, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !ff_encode(&maps.x, a.x, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B))
+    return TG_ERR_LAUNCH;
+  GrpWgradParams p;
+  std::memset(&p, 0, sizeof p);
+  p.c = const_cast<void*>(a.dw.m.p);
+  p.ldc = a.dw.m.ld;
+  p.stride_c = a.dw.stride;
+  p.ends = ends;
+  p.M = static_cast<int>(a.M);
+  p.groups = a.groups;
+  p.N = static_cast<int>(a.N);
+  p.K = static_cast<int>(a.K);
+  p.n_tiles = (p.N + Cfg::TILE - 1) / Cfg::TILE;
+  p.k_tiles = (p.K + Cfg::TILE - 1) / Cfg::TILE;
+  const int64_t tiles = static_cast<int64_t>(p.n_tiles) * p.k_tiles * a.groups;
+  if (tiles > INT_MAX - 65536) return TG_ERR_INVALID_ARG;
+  p.num_tiles = static_cast<int>(tiles);
+  p.vec = a.dw.on16() ? 1 : 0;
+  p.bf16 = a.bf16 ? 1 : 0;
+  p.idesc = make_idesc_ff(kFfF16, a.bf16, Cfg::TILE, Cfg::TILE, true, true);
+  p.wait_budget_ns = wait_budget((a.M + 63) / 64);
+  const int64_t pairs = info->sm_count / 2, clusters = tiles < pairs ? tiles : pairs;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(a.groups));
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 2);
+  if (cudaLaunchKernelEx(&cfg, grp_wgrad_kernel, maps, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
+// Every row of a stack's matrices set to +0.
+tg_status grp_zero_stack(const GrpStack& s, cudaStream_t stream) {
+  if (s.empty()) return TG_OK;
+  if (s.even_rows()) return ff_zero(s.rows(), stream);
+  for (int64_t g = 0; g < s.mats; ++g) {
+    FfMat m = s.m;
+    m.p = static_cast<const uint8_t*>(m.p) + 2 * g * s.stride;
+    const tg_status st = ff_zero(m, stream);
+    if (st != TG_OK) return st;
+  }
+  return TG_OK;
+}
+
+tg_status run_grouped_grad(GroupedArgs& a, const int32_t* ends, void* stream_ptr, void* ws_ptr, int64_t ws_bytes) {
+  const bool want_x = a.dx.p != nullptr && !a.dx.empty(), want_w = a.dw.m.p != nullptr && !a.dw.empty();
+  if (!want_x && !want_w) return TG_OK;
+  const FfMat e = vec32(ends, a.groups);
+  const int64_t need = grouped_grad_workspace(a);
+  if (!a.x.valid() || !a.w.valid(false) || !a.y.valid() || !e.valid() || need < 0) return TG_ERR_INVALID_ARG;
+  FfMat all[6] = {a.x, a.w.span(), e, a.y};
+  int n = 4;
+  if (want_x) {
+    if (!a.dx.valid()) return TG_ERR_INVALID_ARG;
+    all[n++] = a.dx;
+  }
+  if (want_w) {
+    if (!a.dw.valid(true)) return TG_ERR_INVALID_ARG;
+    all[n++] = a.dw.span();
+  }
+  if (!ff_disjoint(all, 4, all + 4, n - 4) || !ff_workspace_valid(ws_ptr, ws_bytes, need, all, n)) return TG_ERR_INVALID_ARG;
+  int dev = 0;
+  DeviceInfo* info = nullptr;
+  tg_status st = current_device(dev, info);
+  if (st != TG_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (a.M == 0 || a.N == 0 || a.groups == 0) {  // sums over nothing
+    if (want_w && (st = grp_zero_stack(a.dw, stream)) != TG_OK) return st;
+    return want_x ? grp_zero(a.dx, ends, a.groups, a.rest, stream, info) : TG_OK;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
+  if ((st = grp_make_copies(&a.y, want_w ? &a.x : nullptr, want_x ? &a.w : nullptr, ws, stream, info)) != TG_OK) return st;
+  if (want_w && (st = launch_grp_wgrad(a, ends, stream, info)) != TG_OK) return st;
+  if (!want_x) return TG_OK;
+  GrpProduct f;
+  f.a = a.y;
+  f.c = a.dx;
+  f.w = a.w;
+  f.ends = ends;
+  f.groups = a.groups;
+  f.out = a.K;
+  f.red = a.N;
+  f.transposed = true;
+  f.rest = a.rest;
+  f.bf16 = a.bf16;
+  return launch_grp(f, stream, info);
+}
+
+// ---------------------------------------------------------------------------
+// Adapters
+// ---------------------------------------------------------------------------
+struct LoraArgs {
+  FfMat x, w, y;
+  GrpStack a, b;
+  int64_t M, N, K, rank, adapters;
+  bool bf16;
+};
+
+bool lora_args(LoraArgs& l, const void* X, const void* W, const void* A, const void* B, const void* Y, int64_t M, int64_t N,
+               int64_t K, int64_t rank, int64_t adapters, const tg_lora_options* opt) {
+  tg_lora_options o;
+  std::memset(&o, 0, sizeof o);
+  if (opt) o = *opt;
+  if (o.reserved != 0 || !ff_type_valid(o.type) || !ff_sizes_valid(M, N, K) || rank < 0 || rank > kLoraMaxRank ||
+      rank % 8 != 0 || adapters < 0 || adapters > kLoraMaxAdapters)
+    return false;
+  if (o.ldx < 0 || o.ldw < 0 || o.ldy < 0 || o.lda < 0 || o.stride_a < 0 || o.ldb < 0 || o.stride_b < 0) return false;
+  if (rank == 0) adapters = 0;
+  l.x = mat16(X, M, K, o.ldx);
+  l.w = mat16(W, N, K, o.ldw);
+  l.y = mat16(Y, M, N, o.ldy);
+  l.a = grp_stack(A, adapters, rank, K, o.lda, o.stride_a);
+  l.b = grp_stack(B, adapters, N, rank, o.ldb, o.stride_b);
+  l.M = M;
+  l.N = N;
+  l.K = K;
+  l.rank = rank;
+  l.adapters = adapters;
+  l.bf16 = o.type == TG_TYPE_BF16;
+  return true;
+}
+
+int64_t lora_inner_bytes(const LoraArgs& l) { return l.adapters == 0 ? 0 : up256(2 * l.M * l.rank); }
+
+int64_t lora_workspace(const LoraArgs& l) {
+  if (l.M == 0 || l.N == 0 || l.K == 0) return 0;
+  const int64_t inner = l.adapters == 0 ? 0 : lora_inner_bytes(l) + up256((l.M + 31) / 32 * 4);
+  return inner + ff_copy_bytes(l.x) + ff_copy_bytes(l.w);
+}
+
+template <int NT>
+tg_status launch_lora_shrink(const LoraShrinkParams& p, int y, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>((p.M + 31) / 32), static_cast<unsigned>(y),
+                     static_cast<unsigned>((p.rank + NT * 8 - 1) / (NT * 8)));
+  cfg.blockDim = dim3(kShrinkWarps * 32, 1, 1);
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 1);
+  auto kernel = p.bf16 ? lora_shrink_kernel<NT, true> : lora_shrink_kernel<NT, false>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
+tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const void* bias, void* stream_ptr, void* ws_ptr,
+                   int64_t ws_bytes) {
+  if (l.M == 0 || l.N == 0) return TG_OK;
+  const bool adapted = l.adapters > 0 && l.K > 0;
+  const int64_t need = lora_workspace(l);
+  const FfMat s = vec32(scale, scale ? l.adapters : 0), i = vec32(index, adapted ? l.M : 0);
+  const FfMat bv = mat16(bias, bias ? 1 : 0, l.N, l.N);
+  if (!l.x.valid() || !l.w.valid() || !l.y.valid() || !s.valid() || !i.valid() || !bv.valid()) return TG_ERR_INVALID_ARG;
+  if (adapted && (!l.a.valid(false) || !l.b.valid(false) || !l.a.on16() || !l.b.on16())) return TG_ERR_INVALID_ARG;
+  FfMat all[8] = {l.x, l.w, s, i, bv, l.y, l.a.span(), l.b.span()};
+  if (!adapted) all[6] = all[7] = FfMat{nullptr, 0, 0, 1, 2};
+  for (int q = 0; q < 8; ++q)
+    if (q != 5 && l.y.overlaps(all[q])) return TG_ERR_INVALID_ARG;
+  if (!ff_workspace_valid(ws_ptr, ws_bytes, need, all, 8)) return TG_ERR_INVALID_ARG;
+  int dev = 0;
+  DeviceInfo* info = nullptr;
+  tg_status st = current_device(dev, info);
+  if (st != TG_OK) return st;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
+  if (l.K == 0) {
+    const BiasFillParams b{const_cast<void*>(l.y.p), bias, l.y.ld, static_cast<int>(l.M), static_cast<int>(l.N), 0, l.bf16 ? 1 : 0};
+    return launch_simple(bias_fill_kernel, b, l.M * l.N, 1, stream, info);
+  }
+  uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
+  GrpProduct f;
+  std::memset(&f.l, 0, sizeof f.l);
+  f.lora = true;
+  f.l.bias = bias;
+  if (adapted) {
+    f.l.index = index;
+    f.l.t = ws;
+    f.l.kind = reinterpret_cast<const int*>(ws + lora_inner_bytes(l));
+    f.l.b = l.b.m.p;
+    f.l.ldb = l.b.m.ld;
+    f.l.stride_b = l.b.stride;
+    f.l.rank = static_cast<int>(l.rank);
+    f.l.adapters = static_cast<int>(l.adapters);
+    f.lb = l.b;
+    f.t = FfMat{ws, l.M, l.rank, l.rank, 2};
+    ws += lora_inner_bytes(l) + up256((l.M + 31) / 32 * 4);
+  }
+  FfMat* const operands[2] = {&l.x, &l.w};
+  if ((st = ff_make_copies(operands, 2, ws, stream, info)) != TG_OK) return st;
+  if (adapted) {
+    LoraShrinkParams p;
+    std::memset(&p, 0, sizeof p);
+    p.x = l.x.p;
+    p.a = l.a.m.p;
+    p.index = index;
+    p.scale = scale;
+    p.t = const_cast<void*>(f.l.t);
+    p.kind = const_cast<int*>(f.l.kind);
+    p.ldx = l.x.ld;
+    p.lda = l.a.m.ld;
+    p.stride_a = l.a.stride;
+    p.M = static_cast<int>(l.M);
+    p.K = static_cast<int>(l.K);
+    p.rank = static_cast<int>(l.rank);
+    p.adapters = static_cast<int>(l.adapters);
+    p.bf16 = l.bf16 ? 1 : 0;
+    // Blocks for the adapters of 32 tokens: as many as there may be, while they find SMs.
+    const int64_t blocks = (l.M + 31) / 32;
+    int y = static_cast<int>(l.M < 32 ? l.M : 32);
+    while (y > 1 && blocks * y > 4 * info->sm_count) y = (y + 1) / 2;
+    st = l.rank <= 8    ? launch_lora_shrink<1>(p, y, stream)
+         : l.rank <= 16 ? launch_lora_shrink<2>(p, y, stream)
+         : l.rank <= 32 ? launch_lora_shrink<4>(p, y, stream)
+                        : launch_lora_shrink<8>(p, y, stream);
+    if (st != TG_OK) return st;
+  }
+  f.a = l.x;
+  f.c = l.y;
+  f.w = GrpStack{l.w, 1, 0};
+  f.out = l.N;
+  f.red = l.K;
+  f.bf16 = l.bf16;
+  return launch_grp(f, stream, info);
+}
+
+}  // namespace
+}  // namespace tg
+
+extern "C" {
+
+tg_status tg_grouped(const void* X, const void* W, const int32_t* ends, void* Y, int32_t groups, int64_t M, int64_t N,
+                     int64_t K, const tg_grouped_options* options, void* stream, void* workspace,
+                     int64_t workspace_bytes) {
+  tg::GroupedArgs a;
+  if (!tg::grouped_args(a, X, W, Y, nullptr, nullptr, groups, M, N, K, options)) return TG_ERR_INVALID_ARG;
+  return tg::run_grouped(a, ends, stream, workspace, workspace_bytes);
+}
+
+int64_t tg_grouped_workspace_size(const void* X, const void* W, int32_t groups, int64_t M, int64_t N, int64_t K,
+                                  const tg_grouped_options* options) {
+  tg::GroupedArgs a;
+  if (!tg::grouped_args(a, X, W, nullptr, nullptr, nullptr, groups, M, N, K, options)) return -1;
+  return tg::grouped_workspace(a);
+}
+
+tg_status tg_grouped_backward(const void* dY, const void* X, const void* W, const int32_t* ends, void* dX, void* dW,
+                              int32_t groups, int64_t M, int64_t N, int64_t K, const tg_grouped_options* options,
+                              void* stream, void* workspace, int64_t workspace_bytes) {
+  tg::GroupedArgs a;
+  if (!tg::grouped_args(a, X, W, dY, dX, dW, groups, M, N, K, options)) return TG_ERR_INVALID_ARG;
+  return tg::run_grouped_grad(a, ends, stream, workspace, workspace_bytes);
+}
+
+int64_t tg_grouped_backward_workspace_size(const void* dY, const void* X, const void* W, const void* dX, const void* dW,
+                                           int32_t groups, int64_t M, int64_t N, int64_t K,
+                                           const tg_grouped_options* options) {
+  tg::GroupedArgs a;
+  if (!tg::grouped_args(a, X, W, dY, dX, dW, groups, M, N, K, options)) return -1;
+  return tg::grouped_grad_workspace(a);
+}
+
+tg_status tg_lora(const void* X, const void* W, const void* A, const void* B, const float* scale, const int32_t* index,
+                  const void* bias, void* Y, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
+                  const tg_lora_options* options, void* stream, void* workspace, int64_t workspace_bytes) {
+  tg::LoraArgs l;
+  if (!tg::lora_args(l, X, W, A, B, Y, M, N, K, rank, adapters, options)) return TG_ERR_INVALID_ARG;
+  return tg::run_lora(l, scale, index, bias, stream, workspace, workspace_bytes);
+}
+
+int64_t tg_lora_workspace_size(const void* X, const void* W, int64_t M, int64_t N, int64_t K, int64_t rank, int64_t adapters,
+                               const tg_lora_options* options) {
+  tg::LoraArgs l;
+  if (!tg::lora_args(l, X, W, nullptr, nullptr, nullptr, M, N, K, rank, adapters, options)) return -1;
+  return tg::lora_workspace(l);
+}
+
+}  // extern "C"

@@ -53,6 +53,8 @@ struct DeviceInfo {
   bool w4_decode_attr = false;
   unsigned ff_attr = 0;       // one bit per feed-forward kernel instance with its attribute set
   short ff_clusters[9] = {};  // clusters of 1 .. 8 CTAs, one per SM, that fit on the device (0: not asked yet)
+  unsigned grp_attr = 0;      // one bit per instance of the grouped products' and adapters' kernels
+  short grp_clusters[9] = {}; // as ff_clusters, of the narrow kernel of the grouped products
   void* static_ws = nullptr;  // device address of g_static_workspace on this device
 };
 
@@ -1528,6 +1530,7 @@ tg_status run_w4a16(const void* A, const void* Wq, const void* S, void* C, int64
 }  // namespace tg
 
 #include "ff_host.cuh"
+#include "grp_host.cuh"
 
 extern "C" {
 

@@ -1,5 +1,5 @@
-// torch_calls.cpp -- the torch side of the feed-forward calls, as a CPython
-// module: argument checks, allocation of results, and one call into the C ABI.
+// torch_calls.cpp -- the torch side of the feed-forward calls, the grouped
+// products and the adapters, as a CPython module: argument checks, allocation of results, and one call into the C ABI.
 //
 // A decoding step makes these calls for 2-15 us of GPU work each, so what the
 // host spends on them counts.  Host time of a call at 16 x 64 x 64, written in
@@ -396,6 +396,143 @@ PyObject* gated_i8(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   END_HANDLE_TH_ERRORS
 }
 
+// Strides of stacked matrices (n, rows, cols) of this type: between rows and between matrices, 0 for dense ones.
+struct Stack {
+  int64_t ld = 0, stride = 0;
+};
+
+Stack stack(const at::Tensor& t, const char* name, int64_t n, int64_t rows, int64_t cols, at::ScalarType type,
+            const at::Device& device) {
+  TORCH_CHECK_TYPE(t.scalar_type() == type, name, " must be ", type, ", got ", t.scalar_type());
+  TORCH_CHECK_VALUE(t.device() == device, name, " must be on ", device, ", got ", t.device());
+  TORCH_CHECK_VALUE(t.dim() == 3 && t.size(0) == n && t.size(1) == rows && t.size(2) == cols, name, " must have shape (", n,
+                    ", ", rows, ", ", cols, "), got ", t.sizes());
+  Stack s;
+  if (t.is_contiguous() || t.numel() == 0) return s;
+  TORCH_CHECK_VALUE((cols == 1 || t.stride(2) == 1) && (rows == 1 || t.stride(1) >= cols) && (n == 1 || t.stride(0) >= cols),
+                    name, " must have adjacent columns and rows that do not overlap, got strides ", t.strides());
+  if (rows > 1) s.ld = t.stride(1);
+  if (n > 1) s.stride = t.stride(0);
+  return s;
+}
+
+// grouped(x, w, ends, out, workspace)
+PyObject* grouped(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  want_args(nargs, 5);
+  const at::Tensor& x = cuda_tensor(args[0], "x");
+  const at::Tensor &w = tensor_of(args[1], "w"), &ends = tensor_of(args[2], "ends");
+  const at::Device device = x.device();
+  const c10::cuda::CUDAGuard guard(device);
+  const at::ScalarType type = x.scalar_type();
+  const Rows xr = rows_of(x, "x");
+  tg_grouped_options o{};
+  o.type = type_code(type);
+  TORCH_CHECK_VALUE(w.dim() == 3, "w must be (groups, N, K), got ", w.sizes());
+  const int64_t G = w.size(0), M = xr.rows, K = xr.cols, N = w.size(1);
+  o.ldx = xr.ld;
+  const Stack ws3 = stack(w, "w", G, N, K, type, device);
+  o.ldw = ws3.ld;
+  o.stride_w = ws3.stride;
+  const void* pe = vector(ends, "ends", G, at::kInt, device);
+  const bool given = args[3] != Py_None;
+  // A new result has defined rows throughout; a given one keeps those that belong to no group.
+  o.rest = given ? 0 : 1;
+  const at::Tensor out = given ? given_rows(args[3], "out", x, M, N, type, &o.ldy) : new_rows(x, N, 0, type);
+  TORCH_CHECK_VALUE(G <= INT32_MAX, "too many groups");
+  const int32_t groups = static_cast<int32_t>(G);
+  const void *px = x.data_ptr(), *pw = w.data_ptr();
+  const Scratch ws(args[4], tg_grouped_workspace_size(px, pw, groups, M, N, K, &o), device);
+  call("tg_grouped", [&] {
+    return tg_grouped(px, pw, static_cast<const int32_t*>(pe), out.data_ptr(), groups, M, N, K, &o, stream_of(device), ws.ptr,
+                      ws.bytes);
+  });
+  return given ? written(args[3]) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// grouped_backward(grad, x, w, ends, need_x, need_w, workspace)
+PyObject* grouped_backward(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  want_args(nargs, 7);
+  const at::Tensor& x = cuda_tensor(args[1], "x");
+  const at::Tensor &grad = tensor_of(args[0], "grad"), &w = tensor_of(args[2], "w"), &ends = tensor_of(args[3], "ends");
+  const at::Device device = x.device();
+  const c10::cuda::CUDAGuard guard(device);
+  const at::ScalarType type = x.scalar_type();
+  const Rows xr = rows_of(x, "x");
+  tg_grouped_options o{};
+  o.type = type_code(type);
+  o.rest = 1;
+  TORCH_CHECK_VALUE(w.dim() == 3, "w must be (groups, N, K), got ", w.sizes());
+  const int64_t G = w.size(0), M = xr.rows, K = xr.cols, N = w.size(1);
+  o.ldx = xr.ld;
+  const Stack ws3 = stack(w, "w", G, N, K, type, device);
+  o.ldw = ws3.ld;
+  o.stride_w = ws3.stride;
+  o.ldy = matrix(grad, "grad", M, N, type, device, false);
+  const void* pe = vector(ends, "ends", G, at::kInt, device);
+  TORCH_CHECK_VALUE(G <= INT32_MAX, "too many groups");
+  const int32_t groups = static_cast<int32_t>(G);
+  at::Tensor dx, dw;
+  if (truth(args[4])) dx = new_rows(x, K, 0, type);
+  if (truth(args[5])) dw = at::detail::empty_cuda({G, N, K}, type, device, std::nullopt);
+  auto ptr = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+  auto wrap = [](const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : new_ref(Py_None); };
+  const void *pd = grad.data_ptr(), *px = x.data_ptr(), *pw = w.data_ptr();
+  const Scratch ws(args[6], tg_grouped_backward_workspace_size(pd, px, pw, ptr(dx), ptr(dw), groups, M, N, K, &o), device);
+  call("tg_grouped_backward", [&] {
+    return tg_grouped_backward(pd, px, pw, static_cast<const int32_t*>(pe), ptr(dx), ptr(dw), groups, M, N, K, &o,
+                               stream_of(device), ws.ptr, ws.bytes);
+  });
+  return tuple_of(wrap(dx), wrap(dw));
+  END_HANDLE_TH_ERRORS
+}
+
+// lora(x, w, a, b, index, scale, bias, out, workspace)
+PyObject* lora(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
+  HANDLE_TH_ERRORS
+  want_args(nargs, 9);
+  const at::Tensor& x = cuda_tensor(args[0], "x");
+  const at::Tensor &w = tensor_of(args[1], "w"), &a = tensor_of(args[2], "a"), &b = tensor_of(args[3], "b"),
+                   &index = tensor_of(args[4], "index");
+  const at::Device device = x.device();
+  const c10::cuda::CUDAGuard guard(device);
+  const at::ScalarType type = x.scalar_type();
+  const Rows xr = rows_of(x, "x");
+  tg_lora_options o{};
+  o.type = type_code(type);
+  TORCH_CHECK_VALUE(w.dim() == 2, "w must be (N, K), got ", w.sizes());
+  TORCH_CHECK_VALUE(a.dim() == 3, "a must be (adapters, rank, K), got ", a.sizes());
+  const int64_t M = xr.rows, K = xr.cols, N = w.size(0), R = a.size(0), rank = a.size(1);
+  o.ldx = xr.ld;
+  o.ldw = matrix(w, "w", N, K, type, device);
+  const Stack sa = stack(a, "a", R, rank, K, type, device), sb = stack(b, "b", R, N, rank, type, device);
+  o.lda = sa.ld;
+  o.stride_a = sa.stride;
+  o.ldb = sb.ld;
+  o.stride_b = sb.stride;
+  TORCH_CHECK_VALUE(rank % 8 == 0, "the adapters' rank must be a multiple of 8, got ", rank);
+  const auto off16 = [&](const at::Tensor& t, const Stack& s, int64_t cols) {
+    return t.numel() != 0 && (reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 != 0 || (s.ld ? s.ld : cols) % 8 != 0 || s.stride % 8 != 0);
+  };
+  TORCH_CHECK_VALUE(!off16(a, sa, K) && !off16(b, sb, rank), "rows of a and b must start on 16-byte boundaries");
+  const void* pi = vector(index, "index", M, at::kInt, device);
+  const float* ps = args[5] == Py_None ? nullptr
+                                       : static_cast<const float*>(vector(tensor_of(args[5], "scale"), "scale", R, at::kFloat, device));
+  const void* bias = args[6] == Py_None ? nullptr : vector(tensor_of(args[6], "bias"), "bias", N, type, device);
+  const bool given = args[7] != Py_None;
+  const at::Tensor out = given ? given_rows(args[7], "out", x, M, N, type, &o.ldy) : new_rows(x, N, 0, type);
+  const void *px = x.data_ptr(), *pw = w.data_ptr();
+  const Scratch ws(args[8], tg_lora_workspace_size(px, pw, M, N, K, rank, R, &o), device);
+  call("tg_lora", [&] {
+    return tg_lora(px, pw, a.data_ptr(), b.data_ptr(), ps, static_cast<const int32_t*>(pi), bias, out.data_ptr(), M, N, K, rank, R,
+                   &o, stream_of(device), ws.ptr, ws.bytes);
+  });
+  return given ? written(args[7]) : THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
 // has_tangent(tensors...): whether any is a dual tensor of forward-mode differentiation.
 PyObject* has_tangent(PyObject*, PyObject* const* args, Py_ssize_t nargs) {
   HANDLE_TH_ERRORS
@@ -425,12 +562,15 @@ PyMethodDef g_methods[] = {
     {"quantize_i8", fast(quantize_i8), METH_FASTCALL, nullptr},
     {"gemm_i8", fast(gemm_i8), METH_FASTCALL, nullptr},
     {"gated_i8", fast(gated_i8), METH_FASTCALL, nullptr},
+    {"grouped", fast(grouped), METH_FASTCALL, nullptr},
+    {"grouped_backward", fast(grouped_backward), METH_FASTCALL, nullptr},
+    {"lora", fast(lora), METH_FASTCALL, nullptr},
     {"has_tangent", fast(has_tangent), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the feed-forward calls.", -1, g_methods,
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_calls", "Marshalling of the feed-forward and grouped calls.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
