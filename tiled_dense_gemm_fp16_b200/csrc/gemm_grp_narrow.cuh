@@ -3,11 +3,11 @@
 // streaming the weights that have rows once) and small results.
 //
 // A cluster of S CTAs takes a panel of 128 weight rows and up to `tokens` rows of
-// one group, splits the sum over its CTAs, and adds the S partials out of each
-// other's shared memory in rank order (so results do not depend on timing).  The
-// kernel is persistent: which groups have rows is known on the device only, so
-// each cluster walks the tiles there are, its loads running ahead into the next
-// tile while the partials of the last one are added.
+// one group and splits the sum over its CTAs.  Each CTA finishes 128 / S of the
+// panel's columns: the others write their partials into its shared memory, and
+// it adds them in rank order, so results do not depend on timing.  The kernel is persistent: which groups have rows is known on the device
+// only, so each cluster walks the tiles there are, its loads running ahead into
+// the next tile while the partials of the last one are added.
 #pragma once
 
 #include "gemm_ff_skinny.cuh"
@@ -31,8 +31,10 @@ struct GrpNarrowCfg {
   static constexpr int THREADS = 192;
   static constexpr int MAX_STAGES = 10;
   static constexpr int BAR_BYTES = 256;
+  // Partials of a tile: [source][column][tokens + 4], the 4 to spread the columns over the banks.
+  __host__ __device__ static constexpr int recv_bytes(int tokens) { return PANEL * (tokens + 4) * 4; }
   static constexpr int smem_bytes(int tokens, int stages, int groups) {
-    return 1024 + stages * (W_BYTES + tokens * 128) + tokens * PANEL * 4 + BAR_BYTES + grp_plan_bytes(groups);
+    return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_bytes(groups);
   }
   // As deep as fits a CTA an SM.
   static constexpr int stages(int tokens, int groups) {
@@ -43,29 +45,16 @@ struct GrpNarrowCfg {
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
 };
 
-// Four results of a token from its partials on, with the adapter's part.
+// Results of one column and up to four tokens, with the adapters' part.
 template <bool LORA>
-__device__ __forceinline__ void grp_narrow_finish(const GrpNarrowParams& p, float (&v)[4], int m, int n, bool early) {
-  const bool bf16 = p.g.bf16 != 0;
-  if (LORA) {
-    const LoraParams& l = p.g.lora;
-    if (early) {
-      const int a = __ldg(l.index + m);
-      if (a >= 0 && a < l.adapters) {
-        const unsigned short* trow = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m) * l.rank;
-        const unsigned short* brow = static_cast<const unsigned short*>(l.b) + a * l.stride_b + n * l.ldb;
+__device__ __forceinline__ void grp_narrow_finish(const GrpParams& p, const float4& sum, int m0, int count, int n, bool early) {
+  const bool bf16 = p.bf16 != 0;
+  float v[4] = {sum.x, sum.y, sum.z, sum.w};
+  if (LORA && early) lora_add4(p.lora, v, m0, count, n, bf16);
+  const float bias = LORA && p.lora.bias != nullptr ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (n + q < p.g.out) v[q] += lora_dot(brow + q * l.ldb, trow, l.rank, bf16);
-      }
-    }
-    if (l.bias != nullptr) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (n + q < p.g.out) v[q] += load_16(static_cast<const unsigned short*>(l.bias) + n + q, bf16);
-    }
-  }
-  ff_store4(p.g.c, p.g.ldc, p.g.vec != 0, m, n, p.g.out, v, bf16);
+  for (int q = 0; q < 4; ++q)
+    if (q < count) static_cast<unsigned short*>(p.c)[(m0 + q) * p.ldc + n] = round_16(LORA ? v[q] + bias : v[q], bf16);
 }
 
 template <bool LORA>
@@ -77,14 +66,14 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
   const uint32_t x_bytes = p.tokens * 128;
   uint8_t* w_smem = smem;
   uint8_t* x_smem = smem + p.stages * Cfg::W_BYTES;
-  float* partial = reinterpret_cast<float*>(smem + p.stages * (Cfg::W_BYTES + x_bytes));  // [tokens][128]
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(partial) + p.tokens * Cfg::PANEL * 4);
+  float* recv = reinterpret_cast<float*>(smem + p.stages * (Cfg::W_BYTES + x_bytes));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::recv_bytes(p.tokens));
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + Cfg::MAX_STAGES;
   uint64_t* acc_full_bar = bars + 2 * Cfg::MAX_STAGES;
   uint64_t* acc_empty_bar = acc_full_bar + 2;
-  uint64_t* part_full_bar = acc_empty_bar + 2;   // every CTA's partial is written
-  uint64_t* part_empty_bar = part_full_bar + 1;  // every CTA has read this one's
+  uint64_t* part_full_bar = acc_empty_bar + 2;   // every CTA's partials of this one's columns are here
+  uint64_t* part_empty_bar = part_full_bar + 1;  // every CTA has added what this one sent
   uint64_t* mma_done_bar = part_empty_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -109,7 +98,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       mbar_init(&acc_full_bar[b], 1);
       mbar_init(&acc_empty_bar[b], 4);
     }
-    mbar_init(part_full_bar, 4 * p.splits);
+    mbar_init(part_full_bar, 4);  // S sources, of each the 4 / S warps that hold this CTA's columns
     mbar_init(part_empty_bar, 4 * p.splits);
     mbar_init(mma_done_bar, 1);
     *abort_flag = 0;
@@ -136,28 +125,28 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
   const int num_tiles = plan.first[p.g.groups + 1];
 
   if (warp == 0) {
-    // Producer: this CTA's slice of the sum.
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[Cfg::MAX_STAGES];
-#pragma unroll
-      for (int s = 0; s < Cfg::MAX_STAGES; ++s) last_parity[s] = -1;
-      bool ok = true;
-      const uint64_t pol_w = l2_policy_evict_first();
-      const uint64_t pol_x = l2_policy_evict_last();
-      GrpWalk walk;
-      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-        const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
-        if (f.g == p.g.groups) break;
-        const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-        const int n0 = f.col_blk * Cfg::PANEL;
-        const uint32_t tx = Cfg::W_BYTES + width * 128;
-        for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb1)) {
-            ok = false;
-            break;
-          }
+    // Producer: this CTA's slice of the sum.  The loop is the warp's, so that
+    // addresses and coordinates are in uniform registers where the TMA and MMA
+    // instructions want them; one lane issues.
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, used = 0, parities = 0;
+    bool ok = true;
+    const uint64_t pol_w = l2_policy_evict_first();
+    const uint64_t pol_x = l2_policy_evict_last();
+    GrpWalk walk;
+    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+      const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
+      if (f.g == p.g.groups) break;
+      const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+      const int n0 = f.col_blk * Cfg::PANEL;
+      const uint32_t tx = Cfg::W_BYTES + width * 128;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb1)) {
+          ok = false;
+          break;
+        }
+        if (one) {
           mbar_arrive_expect_tx(&full_bar[stage], tx);
           const int k0 = kb * 64;
           uint8_t* wdst = w_smem + stage * Cfg::W_BYTES;
@@ -171,138 +160,160 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
           grp_token_boxes(width, [&](int b, int at) {
             tma_load_2d_hint(xdst + at * 128, &maps.x[b], &full_bar[stage], k0, f.tok0 + at, pol_x);
           });
-          last_parity[stage] = static_cast<int>(phase);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        used |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | phase << stage;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-#pragma unroll
-      for (int s = 0; s < Cfg::MAX_STAGES; ++s) {
-        if (last_parity[s] >= 0) {
-          volatile int no_abort = 0;
-          mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.g.wait_budget_ns, 0xb2);
-        }
+    }
+    for (int s = 0; s < p.stages; ++s) {
+      if (used >> s & 1u) {
+        volatile int no_abort = 0;
+        mbar_wait(&full_bar[s], parities >> s & 1u, &no_abort, p.g.wait_budget_ns, 0xb2);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int local = 0;
-      bool ok = true;
-      const uint64_t w_desc0 = make_sw128_desc(smem_u32(w_smem), p.g.w_mn ? Cfg::HALF_BYTES : 16, 1024);
-      const uint64_t x_desc0 = make_sw128_desc(smem_u32(x_smem), 16, 1024);
-      const uint32_t w_step = p.g.w_mn ? 2048 / 16 : 32 / 16;
-      GrpWalk walk;
-      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++local) {
-        const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
-        if (f.g == p.g.groups) break;
-        const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-        const uint32_t idesc = p.g.idesc | static_cast<uint32_t>(width >> 3) << 17;
-        const int acc = local & 1;
-        if (!mbar_wait(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb3)) break;
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    int local = 0;
+    bool ok = true;
+    const uint64_t w_desc0 = make_sw128_desc(smem_u32(w_smem), p.g.w_mn ? Cfg::HALF_BYTES : 16, 1024);
+    const uint64_t x_desc0 = make_sw128_desc(smem_u32(x_smem), 16, 1024);
+    const uint32_t w_step = p.g.w_mn ? 2048 / 16 : 32 / 16;
+    const uint32_t tmem = uniform(tmem_base);
+    GrpWalk walk;
+    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++local) {
+      const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
+      if (f.g == p.g.groups) break;
+      const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+      const uint32_t idesc = p.g.idesc | static_cast<uint32_t>(width >> 3) << 17;
+      const int acc = local & 1;
+      if (!mbar_wait_warp(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb3)) break;
+      tcgen05_fence_after_sync();
+      const uint32_t d_tmem = tmem + acc * p.tokens;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.g.wait_budget_ns, 0xb4)) {
+          ok = false;
+          break;
+        }
         tcgen05_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * p.tokens;
-        for (int kb = kb_lo; kb < kb_hi; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.g.wait_budget_ns, 0xb4)) {
-            ok = false;
-            break;
-          }
-          tcgen05_fence_after_sync();
-          const uint64_t w_desc = w_desc0 + stage * (Cfg::W_BYTES / 16), x_desc = x_desc0 + stage * (x_bytes / 16);
+        const uint64_t w_desc = w_desc0 + stage * (Cfg::W_BYTES / 16), x_desc = x_desc0 + stage * (x_bytes / 16);
+        if (one) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            umma_f16_ss(d_tmem, w_desc + k * w_step, x_desc + k * 2, idesc, (kb - kb_lo) | k ? 1u : 0u);
+            umma_f16_ss(d_tmem, w_desc + k * w_step, x_desc + k * 2, idesc, kb > kb_lo || k > 0 ? 1u : 0u);
           umma_commit(&empty_bar[stage]);
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        umma_commit(&acc_full_bar[acc]);
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      umma_commit(mma_done_bar);
-      volatile int no_abort = 0;
-      mbar_wait(mma_done_bar, 0, &no_abort, p.g.wait_budget_ns, 0xb5);
+      if (!ok) break;
+      if (one) umma_commit(&acc_full_bar[acc]);
     }
+    if (one) umma_commit(mma_done_bar);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(mma_done_bar, 0, &no_abort, p.g.wait_budget_ns, 0xb5);
     __syncwarp();
   } else {
     const int quad = warp & 3;
     const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
-    const int step = p.splits * 128;
+    const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
+    const int pitch = p.tokens + 4;
+    const int sent = quad * 32 + lane;      // the column that this thread sends
+    const uint32_t owner = sent / own;
+    const uint32_t to = mapa_shared(smem_u32(recv) + (rank * own + sent % own) * pitch * 4, owner);
+    const uint32_t to_bar = mapa_shared(smem_u32(part_full_bar), owner);
     GrpWalk walk;
     int local = 0;
     bool waited = false;
     for (int t = cluster_id; t < num_tiles; t += num_clusters) {
       const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
-      const int n0 = f.col_blk * Cfg::PANEL;
-      const int items = f.cnt * 32;  // (token, four columns)
+      const int n0 = f.col_blk * Cfg::PANEL + rank * own;
+      const int items = own * ((f.cnt + 3) / 4);  // (column, four tokens)
       if (f.g == p.g.groups) {
-        for (int it = rank * 128 + e; it < items; it += step) {
-          const int n = n0 + (it & 31) * 4;
-          const float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (n < p.g.out) ff_store4(p.g.c, p.g.ldc, p.g.vec != 0, f.tok0 + (it >> 5), n, p.g.out, v, p.g.bf16 != 0);
-        }
+        const unsigned short zero = 0;
+        for (int it = e; it < own * f.cnt; it += 128)
+          if (n0 + it % own < p.g.out)
+            static_cast<unsigned short*>(p.g.c)[(f.tok0 + it / own) * p.g.ldc + n0 + it % own] = zero;
         continue;
       }
-      if (early && !waited) {
+      const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+      if (LORA && early && !waited) {
         // The adapters' rows that this tile's results need come into L2 meanwhile.
-        for (int it = rank * 128 + e; it < items; it += step) {
-          const int n = n0 + (it & 31) * 4;
-          const int a = __ldg(p.g.lora.index + f.tok0 + (it >> 5));
+        for (int it = e; it < own * f.cnt; it += 128) {
+          const int n = n0 + it % own, a = __ldg(p.g.lora.index + f.tok0 + it / own);
           if (a < 0 || a >= p.g.lora.adapters || n >= p.g.out) continue;
-          const char* row = reinterpret_cast<const char*>(static_cast<const unsigned short*>(p.g.lora.b) + a * p.g.lora.stride_b +
-                                                          n * p.g.lora.ldb);
-          const int64_t pitch = p.g.lora.ldb * 2;
-          for (int q = 0; q < 4 && n + q < p.g.out; ++q)
-            for (int at = 0; at < p.g.lora.rank * 2; at += 128)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(row + q * pitch + at));
+          const unsigned short* row = static_cast<const unsigned short*>(p.g.lora.b) + a * p.g.lora.stride_b + n * p.g.lora.ldb;
+          for (int at = 0; at < p.g.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
         }
       }
       const int acc = local & 1;
       bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb6);
-      // Every CTA has read the partial before.
-      if (ready) ready = mbar_wait_cluster(part_empty_bar, (local & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb7);
+      // Every CTA has added the partials before.
+      if (ready && p.splits > 1) ready = mbar_wait_cluster(part_empty_bar, (local & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb7);
       if (!__all_sync(0xffffffffu, ready)) break;
       tcgen05_fence_after_sync();
-      for (int c = 0; c < (f.cnt + 15) / 16; ++c) {
+      if (LORA && early && !waited && p.splits == 1) {
+        grid_dependency_wait();  // T
+        grid_launch_dependents();
+        waited = true;
+      }
+      for (int c = 0; c < width; c += 16) {
         uint32_t r[16];
-        tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * p.tokens + c * 16, r);
+        tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * p.tokens + c, r);
         tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 16; ++q) partial[(c * 16 + q) * Cfg::PANEL + quad * 32 + lane] = __uint_as_float(r[q]);
+        for (int q = 0; q < 16; q += 4) {
+          if (p.splits > 1) {
+            st_cluster_v4(to + (c + q) * 4, r[q], r[q + 1], r[q + 2], r[q + 3]);
+          } else if (n0 + sent < p.g.out) {
+            const float4 sum = make_float4(__uint_as_float(r[q]), __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
+                                           __uint_as_float(r[q + 3]));
+            grp_narrow_finish<LORA>(p.g, sum, f.tok0 + c + q, f.cnt - c - q, n0 + sent, early);
+          }
+        }
       }
       tcgen05_fence_before_sync();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&acc_empty_bar[acc]);
-        for (int s = 0; s < p.splits; ++s) mbar_arrive_cluster(mapa_shared(smem_u32(part_full_bar), s));
+        if (p.splits > 1) mbar_arrive_cluster(to_bar);
       }
-      ready = mbar_wait_cluster(part_full_bar, local & 1, abort_flag, p.g.wait_budget_ns, 0xb8);
-      if (!__all_sync(0xffffffffu, ready)) break;
-      if (early && !waited) {
-        grid_dependency_wait();  // T
+      ++local;
+      if (p.splits == 1) continue;
+      if (LORA && early && !waited) {
+        grid_dependency_wait();
         grid_launch_dependents();
         waited = true;
       }
-      for (int it = rank * 128 + e; it < items; it += step) {
-        const int n = n0 + (it & 31) * 4;
-        if (n >= p.g.out) continue;
-        float4 x[8];
-        ff_cluster_read(smem_u32(partial) + ((it >> 5) * Cfg::PANEL + (it & 31) * 4) * 4, p.splits, x);
-        float v[4];
-        ff_cluster_sum<kFfF16>(x, p.splits, v);
-        grp_narrow_finish<LORA>(p, v, f.tok0 + (it >> 5), n, early);
+      ready = mbar_wait_cluster(part_full_bar, (local - 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb8);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      for (int it = e; it < items; it += 128) {
+        const int col = it % own, tok = it / own * 4;
+        const float* at = recv + col * pitch + tok;
+        float4 s = *reinterpret_cast<const float4*>(at);
+        for (int q = 1; q < p.splits; ++q) {
+          const float4 x = *reinterpret_cast<const float4*>(at + q * own * pitch);
+          s.x += x.x;
+          s.y += x.y;
+          s.z += x.z;
+          s.w += x.w;
+        }
+        if (n0 + col < p.g.out) grp_narrow_finish<LORA>(p.g, s, f.tok0 + tok, f.cnt - tok, n0 + col, early);
       }
       __syncwarp();
+      // Relaxed: the values read have been used, and nothing else is ordered.
       if (lane == 0)
-        for (int s = 0; s < p.splits; ++s) mbar_arrive_cluster(mapa_shared(smem_u32(part_empty_bar), s));
-      ++local;
+        for (int q = 0; q < p.splits; ++q) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(part_empty_bar), q));
     }
-    if (early && !waited) {  // nothing to do: the grid still ends after the one before
+    if (LORA && early && !waited) {  // nothing to do: the grid still ends after the one before
       grid_dependency_wait();
       grid_launch_dependents();
     }
@@ -310,7 +321,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
 
   tcgen05_fence_before_sync();
   __syncthreads();
-  cluster_sync();  // peers are done reading this CTA's partial
+  cluster_sync();  // nobody writes to a CTA that has left
   if (warp == 1) {
     tcgen05_fence_after_sync();
     tmem_dealloc(tmem_base, p.tmem_cols);

@@ -70,36 +70,58 @@ __device__ __forceinline__ int ld_global_s32(const int* p) {
   return v;
 }
 
-// Runs of 32-token groups of a tile that share an adapter, in order.
+// Runs of 32-token groups of a tile that share an adapter, in order; for a whole warp.
 struct LoraRun {
   int first, count, adapter;
 };
 __device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraRun& run) {
   int i = run.first + run.count;
   int r = kLoraNone;
-  while (i < groups && (r = ld_global_s32(kind + i)) < 0) ++i;
+  while (i < groups && (r = uniform(ld_global_s32(kind + i))) < 0) ++i;
   if (i >= groups) return false;
   run.first = i;
   run.adapter = r;
-  while (++i < groups && ld_global_s32(kind + i) == r) {
+  while (++i < groups && uniform(ld_global_s32(kind + i)) == r) {
   }
   run.count = i - run.first;
   return true;
 }
 
-// sum_j B_a[n][j] T[m][j] in fp32, for one column and one token.
-__device__ __forceinline__ float lora_dot(const unsigned short* b, const unsigned short* t, int rank, bool bf16) {
-  float2 s = make_float2(0.0f, 0.0f);
-#pragma unroll 2
-  for (int j = 0; j < rank; j += 8) {
-    const uint4 x = __ldg(reinterpret_cast<const uint4*>(b + j));
-    const uint4 y = ld_global_v4(t + j);
-    s = fma2(unpack_16(x.x, bf16), unpack_16(y.x, bf16), s);
-    s = fma2(unpack_16(x.y, bf16), unpack_16(y.y, bf16), s);
-    s = fma2(unpack_16(x.z, bf16), unpack_16(y.z, bf16), s);
-    s = fma2(unpack_16(x.w, bf16), unpack_16(y.w, bf16), s);
+// v[q] += sum_j B_a[n][j] T[m][j] in fp32 for tokens m = m0 + q, q < count, each with its adapter a, and column n.  The loads
+// of four tokens are in flight together.
+__device__ __forceinline__ void lora_add4(const LoraParams& l, float (&v)[4], int m0, int count, int n, bool bf16) {
+  int a[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    a[q] = q < count ? __ldg(l.index + m0 + q) : -1;
+    if (a[q] >= l.adapters) a[q] = -1;
   }
-  return s.x + s.y;
+  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0) * l.rank;
+  const unsigned short* b = static_cast<const unsigned short*>(l.b) + n * l.ldb;
+  float2 s[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) s[q] = make_float2(0.0f, 0.0f);
+  for (int j = 0; j < l.rank; j += 8) {
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      x[q] = y[q] = make_uint4(0u, 0u, 0u, 0u);
+      if (a[q] >= 0) {
+        x[q] = __ldg(reinterpret_cast<const uint4*>(b + a[q] * l.stride_b + j));
+        y[q] = ld_global_v4(t + q * l.rank + j);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      s[q] = fma2(unpack_16(x[q].x, bf16), unpack_16(y[q].x, bf16), s[q]);
+      s[q] = fma2(unpack_16(x[q].y, bf16), unpack_16(y[q].y, bf16), s[q]);
+      s[q] = fma2(unpack_16(x[q].z, bf16), unpack_16(y[q].z, bf16), s[q]);
+      s[q] = fma2(unpack_16(x[q].w, bf16), unpack_16(y[q].w, bf16), s[q]);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (a[q] >= 0) v[q] += s[q].x + s[q].y;
 }
 
 struct GrpPairCfg {
@@ -206,37 +228,39 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   const int num_tiles = plan.first[p.groups + 1];
 
   if (warp == 0) {
-    // Producer (both CTAs): this CTA's half of the weight's rows and of the tokens.
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[Cfg::STAGES];
-#pragma unroll
-      for (int s = 0; s < Cfg::STAGES; ++s) last_parity[s] = -1;
-      bool ok = true, waited = false;
-      const uint64_t pol = l2_policy_evict_normal();
-      const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
-      GrpWalk walk;
-      auto next = [&]() {
-        last_parity[stage] = static_cast<int>(phase);
-        if (++stage == Cfg::STAGES) {
-          stage = 0;
-          phase ^= 1u;
+    // Producer (both CTAs): this CTA's half of the weight's rows and of the
+    // tokens.  The loop is the warp's, so that addresses and coordinates are in
+    // uniform registers where the TMA and MMA instructions want them; one lane
+    // issues.
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, used = 0, parities = 0;
+    bool ok = true, waited = false;
+    const uint64_t pol = l2_policy_evict_normal();
+    const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
+    GrpWalk walk;
+    auto next = [&]() {
+      used |= 1u << stage;
+      parities = (parities & ~(1u << stage)) | phase << stage;
+      if (++stage == Cfg::STAGES) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    };
+    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+      if (f.g == p.groups) break;  // zeros from here on
+      const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
+      const int rows = width / 2;
+      const int tok = f.tok0 + static_cast<int>(rank) * rows;
+      const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
+      const uint32_t tx = 2 * (Cfg::A_BYTES + rows * 128);
+      for (int kb = 0; kb < p.k_blocks; ++kb) {
+        if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
+          ok = false;
+          break;
         }
-      };
-      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-        const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
-        if (f.g == p.groups) break;  // zeros from here on
-        const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-        const int rows = width / 2;
-        const int tok = f.tok0 + static_cast<int>(rank) * rows;
-        const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
-        const uint32_t tx = 2 * (Cfg::A_BYTES + rows * 128);
-        for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
-            ok = false;
-            break;
-          }
+        if (one) {
           const uint32_t full = full_even0 + stage * 8;
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const int k0 = kb * 64;
@@ -251,18 +275,20 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           grp_token_boxes(rows, [&](int b, int at) {
             tma_load_2d_pair_hint(bdst + at * 128, &maps.x[b], full, k0, tok + at, pol);
           });
-          next();
         }
-        if (early && ok) {
-          if (!waited) grid_dependency_wait();
-          waited = true;
-          LoraRun run{0, 0, 0};
-          while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
-            for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
-              if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
-                ok = false;
-                break;
-              }
+        next();
+      }
+      if (early && ok) {
+        if (!waited) grid_dependency_wait();
+        waited = true;
+        LoraRun run{0, 0, 0};
+        while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
+          for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
+            if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
+              ok = false;
+              break;
+            }
+            if (one) {
               const uint32_t full = full_even0 + stage * 8;
               if (leader) mbar_arrive_expect_tx(&full_bar[stage], 2 * (Cfg::A_BYTES + run.count * 2048));
               tma_load_3d_pair_hint(a_smem + stage * Cfg::A_BYTES, &maps.lb, full, j0, n0, run.adapter, pol);
@@ -270,26 +296,26 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
               for (int i = 0; i < run.count; ++i)
                 tma_load_2d_pair_hint(b_smem + stage * Cfg::B_BYTES + i * 2048, &maps.lt, full, j0,
                                       f.tok0 + (run.first + i) * 32 + static_cast<int>(rank) * 16, pol);
-              next();
             }
+            next();
           }
         }
       }
-      // The even CTA's full barriers count both CTAs' bytes: once they have
-      // completed, every load of the pair has landed.
-      if (leader) {
-#pragma unroll 1
-        for (int s = 0; s < Cfg::STAGES; ++s) {
-          if (last_parity[s] >= 0) {
-            volatile int no_abort = 0;
-            mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.wait_budget_ns, 0xa2);
-          }
+    }
+    // The even CTA's full barriers count both CTAs' bytes: once they have
+    // completed, every load of the pair has landed.
+    if (leader) {
+      for (int s = 0; s < Cfg::STAGES; ++s) {
+        if (used >> s & 1u) {
+          volatile int no_abort = 0;
+          mbar_wait(&full_bar[s], parities >> s & 1u, &no_abort, p.wait_budget_ns, 0xa2);
         }
       }
     }
   } else if (warp == Cfg::MMA_WARP) {
     // MMA issuer (even CTA only).
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool one = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
@@ -299,9 +325,9 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const uint64_t lb_desc0 = make_sw128_desc(smem_u32(a_smem), 16, 1024);
       const uint64_t b_desc0 = make_sw128_desc(smem_u32(b_smem), 16, 1024);
       const uint32_t a_step = p.w_mn ? 2048 / 16 : 32 / 16;
+      const uint32_t tmem = uniform(tmem_base);
       GrpWalk walk;
       auto next = [&]() {
-        umma_commit_pair_mc(&empty_bar[stage], 0x3);  // both CTAs may refill this stage
         if (++stage == Cfg::STAGES) {
           stage = 0;
           phase ^= 1u;
@@ -313,19 +339,22 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
         const uint32_t idesc = p.idesc | static_cast<uint32_t>(width >> 3) << 17;
         const int acc = local & 1;
-        if (!mbar_wait(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xa3)) break;
+        if (!mbar_wait_warp(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xa3)) break;
         tcgen05_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * Cfg::TOKENS;
+        const uint32_t d_tmem = tmem + acc * Cfg::TOKENS;
         for (int kb = 0; kb < p.k_blocks; ++kb) {
-          if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
+          if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
             ok = false;
             break;
           }
           tcgen05_fence_after_sync();
           const uint64_t a_desc = a_desc0 + stage * (Cfg::A_BYTES / 16), b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16);
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f16_ss_pair(d_tmem, a_desc + k * a_step, b_desc + k * 2, idesc, (kb | k) != 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ss_pair(d_tmem, a_desc + k * a_step, b_desc + k * 2, idesc, (kb | k) != 0 ? 1u : 0u);
+            umma_commit_pair_mc(&empty_bar[stage], 0x3);  // both CTAs may refill this stage
+          }
           next();
         }
         if (early && ok) {
@@ -335,26 +364,30 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           LoraRun run{0, 0, 0};
           while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
             for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
-              if (!mbar_wait(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
+              if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
                 ok = false;
                 break;
               }
               tcgen05_fence_after_sync();
               const int steps = (min(p.lora.rank - j0, 64) + 15) / 16;
               const uint64_t a_desc = lb_desc0 + stage * (Cfg::A_BYTES / 16);
-              for (int i = 0; i < run.count; ++i) {
-                const uint64_t b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16) + i * (2048 / 16);
-                for (int k = 0; k < steps; ++k)
-                  umma_f16_ss_pair(d_tmem + (run.first + i) * 32, a_desc + k * 2, b_desc + k * 2, idesc32, 1u);
+              if (one) {
+                for (int i = 0; i < run.count; ++i) {
+                  const uint64_t b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16) + i * (2048 / 16);
+                  for (int k = 0; k < steps; ++k)
+                    umma_f16_ss_pair(d_tmem + (run.first + i) * 32, a_desc + k * 2, b_desc + k * 2, idesc32, 1u);
+                }
+                umma_commit_pair_mc(&empty_bar[stage], 0x3);
               }
               next();
             }
           }
         }
         if (!ok) break;
-        umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
+        if (one) umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
       }
-      umma_commit_pair_mc(mma_done_bar, 0x1);
+      if (one) umma_commit_pair_mc(mma_done_bar, 0x1);
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0xa5);
     }
@@ -397,16 +430,17 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         if (LORA) {
           const int n = n0 + lane;
           if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
-            const int m0 = f.tok0 + b * 32;
-            const int mine = lane < rows ? __ldg(p.lora.index + m0 + lane) : -1;
-            const unsigned short* brow = static_cast<const unsigned short*>(p.lora.b) + n * p.lora.ldb;
-            const unsigned short* trow = static_cast<const unsigned short*>(p.lora.t) + static_cast<int64_t>(m0) * p.lora.rank;
+            if (n < p.out) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int a = __shfl_sync(0xffffffffu, mine, e);
-              if (a >= 0 && a < p.lora.adapters && n < p.out)
-                r[e] = __float_as_uint(__uint_as_float(r[e]) +
-                                       lora_dot(brow + a * p.lora.stride_b, trow + e * p.lora.rank, p.lora.rank, bf16));
+              for (int e = 0; e < 32; e += 4) {
+                if (e >= rows) break;
+                float v[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[q] = __uint_as_float(r[e + q]);
+                lora_add4(p.lora, v, f.tok0 + b * 32 + e, rows - e, n, bf16);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) r[e + q] = __float_as_uint(v[q]);
+              }
             }
           }
           if (p.lora.bias != nullptr && n < p.out) {

@@ -205,11 +205,13 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
   p.stages = Cfg::stages(tokens, f.groups);
-  uint32_t cols = 32;
-  while (cols < static_cast<uint32_t>(2 * tokens)) cols <<= 1;
-  p.tmem_cols = cols;
-  int splits = tune_int("TG_TUNE_GRP_SPLITS", 4);
-  if (splits > p.g.k_blocks) splits = p.g.k_blocks;
+  // Beside the kernel that makes T, which is still at work (launch_lora_shrink).
+  const int room = 232448 - 100 * 1024 - Cfg::smem_bytes(tokens, 0, f.groups);
+  if (f.lora && f.l.adapters > 0 && p.stages > room / (Cfg::W_BYTES + tokens * 128) && room / (Cfg::W_BYTES + tokens * 128) >= 3)
+    p.stages = room / (Cfg::W_BYTES + tokens * 128);
+  p.tmem_cols = static_cast<uint32_t>(2 * tokens);
+  int splits = tune_int("TG_TUNE_GRP_SPLITS", 2);
+  while (splits > p.g.k_blocks) splits >>= 1;
   p.splits = splits;
   const int64_t most = ((f.a.rows + tokens - 1) / tokens + f.groups) * p.g.col_tiles;
   const int64_t fit = grp_resident_clusters(splits, info), clusters = most < fit ? most : fit;
@@ -492,18 +494,55 @@ int64_t lora_workspace(const LoraArgs& l) {
   return inner + ff_copy_bytes(l.x) + ff_copy_bytes(l.w);
 }
 
-template <int NT>
-tg_status launch_lora_shrink(const LoraShrinkParams& p, int y, cudaStream_t stream) {
+// T and the kinds of 32 tokens.
+tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float* scale, cudaStream_t stream, DeviceInfo* info) {
+  using Cfg = LoraShrinkCfg;
+  if (!ff_set_smem(reinterpret_cast<const void*>(lora_shrink_kernel), info->grp_attr, 32u, 210 * 1024)) return TG_ERR_LAUNCH;
+  LoraShrinkMaps maps;
+  std::memset(&maps, 0, sizeof maps);
+  LoraShrinkParams p;
+  std::memset(&p, 0, sizeof p);
+  p.a_rows = static_cast<int>(l.rank < 128 ? l.rank : 128);
+  if (!grp_encode3(&maps.a, l.a, 64, p.a_rows)) return TG_ERR_LAUNCH;
+  for (int i = 0; i < 4; ++i)
+    if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
+  p.index = f.l.index;
+  p.scale = scale;
+  p.t = const_cast<void*>(f.l.t);
+  p.kind = const_cast<int*>(f.l.kind);
+  p.M = static_cast<int>(l.M);
+  p.rank = static_cast<int>(l.rank);
+  p.adapters = static_cast<int>(l.adapters);
+  p.k_blocks = static_cast<int>((l.K + 63) / 64);
+  p.tokens = 16;
+  while (p.tokens < 128 && p.tokens < l.M) p.tokens <<= 1;
+  const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
+  const int64_t deep = (l.rank + 127) / 128;
+  p.splits = 1;
+  const int64_t most = tune_int("TG_TUNE_SHRINK_SPLITS", 4);
+  while (p.splits < most && 4 * p.splits <= p.k_blocks && blocks * deep * p.splits * 2 <= 2 * info->sm_count) p.splits *= 2;
+  // Clusters for the items of a block: as many as it may have, while they find SMs.
+  int64_t y = 4 * info->sm_count / (blocks * deep * p.splits);
+  const int64_t items = l.M < p.tokens ? l.M : p.tokens;
+  y = y < 1 ? 1 : y > items ? items : y;
+  y = y > l.adapters ? l.adapters : y;
+  const int budget = l.M <= 128 ? 96 * 1024 : 200 * 1024;
+  p.stages = (budget - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
+  if (p.stages < 2) p.stages = 2;
+  p.bf16 = l.bf16 ? 1 : 0;
+  p.tmem_cols = p.tokens < 32 ? 32 : p.tokens;
+  p.idesc = make_idesc_ff(kFfF16, l.bf16, 128, 0, false, false);
+  p.wait_budget_ns = wait_budget(p.k_blocks);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(static_cast<unsigned>((p.M + 31) / 32), static_cast<unsigned>(y),
-                     static_cast<unsigned>((p.rank + NT * 8 - 1) / (NT * 8)));
-  cfg.blockDim = dim3(kShrinkWarps * 32, 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * p.splits), static_cast<unsigned>(y), static_cast<unsigned>(deep));
+  cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(p.tokens, p.splits, p.a_rows, p.stages));
   cfg.stream = stream;
   LaunchAttrs la;
-  la.fill(cfg, 1);
-  auto kernel = p.bf16 ? lora_shrink_kernel<NT, true> : lora_shrink_kernel<NT, false>;
-  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+  la.fill(cfg, static_cast<unsigned>(p.splits));
+  if (cudaLaunchKernelEx(&cfg, lora_shrink_kernel, maps, p) != cudaSuccess) {
     cudaGetLastError();
     return TG_ERR_LAUNCH;
   }
@@ -553,33 +592,7 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
   }
   FfMat* const operands[2] = {&l.x, &l.w};
   if ((st = ff_make_copies(operands, 2, ws, stream, info)) != TG_OK) return st;
-  if (adapted) {
-    LoraShrinkParams p;
-    std::memset(&p, 0, sizeof p);
-    p.x = l.x.p;
-    p.a = l.a.m.p;
-    p.index = index;
-    p.scale = scale;
-    p.t = const_cast<void*>(f.l.t);
-    p.kind = const_cast<int*>(f.l.kind);
-    p.ldx = l.x.ld;
-    p.lda = l.a.m.ld;
-    p.stride_a = l.a.stride;
-    p.M = static_cast<int>(l.M);
-    p.K = static_cast<int>(l.K);
-    p.rank = static_cast<int>(l.rank);
-    p.adapters = static_cast<int>(l.adapters);
-    p.bf16 = l.bf16 ? 1 : 0;
-    // Blocks for the adapters of 32 tokens: as many as there may be, while they find SMs.
-    const int64_t blocks = (l.M + 31) / 32;
-    int y = static_cast<int>(l.M < 32 ? l.M : 32);
-    while (y > 1 && blocks * y > 4 * info->sm_count) y = (y + 1) / 2;
-    st = l.rank <= 8    ? launch_lora_shrink<1>(p, y, stream)
-         : l.rank <= 16 ? launch_lora_shrink<2>(p, y, stream)
-         : l.rank <= 32 ? launch_lora_shrink<4>(p, y, stream)
-                        : launch_lora_shrink<8>(p, y, stream);
-    if (st != TG_OK) return st;
-  }
+  if (adapted && (st = launch_lora_shrink(l, f, scale, stream, info)) != TG_OK) return st;
   f.a = l.x;
   f.c = l.y;
   f.w = GrpStack{l.w, 1, 0};

@@ -34,6 +34,33 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const CUtensorM
       : "memory");
 }
 
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(one));
+  return one != 0u;
+}
+// A value that is the same in all lanes, as one that the compiler knows to be.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+// mbar_wait by a whole warp, with one answer.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t budget_ns,
+                                               unsigned int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, budget_ns, site));
+}
+
+// 16 bytes into the shared memory of a CTA of the cluster.
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// What this thread (and, after __syncwarp, its warp) has written is seen by a
+// CTA of the cluster that acquires a later relaxed arrival.  One fence for several
+// arrivals: each release at cluster scope measured about 1 us.
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 // ----------------------------------------------------------------------------
 // Groups
 // ----------------------------------------------------------------------------
@@ -47,13 +74,28 @@ __device__ __forceinline__ int grp_end(const int* ends, int g, int M) {
   return ends == nullptr ? M : max(0, min(__ldg(ends + g), M));
 }
 
-// A group's rows in tiles of at most `most`: as many as are needed, of equal
-// width up to `unit`, so that no tile is a sliver.  The last one starts before
-// the group's end, since tiles - 1 of the widest would not hold the group.
-__device__ __forceinline__ int grp_tile_width(int rows, int most, int unit) {
-  const int tiles = (rows + most - 1) / most;
-  const int even = (rows + tiles - 1) / tiles;
-  return (even + unit - 1) / unit * unit;
+// A group's rows as tiles of `most`, whose last two share what a short last one
+// would leave between them (a tile of few tokens still loads its whole weight
+// tile).  All but the group's last width are multiples of `unit`.
+struct GrpCut {
+  int tiles, whole, width;  // `whole` tiles of `most`, one of `width` rows, and the rest in the last
+};
+__device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
+  GrpCut c;
+  c.tiles = (rows + most - 1) / most;
+  c.whole = c.tiles - 1;
+  c.width = 0;
+  const int last = rows - c.whole * most;
+  if (c.tiles >= 2 && 2 * last < most) {
+    --c.whole;
+    c.width = ((most + last + 1) / 2 + unit - 1) / unit * unit;
+  }
+  return c;
+}
+// First row and number of rows of tile i.
+__device__ __forceinline__ void grp_cut_tile(const GrpCut& c, int rows, int most, int i, int& first, int& count) {
+  first = min(i, c.whole) * most + (i > c.whole ? c.width : 0);
+  count = i < c.whole ? most : (i == c.whole && c.width != 0 ? c.width : rows - first);
 }
 
 // Starts and running numbers of tiles, in shared memory: group G stands for the
@@ -104,6 +146,7 @@ struct GrpTile {
   int col_blk;    // tile of result columns
 };
 
+// The walk of a whole warp.
 struct GrpWalk {
   int g = 0;
   __device__ __forceinline__ GrpTile at(const GrpPlan& plan, int t, int col_tiles, int super, int most, int unit) {
@@ -111,15 +154,18 @@ struct GrpWalk {
     GrpTile f;
     f.g = g;
     const int lo = plan.lo[g], rows = plan.lo[g + 1] - lo;
-    const int tiles = (rows + most - 1) / most, width = grp_tile_width(rows, most, unit);
+    const GrpCut cut = grp_cut(rows, most, unit);
     const int local = t - plan.first[g];
     const int s = local / (super * col_tiles);
-    const int wide = min(super, tiles - s * super);
+    const int wide = min(super, cut.tiles - s * super);
     const int in = local - s * super * col_tiles;
     f.col_blk = in / wide;
-    const int i = s * super + in - f.col_blk * wide;
-    f.tok0 = lo + i * width;
-    f.cnt = min(width, rows - i * width);
+    grp_cut_tile(cut, rows, most, s * super + in - f.col_blk * wide, f.tok0, f.cnt);
+    f.tok0 += lo;
+    f.g = uniform(f.g);
+    f.tok0 = uniform(f.tok0);
+    f.cnt = uniform(f.cnt);
+    f.col_blk = uniform(f.col_blk);
     return f;
   }
 };

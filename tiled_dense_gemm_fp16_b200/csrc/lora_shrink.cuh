@@ -1,146 +1,315 @@
 // lora_shrink.cuh -- the first half of the low-rank adapters:
 // T[m][j] = scale_a sum_k A_a[j][k] X[m][k] with a = index[m].
 //
-// A block takes 32 tokens and one of the adapters among them (most blocks of a
-// prompt find one, decoding requests up to 32, over blockIdx.y), up to 64 rows
-// of A.  Its 8 warps split K; each multiplies 32 x 16 by 16 x 8 on the warp-level
-// tensor cores, whose rows are independent: tokens of other adapters are read as
-// zeros and not written.  Within 32 values of K a thread's fragments are 8
-// adjacent ones (the sum's order is free), so every load is 16 bytes, straight
-// into registers.  Bound by reading X and the adapters' A.  T is rounded once to the 16-bit
-// type, as the tensor cores read it (and as two linear layers in a row would).
+// Bound by reading X and the used adapters' A.  An item is one adapter among a
+// block of 128 tokens, and up to 128 rows of its A: these are the MMA's M side
+// (rows behind the rank are whatever lies in shared memory behind them, in lanes
+// that nobody reads), the tokens from the adapter's first to its last in the block the N side.
+// Columns of D are independent, so tokens of other adapters in between cost
+// nothing but their loads, and are not written.  A cluster of S CTAs splits the
+// sum over K; each finishes every S-th four tokens from the partials that the
+// others write into its shared memory, in rank order.  Blocks of a prompt have one item, those of a
+// decoding batch up to 128, spread over blockIdx.y.  T is rounded once to the
+// 16-bit type, as the tensor cores read it (and as two linear layers in a row would).
+//
+// A decoding batch's main product runs meanwhile (it waits for T only when it has
+// its own sums), so for few tokens the ring is kept small enough for both on an SM.
 #pragma once
 
-#include "grp_ops.cuh"
-#include "gemm_grp_pair.cuh"
+#include "gemm_grp_narrow.cuh"
 
 namespace tg {
 
-struct LoraShrinkParams {
-  const void* x;
-  const void* a;
-  const int* index;
-  const float* scale;        // of each adapter, or nullptr
-  void* t;
-  int* kind;
-  int64_t ldx, lda, stride_a;
-  int M, K, rank, adapters;
-  int bf16;
+struct LoraShrinkMaps {
+  CUtensorMap a;     // adapters' A: boxes of 64 x min(128, rank)
+  CUtensorMap x[4];  // X: boxes of 64 columns and 16, 32, 64, 128 rows
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1, bool bf16) {
-  if (bf16)
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+struct LoraShrinkParams {
+  const int* index;
+  const float* scale;  // of each adapter, or nullptr
+  void* t;
+  int* kind;
+  int M, rank, adapters;
+  int k_blocks, splits, stages;
+  int tokens;          // most of an item, and rows of a block: 16, 32, 64 or 128
+  int a_rows;          // of a box: min(128, rank)
+  int bf16;
+  uint32_t tmem_cols;
+  uint32_t idesc;      // without N
+  uint64_t wait_budget_ns;
+};
 
-// 8 values from p on, of which n (any number) are in the row; p on 16 bytes.
-__device__ __forceinline__ uint4 row8(const unsigned short* p, int n) {
-  if (n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (e < n) w[e >> 1] |= static_cast<uint32_t>(__ldg(p + e)) << ((e & 1) * 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+struct LoraShrinkCfg {
+  static constexpr int EPI_WARP0 = 2;
+  static constexpr int THREADS = 192;
+  static constexpr int MAX_STAGES = 16;
+  static constexpr int BAR_BYTES = 512;
+  // Partials: [source][four tokens][row of A] of 16 bytes, for this CTA's share of the tokens.
+  __host__ __device__ static constexpr int recv_bytes(int tokens, int splits, int a_rows) {
+    return splits * ((tokens / 4 + splits - 1) / splits) * a_rows * 16;
+  }
+  // The MMAs read 128 rows from each stage's A on, the last ones of other stages and of X.
+  static constexpr int smem_bytes(int tokens, int splits, int a_rows, int stages) {
+    const int n = stages * (a_rows + tokens) * 128 + recv_bytes(tokens, splits, a_rows) + BAR_BYTES;
+    const int least = (stages * a_rows + 128) * 128;
+    return 1024 + (n < least ? least : n);
+  }
+  static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
+};
 
-constexpr int kShrinkWarps = 8;
+// The adapters among a block's tokens, in order of their first.
+struct LoraItems {
+  int count;
+  int adapter[128], first[128], last[128];
+};
 
-// NT: tiles of 8 rows of A.
-template <int NT, bool BF16>
-__global__ void __launch_bounds__(kShrinkWarps * 32) lora_shrink_kernel(const LoraShrinkParams p) {
-  __shared__ float sums[4][32 * NT * 8];
+__global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
+    lora_shrink_kernel(const __grid_constant__ LoraShrinkMaps maps, const LoraShrinkParams p) {
+  using Cfg = LoraShrinkCfg;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t a_bytes = p.a_rows * 128, x_bytes = p.tokens * 128;
+  uint8_t* a_smem = smem;
+  uint8_t* x_smem = smem + p.stages * a_bytes;
+  float4* recv = reinterpret_cast<float4*>(smem + p.stages * (a_bytes + x_bytes));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::recv_bytes(p.tokens, p.splits, p.a_rows));
+  uint64_t* full_bar = bars;
+  uint64_t* empty_bar = bars + Cfg::MAX_STAGES;
+  uint64_t* acc_full_bar = bars + 2 * Cfg::MAX_STAGES;
+  uint64_t* acc_empty_bar = acc_full_bar + 1;
+  uint64_t* part_full_bar = acc_empty_bar + 1;
+  uint64_t* part_empty_bar = part_full_bar + 1;
+  uint64_t* mma_done_bar = part_empty_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
   grid_dependency_wait();
   grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int m0 = blockIdx.x * 32, j0 = blockIdx.z * NT * 8;
-  const int a_of = m0 + lane < p.M ? __ldg(p.index + m0 + lane) : -1;
-  const int mine = a_of >= 0 && a_of < p.adapters ? a_of : -1;
-  const unsigned valid = __ballot_sync(0xffffffffu, m0 + lane < p.M);
-  unsigned left = __ballot_sync(0xffffffffu, mine >= 0);
-  if (blockIdx.y == 0 && blockIdx.z == 0 && warp == 0) {
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int m0 = static_cast<int>(blockIdx.x / p.splits) * p.tokens;
+  const int j0 = static_cast<int>(blockIdx.z) * 128;
+  const int rows = min(128, p.rank - j0);  // of A
+  // Each of 128 threads looks for its token's adapter among the tokens before.
+  __shared__ __align__(16) int owner_of[128];
+  __shared__ int firsts[4];
+  __shared__ LoraItems items;
+  int mine = -1;
+  const int tok = threadIdx.x;
+  if (tok < 128) {
+    const bool valid = tok < p.tokens && m0 + tok < p.M;
+    const int a = valid ? __ldg(p.index + m0 + tok) : -1;
+    mine = a >= 0 && a < p.adapters ? a : -1;
+    owner_of[tok] = mine;
     const int r0 = __shfl_sync(0xffffffffu, mine, 0);
-    const unsigned same = __ballot_sync(0xffffffffu, mine == r0) & valid;
-    if (lane == 0) p.kind[blockIdx.x] = left == 0 ? kLoraNone : same == valid ? r0 : kLoraMixed;
+    const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
+    // What each 32 tokens are to the main product.
+    if (lane == 0 && valid && blockIdx.y == 0 && blockIdx.z == 0 && rank == 0)
+      p.kind[(m0 + tok) / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
   }
-  for (int d = 0; left != 0; ++d) {
-    const int r = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
-    const unsigned rows = __ballot_sync(0xffffffffu, mine == r);
-    left &= ~rows;
-    if (d % gridDim.y != blockIdx.y) continue;
-    float acc[2][NT][4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
-    const int row = lane >> 2, q = lane & 3;
-    const unsigned short* x = static_cast<const unsigned short*>(p.x) + static_cast<int64_t>(m0 + row) * p.ldx;
-    const unsigned short* a = static_cast<const unsigned short*>(p.a) + r * p.stride_a + static_cast<int64_t>(j0 + row) * p.lda;
-    for (int k = warp * 32 + q * 8; k - q * 8 < p.K; k += kShrinkWarps * 32) {
-      uint4 xv[4], av[NT];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        xv[i] = (rows >> (row + 8 * i)) & 1u ? row8(x + 8 * i * p.ldx + k, p.K - k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        av[n] = j0 + n * 8 + row < p.rank ? row8(a + n * 8 * p.lda + k, p.K - k) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          mma_16816(acc[i][n], xv[2 * i].x, xv[2 * i + 1].x, xv[2 * i].y, xv[2 * i + 1].y, av[n].x, av[n].y, BF16);
-          mma_16816(acc[i][n], xv[2 * i].z, xv[2 * i + 1].z, xv[2 * i].w, xv[2 * i + 1].w, av[n].z, av[n].w, BF16);
+  __syncthreads();
+  int before = 128;  // the first token of this one's adapter, from the end of the search on
+  if (tok < 128) {
+    for (int s = (tok & ~31) + 28; s >= 0; s -= 4) {
+      const int4 o = *reinterpret_cast<const int4*>(owner_of + s);
+      if (o.w == mine) before = s + 3;
+      if (o.z == mine) before = s + 2;
+      if (o.y == mine) before = s + 1;
+      if (o.x == mine) before = s;
+    }
+    const unsigned opens = __ballot_sync(0xffffffffu, mine >= 0 && before == tok);
+    if (lane == 0) firsts[warp] = __popc(opens);
+    if (mine >= 0 && before == tok) items.last[tok] = tok;  // by the first token for now
+    before = mine < 0 ? -1 : before;
+    mine = __popc(opens & ((1u << lane) - 1));  // its number in this warp
+  }
+  __syncthreads();
+  if (tok < 128 && before >= 0 && before != tok) atomicMax(&items.last[before], tok);
+  __syncthreads();
+  int last = 0;
+  if (tok < 128 && before == tok) last = items.last[tok];
+  __syncthreads();
+  if (tok < 128) {
+    for (int w = 0; w < warp; ++w) mine += firsts[w];
+    if (before == tok) {
+      items.adapter[mine] = owner_of[tok];
+      items.first[mine] = tok;
+      items.last[mine] = last;
+    }
+    if (tok == 0) items.count = firsts[0] + firsts[1] + firsts[2] + firsts[3];
+  }
+  __syncthreads();
+  const int count = items.count, step = static_cast<int>(gridDim.y);
+  if (static_cast<int>(blockIdx.y) >= count) return;  // nothing for this cluster: the same in all of its CTAs
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(acc_full_bar, 1);
+    mbar_init(acc_empty_bar, 4);
+    mbar_init(part_full_bar, 4 * p.splits);
+    mbar_init(part_empty_bar, 4 * p.splits);
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish_alloc_permit();
+  }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tcgen05_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
+  const int kb_lo = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
+  const int kb_hi = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
+
+  if (warp == 0) {
+    // As in the narrow kernel: the warp loops, one lane issues.
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, used = 0, parities = 0;
+    bool ok = true;
+    const uint64_t pol_a = l2_policy_evict_first(), pol_x = l2_policy_evict_normal();
+    for (int d = blockIdx.y; ok && d < count; d += step) {
+      const int adapter = uniform(items.adapter[d]), t0 = uniform(items.first[d] & ~15);
+      const int width = uniform((items.last[d] & ~15) + 16) - t0;
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xd1)) {
+          ok = false;
+          break;
         }
-    }
-    // The warps' sums, pairwise in a fixed order: 4 to 7 onto 0 to 3, 2 and 3 onto 0 and 1, 1 onto 0.
-#pragma unroll
-    for (int half = kShrinkWarps / 2; half > 0; half >>= 1) {
-      __syncthreads();
-      if (warp >= half && warp < 2 * half) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sums[warp - half][((i * NT + n) * 4 + e) * 32 + lane] = acc[i][n][e];
-      }
-      __syncthreads();
-      if (warp < half) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[i][n][e] += sums[warp][((i * NT + n) * 4 + e) * 32 + lane];
+        if (one) {
+          mbar_arrive_expect_tx(&full_bar[stage], (p.a_rows + width) * 128);
+          tma_load_3d_hint(a_smem + stage * a_bytes, &maps.a, &full_bar[stage], kb * 64, j0, adapter, pol_a);
+          grp_token_boxes(width, [&](int b, int at) {
+            tma_load_2d_hint(x_smem + stage * x_bytes + at * 128, &maps.x[b], &full_bar[stage], kb * 64, m0 + t0 + at, pol_x);
+          });
+        }
+        used |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | phase << stage;
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
     }
-    if (warp == 0) {
-      const float s = p.scale != nullptr ? __ldg(p.scale + r) : 1.0f;
+    for (int s = 0; s < p.stages; ++s) {
+      if (used >> s & 1u) {
+        volatile int no_abort = 0;
+        mbar_wait(&full_bar[s], parities >> s & 1u, &no_abort, p.wait_budget_ns, 0xd2);
+      }
+    }
+  } else if (warp == 1) {
+    const bool one = elect_one();
+    int stage = 0, local = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), 16, 1024);
+    const uint64_t x_desc0 = make_sw128_desc(smem_u32(x_smem), 16, 1024);
+    const uint32_t d_tmem = uniform(tmem_base);
+    for (int d = blockIdx.y; ok && d < count; d += step, ++local) {
+      const int width = uniform(((items.last[d] & ~15) + 16) - (items.first[d] & ~15));
+      const uint32_t idesc = p.idesc | static_cast<uint32_t>(width >> 3) << 17;
+      if (!mbar_wait_warp(acc_empty_bar, (local & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xd3)) break;
+      tcgen05_fence_after_sync();
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+        if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xd4)) {
+          ok = false;
+          break;
+        }
+        tcgen05_fence_after_sync();
+        const uint64_t a_desc = a_desc0 + stage * (a_bytes / 16), x_desc = x_desc0 + stage * (x_bytes / 16);
+        if (one) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+          for (int k = 0; k < 4; ++k)
+            umma_f16_ss(d_tmem, a_desc + k * 2, x_desc + k * 2, idesc, kb > kb_lo || k > 0 ? 1u : 0u);
+          umma_commit(&empty_bar[stage]);
+        }
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (ok && one) umma_commit(acc_full_bar);
+    }
+    if (one) umma_commit(mma_done_bar);
+    __syncwarp();
+    volatile int no_abort = 0;
+    mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0xd5);
+    __syncwarp();
+  } else {
+    const int quad = warp & 3;
+    const int j = quad * 32 + lane;  // row of A
+    const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
+    const int share = (p.tokens / 4 + p.splits - 1) / p.splits;  // four tokens each, of a source
+    int local = 0;
+    for (int d = blockIdx.y; d < count; d += step) {
+      const int adapter = items.adapter[d], t0 = items.first[d] & ~15, width = ((items.last[d] & ~15) + 16) - t0;
+      const int fours = width / 4, mine = (fours - rank + p.splits - 1) / p.splits;  // those of this CTA: rank, rank + splits, ...
+      bool ready = mbar_wait(acc_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd6);
+      if (ready) ready = mbar_wait_cluster(part_empty_bar, (local & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xd7);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tcgen05_fence_after_sync();
+      if (quad * 32 < rows) {
+        for (int c = 0; c < width; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c, r);
+          tmem_ld_wait();
+          if (j < rows) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int m = 16 * i + 8 * h + row;
-          if (!((rows >> m) & 1u)) continue;
-          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<unsigned short*>(p.t) + static_cast<int64_t>(m0 + m) * p.rank + j0) + q;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (j0 + n * 8 >= p.rank) break;  // rank is a multiple of 8
-            const float u = acc[i][n][2 * h] * s, v = acc[i][n][2 * h + 1] * s;
-            dst[n * 4] = BF16 ? pack_bf16(u, v) : pack_f16(u, v);
+            for (int q = 0; q < 4; ++q) {
+              const int four = c / 4 + q;
+              const uint32_t owner = four % p.splits;
+              st_cluster_v4(mapa_shared(smem_u32(recv + (rank * share + four / p.splits) * p.a_rows + j), owner), r[4 * q],
+                            r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+            }
           }
         }
+      }
+      tcgen05_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(acc_empty_bar);
+        fence_cluster();
+        for (int q = 0; q < p.splits; ++q) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(part_full_bar), q));
+      }
+      ready = mbar_wait_cluster(part_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd8);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
+      for (int it = e; it < mine * rows; it += 128) {
+        const int four = it / rows, row = it - four * rows;
+        float4 s = recv[four * p.a_rows + row];
+        for (int q = 1; q < p.splits; ++q) {
+          const float4 x = recv[(q * share + four) * p.a_rows + row];
+          s.x += x.x;
+          s.y += x.y;
+          s.z += x.z;
+          s.w += x.w;
+        }
+        const float v[4] = {s.x, s.y, s.z, s.w};
+        const int m = m0 + t0 + (four * p.splits + rank) * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (m + q < p.M && __ldg(p.index + m + q) == adapter)
+            static_cast<unsigned short*>(p.t)[static_cast<int64_t>(m + q) * p.rank + j0 + row] = round_16(v[q] * scale, p.bf16 != 0);
+      }
+      __syncwarp();
+      if (lane == 0)
+        for (int q = 0; q < p.splits; ++q) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(part_empty_bar), q));
+      ++local;
     }
+  }
+
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // nobody writes to a CTA that has left
+  if (warp == 1) {
+    tcgen05_fence_after_sync();
+    tmem_dealloc(tmem_base, p.tmem_cols);
   }
 }
 
