@@ -18,7 +18,8 @@ namespace tg {
 struct GrpNarrowParams {
   GrpParams g;         // col_tiles: panels of 128 columns; idesc without N
   int tokens;          // most of a tile: 16, 32, 64 or 128
-  int splits, stages;
+  int splits, stages;  // 1, 2 or 4 splits
+  int per_stage;       // k-blocks of a stage of the ring
   uint32_t tmem_cols;  // two accumulators
 };
 
@@ -34,26 +35,43 @@ struct GrpNarrowCfg {
   // Partials of a tile: [source][column][tokens + 4], the 4 to spread the columns over the banks.
   __host__ __device__ static constexpr int recv_bytes(int tokens) { return PANEL * (tokens + 4) * 4; }
   static constexpr int smem_bytes(int tokens, int stages, int groups) {
-    return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_bytes(groups);
-  }
-  // As deep as fits a CTA an SM.
-  static constexpr int stages(int tokens, int groups) {
-    const int n = (232448 - smem_bytes(tokens, 0, groups)) / (W_BYTES + tokens * 128);
-    return n > MAX_STAGES ? MAX_STAGES : n;
+    return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups) + 4 * kLoraTBytes;
   }
   static_assert((2 * MAX_STAGES + 7) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
 };
 
-// Results of one column and up to four tokens, with the adapters' part.
+// The adapters of a tile's tokens: a warp's lane holds those of lane + 32 i.
+struct GrpTileAdapters {
+  int a[4];
+  __device__ __forceinline__ void load(const LoraParams& l, int tok0, int cnt, int lane) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = 32 * i + lane < cnt ? lora_adapter(l, tok0 + 32 * i + lane) : -1;
+  }
+  // Of token t, the same in the whole warp.
+  __device__ __forceinline__ int of(int t) const {
+    const int i = t >> 5;
+    return __shfl_sync(0xffffffffu, i == 0 ? a[0] : i == 1 ? a[1] : i == 2 ? a[2] : a[3], t & 31);
+  }
+};
+
+// Results of column n and up to eight tokens from `tok` of the tile on, with the adapters' part.  For a whole warp with
+// the same tokens in all lanes.
 template <bool LORA>
-__device__ __forceinline__ void grp_narrow_finish(const GrpParams& p, const float4& sum, int m0, int count, int n, bool early) {
+__device__ __forceinline__ void grp_narrow_finish(const GrpParams& p, float (&v)[8], const GrpTile& f, int tok, int n,
+                                                  const GrpTileAdapters& adapters, bool early, uint8_t* tbuf, int lane) {
   const bool bf16 = p.bf16 != 0;
-  float v[4] = {sum.x, sum.y, sum.z, sum.w};
-  if (LORA && early) lora_add4(p.lora, v, m0, count, n, bf16);
+  const int m0 = f.tok0 + tok, count = f.cnt - tok;
+  if (LORA && early) {
+    int a[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) a[q] = adapters.of(tok + q);
+    lora_add(p.lora, v, a, m0, n, n < p.out, tbuf, lane, bf16);
+  }
+  if (n >= p.out) return;
   const float bias = LORA && p.lora.bias != nullptr ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < 8; ++q)
     if (q < count) static_cast<unsigned short*>(p.c)[(m0 + q) * p.ldc + n] = round_16(LORA ? v[q] + bias : v[q], bf16);
 }
 
@@ -65,8 +83,8 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t x_bytes = p.tokens * 128;
   uint8_t* w_smem = smem;
-  uint8_t* x_smem = smem + p.stages * Cfg::W_BYTES;
-  float* recv = reinterpret_cast<float*>(smem + p.stages * (Cfg::W_BYTES + x_bytes));
+  uint8_t* x_smem = smem + p.stages * p.per_stage * Cfg::W_BYTES;
+  float* recv = reinterpret_cast<float*>(smem + p.stages * p.per_stage * (Cfg::W_BYTES + x_bytes));
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::recv_bytes(p.tokens));
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + Cfg::MAX_STAGES;
@@ -104,12 +122,16 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&maps.w);
-    tma_prefetch_desc(&maps.x[0]);
+    for (int b = 0; b < 4 && 16 << b <= p.tokens; ++b) tma_prefetch_desc(&maps.x[b]);
   }
   if (warp == 1) {
     tmem_alloc(tmem_slot, p.tmem_cols);
     tmem_relinquish_alloc_permit();
   }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // every CTA's barriers are initialised before any remote use
+  tcgen05_fence_after_sync();
   const bool early = LORA && p.g.lora.adapters > 0;  // as in the pair kernel
   if (!early) {
     grid_dependency_wait();
@@ -117,10 +139,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
   }
   if (warp == Cfg::EPI_WARP0)
     grp_make_plan(plan, p.g.ends, p.g.groups, p.g.M, p.tokens, p.g.col_tiles, p.g.rest != 0, lane);
-  tcgen05_fence_before_sync();
   __syncthreads();
-  cluster_sync();  // every CTA's barriers are initialised before any remote use
-  tcgen05_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   const int num_tiles = plan.first[p.g.groups + 1];
 
@@ -141,25 +160,28 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
       const int n0 = f.col_blk * Cfg::PANEL;
       const uint32_t tx = Cfg::W_BYTES + width * 128;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; kb += p.per_stage) {
         if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb1)) {
           ok = false;
           break;
         }
         if (one) {
-          mbar_arrive_expect_tx(&full_bar[stage], tx);
-          const int k0 = kb * 64;
-          uint8_t* wdst = w_smem + stage * Cfg::W_BYTES;
-          uint8_t* xdst = x_smem + stage * x_bytes;
-          if (p.g.w_mn) {
-            tma_load_3d_hint(wdst, &maps.w, &full_bar[stage], n0, k0, f.g, pol_w);
-            tma_load_3d_hint(wdst + Cfg::HALF_BYTES, &maps.w, &full_bar[stage], n0 + 64, k0, f.g, pol_w);
-          } else {
-            tma_load_3d_hint(wdst, &maps.w, &full_bar[stage], k0, n0, f.g, pol_w);
+          const int n = min(p.per_stage, kb_hi - kb);
+          mbar_arrive_expect_tx(&full_bar[stage], n * tx);
+          for (int i = 0; i < n; ++i) {
+            const int k0 = (kb + i) * 64;
+            uint8_t* wdst = w_smem + (stage * p.per_stage + i) * Cfg::W_BYTES;
+            uint8_t* xdst = x_smem + (stage * p.per_stage + i) * x_bytes;
+            if (p.g.w_mn) {
+              tma_load_3d_hint(wdst, &maps.w, &full_bar[stage], n0, k0, f.g, pol_w);
+              tma_load_3d_hint(wdst + Cfg::HALF_BYTES, &maps.w, &full_bar[stage], n0 + 64, k0, f.g, pol_w);
+            } else {
+              tma_load_3d_hint(wdst, &maps.w, &full_bar[stage], k0, n0, f.g, pol_w);
+            }
+            grp_token_boxes(width, [&](int b, int at) {
+              tma_load_2d_hint(xdst + at * 128, &maps.x[b], &full_bar[stage], k0, f.tok0 + at, pol_x);
+            });
           }
-          grp_token_boxes(width, [&](int b, int at) {
-            tma_load_2d_hint(xdst + at * 128, &maps.x[b], &full_bar[stage], k0, f.tok0 + at, pol_x);
-          });
         }
         used |= 1u << stage;
         parities = (parities & ~(1u << stage)) | phase << stage;
@@ -195,17 +217,21 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       if (!mbar_wait_warp(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb3)) break;
       tcgen05_fence_after_sync();
       const uint32_t d_tmem = tmem + acc * p.tokens;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; kb += p.per_stage) {
         if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.g.wait_budget_ns, 0xb4)) {
           ok = false;
           break;
         }
         tcgen05_fence_after_sync();
-        const uint64_t w_desc = w_desc0 + stage * (Cfg::W_BYTES / 16), x_desc = x_desc0 + stage * (x_bytes / 16);
+        const int n = min(p.per_stage, kb_hi - kb);
+        const uint64_t w_desc = w_desc0 + stage * p.per_stage * (Cfg::W_BYTES / 16);
+        const uint64_t x_desc = x_desc0 + stage * p.per_stage * (x_bytes / 16);
         if (one) {
+          for (int i = 0; i < n; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f16_ss(d_tmem, w_desc + k * w_step, x_desc + k * 2, idesc, kb > kb_lo || k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ss(d_tmem, w_desc + i * (Cfg::W_BYTES / 16) + k * w_step, x_desc + i * (x_bytes / 16) + k * 2, idesc,
+                          kb > kb_lo || i > 0 || k > 0 ? 1u : 0u);
           umma_commit(&empty_bar[stage]);
         }
         if (++stage == p.stages) {
@@ -223,6 +249,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     __syncwarp();
   } else {
     const int quad = warp & 3;
+    uint8_t* tbuf = reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + quad * kLoraTBytes;
     const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
     const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
     const int pitch = p.tokens + 4;
@@ -236,7 +263,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     for (int t = cluster_id; t < num_tiles; t += num_clusters) {
       const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
       const int n0 = f.col_blk * Cfg::PANEL + rank * own;
-      const int items = own * ((f.cnt + 3) / 4);  // (column, four tokens)
+      const int items = own * ((f.cnt + 7) / 8);  // (column, eight tokens)
       if (f.g == p.g.groups) {
         const unsigned short zero = 0;
         for (int it = e; it < own * f.cnt; it += 128)
@@ -245,14 +272,17 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
         continue;
       }
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-      if (LORA && early && !waited) {
-        // The adapters' rows that this tile's results need come into L2 meanwhile.
+      GrpTileAdapters adapters;
+      if (LORA && early) {
+        adapters.load(p.g.lora, f.tok0, f.cnt, lane);
+        // Their rows that this tile's results need come into L2 meanwhile.
         for (int it = e; it < own * f.cnt; it += 128) {
-          const int n = n0 + it % own, a = __ldg(p.g.lora.index + f.tok0 + it / own);
-          if (a < 0 || a >= p.g.lora.adapters || n >= p.g.out) continue;
+          const int n = n0 + it % own, a = adapters.of(it / own);
+          if (a < 0 || n >= p.g.out) continue;
           const unsigned short* row = static_cast<const unsigned short*>(p.g.lora.b) + a * p.g.lora.stride_b + n * p.g.lora.ldb;
           for (int at = 0; at < p.g.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
         }
+        __syncwarp();
       }
       const int acc = local & 1;
       bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb6);
@@ -269,14 +299,16 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * p.tokens + c, r);
         tmem_ld_wait();
+        if (p.splits > 1) {
 #pragma unroll
-        for (int q = 0; q < 16; q += 4) {
-          if (p.splits > 1) {
-            st_cluster_v4(to + (c + q) * 4, r[q], r[q + 1], r[q + 2], r[q + 3]);
-          } else if (n0 + sent < p.g.out) {
-            const float4 sum = make_float4(__uint_as_float(r[q]), __uint_as_float(r[q + 1]), __uint_as_float(r[q + 2]),
-                                           __uint_as_float(r[q + 3]));
-            grp_narrow_finish<LORA>(p.g, sum, f.tok0 + c + q, f.cnt - c - q, n0 + sent, early);
+          for (int q = 0; q < 16; q += 4) st_cluster_v4(to + (c + q) * 4, r[q], r[q + 1], r[q + 2], r[q + 3]);
+        } else {
+#pragma unroll
+          for (int h = 0; h < 16; h += 8) {
+            float v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[h + q]);
+            if (c + h < f.cnt) grp_narrow_finish<LORA>(p.g, v, f, c + h, n0 + sent, adapters, early, tbuf, lane);
           }
         }
       }
@@ -295,18 +327,21 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       }
       ready = mbar_wait_cluster(part_full_bar, (local - 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb8);
       if (!__all_sync(0xffffffffu, ready)) break;
-      for (int it = e; it < items; it += 128) {
-        const int col = it % own, tok = it / own * 4;
+      for (int it = e; it < items; it += 128) {  // whole warps: own is a multiple of 32
+        const int col = it % own, tok = it / own * 8;
         const float* at = recv + col * pitch + tok;
-        float4 s = *reinterpret_cast<const float4*>(at);
-        for (int q = 1; q < p.splits; ++q) {
-          const float4 x = *reinterpret_cast<const float4*>(at + q * own * pitch);
-          s.x += x.x;
-          s.y += x.y;
-          s.z += x.z;
-          s.w += x.w;
+        float v[8];
+        for (int q = 0; q < p.splits; ++q) {
+#pragma unroll
+          for (int h = 0; h < 8; h += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(at + q * own * pitch + h);
+            v[h] = q == 0 ? x.x : v[h] + x.x;
+            v[h + 1] = q == 0 ? x.y : v[h + 1] + x.y;
+            v[h + 2] = q == 0 ? x.z : v[h + 2] + x.z;
+            v[h + 3] = q == 0 ? x.w : v[h + 3] + x.w;
+          }
         }
-        if (n0 + col < p.g.out) grp_narrow_finish<LORA>(p.g, s, f.tok0 + tok, f.cnt - tok, n0 + col, early);
+        grp_narrow_finish<LORA>(p.g, v, f, tok, n0 + col, adapters, early, tbuf, lane);
       }
       __syncwarp();
       // Relaxed: the values read have been used, and nothing else is ordered.

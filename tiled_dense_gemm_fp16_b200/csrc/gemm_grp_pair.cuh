@@ -87,41 +87,67 @@ __device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraR
   return true;
 }
 
-// v[q] += sum_j B_a[n][j] T[m][j] in fp32 for tokens m = m0 + q, q < count, each with its adapter a, and column n.  The loads
-// of four tokens are in flight together.
-__device__ __forceinline__ void lora_add4(const LoraParams& l, float (&v)[4], int m0, int count, int n, bool bf16) {
-  int a[4];
+// v[q] += sum_j B_a[n][j] T[m][j] in fp32 for 8 tokens m = m0 + q, each with its adapter a[q] (negative: none), and this
+// lane's column n.  By a whole warp with the same tokens: T comes by way of `tbuf` (512 bytes of shared memory), 32 ranks at a
+// time, and B's rows from L2 with 16 loads of a lane in flight.
+constexpr int kLoraTokens = 8;
+constexpr int kLoraTBytes = kLoraTokens * 32 * 2;
+__device__ __forceinline__ void lora_add(const LoraParams& l, float (&v)[kLoraTokens], const int (&a)[kLoraTokens], int m0, int n,
+                                         bool column, uint8_t* tbuf, int lane, bool bf16) {
+  bool any = false;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    a[q] = q < count ? __ldg(l.index + m0 + q) : -1;
-    if (a[q] >= l.adapters) a[q] = -1;
-  }
-  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0) * l.rank;
+  for (int q = 0; q < kLoraTokens; ++q) any = any || a[q] >= 0;
+  if (!any) return;
   const unsigned short* b = static_cast<const unsigned short*>(l.b) + n * l.ldb;
-  float2 s[4];
+  // Lane i fetches 8 ranks of token i / 4.
+  int ta = -1;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) s[q] = make_float2(0.0f, 0.0f);
-  for (int j = 0; j < l.rank; j += 8) {
-    uint4 x[4], y[4];
+  for (int q = 0; q < kLoraTokens; ++q) ta = (lane >> 2) == q ? a[q] : ta;
+  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0 + (lane >> 2)) * l.rank + (lane & 3) * 8;
+  float2 s[kLoraTokens];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      x[q] = y[q] = make_uint4(0u, 0u, 0u, 0u);
-      if (a[q] >= 0) {
-        x[q] = __ldg(reinterpret_cast<const uint4*>(b + a[q] * l.stride_b + j));
-        y[q] = ld_global_v4(t + q * l.rank + j);
+  for (int q = 0; q < kLoraTokens; ++q) s[q] = make_float2(0.0f, 0.0f);
+  for (int j = 0; j < l.rank; j += 32) {
+    uint4 tv = make_uint4(0u, 0u, 0u, 0u);
+    if (ta >= 0 && j + (lane & 3) * 8 < l.rank) tv = ld_global_v4(t + j);
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      if (j + h >= l.rank) break;
+      uint4 x[kLoraTokens][2];
+#pragma unroll
+      for (int q = 0; q < kLoraTokens; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          x[q][i] = make_uint4(0u, 0u, 0u, 0u);
+          if (column && a[q] >= 0 && j + h + 8 * i < l.rank)
+            x[q][i] = __ldg(reinterpret_cast<const uint4*>(b + a[q] * l.stride_b + j + h + 8 * i));
+        }
+      if (h == 0) {
+        __syncwarp();  // the ranks before have been read
+        *reinterpret_cast<uint4*>(tbuf + lane * 16) = tv;
+        __syncwarp();
       }
-    }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      s[q] = fma2(unpack_16(x[q].x, bf16), unpack_16(y[q].x, bf16), s[q]);
-      s[q] = fma2(unpack_16(x[q].y, bf16), unpack_16(y[q].y, bf16), s[q]);
-      s[q] = fma2(unpack_16(x[q].z, bf16), unpack_16(y[q].z, bf16), s[q]);
-      s[q] = fma2(unpack_16(x[q].w, bf16), unpack_16(y[q].w, bf16), s[q]);
+      for (int q = 0; q < kLoraTokens; ++q)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint4 y = *reinterpret_cast<const uint4*>(tbuf + q * 64 + (h / 8 + i) * 16);
+          s[q] = fma2(unpack_16(x[q][i].x, bf16), unpack_16(y.x, bf16), s[q]);
+          s[q] = fma2(unpack_16(x[q][i].y, bf16), unpack_16(y.y, bf16), s[q]);
+          s[q] = fma2(unpack_16(x[q][i].z, bf16), unpack_16(y.z, bf16), s[q]);
+          s[q] = fma2(unpack_16(x[q][i].w, bf16), unpack_16(y.w, bf16), s[q]);
+        }
     }
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < kLoraTokens; ++q)
     if (a[q] >= 0) v[q] += s[q].x + s[q].y;
+}
+
+// A token's adapter, or -1.
+__device__ __forceinline__ int lora_adapter(const LoraParams& l, int m) {
+  const int a = __ldg(l.index + m);
+  return a >= 0 && a < l.adapters ? a : -1;
 }
 
 struct GrpPairCfg {
@@ -203,12 +229,16 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&maps.w);
-    tma_prefetch_desc(&maps.x[3]);
+    for (int b = 0; b < 4; ++b) tma_prefetch_desc(&maps.x[b]);
   }
   if (warp == Cfg::MMA_WARP) {
     tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish_alloc_permit_pair();
   }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote use
+  tcgen05_fence_after_sync();
   // Adapters: the kernel before this one on the stream makes T.  It waited for
   // what came before it and then let this one start, so X, W, index and the
   // workspace's copies are there already; only T and kind are waited for, by
@@ -220,10 +250,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   }
   if (warp == Cfg::EPI_WARP0)
     grp_make_plan(plan, p.ends, p.groups, p.M, Cfg::TOKENS, p.col_tiles, p.rest != 0, lane);
-  tcgen05_fence_before_sync();
   __syncthreads();
-  cluster_sync();  // both CTAs' barriers are initialised before any remote use
-  tcgen05_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
   const int num_tiles = plan.first[p.groups + 1];
 
@@ -410,6 +437,21 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM + quad * 32;
       const bool zero = f.g == p.groups;
       const int acc = local & 1;
+      if (early) {
+        // The rows of B that the epilogue will read come into L2 while the tile is computed.
+        for (int b = part; b * 32 < f.cnt && n0 < p.out; b += Cfg::EPI_WARPS / 4) {
+          const int mine = b * 32 + lane < f.cnt ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
+          const int first = __shfl_sync(0xffffffffu, mine, 0);
+          if (__all_sync(0xffffffffu, mine == first || b * 32 + lane >= f.cnt)) continue;
+          for (int e = 0; e < 32; ++e) {
+            const int a = __shfl_sync(0xffffffffu, mine, e);
+            if (a < 0 || n0 + lane >= p.out) continue;
+            const unsigned short* row = static_cast<const unsigned short*>(p.lora.b) + a * p.lora.stride_b + (n0 + lane) * p.lora.ldb;
+            for (int at = 0; at < p.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+          }
+        }
+        __syncwarp();
+      }
       if (!zero) {
         const bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.wait_budget_ns, 0xa6);
         if (!__all_sync(0xffffffffu, ready)) break;
@@ -430,17 +472,20 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         if (LORA) {
           const int n = n0 + lane;
           if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
-            if (n < p.out) {
+            const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
+            __syncwarp();  // the box before has left: T takes its place for a while
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                if (e >= rows) break;
-                float v[4];
+            for (int e = 0; e < 32; e += kLoraTokens) {
+              float v[kLoraTokens];
+              int a[kLoraTokens];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) v[q] = __uint_as_float(r[e + q]);
-                lora_add4(p.lora, v, f.tok0 + b * 32 + e, rows - e, n, bf16);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) r[e + q] = __float_as_uint(v[q]);
+              for (int q = 0; q < kLoraTokens; ++q) {
+                v[q] = __uint_as_float(r[e + q]);
+                a[q] = __shfl_sync(0xffffffffu, mine, e + q);
               }
+              lora_add(p.lora, v, a, f.tok0 + b * 32 + e, n, n < p.out, box, lane, bf16);
+#pragma unroll
+              for (int q = 0; q < kLoraTokens; ++q) r[e + q] = __float_as_uint(v[q]);
             }
           }
           if (p.lora.bias != nullptr && n < p.out) {
@@ -449,14 +494,21 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
             for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + bias);
           }
         }
-        __syncwarp();  // the box before has left
+        unsigned short* c = static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32) * p.ldc + n0;
+        if (p.vec) {
+          __syncwarp();  // the box before has left
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
-              round_16(__uint_as_float(r[e]), bf16);
-        __syncwarp();
-        grp_store_box(static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32) * p.ldc + n0, p.ldc, rows,
-                      min(32, p.out - n0), p.vec != 0, box, lane);
+          for (int e = 0; e < 32; ++e)
+            *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
+                round_16(__uint_as_float(r[e]), bf16);
+          __syncwarp();
+          grp_store_box(c, p.ldc, rows, min(32, p.out - n0), box, lane);
+        } else if (n0 + lane < p.out) {  // rows off 16 bytes: a warp's 32 columns of a token, 64 bytes a store
+          c += lane;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e < rows) c[e * p.ldc] = round_16(__uint_as_float(r[e]), bf16);
+        }
       }
       if (!zero) {
         tcgen05_fence_before_sync();

@@ -69,8 +69,8 @@ __device__ __forceinline__ GrpWgradTile grp_wgrad_tile(const GrpWgradParams& p, 
   const int in = local - s * 8 * p.k_tiles;
   f.k_blk = in / wide;
   f.n_blk = 8 * s + in - f.k_blk * wide;
-  f.lo = ends[f.g];
-  f.rows = max(0, ends[f.g + 1] - f.lo);
+  f.lo = uniform(ends[f.g]);
+  f.rows = max(0, uniform(ends[f.g + 1]) - f.lo);
   return f;
 }
 
@@ -120,34 +120,34 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
     tmem_relinquish_alloc_permit_pair();
   }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised before any remote use
+  tcgen05_fence_after_sync();
   grid_dependency_wait();
   grid_launch_dependents();
   for (int g = threadIdx.x; g <= p.groups; g += Cfg::THREADS) ends[g] = grp_end(p.ends, g - 1, p.M);
-  tcgen05_fence_before_sync();
   __syncthreads();
-  cluster_sync();
-  tcgen05_fence_after_sync();
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      int last_parity[Cfg::STAGES];
-#pragma unroll
-      for (int s = 0; s < Cfg::STAGES; ++s) last_parity[s] = -1;
-      bool ok = true;
-      const uint64_t pol = l2_policy_evict_normal();
-      const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
-      for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
-        const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
-        const int n0 = f.n_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
-        const int k0 = f.k_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
-        for (int r = 0; r < f.rows; r += 64) {
-          if (!mbar_wait(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xc1)) {
-            ok = false;
-            break;
-          }
+    // As in gemm_grp_pair.cuh: the warp loops, one lane issues.
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0, used = 0, parities = 0;
+    bool ok = true;
+    const uint64_t pol = l2_policy_evict_normal();
+    const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
+    for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
+      const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
+      const int n0 = f.n_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
+      const int k0 = f.k_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
+      for (int r = 0; r < f.rows; r += 64) {
+        if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xc1)) {
+          ok = false;
+          break;
+        }
+        if (one) {
           uint8_t* adst = a_smem + stage * Cfg::A_BYTES;
           uint8_t* bdst = b_smem + stage * Cfg::B_BYTES;
           const int y = f.lo + r;
@@ -168,63 +168,68 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
             tma_load_2d_hint(bdst, &maps.x, &tail_bar[stage], k0, y, pol);
             tma_load_2d_hint(bdst + Cfg::PANEL_BYTES, &maps.x, &tail_bar[stage], k0 + 64, y, pol);
           }
-          last_parity[stage] = static_cast<int>(phase);
-          if (++stage == Cfg::STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+        }
+        used |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | phase << stage;
+        if (++stage == Cfg::STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // The even CTA's full barriers count both CTAs' bytes, or both zeroing warps.
-      if (leader) {
-#pragma unroll 1
-        for (int s = 0; s < Cfg::STAGES; ++s) {
-          if (last_parity[s] >= 0) {
-            volatile int no_abort = 0;
-            mbar_wait(&full_bar[s], static_cast<uint32_t>(last_parity[s]), &no_abort, p.wait_budget_ns, 0xc2);
-          }
+    }
+    // The even CTA's full barriers count both CTAs' bytes, or both zeroing warps.
+    if (leader) {
+      for (int s = 0; s < Cfg::STAGES; ++s) {
+        if (used >> s & 1u) {
+          volatile int no_abort = 0;
+          mbar_wait(&full_bar[s], parities >> s & 1u, &no_abort, p.wait_budget_ns, 0xc2);
         }
       }
     }
   } else if (warp == Cfg::MMA_WARP) {
-    if (leader && lane == 0) {
+    if (leader) {
+      const bool one = elect_one();
       int stage = 0;
       uint32_t phase = 0;
       int local = 0;
       bool ok = true;
       const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), Cfg::PANEL_BYTES, 1024);
       const uint64_t b_desc0 = make_sw128_desc(smem_u32(b_smem), Cfg::PANEL_BYTES, 1024);
+      const uint32_t tmem = uniform(tmem_base);
       for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
         const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
         if (f.rows == 0) continue;
         const int acc = local & 1;
-        if (!mbar_wait(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xc3)) break;
+        if (!mbar_wait_warp(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xc3)) break;
         tcgen05_fence_after_sync();
-        const uint32_t d_tmem = tmem_base + acc * Cfg::TILE;
+        const uint32_t d_tmem = tmem + acc * Cfg::TILE;
         for (int r = 0; r < f.rows; r += 64) {
           // Acquire at cluster scope: the other CTA's zeroing warp may have arrived.
-          if (!mbar_wait_cluster(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xc4)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_cluster(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xc4))) {
             ok = false;
             break;
           }
           tcgen05_fence_after_sync();
           const uint64_t a_desc = a_desc0 + stage * (Cfg::A_BYTES / 16), b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16);
           const int steps = (min(64, f.rows - r) + 15) / 16;
+          if (one) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              umma_f16_ss_pair(d_tmem, a_desc + k * (2048 / 16), b_desc + k * (2048 / 16), p.idesc, (r | k) != 0 ? 1u : 0u);
-          umma_commit_pair_mc(&empty_bar[stage], 0x3);
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                umma_f16_ss_pair(d_tmem, a_desc + k * (2048 / 16), b_desc + k * (2048 / 16), p.idesc, (r | k) != 0 ? 1u : 0u);
+            umma_commit_pair_mc(&empty_bar[stage], 0x3);
+          }
           if (++stage == Cfg::STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
         if (!ok) break;
-        umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
+        if (one) umma_commit_pair_mc(&acc_full_bar[acc], 0x3);
         ++local;
       }
-      umma_commit_pair_mc(mma_done_bar, 0x1);
+      if (one) umma_commit_pair_mc(mma_done_bar, 0x1);
+      __syncwarp();
       volatile int no_abort = 0;
       mbar_wait(mma_done_bar, 0, &no_abort, p.wait_budget_ns, 0xc5);
     }
@@ -295,7 +300,11 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
         for (int q = 0; q < 4; ++q)
           *reinterpret_cast<uint4*>(box + grp_box_at(lane, q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
         __syncwarp();
-        grp_store_box(dst + k0, p.ldc, min(32, p.N - n0), min(32, p.K - k0), p.vec != 0, box, lane);
+        const int rows = min(32, p.N - n0), cols = min(32, p.K - k0);
+        if (p.vec)
+          grp_store_box(dst + k0, p.ldc, rows, cols, box, lane);
+        else
+          grp_store_box_any(dst + k0, p.ldc, rows, cols, box, lane);
       }
       if (!zero) {
         tcgen05_fence_before_sync();

@@ -104,11 +104,11 @@ struct GrpProduct {
   FfMat t;
 };
 
-bool grp_fill(const GrpProduct& f, GrpMaps& maps, GrpParams& p, int weight_rows) {
+bool grp_fill(const GrpProduct& f, GrpMaps& maps, GrpParams& p, int weight_rows, int tokens) {
   std::memset(&maps, 0, sizeof maps);
   std::memset(&p, 0, sizeof p);
   if (!grp_encode3(&maps.w, f.w, 64, f.transposed ? 64 : 128)) return false;
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4 && 16 << i <= tokens; ++i)
     if (!ff_encode(&maps.x[i], f.a, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return false;
   if (f.lora) {
     p.lora = f.l;
@@ -145,7 +145,7 @@ tg_status launch_grp_pair(const GrpProduct& f, cudaStream_t stream, DeviceInfo* 
     return TG_ERR_LAUNCH;
   GrpMaps maps;
   GrpParams p;
-  if (!grp_fill(f, maps, p, Cfg::PAIR_M)) return TG_ERR_LAUNCH;
+  if (!grp_fill(f, maps, p, Cfg::PAIR_M, Cfg::TOKENS / 2)) return TG_ERR_LAUNCH;
   p.vec = f.c.rows_on(16) ? 1 : 0;
   p.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PAIR_M, 0, f.transposed, false);
   p.super = tune_int("TG_TUNE_GRP_SUPER", 8);
@@ -176,7 +176,7 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
     std::memset(&cfg, 0, sizeof cfg);
     cfg.gridDim = dim3(static_cast<unsigned>(splits) * 1024, 1, 1);
     cfg.blockDim = dim3(GrpNarrowCfg::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(GrpNarrowCfg::smem_bytes(128, GrpNarrowCfg::stages(128, 1), 1));
+    cfg.dynamicSmemBytes = static_cast<size_t>(GrpNarrowCfg::smem_bytes(128, 4, 1));
     LaunchAttrs la;
     la.fill(cfg, static_cast<unsigned>(splits));
     int n = 0;
@@ -198,17 +198,20 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   GrpMaps maps;
   GrpNarrowParams p;
   std::memset(&p, 0, sizeof p);
-  if (!grp_fill(f, maps, p.g, Cfg::PANEL)) return TG_ERR_LAUNCH;
+  if (!grp_fill(f, maps, p.g, Cfg::PANEL, tokens)) return TG_ERR_LAUNCH;
   p.g.vec = f.c.rows_on(8) ? 1 : 0;
   p.g.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PANEL, 0, f.transposed, false);
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
-  p.stages = Cfg::stages(tokens, f.groups);
-  // Beside the kernel that makes T, which is still at work (launch_lora_shrink).
-  const int room = 232448 - 100 * 1024 - Cfg::smem_bytes(tokens, 0, f.groups);
-  if (f.lora && f.l.adapters > 0 && p.stages > room / (Cfg::W_BYTES + tokens * 128) && room / (Cfg::W_BYTES + tokens * 128) >= 3)
-    p.stages = room / (Cfg::W_BYTES + tokens * 128);
+  // As deep as fits a CTA an SM, or (adapters) beside the kernel that makes T, which is still at work.
+  const int stage_bytes = Cfg::W_BYTES + tokens * 128, left = 232448 - Cfg::smem_bytes(tokens, 0, f.groups);
+  int deepest = left / stage_bytes;
+  if (f.lora && f.l.adapters > 0 && (left - 100 * 1024) / stage_bytes >= 3) deepest = (left - 100 * 1024) / stage_bytes;
+  p.per_stage = tune_int("TG_TUNE_GRP_PER", 2);
+  while (p.per_stage > 1 && deepest < 3 * p.per_stage) p.per_stage >>= 1;
+  p.stages = deepest / p.per_stage;
+  if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
   p.tmem_cols = static_cast<uint32_t>(2 * tokens);
   int splits = tune_int("TG_TUNE_GRP_SPLITS", 2);
   while (splits > p.g.k_blocks) splits >>= 1;
@@ -219,7 +222,7 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(splits * clusters), 1, 1);
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(tokens, p.stages, f.groups));
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(tokens, p.stages * p.per_stage, f.groups));
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, static_cast<unsigned>(splits));
@@ -504,8 +507,6 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   std::memset(&p, 0, sizeof p);
   p.a_rows = static_cast<int>(l.rank < 128 ? l.rank : 128);
   if (!grp_encode3(&maps.a, l.a, 64, p.a_rows)) return TG_ERR_LAUNCH;
-  for (int i = 0; i < 4; ++i)
-    if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   p.index = f.l.index;
   p.scale = scale;
   p.t = const_cast<void*>(f.l.t);
@@ -516,6 +517,8 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.k_blocks = static_cast<int>((l.K + 63) / 64);
   p.tokens = 16;
   while (p.tokens < 128 && p.tokens < l.M) p.tokens <<= 1;
+  for (int i = 0; i < 4 && 16 << i <= p.tokens; ++i)
+    if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
   const int64_t deep = (l.rank + 127) / 128;
   p.splits = 1;
@@ -526,8 +529,11 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   const int64_t items = l.M < p.tokens ? l.M : p.tokens;
   y = y < 1 ? 1 : y > items ? items : y;
   y = y > l.adapters ? l.adapters : y;
-  const int budget = l.M <= 128 ? 96 * 1024 : 200 * 1024;
-  p.stages = (budget - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  const int budget = 96 * 1024;
+  const int deepest = (budget - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  p.per_stage = tune_int("TG_TUNE_SHRINK_PER", 2);
+  while (p.per_stage > 1 && deepest < 4 * p.per_stage) p.per_stage >>= 1;
+  p.stages = deepest / p.per_stage;
   if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
   if (p.stages < 2) p.stages = 2;
   p.bf16 = l.bf16 ? 1 : 0;
@@ -538,7 +544,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(blocks * p.splits), static_cast<unsigned>(y), static_cast<unsigned>(deep));
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(p.tokens, p.splits, p.a_rows, p.stages));
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(p.tokens, p.splits, p.a_rows, p.stages * p.per_stage));
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, static_cast<unsigned>(p.splits));

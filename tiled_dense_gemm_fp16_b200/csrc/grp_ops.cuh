@@ -82,7 +82,7 @@ struct GrpCut {
 };
 __device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
   GrpCut c;
-  c.tiles = (rows + most - 1) / most;
+  c.tiles = (rows + most - 1) / most;  // `most` and `unit` are powers of two
   c.whole = c.tiles - 1;
   c.width = 0;
   const int last = rows - c.whole * most;
@@ -105,7 +105,8 @@ struct GrpPlan {
   int* first;  // G + 2 numbers of tiles before the group, in tiles of the whole result
 };
 
-constexpr int grp_plan_bytes(int groups) { return (groups + 2) * 8; }
+__host__ __device__ constexpr int grp_plan_bytes(int groups) { return (groups + 2) * 8; }
+__host__ __device__ constexpr int grp_plan_align(int groups) { return (grp_plan_bytes(groups) + 15) / 16 * 16; }
 
 // By one warp; the others wait for it.
 __device__ __forceinline__ void grp_make_plan(GrpPlan plan, const int* ends, int G, int M, int most, int col_tiles,
@@ -156,11 +157,16 @@ struct GrpWalk {
     const int lo = plan.lo[g], rows = plan.lo[g + 1] - lo;
     const GrpCut cut = grp_cut(rows, most, unit);
     const int local = t - plan.first[g];
-    const int s = local / (super * col_tiles);
-    const int wide = min(super, cut.tiles - s * super);
-    const int in = local - s * super * col_tiles;
-    f.col_blk = in / wide;
-    grp_cut_tile(cut, rows, most, s * super + in - f.col_blk * wide, f.tok0, f.cnt);
+    int i = 0;
+    f.col_blk = local;
+    if (cut.tiles > 1) {  // divisions only where there is something to divide
+      const int s = cut.tiles > super ? local / (super * col_tiles) : 0;
+      const int wide = min(super, cut.tiles - s * super);
+      const int in = local - s * super * col_tiles;
+      f.col_blk = in / wide;
+      i = s * super + in - f.col_blk * wide;
+    }
+    grp_cut_tile(cut, rows, most, i, f.tok0, f.cnt);
     f.tok0 += lo;
     f.g = uniform(f.g);
     f.tok0 = uniform(f.tok0);
@@ -180,37 +186,36 @@ __device__ __forceinline__ uint32_t grp_box_at(int row, int piece) {
   return static_cast<uint32_t>(row * 64 + ((piece ^ ((row >> 1) & 3)) << 4));
 }
 
-// The box's first `rows` rows and `cols` columns to `c`.  vec: rows of the result
-// start on 16-byte boundaries (and c's column is a multiple of 8): 16 bytes a
-// lane, 8 rows a store.  Else value by value, a row a store.
-__device__ __forceinline__ void grp_store_box(unsigned short* c, int64_t ld, int rows, int cols, bool vec,
-                                              const uint8_t* box, int lane) {
-  if (vec) {
-    const int piece = lane & 3;
-    const int n = cols - piece * 8;
+// The box's first `rows` rows and `cols` columns to `c`, whose rows start on
+// 16-byte boundaries (and c's column is a multiple of 8): 16 bytes a lane, 8 rows a
+// store.
+__device__ __forceinline__ void grp_store_box(unsigned short* c, int64_t ld, int rows, int cols, const uint8_t* box, int lane) {
+  const int piece = lane & 3;
+  const int n = cols - piece * 8;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = i * 8 + (lane >> 2);
-      if (r >= rows || n <= 0) continue;
-      const uint4 v = *reinterpret_cast<const uint4*>(box + grp_box_at(r, piece));
-      unsigned short* dst = c + r * ld + piece * 8;
-      if (n >= 8) {
-        *reinterpret_cast<uint4*>(dst) = v;
-      } else {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    if (r >= rows || n <= 0) continue;
+    const uint4 v = *reinterpret_cast<const uint4*>(box + grp_box_at(r, piece));
+    unsigned short* dst = c + r * ld + piece * 8;
+    if (n >= 8) {
+      *reinterpret_cast<uint4*>(dst) = v;
+    } else {
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 7; ++e)
-          if (e < n) dst[e] = static_cast<unsigned short>(w[e >> 1] >> ((e & 1) * 16));
-      }
-    }
-  } else if (lane < cols) {
-    unsigned short* dst = c + lane;
-#pragma unroll 4
-    for (int r = 0; r < 32; ++r) {
-      if (r >= rows) break;
-      dst[r * ld] = *reinterpret_cast<const unsigned short*>(box + grp_box_at(r, lane >> 3) + (lane & 7) * 2);
+      for (int e = 0; e < 7; ++e)
+        if (e < n) dst[e] = static_cast<unsigned short>(w[e >> 1] >> ((e & 1) * 16));
     }
   }
+}
+
+// The same for rows that start anywhere: a row a store, value by value.
+__device__ __forceinline__ void grp_store_box_any(unsigned short* c, int64_t ld, int rows, int cols, const uint8_t* box, int lane) {
+  if (lane >= cols) return;
+  unsigned short* dst = c + lane;
+#pragma unroll 8
+  for (int r = 0; r < 32; ++r)
+    if (r < rows) dst[r * ld] = *reinterpret_cast<const unsigned short*>(box + grp_box_at(r, lane >> 3) + (lane & 7) * 2);
 }
 
 }  // namespace tg

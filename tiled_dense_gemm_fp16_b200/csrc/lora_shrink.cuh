@@ -32,6 +32,7 @@ struct LoraShrinkParams {
   int* kind;
   int M, rank, adapters;
   int k_blocks, splits, stages;
+  int per_stage;       // k-blocks of a stage of the ring
   int tokens;          // most of an item, and rows of a block: 16, 32, 64 or 128
   int a_rows;          // of a box: min(128, rank)
   int bf16;
@@ -71,8 +72,8 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t a_bytes = p.a_rows * 128, x_bytes = p.tokens * 128;
   uint8_t* a_smem = smem;
-  uint8_t* x_smem = smem + p.stages * a_bytes;
-  float4* recv = reinterpret_cast<float4*>(smem + p.stages * (a_bytes + x_bytes));
+  uint8_t* x_smem = smem + p.stages * p.per_stage * a_bytes;
+  float4* recv = reinterpret_cast<float4*>(smem + p.stages * p.per_stage * (a_bytes + x_bytes));
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(recv) + Cfg::recv_bytes(p.tokens, p.splits, p.a_rows));
   uint64_t* full_bar = bars;
   uint64_t* empty_bar = bars + Cfg::MAX_STAGES;
@@ -84,9 +85,33 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full_bar[s], 1);
+      mbar_init(&empty_bar[s], 1);
+    }
+    mbar_init(acc_full_bar, 1);
+    mbar_init(acc_empty_bar, 4);
+    mbar_init(part_full_bar, 4 * p.splits);
+    mbar_init(part_empty_bar, 4 * p.splits);
+    mbar_init(mma_done_bar, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&maps.a);
+    for (int b = 0; b < 4 && 16 << b <= p.tokens; ++b) tma_prefetch_desc(&maps.x[b]);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, p.tmem_cols);
+    tmem_relinquish_alloc_permit();
+  }
+  tcgen05_fence_before_sync();
+  __syncthreads();
+  cluster_sync();
+  tcgen05_fence_after_sync();
+  const uint32_t tmem_base = *tmem_slot;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   const int m0 = static_cast<int>(blockIdx.x / p.splits) * p.tokens;
   const int j0 = static_cast<int>(blockIdx.z) * 128;
@@ -140,30 +165,7 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
     if (tok == 0) items.count = firsts[0] + firsts[1] + firsts[2] + firsts[3];
   }
   __syncthreads();
-  const int count = items.count, step = static_cast<int>(gridDim.y);
-  if (static_cast<int>(blockIdx.y) >= count) return;  // nothing for this cluster: the same in all of its CTAs
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full_bar[s], 1);
-      mbar_init(&empty_bar[s], 1);
-    }
-    mbar_init(acc_full_bar, 1);
-    mbar_init(acc_empty_bar, 4);
-    mbar_init(part_full_bar, 4 * p.splits);
-    mbar_init(part_empty_bar, 4 * p.splits);
-    mbar_init(mma_done_bar, 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-  }
-  if (warp == 1) {
-    tmem_alloc(tmem_slot, p.tmem_cols);
-    tmem_relinquish_alloc_permit();
-  }
-  tcgen05_fence_before_sync();
-  __syncthreads();
-  cluster_sync();
-  tcgen05_fence_after_sync();
-  const uint32_t tmem_base = *tmem_slot;
+  const int count = items.count, step = static_cast<int>(gridDim.y);  // clusters without an item only take leave
   const int kb_lo = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
   const int kb_hi = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
 
@@ -177,17 +179,21 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
     for (int d = blockIdx.y; ok && d < count; d += step) {
       const int adapter = uniform(items.adapter[d]), t0 = uniform(items.first[d] & ~15);
       const int width = uniform((items.last[d] & ~15) + 16) - t0;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; kb += p.per_stage) {
         if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xd1)) {
           ok = false;
           break;
         }
         if (one) {
-          mbar_arrive_expect_tx(&full_bar[stage], (p.a_rows + width) * 128);
-          tma_load_3d_hint(a_smem + stage * a_bytes, &maps.a, &full_bar[stage], kb * 64, j0, adapter, pol_a);
-          grp_token_boxes(width, [&](int b, int at) {
-            tma_load_2d_hint(x_smem + stage * x_bytes + at * 128, &maps.x[b], &full_bar[stage], kb * 64, m0 + t0 + at, pol_x);
-          });
+          const int n = min(p.per_stage, kb_hi - kb);
+          mbar_arrive_expect_tx(&full_bar[stage], n * (p.a_rows + width) * 128);
+          for (int i = 0; i < n; ++i) {
+            const int at_k = (kb + i) * 64, slot = stage * p.per_stage + i;
+            tma_load_3d_hint(a_smem + slot * a_bytes, &maps.a, &full_bar[stage], at_k, j0, adapter, pol_a);
+            grp_token_boxes(width, [&](int b, int at) {
+              tma_load_2d_hint(x_smem + slot * x_bytes + at * 128, &maps.x[b], &full_bar[stage], at_k, m0 + t0 + at, pol_x);
+            });
+          }
         }
         used |= 1u << stage;
         parities = (parities & ~(1u << stage)) | phase << stage;
@@ -216,17 +222,21 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
       const uint32_t idesc = p.idesc | static_cast<uint32_t>(width >> 3) << 17;
       if (!mbar_wait_warp(acc_empty_bar, (local & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xd3)) break;
       tcgen05_fence_after_sync();
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; kb += p.per_stage) {
         if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xd4)) {
           ok = false;
           break;
         }
         tcgen05_fence_after_sync();
-        const uint64_t a_desc = a_desc0 + stage * (a_bytes / 16), x_desc = x_desc0 + stage * (x_bytes / 16);
+        const int n = min(p.per_stage, kb_hi - kb);
+        const uint64_t a_desc = a_desc0 + stage * p.per_stage * (a_bytes / 16);
+        const uint64_t x_desc = x_desc0 + stage * p.per_stage * (x_bytes / 16);
         if (one) {
+          for (int i = 0; i < n; ++i)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            umma_f16_ss(d_tmem, a_desc + k * 2, x_desc + k * 2, idesc, kb > kb_lo || k > 0 ? 1u : 0u);
+            for (int k = 0; k < 4; ++k)
+              umma_f16_ss(d_tmem, a_desc + i * (a_bytes / 16) + k * 2, x_desc + i * (x_bytes / 16) + k * 2, idesc,
+                          kb > kb_lo || i > 0 || k > 0 ? 1u : 0u);
           umma_commit(&empty_bar[stage]);
         }
         if (++stage == p.stages) {
