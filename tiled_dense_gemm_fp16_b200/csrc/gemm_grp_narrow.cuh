@@ -34,8 +34,13 @@ struct GrpNarrowCfg {
   static constexpr int BAR_BYTES = 256;
   // Partials of a tile: [source][column][tokens + 4], the 4 to spread the columns over the banks.
   __host__ __device__ static constexpr int recv_bytes(int tokens) { return PANEL * (tokens + 4) * 4; }
+  // The adapters' part of this CTA's columns: [column][tokens + 4].
+  static constexpr int delta_bytes(int tokens, int splits) { return PANEL / splits * (tokens + 4) * 4; }
   static constexpr int smem_bytes(int tokens, int stages, int groups) {
-    return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups) + 4 * kLoraTBytes;
+    return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups);
+  }
+  static constexpr int lora_bytes(int tokens, int splits) {
+    return 4 * kLoraTBytes + delta_bytes(tokens, splits);
   }
   static_assert((2 * MAX_STAGES + 7) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
@@ -55,27 +60,21 @@ struct GrpTileAdapters {
   }
 };
 
-// Results of column n and up to eight tokens from `tok` of the tile on, with the adapters' part.  For a whole warp with
-// the same tokens in all lanes.
-template <bool LORA>
-__device__ __forceinline__ void grp_narrow_finish(const GrpParams& p, float (&v)[8], const GrpTile& f, int tok, int n,
-                                                  const GrpTileAdapters& adapters, bool early, uint8_t* tbuf, int lane) {
-  const bool bf16 = p.bf16 != 0;
-  const int m0 = f.tok0 + tok, count = f.cnt - tok;
-  if (LORA && early) {
-    int a[8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) a[q] = adapters.of(tok + q);
-    lora_add(p.lora, v, a, m0, n, n < p.out, tbuf, lane, bf16);
-  }
+// Results of column n and up to eight tokens from `tok` of the tile on; `delta` holds the adapters' part, if there is one.
+__device__ __forceinline__ void grp_narrow_store(const GrpParams& p, float (&v)[8], const GrpTile& f, int tok, int n,
+                                                 const float* delta, float bias) {
   if (n >= p.out) return;
-  const float bias = LORA && p.lora.bias != nullptr ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
+  const bool bf16 = p.bf16 != 0;
+  unsigned short* c = static_cast<unsigned short*>(p.c) + (f.tok0 + tok) * p.ldc + n;
 #pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (q < count) static_cast<unsigned short*>(p.c)[(m0 + q) * p.ldc + n] = round_16(LORA ? v[q] + bias : v[q], bf16);
+  for (int q = 0; q < 8; ++q) {
+    if (delta != nullptr) v[q] += delta[q];
+    if (q < f.cnt - tok) c[q * p.ldc] = round_16(v[q] + bias, bf16);
+  }
 }
 
-template <bool LORA>
+// LORA as in the pair kernel.
+template <int LORA>
 __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     grp_narrow_kernel(const __grid_constant__ GrpMaps maps, const GrpNarrowParams p) {
   using Cfg = GrpNarrowCfg;
@@ -132,7 +131,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
   __syncthreads();
   cluster_sync();  // every CTA's barriers are initialised before any remote use
   tcgen05_fence_after_sync();
-  const bool early = LORA && p.g.lora.adapters > 0;  // as in the pair kernel
+  const bool early = LORA != 0 && p.g.lora.adapters > 0;  // as in the pair kernel
   if (!early) {
     grid_dependency_wait();
     grid_launch_dependents();
@@ -249,11 +248,12 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     __syncwarp();
   } else {
     const int quad = warp & 3;
-    uint8_t* tbuf = reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + quad * kLoraTBytes;
-    const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
+    uint8_t* tbuf = reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + quad * kLoraTBytes;  // adapters only
+    float* delta = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + 4 * kLoraTBytes);
+    const int e = quad * 32 + lane;  // also the column of the panel that this thread sends
     const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
     const int pitch = p.tokens + 4;
-    const int sent = quad * 32 + lane;      // the column that this thread sends
+    const int sent = e;
     const uint32_t owner = sent / own;
     const uint32_t to = mapa_shared(smem_u32(recv) + (rank * own + sent % own) * pitch * 4, owner);
     const uint32_t to_bar = mapa_shared(smem_u32(part_full_bar), owner);
@@ -272,17 +272,37 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
         continue;
       }
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-      GrpTileAdapters adapters;
       if (LORA && early) {
+        // The adapters' part, while the tile is computed: it is this thread's own
+        // until the sums are there.  The first tile's rows of B come into L2 before
+        // T is waited for.
+        GrpTileAdapters adapters;
         adapters.load(p.g.lora, f.tok0, f.cnt, lane);
-        // Their rows that this tile's results need come into L2 meanwhile.
-        for (int it = e; it < own * f.cnt; it += 128) {
-          const int n = n0 + it % own, a = adapters.of(it / own);
-          if (a < 0 || n >= p.g.out) continue;
-          const unsigned short* row = static_cast<const unsigned short*>(p.g.lora.b) + a * p.g.lora.stride_b + n * p.g.lora.ldb;
-          for (int at = 0; at < p.g.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+        if (!waited) {
+          for (int it = e; it < own * f.cnt; it += 128) {
+            const int n = n0 + it % own, a = adapters.of(it / own);
+            if (a < 0 || n >= p.g.out) continue;
+            const unsigned short* row = static_cast<const unsigned short*>(p.g.lora.b) + a * p.g.lora.stride_b + n * p.g.lora.ldb;
+            for (int at = 0; at < p.g.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
+          }
+          __syncwarp();
+          grid_dependency_wait();
+          grid_launch_dependents();
+          waited = true;
         }
-        __syncwarp();
+        for (int it = e; it < items; it += 128) {  // whole warps: own is a multiple of 32
+          const int col = it % own, tok = it / own * 8;
+          int a[kLoraTokens];
+          float d[kLoraTokens];
+#pragma unroll
+          for (int q = 0; q < kLoraTokens; ++q) {
+            a[q] = adapters.of(tok + q);
+            d[q] = 0.0f;
+          }
+          lora_add<LORA == 2>(p.g.lora, d, a, f.tok0 + tok, n0 + col, n0 + col < p.g.out, tbuf, lane);
+#pragma unroll
+          for (int q = 0; q < kLoraTokens; ++q) delta[col * pitch + tok + q] = d[q];
+        }
       }
       const int acc = local & 1;
       bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb6);
@@ -290,11 +310,6 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       if (ready && p.splits > 1) ready = mbar_wait_cluster(part_empty_bar, (local & 1) ^ 1u, abort_flag, p.g.wait_budget_ns, 0xb7);
       if (!__all_sync(0xffffffffu, ready)) break;
       tcgen05_fence_after_sync();
-      if (LORA && early && !waited && p.splits == 1) {
-        grid_dependency_wait();  // T
-        grid_launch_dependents();
-        waited = true;
-      }
       for (int c = 0; c < width; c += 16) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * p.tokens + c, r);
@@ -308,7 +323,10 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[h + q]);
-            if (c + h < f.cnt) grp_narrow_finish<LORA>(p.g, v, f, c + h, n0 + sent, adapters, early, tbuf, lane);
+            grp_narrow_store(p.g, v, f, c + h, n0 + sent, LORA && early ? delta + sent * pitch + c + h : nullptr,
+                             LORA && p.g.lora.bias != nullptr && n0 + sent < p.g.out
+                                 ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + sent, p.g.bf16 != 0)
+                                 : 0.0f);
           }
         }
       }
@@ -320,11 +338,6 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       }
       ++local;
       if (p.splits == 1) continue;
-      if (LORA && early && !waited) {
-        grid_dependency_wait();
-        grid_launch_dependents();
-        waited = true;
-      }
       ready = mbar_wait_cluster(part_full_bar, (local - 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb8);
       if (!__all_sync(0xffffffffu, ready)) break;
       for (int it = e; it < items; it += 128) {  // whole warps: own is a multiple of 32
@@ -341,7 +354,10 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
             v[h + 3] = q == 0 ? x.w : v[h + 3] + x.w;
           }
         }
-        grp_narrow_finish<LORA>(p.g, v, f, tok, n0 + col, adapters, early, tbuf, lane);
+        grp_narrow_store(p.g, v, f, tok, n0 + col, LORA && early ? delta + col * pitch + tok : nullptr,
+                         LORA && p.g.lora.bias != nullptr && n0 + col < p.g.out
+                             ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + col, p.g.bf16 != 0)
+                             : 0.0f);
       }
       __syncwarp();
       // Relaxed: the values read have been used, and nothing else is ordered.

@@ -52,6 +52,7 @@ struct GrpParams {
   int k_blocks;
   int w_mn;                   // the weight is read MN-major (dX)
   int rest;                   // rows behind the last group get zeros
+  int adapt;                  // few tiles: their width is chosen in the kernel
   int vec;                    // rows of the result start on 16-byte boundaries
   int bf16;
   uint32_t idesc;             // without N
@@ -89,11 +90,13 @@ __device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraR
 
 // v[q] += sum_j B_a[n][j] T[m][j] in fp32 for 8 tokens m = m0 + q, each with its adapter a[q] (negative: none), and this
 // lane's column n.  By a whole warp with the same tokens: T comes by way of `tbuf` (512 bytes of shared memory), 32 ranks at a
-// time, and B's rows from L2 with 16 loads of a lane in flight.
+// time, and B's rows from L2 with 16 loads of a lane in flight (8, one step ahead of the products, took twice the time).  Tokens
+// with the adapter of the one before them share its row.
 constexpr int kLoraTokens = 8;
 constexpr int kLoraTBytes = kLoraTokens * 32 * 2;
+template <bool BF16>
 __device__ __forceinline__ void lora_add(const LoraParams& l, float (&v)[kLoraTokens], const int (&a)[kLoraTokens], int m0, int n,
-                                         bool column, uint8_t* tbuf, int lane, bool bf16) {
+                                         bool column, uint8_t* tbuf, int lane) {
   bool any = false;
 #pragma unroll
   for (int q = 0; q < kLoraTokens; ++q) any = any || a[q] >= 0;
@@ -107,38 +110,39 @@ __device__ __forceinline__ void lora_add(const LoraParams& l, float (&v)[kLoraTo
   float2 s[kLoraTokens];
 #pragma unroll
   for (int q = 0; q < kLoraTokens; ++q) s[q] = make_float2(0.0f, 0.0f);
-  for (int j = 0; j < l.rank; j += 32) {
-    uint4 tv = make_uint4(0u, 0u, 0u, 0u);
-    if (ta >= 0 && j + (lane & 3) * 8 < l.rank) tv = ld_global_v4(t + j);
+#pragma unroll 1
+  for (int j = 0; j < l.rank; j += 16) {
+    uint4 x[kLoraTokens][2], tv = make_uint4(0u, 0u, 0u, 0u);
+    if ((j & 16) == 0 && ta >= 0 && j + (lane & 3) * 8 < l.rank) tv = ld_global_v4(t + j);
 #pragma unroll
-    for (int h = 0; h < 32; h += 16) {
-      if (j + h >= l.rank) break;
-      uint4 x[kLoraTokens][2];
-#pragma unroll
-      for (int q = 0; q < kLoraTokens; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          x[q][i] = make_uint4(0u, 0u, 0u, 0u);
-          if (column && a[q] >= 0 && j + h + 8 * i < l.rank)
-            x[q][i] = __ldg(reinterpret_cast<const uint4*>(b + a[q] * l.stride_b + j + h + 8 * i));
-        }
-      if (h == 0) {
-        __syncwarp();  // the ranks before have been read
-        *reinterpret_cast<uint4*>(tbuf + lane * 16) = tv;
-        __syncwarp();
+    for (int q = 0; q < kLoraTokens; ++q) {
+      if (q > 0 && a[q] == a[q - 1]) {
+        x[q][0] = x[q - 1][0];
+        x[q][1] = x[q - 1][1];
+        continue;
       }
-#pragma unroll
-      for (int q = 0; q < kLoraTokens; ++q)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint4 y = *reinterpret_cast<const uint4*>(tbuf + q * 64 + (h / 8 + i) * 16);
-          s[q] = fma2(unpack_16(x[q][i].x, bf16), unpack_16(y.x, bf16), s[q]);
-          s[q] = fma2(unpack_16(x[q][i].y, bf16), unpack_16(y.y, bf16), s[q]);
-          s[q] = fma2(unpack_16(x[q][i].z, bf16), unpack_16(y.z, bf16), s[q]);
-          s[q] = fma2(unpack_16(x[q][i].w, bf16), unpack_16(y.w, bf16), s[q]);
-        }
+      x[q][0] = x[q][1] = make_uint4(0u, 0u, 0u, 0u);
+      const unsigned short* row = b + a[q] * l.stride_b + j;
+      if (column && a[q] >= 0) x[q][0] = __ldg(reinterpret_cast<const uint4*>(row));
+      if (column && a[q] >= 0 && j + 8 < l.rank) x[q][1] = __ldg(reinterpret_cast<const uint4*>(row + 8));
     }
+    if ((j & 16) == 0) {
+      __syncwarp();  // the ranks before have been read
+      *reinterpret_cast<uint4*>(tbuf + lane * 16) = tv;
+      __syncwarp();
+    }
+#pragma unroll
+    for (int q = 0; q < kLoraTokens; ++q)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint4 y = *reinterpret_cast<const uint4*>(tbuf + q * 64 + (j & 16) * 2 + i * 16);
+        s[q] = fma2(unpack_16(x[q][i].x, BF16), unpack_16(y.x, BF16), s[q]);
+        s[q] = fma2(unpack_16(x[q][i].y, BF16), unpack_16(y.y, BF16), s[q]);
+        s[q] = fma2(unpack_16(x[q][i].z, BF16), unpack_16(y.z, BF16), s[q]);
+        s[q] = fma2(unpack_16(x[q][i].w, BF16), unpack_16(y.w, BF16), s[q]);
+      }
   }
+  __syncwarp();
 #pragma unroll
   for (int q = 0; q < kLoraTokens; ++q)
     if (a[q] >= 0) v[q] += s[q].x + s[q].y;
@@ -156,6 +160,7 @@ struct GrpPairCfg {
   static constexpr int PAIR_M = 256;
   static constexpr int TOKENS = 256;               // most of a tile
   static constexpr int UNIT = 32;                  // its width is a multiple of
+  static constexpr int WIDTHS = 6;                 // 256, 224, .. 96 tokens to choose from
   static constexpr int A_BYTES = BM * 128;
   static constexpr int B_BYTES = TOKENS / 2 * 128;
   static constexpr int PANEL_BYTES = 64 * 128;
@@ -167,8 +172,10 @@ struct GrpPairCfg {
   static constexpr int STAGING = EPI_WARPS * kGrpBoxBytes;
   static constexpr int BAR_BYTES = 256;
   static constexpr int FIXED_SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + STAGING + BAR_BYTES;
-  static constexpr int smem_bytes(int groups) { return FIXED_SMEM + grp_plan_bytes(groups); }
-  static_assert(FIXED_SMEM + (kGrpMaxGroups + 2) * 8 <= 232448, "dynamic shared memory per CTA");
+  static constexpr int smem_bytes(int groups, bool lora) {
+    return FIXED_SMEM + (lora ? grp_plan_align(1) + EPI_WARPS * kLoraTBytes : grp_plan_align(groups));
+  }
+  static_assert(FIXED_SMEM + (kGrpMaxGroups + 4) * 8 + WIDTHS * 4 <= 232448, "dynamic shared memory per CTA");
   static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(A_BYTES % 1024 == 0 && PANEL_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && UNIT / 2 * 128 % 1024 == 0,
                 "operand tiles, and the pieces of rows they are loaded in, start on the swizzle's 1024 bytes");
@@ -188,7 +195,8 @@ __device__ __forceinline__ void grp_token_boxes(int rows, Load&& load) {
   }
 }
 
-template <bool LORA>
+// LORA: 0 for groups, else the adapters' type: 1 fp16, 2 bf16.
+template <int LORA>
 __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     grp_pair_kernel(const __grid_constant__ GrpMaps maps, const GrpParams p) {
   using Cfg = GrpPairCfg;
@@ -205,6 +213,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   uint64_t* mma_done_bar = acc_empty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  __shared__ int costs[Cfg::WIDTHS];
   GrpPlan plan;
   plan.lo = reinterpret_cast<int*>(staging + Cfg::STAGING + Cfg::BAR_BYTES);
   plan.first = plan.lo + p.groups + 2;
@@ -243,13 +252,39 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   // what came before it and then let this one start, so X, W, index and the
   // workspace's copies are there already; only T and kind are waited for, by
   // the threads that read them.
-  const bool early = LORA && p.lora.adapters > 0;
+  const bool early = LORA != 0 && p.lora.adapters > 0;
   if (!early) {
     grid_dependency_wait();
     grid_launch_dependents();
   }
+  // Tokens of a tile.  Few tiles leave pairs idle in the last wave, so the width is
+  // chosen by the number of waves that it gives, at a tile's time of (256 + width):
+  // its MMAs take 2 width cycles a k-block, its loads 128 (128 + width / 2) bytes at
+  // about 50 a cycle.
+  if (p.adapt && warp >= Cfg::EPI_WARP0 && warp < Cfg::EPI_WARP0 + Cfg::WIDTHS) {
+    const int width = Cfg::TOKENS - 32 * (warp - Cfg::EPI_WARP0);
+    int tiles = 0;
+    for (int g = lane; g < p.groups; g += 32) {
+      const int rows = grp_end(p.ends, g, p.M) - grp_end(p.ends, g - 1, p.M);
+      if (rows > 0) tiles += (rows + width - 1) / width;
+    }
+    tiles = __reduce_add_sync(0xffffffffu, tiles) * p.col_tiles;
+    if (lane == 0) costs[warp - Cfg::EPI_WARP0] = (tiles + num_clusters - 1) / num_clusters * (Cfg::TOKENS + width);
+  }
+  if (p.adapt) __syncthreads();
+  int most = Cfg::TOKENS;
+  if (p.adapt) {
+    int best = costs[0];
+#pragma unroll
+    for (int i = 1; i < Cfg::WIDTHS; ++i)
+      if (costs[i] < best) {
+        best = costs[i];
+        most = Cfg::TOKENS - 32 * i;
+      }
+    most = uniform(most);
+  }
   if (warp == Cfg::EPI_WARP0)
-    grp_make_plan(plan, p.ends, p.groups, p.M, Cfg::TOKENS, p.col_tiles, p.rest != 0, lane);
+    grp_make_plan(plan, p.ends, p.groups, p.M, most, p.col_tiles, p.rest != 0, lane);
   __syncthreads();
   const uint32_t tmem_base = *tmem_slot;
   const int num_tiles = plan.first[p.groups + 1];
@@ -275,7 +310,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       }
     };
     for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
-      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, most, Cfg::UNIT);
       if (f.g == p.groups) break;  // zeros from here on
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
       const int rows = width / 2;
@@ -361,7 +396,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         }
       };
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, ++local) {
-        const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+        const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, most, Cfg::UNIT);
         if (f.g == p.groups) break;
         const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
         const uint32_t idesc = p.idesc | static_cast<uint32_t>(width >> 3) << 17;
@@ -429,11 +464,14 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     const int quad = warp & 3;
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
     uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
-    const bool bf16 = p.bf16 != 0;
+    uint8_t* tbuf = staging + Cfg::STAGING + Cfg::BAR_BYTES + grp_plan_align(p.groups) +
+                    (warp - Cfg::EPI_WARP0) * kLoraTBytes;  // adapters only
+    constexpr bool BF16 = LORA == 2;
+    const bool bf16 = LORA ? BF16 : p.bf16 != 0;
     GrpWalk walk;
     int local = 0;
     for (int t = cluster_id; t < num_tiles; t += num_clusters) {
-      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, Cfg::TOKENS, Cfg::UNIT);
+      const GrpTile f = walk.at(plan, t, p.col_tiles, p.super, most, Cfg::UNIT);
       const int n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM + quad * 32;
       const bool zero = f.g == p.groups;
       const int acc = local & 1;
@@ -460,54 +498,61 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::TOKENS;
       const int boxes = (f.cnt + 31) / 32;
       for (int b = part; b < boxes && n0 < p.out; b += Cfg::EPI_WARPS / 4) {
-        uint32_t r[32];
-        if (!zero) {
-          tmem_ld_32x32b_x32(taddr + b * 32, r);
-          tmem_ld_wait();
-        } else {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) r[e] = 0u;
-        }
-        const int rows = min(32, f.cnt - b * 32);
-        if (LORA) {
-          const int n = n0 + lane;
-          if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
-            const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
-            __syncwarp();  // the box before has left: T takes its place for a while
-#pragma unroll
-            for (int e = 0; e < 32; e += kLoraTokens) {
-              float v[kLoraTokens];
-              int a[kLoraTokens];
-#pragma unroll
-              for (int q = 0; q < kLoraTokens; ++q) {
-                v[q] = __uint_as_float(r[e + q]);
-                a[q] = __shfl_sync(0xffffffffu, mine, e + q);
-              }
-              lora_add(p.lora, v, a, f.tok0 + b * 32 + e, n, n < p.out, box, lane, bf16);
-#pragma unroll
-              for (int q = 0; q < kLoraTokens; ++q) r[e + q] = __float_as_uint(v[q]);
-            }
-          }
-          if (p.lora.bias != nullptr && n < p.out) {
-            const float bias = load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) + bias);
-          }
-        }
+        const int rows = min(32, f.cnt - b * 32), n = n0 + lane;
         unsigned short* c = static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32) * p.ldc + n0;
-        if (p.vec) {
-          __syncwarp();  // the box before has left
+        const float bias = LORA && p.lora.bias != nullptr && n < p.out
+                               ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
+        // This lane's column of token e, staged, or (rows off 16 bytes) stored: a
+        // warp's 32 columns of a token, 64 bytes a store.
+        auto put = [&](int e, float y) {
+          const unsigned short h = round_16(LORA ? y + bias : y, bf16);
+          if (p.vec)
+            *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) = h;
+          else if (e < rows && n < p.out)
+            c[e * p.ldc + lane] = h;
+        };
+        __syncwarp();  // the box before has left
+        if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
+          const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
+#pragma unroll 1
+          for (int e = 0; e < rows; e += kLoraTokens) {
+            uint32_t r[kLoraTokens];
+            float v[kLoraTokens];
+            int a[kLoraTokens];
+            tmem_ld_32x32b_x8(taddr + b * 32 + e, r);
+            tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
-                round_16(__uint_as_float(r[e]), bf16);
+            for (int q = 0; q < kLoraTokens; ++q) {
+              v[q] = __uint_as_float(r[q]);
+              a[q] = __shfl_sync(0xffffffffu, mine, e + q);
+            }
+            lora_add<BF16>(p.lora, v, a, f.tok0 + b * 32 + e, n, n < p.out, tbuf, lane);
+#pragma unroll
+            for (int q = 0; q < kLoraTokens; ++q) put(e + q, v[q]);
+          }
+        } else {
+          uint32_t r[32];
+          if (!zero) {
+            tmem_ld_32x32b_x32(taddr + b * 32, r);
+            tmem_ld_wait();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0u;
+          }
+          if (p.vec) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
+                  round_16(LORA ? __uint_as_float(r[e]) + bias : __uint_as_float(r[e]), bf16);
+          } else if (n < p.out) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (e < rows) c[e * p.ldc + lane] = round_16(LORA ? __uint_as_float(r[e]) + bias : __uint_as_float(r[e]), bf16);
+          }
+        }
+        if (p.vec) {
           __syncwarp();
           grp_store_box(c, p.ldc, rows, min(32, p.out - n0), box, lane);
-        } else if (n0 + lane < p.out) {  // rows off 16 bytes: a warp's 32 columns of a token, 64 bytes a store
-          c += lane;
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e < rows) c[e * p.ldc] = round_16(__uint_as_float(r[e]), bf16);
         }
       }
       if (!zero) {

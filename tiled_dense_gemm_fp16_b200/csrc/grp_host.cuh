@@ -12,6 +12,7 @@ namespace tg {
 namespace {
 
 constexpr int64_t kLoraMaxRank = 512;
+constexpr int kShrinkSmem = 48 * 1024;  // of the kernel that makes T for a decoding batch
 constexpr int64_t kLoraMaxAdapters = int64_t(1) << 20;
 
 // `mats` matrices of 16-bit values, `stride` elements apart.
@@ -140,8 +141,10 @@ bool grp_countable(const GrpParams& p, int64_t most) {
 
 tg_status launch_grp_pair(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = GrpPairCfg;
-  auto kernel = f.lora ? grp_pair_kernel<true> : grp_pair_kernel<false>;
-  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, f.lora ? 2u : 1u, Cfg::smem_bytes(kGrpMaxGroups)))
+  const int kind = f.lora ? (f.bf16 ? 2 : 1) : 0;
+  auto kernel = kind == 0 ? grp_pair_kernel<0> : kind == 1 ? grp_pair_kernel<1> : grp_pair_kernel<2>;
+  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, 1u << kind,
+                   Cfg::smem_bytes(f.lora ? 1 : kGrpMaxGroups, f.lora)))
     return TG_ERR_LAUNCH;
   GrpMaps maps;
   GrpParams p;
@@ -150,13 +153,14 @@ tg_status launch_grp_pair(const GrpProduct& f, cudaStream_t stream, DeviceInfo* 
   p.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PAIR_M, 0, f.transposed, false);
   p.super = tune_int("TG_TUNE_GRP_SUPER", 8);
   if (!grp_countable(p, Cfg::TOKENS)) return TG_ERR_INVALID_ARG;
-  const int64_t most = ((f.a.rows + Cfg::TOKENS - 1) / Cfg::TOKENS + f.groups) * p.col_tiles;
+  const int64_t most = ((f.a.rows + 95) / 96 + f.groups) * p.col_tiles;  // tiles of the least width
   const int64_t pairs = info->sm_count / 2, clusters = most < pairs ? most : pairs;
+  p.adapt = tune_int("TG_TUNE_GRP_ADAPT", (f.a.rows + 255) / 256 * p.col_tiles < 8 * pairs ? 1 : 0);
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(f.groups));
+  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(f.groups, f.lora));
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, 2);
@@ -180,7 +184,7 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
     LaunchAttrs la;
     la.fill(cfg, static_cast<unsigned>(splits));
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, grp_narrow_kernel<false>, &cfg) != cudaSuccess || n < 1) {
+    if (cudaOccupancyMaxActiveClusters(&n, grp_narrow_kernel<0>, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();
       n = info->sm_count / splits > 0 ? info->sm_count / splits : 1;
     }
@@ -191,9 +195,10 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
 
 tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = GrpNarrowCfg;
-  auto kernel = f.lora ? grp_narrow_kernel<true> : grp_narrow_kernel<false>;
-  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, f.lora ? 8u : 4u, 232448)) return TG_ERR_LAUNCH;
-  if (f.lora && !ff_set_smem(reinterpret_cast<const void*>(grp_narrow_kernel<false>), info->grp_attr, 4u, 232448))
+  const int kind = f.lora ? (f.bf16 ? 2 : 1) : 0;
+  auto kernel = kind == 0 ? grp_narrow_kernel<0> : kind == 1 ? grp_narrow_kernel<1> : grp_narrow_kernel<2>;
+  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, 8u << kind, 232448)) return TG_ERR_LAUNCH;
+  if (f.lora && !ff_set_smem(reinterpret_cast<const void*>(grp_narrow_kernel<0>), info->grp_attr, 8u, 232448))
     return TG_ERR_LAUNCH;  // the one that grp_resident_clusters asks about
   GrpMaps maps;
   GrpNarrowParams p;
@@ -204,25 +209,27 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
+  int splits = tune_int("TG_TUNE_GRP_SPLITS", 2);
+  while (splits > p.g.k_blocks) splits >>= 1;
+  p.splits = splits;
   // As deep as fits a CTA an SM, or (adapters) beside the kernel that makes T, which is still at work.
-  const int stage_bytes = Cfg::W_BYTES + tokens * 128, left = 232448 - Cfg::smem_bytes(tokens, 0, f.groups);
-  int deepest = left / stage_bytes;
-  if (f.lora && f.l.adapters > 0 && (left - 100 * 1024) / stage_bytes >= 3) deepest = (left - 100 * 1024) / stage_bytes;
+  const bool adapted = f.lora && f.l.adapters > 0;
+  const int fixed = Cfg::smem_bytes(tokens, 0, f.groups) + (adapted ? Cfg::lora_bytes(tokens, splits) : 0);
+  const int stage_bytes = Cfg::W_BYTES + tokens * 128;
+  int deepest = (232448 - fixed) / stage_bytes;
+  if (adapted && (232448 - fixed - kShrinkSmem - 2048) / stage_bytes >= 3) deepest = (232448 - fixed - kShrinkSmem - 2048) / stage_bytes;
   p.per_stage = tune_int("TG_TUNE_GRP_PER", 2);
   while (p.per_stage > 1 && deepest < 3 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;
   if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
   p.tmem_cols = static_cast<uint32_t>(2 * tokens);
-  int splits = tune_int("TG_TUNE_GRP_SPLITS", 2);
-  while (splits > p.g.k_blocks) splits >>= 1;
-  p.splits = splits;
   const int64_t most = ((f.a.rows + tokens - 1) / tokens + f.groups) * p.g.col_tiles;
   const int64_t fit = grp_resident_clusters(splits, info), clusters = most < fit ? most : fit;
   cudaLaunchConfig_t cfg;
   std::memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3(static_cast<unsigned>(splits * clusters), 1, 1);
   cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = static_cast<size_t>(Cfg::smem_bytes(tokens, p.stages * p.per_stage, f.groups));
+  cfg.dynamicSmemBytes = static_cast<size_t>(fixed + p.stages * p.per_stage * stage_bytes);
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, static_cast<unsigned>(splits));
@@ -356,7 +363,7 @@ int64_t grouped_grad_workspace(const GroupedArgs& a) {
 
 tg_status launch_grp_wgrad(const GroupedArgs& a, const int32_t* ends, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = GrpWgradCfg;
-  if (!ff_set_smem(reinterpret_cast<const void*>(grp_wgrad_kernel), info->grp_attr, 16u, Cfg::smem_bytes(kGrpMaxGroups)))
+  if (!ff_set_smem(reinterpret_cast<const void*>(grp_wgrad_kernel), info->grp_attr, 64u, Cfg::smem_bytes(kGrpMaxGroups)))
     return TG_ERR_LAUNCH;
   GrpWgradMaps maps;
   std::memset(&maps, 0, sizeof maps);
@@ -500,7 +507,7 @@ int64_t lora_workspace(const LoraArgs& l) {
 // T and the kinds of 32 tokens.
 tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float* scale, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = LoraShrinkCfg;
-  if (!ff_set_smem(reinterpret_cast<const void*>(lora_shrink_kernel), info->grp_attr, 32u, 210 * 1024)) return TG_ERR_LAUNCH;
+  if (!ff_set_smem(reinterpret_cast<const void*>(lora_shrink_kernel), info->grp_attr, 128u, 210 * 1024)) return TG_ERR_LAUNCH;
   LoraShrinkMaps maps;
   std::memset(&maps, 0, sizeof maps);
   LoraShrinkParams p;
@@ -515,8 +522,8 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.rank = static_cast<int>(l.rank);
   p.adapters = static_cast<int>(l.adapters);
   p.k_blocks = static_cast<int>((l.K + 63) / 64);
-  p.tokens = 16;
-  while (p.tokens < 128 && p.tokens < l.M) p.tokens <<= 1;
+  // Blocks of 16 tokens for a decoding batch, whose tokens have few neighbours of their own adapter.
+  p.tokens = l.M <= 16 ? 16 : l.M <= 128 ? 32 : 128;
   for (int i = 0; i < 4 && 16 << i <= p.tokens; ++i)
     if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
@@ -529,8 +536,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   const int64_t items = l.M < p.tokens ? l.M : p.tokens;
   y = y < 1 ? 1 : y > items ? items : y;
   y = y > l.adapters ? l.adapters : y;
-  const int budget = 96 * 1024;
-  const int deepest = (budget - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  const int deepest = ((p.tokens == 128 ? 96 * 1024 : kShrinkSmem) - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
   p.per_stage = tune_int("TG_TUNE_SHRINK_PER", 2);
   while (p.per_stage > 1 && deepest < 4 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;
