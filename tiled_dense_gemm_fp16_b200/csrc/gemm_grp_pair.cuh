@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       grid_launch_dependents();
     }
     const int quad = warp & 3;
+    constexpr int PARTS = Cfg::EPI_WARPS / 4;
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
     uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
     uint8_t* tbuf = staging + Cfg::STAGING + Cfg::BAR_BYTES + grp_plan_align(p.groups) +
@@ -477,11 +478,11 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const int acc = local & 1;
       if (early) {
         // The rows of B that the epilogue will read come into L2 while the tile is computed.
-        for (int b = part; b * 32 < f.cnt && n0 < p.out; b += Cfg::EPI_WARPS / 4) {
+        for (int b = 0; b * 32 < f.cnt && n0 < p.out; ++b) {
           const int mine = b * 32 + lane < f.cnt ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
           const int first = __shfl_sync(0xffffffffu, mine, 0);
           if (__all_sync(0xffffffffu, mine == first || b * 32 + lane >= f.cnt)) continue;
-          for (int e = 0; e < 32; ++e) {
+          for (int e = part * (32 / PARTS); e < (part + 1) * (32 / PARTS); ++e) {
             const int a = __shfl_sync(0xffffffffu, mine, e);
             if (a < 0 || n0 + lane >= p.out) continue;
             const unsigned short* row = static_cast<const unsigned short*>(p.lora.b) + a * p.lora.stride_b + (n0 + lane) * p.lora.ldb;
@@ -491,42 +492,51 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         __syncwarp();
       }
       if (!zero) {
-        const bool ready = mbar_wait(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.wait_budget_ns, 0xa6);
-        if (!__all_sync(0xffffffffu, ready)) break;
+        bool ready = mbar_wait_warp(&acc_full_bar[acc], (local >> 1) & 1, abort_flag, p.wait_budget_ns, 0xa6);
+        // The four warps that stage rows together go on or give up together.
+        if (!p.vec) ready = bar_all_128(1 + part, ready);
+        if (!ready) break;
         tcgen05_fence_after_sync();
       }
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::TOKENS;
       const int boxes = (f.cnt + 31) / 32;
-      for (int b = part; b < boxes && n0 < p.out; b += Cfg::EPI_WARPS / 4) {
-        const int rows = min(32, f.cnt - b * 32), n = n0 + lane;
-        unsigned short* c = static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32) * p.ldc + n0;
-        const float bias = LORA && p.lora.bias != nullptr && n < p.out
-                               ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
-        // This lane's column of token e, staged, or (rows off 16 bytes) stored: a
-        // warp's 32 columns of a token, 64 bytes a store.
+      const int cta_n0 = f.col_blk * Cfg::PAIR_M + static_cast<int>(rank) * Cfg::BM;
+      const int n = n0 + lane, cols = p.vec ? min(32, p.out - n0) : min(Cfg::BM, p.out - cta_n0);  // of a warp, or of four
+      const float bias = LORA && p.lora.bias != nullptr && n < p.out
+                             ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
+      for (int b = 0; b < boxes && cols > 0; ++b) {
+        const bool mixed = early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed;
+        if (!mixed && b % PARTS != part) continue;
+        // A mixed box is shared: 16 tokens for each of the two warps that have these columns.
+        const int e0 = mixed ? part * (32 / PARTS) : 0;
+        const int rows = min(mixed ? 32 / PARTS : 32, f.cnt - b * 32 - e0);
+        unsigned short* c = static_cast<unsigned short*>(p.c) + static_cast<int64_t>(f.tok0 + b * 32 + e0) * p.ldc;
+        // This lane's column of row e into staging: a box of the warp's own, or (rows
+        // off 16 bytes) a row of four warps.
+        uint8_t* mine_at = p.vec ? box + (lane & 7) * 2 : staging + part * 4 * kGrpBoxBytes + quad * 64 + lane * 2;
         auto put = [&](int e, float y) {
-          const unsigned short h = round_16(LORA ? y + bias : y, bf16);
-          if (p.vec)
-            *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) = h;
-          else if (e < rows && n < p.out)
-            c[e * p.ldc + lane] = h;
+          *reinterpret_cast<unsigned short*>(mine_at + (p.vec ? grp_box_at(e, lane >> 3) : e * 256)) =
+              round_16(LORA ? y + bias : y, bf16);
         };
-        __syncwarp();  // the box before has left
-        if (early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed) {
-          const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + lane) : -1;
+        if (p.vec)
+          __syncwarp();  // the box before has left
+        else
+          bar_128(1 + part);
+        if (mixed) {
+          const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + e0 + lane) : -1;
 #pragma unroll 1
           for (int e = 0; e < rows; e += kLoraTokens) {
             uint32_t r[kLoraTokens];
             float v[kLoraTokens];
             int a[kLoraTokens];
-            tmem_ld_32x32b_x8(taddr + b * 32 + e, r);
+            tmem_ld_32x32b_x8(taddr + b * 32 + e0 + e, r);
             tmem_ld_wait();
 #pragma unroll
             for (int q = 0; q < kLoraTokens; ++q) {
               v[q] = __uint_as_float(r[q]);
               a[q] = __shfl_sync(0xffffffffu, mine, e + q);
             }
-            lora_add<BF16>(p.lora, v, a, f.tok0 + b * 32 + e, n, n < p.out, tbuf, lane);
+            lora_add<BF16>(p.lora, v, a, f.tok0 + b * 32 + e0 + e, n, n < p.out, tbuf, lane);
 #pragma unroll
             for (int q = 0; q < kLoraTokens; ++q) put(e + q, v[q]);
           }
@@ -542,17 +552,21 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           if (p.vec) {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              *reinterpret_cast<unsigned short*>(box + grp_box_at(e, lane >> 3) + (lane & 7) * 2) =
+              *reinterpret_cast<unsigned short*>(mine_at + grp_box_at(e, lane >> 3)) =
                   round_16(LORA ? __uint_as_float(r[e]) + bias : __uint_as_float(r[e]), bf16);
-          } else if (n < p.out) {
+          } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (e < rows) c[e * p.ldc + lane] = round_16(LORA ? __uint_as_float(r[e]) + bias : __uint_as_float(r[e]), bf16);
+              *reinterpret_cast<unsigned short*>(mine_at + e * 256) =
+                  round_16(LORA ? __uint_as_float(r[e]) + bias : __uint_as_float(r[e]), bf16);
           }
         }
         if (p.vec) {
           __syncwarp();
-          grp_store_box(c, p.ldc, rows, min(32, p.out - n0), box, lane);
+          grp_store_box(c + n0, p.ldc, rows, cols, box, lane);
+        } else {
+          bar_128(1 + part);
+          grp_store_rows(c + cta_n0, p.ldc, rows, cols, staging + part * 4 * kGrpBoxBytes, quad * 32 + lane);
         }
       }
       if (!zero) {

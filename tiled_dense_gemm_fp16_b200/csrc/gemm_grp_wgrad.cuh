@@ -295,16 +295,16 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) h[e] = 0u;
         }
-        __syncwarp();  // the box before has left
+        if (p.vec) {
+          __syncwarp();  // the box before has left
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(box + grp_box_at(lane, q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        __syncwarp();
-        const int rows = min(32, p.N - n0), cols = min(32, p.K - k0);
-        if (p.vec)
-          grp_store_box(dst + k0, p.ldc, rows, cols, box, lane);
-        else
-          grp_store_box_any(dst + k0, p.ldc, rows, cols, box, lane);
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(box + grp_box_at(lane, q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+          __syncwarp();
+          grp_store_box(dst + k0, p.ldc, min(32, p.N - n0), min(32, p.K - k0), box, lane);
+        } else {
+          ff_store_box<1>(nullptr, dst - n0 * p.ldc, p.ldc, false, p.N, p.K, n0, k0, h, box, lane, 0);
+        }
       }
       if (!zero) {
         tcgen05_fence_before_sync();

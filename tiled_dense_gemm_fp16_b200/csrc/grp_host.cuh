@@ -193,6 +193,17 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
   return known;
 }
 
+// CTAs that share a sum.  Two keep the tiles of a decoding batch even over the
+// SMs (60 groups' weights of 2048 x 4096: 157 / 152 / 159 us with 1 / 2 / 4); where
+// few panels are all there is to do, four shorten the way through one (one token
+// through 4096 x 4096 with its adapter: 19 / 16 / 15).  Short sums do not pay for
+// the exchange.
+int grp_splits(const GrpProduct& f, int k_blocks) {
+  if (k_blocks < 8) return 1;
+  const int64_t panels = (f.out + 127) / 128 * (f.a.rows < f.groups ? f.a.rows : f.groups);
+  return k_blocks >= 16 && panels <= 40 ? 4 : 2;
+}
+
 tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = GrpNarrowCfg;
   const int kind = f.lora ? (f.bf16 ? 2 : 1) : 0;
@@ -209,7 +220,7 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
-  int splits = tune_int("TG_TUNE_GRP_SPLITS", 2);
+  int splits = tune_int("TG_TUNE_GRP_SPLITS", grp_splits(f, p.g.k_blocks));
   while (splits > p.g.k_blocks) splits >>= 1;
   p.splits = splits;
   // As deep as fits a CTA an SM, or (adapters) beside the kernel that makes T, which is still at work.

@@ -216,13 +216,51 @@ __device__ __forceinline__ void grp_store_box(unsigned short* c, int64_t ld, int
   }
 }
 
-// The same for rows that start anywhere: a row a store, value by value.
-__device__ __forceinline__ void grp_store_box_any(unsigned short* c, int64_t ld, int rows, int cols, const uint8_t* box, int lane) {
-  if (lane >= cols) return;
-  unsigned short* dst = c + lane;
-#pragma unroll 8
-  for (int r = 0; r < 32; ++r)
-    if (r < rows) dst[r * ld] = *reinterpret_cast<const unsigned short*>(box + grp_box_at(r, lane >> 3) + (lane & 7) * 2);
+// Rows that start anywhere on 2 bytes, by the 128 threads whose warps have staged
+// 32 rows of 128 columns (256 bytes a row).  Four threads a row: the whole 16-byte
+// blocks of the result out of two staged pieces each, then the columns before the
+// first block and behind the last one.
+__device__ __forceinline__ void grp_store_rows(unsigned short* c, int64_t ld, int rows, int cols, const uint8_t* staged, int thread) {
+  const int r = thread >> 2, q = thread & 3;
+  if (r >= rows) return;
+  unsigned short* row = c + r * ld;
+  const uint8_t* from = staged + r * 256;
+  const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 7;  // columns from a boundary to the row's start
+  const int head = (8 - skew) & 7;                                               // columns before the first block
+  const int blocks = (cols - head) >> 3;                                         // negative: cols < head
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int g = q + 4 * i;
+    if (g < blocks) {
+      const uint4* piece = reinterpret_cast<const uint4*>(from) + g;
+      // With head > 0 at most 15 blocks fit, so the piece behind is there.
+      const uint4 v = head == 0 ? piece[0] : edge_realign(piece[0], piece[1], 2 * head);
+      *reinterpret_cast<uint4*>(row + head + 8 * g) = v;
+    }
+  }
+  const unsigned short* values = reinterpret_cast<const unsigned short*>(from);
+  const int tail = blocks > 0 ? head + 8 * blocks : min(head, cols);  // columns from here on are left
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = q + 4 * i;
+    if (e < min(head, cols)) row[e] = values[e];
+    if (tail + e < cols) row[tail + e] = values[tail + e];
+  }
 }
+
+// The 128 threads of a named barrier; whether `all` holds for each of them.
+__device__ __forceinline__ bool bar_all_128(int id, bool all) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %2, 0;\n\t"
+      "barrier.cta.red.and.pred p, %1, 128, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(static_cast<uint32_t>(all))
+      : "memory");
+  return r != 0u;
+}
+__device__ __forceinline__ void bar_128(int id) { asm volatile("barrier.cta.sync %0, 128;" ::"r"(id) : "memory"); }
 
 }  // namespace tg

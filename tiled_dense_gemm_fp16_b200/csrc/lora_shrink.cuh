@@ -116,55 +116,78 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
   const int m0 = static_cast<int>(blockIdx.x / p.splits) * p.tokens;
   const int j0 = static_cast<int>(blockIdx.z) * 128;
   const int rows = min(128, p.rank - j0);  // of A
-  // Each of 128 threads looks for its token's adapter among the tokens before.
   __shared__ __align__(16) int owner_of[128];
   __shared__ int firsts[4];
   __shared__ LoraItems items;
-  int mine = -1;
-  const int tok = threadIdx.x;
-  if (tok < 128) {
-    const bool valid = tok < p.tokens && m0 + tok < p.M;
-    const int a = valid ? __ldg(p.index + m0 + tok) : -1;
-    mine = a >= 0 && a < p.adapters ? a : -1;
-    owner_of[tok] = mine;
-    const int r0 = __shfl_sync(0xffffffffu, mine, 0);
-    const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
-    // What each 32 tokens are to the main product.
-    if (lane == 0 && valid && blockIdx.y == 0 && blockIdx.z == 0 && rank == 0)
-      p.kind[(m0 + tok) / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
-  }
-  __syncthreads();
-  int before = 128;  // the first token of this one's adapter, from the end of the search on
-  if (tok < 128) {
-    for (int s = (tok & ~31) + 28; s >= 0; s -= 4) {
-      const int4 o = *reinterpret_cast<const int4*>(owner_of + s);
-      if (o.w == mine) before = s + 3;
-      if (o.z == mine) before = s + 2;
-      if (o.y == mine) before = s + 1;
-      if (o.x == mine) before = s;
+  if (p.tokens <= 32) {  // each warp by itself finds what it needs; one keeps the list
+    const bool valid = lane < p.tokens && m0 + lane < p.M;
+    const int a = valid ? __ldg(p.index + m0 + lane) : -1;
+    const int mine = a >= 0 && a < p.adapters ? a : -1;
+    const unsigned peers = __match_any_sync(0xffffffffu, mine);
+    const bool opens = mine >= 0 && __ffs(peers) - 1 == lane;
+    const unsigned all = __ballot_sync(0xffffffffu, opens);
+    if (warp == 0) {
+      if (opens) {
+        const int d = __popc(all & ((1u << lane) - 1));
+        items.adapter[d] = mine;
+        items.first[d] = lane;
+        items.last[d] = 31 - __clz(peers);
+      }
+      const int r0 = __shfl_sync(0xffffffffu, mine, 0);
+      const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
+      if (lane == 0) {
+        items.count = __popc(all);
+        if (blockIdx.y == 0 && blockIdx.z == 0 && rank == 0) p.kind[m0 / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
+      }
     }
-    const unsigned opens = __ballot_sync(0xffffffffu, mine >= 0 && before == tok);
-    if (lane == 0) firsts[warp] = __popc(opens);
-    if (mine >= 0 && before == tok) items.last[tok] = tok;  // by the first token for now
-    before = mine < 0 ? -1 : before;
-    mine = __popc(opens & ((1u << lane) - 1));  // its number in this warp
-  }
-  __syncthreads();
-  if (tok < 128 && before >= 0 && before != tok) atomicMax(&items.last[before], tok);
-  __syncthreads();
-  int last = 0;
-  if (tok < 128 && before == tok) last = items.last[tok];
-  __syncthreads();
-  if (tok < 128) {
-    for (int w = 0; w < warp; ++w) mine += firsts[w];
-    if (before == tok) {
-      items.adapter[mine] = owner_of[tok];
-      items.first[mine] = tok;
-      items.last[mine] = last;
+    __syncthreads();
+  } else {  // each of 128 threads looks for its token's adapter among the tokens before
+    int mine = -1;
+    const int tok = threadIdx.x;
+    if (tok < 128) {
+      const bool valid = tok < p.tokens && m0 + tok < p.M;
+      const int a = valid ? __ldg(p.index + m0 + tok) : -1;
+      mine = a >= 0 && a < p.adapters ? a : -1;
+      owner_of[tok] = mine;
+      const int r0 = __shfl_sync(0xffffffffu, mine, 0);
+      const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
+      // What each 32 tokens are to the main product.
+      if (lane == 0 && valid && blockIdx.y == 0 && blockIdx.z == 0 && rank == 0)
+        p.kind[(m0 + tok) / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
     }
-    if (tok == 0) items.count = firsts[0] + firsts[1] + firsts[2] + firsts[3];
+    __syncthreads();
+    int before = 128;  // the first token of this one's adapter, from the end of the search on
+    if (tok < 128) {
+      for (int s = (tok & ~31) + 28; s >= 0; s -= 4) {
+        const int4 o = *reinterpret_cast<const int4*>(owner_of + s);
+        if (o.w == mine) before = s + 3;
+        if (o.z == mine) before = s + 2;
+        if (o.y == mine) before = s + 1;
+        if (o.x == mine) before = s;
+      }
+      const unsigned opens = __ballot_sync(0xffffffffu, mine >= 0 && before == tok);
+      if (lane == 0) firsts[warp] = __popc(opens);
+      if (mine >= 0 && before == tok) items.last[tok] = tok;  // by the first token for now
+      before = mine < 0 ? -1 : before;
+      mine = __popc(opens & ((1u << lane) - 1));  // its number in this warp
+    }
+    __syncthreads();
+    if (tok < 128 && before >= 0 && before != tok) atomicMax(&items.last[before], tok);
+    __syncthreads();
+    int last = 0;
+    if (tok < 128 && before == tok) last = items.last[tok];
+    __syncthreads();
+    if (tok < 128) {
+      for (int w = 0; w < warp; ++w) mine += firsts[w];
+      if (before == tok) {
+        items.adapter[mine] = owner_of[tok];
+        items.first[mine] = tok;
+        items.last[mine] = last;
+      }
+      if (tok == 0) items.count = firsts[0] + firsts[1] + firsts[2] + firsts[3];
+    }
+    __syncthreads();
   }
-  __syncthreads();
   const int count = items.count, step = static_cast<int>(gridDim.y);  // clusters without an item only take leave
   const int kb_lo = static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / p.splits);
   const int kb_hi = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / p.splits);
