@@ -582,7 +582,7 @@ typedef struct tg_grouped_options {
     int32_t type;        /* TG_TYPE_F16 or TG_TYPE_BF16                               */
     int32_t rest;        /* 1: rows without a group are set to +0 in Y, dX            */
     int64_t ldx, ldw, ldy; /* elements between rows of X, of one W, of Y (backward: of dY); 0 = dense */
-    int64_t stride_w;    /* elements between W_g and W_{g+1}; 0 = N * ldw             */
+    int64_t stride_w;    /* elements between one W and the next; 0 = N * ldw          */
     int64_t lddx, lddw;  /* of the gradients                                          */
     int64_t stride_dw;   /* 0 = N * lddw; at least (N - 1) * lddw + K                 */
     int64_t reserved;    /* must be 0                                                 */

@@ -155,7 +155,8 @@ __device__ __forceinline__ int lora_adapter(const LoraParams& l, int m) {
 }
 
 struct GrpPairCfg {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 6;                 // of the widest tiles; more of narrower ones
+  static constexpr int MAX_STAGES = 8;
   static constexpr int BM = 128;                   // weight rows of a CTA
   static constexpr int PAIR_M = 256;
   static constexpr int TOKENS = 256;               // most of a tile
@@ -176,7 +177,7 @@ struct GrpPairCfg {
     return FIXED_SMEM + (lora ? grp_plan_align(1) + EPI_WARPS * kLoraTBytes : grp_plan_align(groups));
   }
   static_assert(FIXED_SMEM + (kGrpMaxGroups + 4) * 8 + WIDTHS * 4 <= 232448, "dynamic shared memory per CTA");
-  static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
+  static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(A_BYTES % 1024 == 0 && PANEL_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && UNIT / 2 * 128 % 1024 == 0,
                 "operand tiles, and the pieces of rows they are loaded in, start on the swizzle's 1024 bytes");
 };
@@ -202,13 +203,11 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   using Cfg = GrpPairCfg;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* a_smem = smem;
-  uint8_t* b_smem = smem + Cfg::STAGES * Cfg::A_BYTES;
   uint8_t* staging = smem + Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES);
   uint64_t* bars = reinterpret_cast<uint64_t*>(staging + Cfg::STAGING);
-  uint64_t* full_bar = bars;                        // used in the even CTA
-  uint64_t* empty_bar = bars + Cfg::STAGES;         // per CTA
-  uint64_t* acc_full_bar = bars + 2 * Cfg::STAGES;  // per CTA
+  uint64_t* full_bar = bars;                            // used in the even CTA
+  uint64_t* empty_bar = bars + Cfg::MAX_STAGES;         // per CTA
+  uint64_t* acc_full_bar = bars + 2 * Cfg::MAX_STAGES;  // per CTA
   uint64_t* acc_empty_bar = acc_full_bar + 2;       // used in the even CTA
   uint64_t* mma_done_bar = acc_empty_bar + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   const int num_clusters = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < Cfg::STAGES; ++s) {
+    for (int s = 0; s < Cfg::MAX_STAGES; ++s) {
       mbar_init(&full_bar[s], 1);
       mbar_init(&empty_bar[s], 1);
     }
@@ -283,6 +282,11 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       }
     most = uniform(most);
   }
+  // The ring: as many stages of `most` tokens as there is room for.  (Adapters' k-blocks fit too: 16 rows of 32 tokens each.)
+  const int b_bytes = most / 2 * 128;
+  const int stages = min(Cfg::MAX_STAGES, Cfg::STAGES * (Cfg::A_BYTES + Cfg::B_BYTES) / (Cfg::A_BYTES + b_bytes));
+  uint8_t* a_smem = smem;
+  uint8_t* b_smem = smem + stages * Cfg::A_BYTES;
   if (warp == Cfg::EPI_WARP0)
     grp_make_plan(plan, p.ends, p.groups, p.M, most, p.col_tiles, p.rest != 0, lane);
   __syncthreads();
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     auto next = [&]() {
       used |= 1u << stage;
       parities = (parities & ~(1u << stage)) | phase << stage;
-      if (++stage == Cfg::STAGES) {
+      if (++stage == stages) {
         stage = 0;
         phase ^= 1u;
       }
@@ -327,7 +331,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
           const int k0 = kb * 64;
           uint8_t* adst = a_smem + stage * Cfg::A_BYTES;
-          uint8_t* bdst = b_smem + stage * Cfg::B_BYTES;
+          uint8_t* bdst = b_smem + stage * b_bytes;
           if (p.w_mn) {
             tma_load_3d_pair_hint(adst, &maps.w, full, n0, k0, f.g, pol);
             tma_load_3d_pair_hint(adst + Cfg::PANEL_BYTES, &maps.w, full, n0 + 64, k0, f.g, pol);
@@ -356,7 +360,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
               tma_load_3d_pair_hint(a_smem + stage * Cfg::A_BYTES, &maps.lb, full, j0, n0, run.adapter, pol);
               // 16 of each 32 tokens, where an MMA of 32 columns wants them.
               for (int i = 0; i < run.count; ++i)
-                tma_load_2d_pair_hint(b_smem + stage * Cfg::B_BYTES + i * 2048, &maps.lt, full, j0,
+                tma_load_2d_pair_hint(b_smem + stage * b_bytes + i * 2048, &maps.lt, full, j0,
                                       f.tok0 + (run.first + i) * 32 + static_cast<int>(rank) * 16, pol);
             }
             next();
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     // The even CTA's full barriers count both CTAs' bytes: once they have
     // completed, every load of the pair has landed.
     if (leader) {
-      for (int s = 0; s < Cfg::STAGES; ++s) {
+      for (int s = 0; s < stages; ++s) {
         if (used >> s & 1u) {
           volatile int no_abort = 0;
           mbar_wait(&full_bar[s], parities >> s & 1u, &no_abort, p.wait_budget_ns, 0xa2);
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const uint32_t tmem = uniform(tmem_base);
       GrpWalk walk;
       auto next = [&]() {
-        if (++stage == Cfg::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1u;
         }
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
             break;
           }
           tcgen05_fence_after_sync();
-          const uint64_t a_desc = a_desc0 + stage * (Cfg::A_BYTES / 16), b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16);
+          const uint64_t a_desc = a_desc0 + stage * (Cfg::A_BYTES / 16), b_desc = b_desc0 + stage * (b_bytes / 16);
           if (one) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -435,7 +439,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
               const uint64_t a_desc = lb_desc0 + stage * (Cfg::A_BYTES / 16);
               if (one) {
                 for (int i = 0; i < run.count; ++i) {
-                  const uint64_t b_desc = b_desc0 + stage * (Cfg::B_BYTES / 16) + i * (2048 / 16);
+                  const uint64_t b_desc = b_desc0 + stage * (b_bytes / 16) + i * (2048 / 16);
                   for (int k = 0; k < steps; ++k)
                     umma_f16_ss_pair(d_tmem + (run.first + i) * 32, a_desc + k * 2, b_desc + k * 2, idesc32, 1u);
                 }

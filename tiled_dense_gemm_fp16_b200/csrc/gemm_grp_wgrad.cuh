@@ -17,7 +17,16 @@ namespace tg {
 struct GrpWgradMaps {
   CUtensorMap d;  // dY, boxes of 64 columns and 64 rows
   CUtensorMap x;  // X, the same
+  CUtensorMap c;  // dW, boxes of 32 x 32 of one matrix
 };
+
+// One box of results to matrix z of a stack.
+__device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap* map, const void* smem_src, int x, int y, int z, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "l"(policy)
+               : "memory");
+}
 
 struct GrpWgradParams {
   void* c;
@@ -266,6 +275,7 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
     uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
     const bool bf16 = p.bf16 != 0;
+    const uint64_t pol = l2_policy_evict_first();
     int local = 0;
     for (int t = cluster_id; t < p.num_tiles; t += num_clusters) {
       const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
@@ -295,15 +305,21 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
 #pragma unroll
           for (int e = 0; e < 16; ++e) h[e] = 0u;
         }
-        if (p.vec) {
-          __syncwarp();  // the box before has left
+        // As ff_store_box, with TMA boxes of one matrix of the stack.
+        if (p.vec && (k0 + 32 <= p.K || (p.K & 7) == 0)) {
+          if (lane == 0) bulk_wait_group_read<0>();  // the box before has left
+          __syncwarp();
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *reinterpret_cast<uint4*>(box + grp_box_at(lane, q)) = make_uint4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
+          fence_proxy_async_smem();
           __syncwarp();
-          grp_store_box(dst + k0, p.ldc, min(32, p.N - n0), min(32, p.K - k0), box, lane);
+          if (lane == 0) {
+            tma_store_3d_hint(&maps.c, box, k0, n0, f.g, pol);
+            bulk_commit_group();
+          }
         } else {
-          ff_store_box<1>(nullptr, dst - n0 * p.ldc, p.ldc, false, p.N, p.K, n0, k0, h, box, lane, 0);
+          ff_store_box<1>(nullptr, dst - n0 * p.ldc, p.ldc, false, p.N, p.K, n0, k0, h, box, lane, pol);
         }
       }
       if (!zero) {
@@ -315,6 +331,7 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     }
   }
 
+  if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait_group<0>();  // the results are written
   tcgen05_fence_before_sync();
   __syncthreads();
   cluster_sync();

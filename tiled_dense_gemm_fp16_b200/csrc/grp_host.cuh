@@ -15,6 +15,24 @@ constexpr int64_t kLoraMaxRank = 512;
 constexpr int kShrinkSmem = 48 * 1024;  // of the kernel that makes T for a decoding batch
 constexpr int64_t kLoraMaxAdapters = int64_t(1) << 20;
 
+// current_device, with the device's context bound to this host thread.  Encoding a
+// tensor map needs one, and a thread that has made no runtime call yet has none
+// (autograd's, whose memory comes out of torch's cache, when a backward pass
+// starts with a product).
+tg_status grp_device(DeviceInfo*& info) {
+  int dev = 0;
+  const tg_status st = current_device(dev, info);
+  static thread_local int bound = -1;
+  if (st == TG_OK && bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) {
+      cudaGetLastError();
+      return TG_ERR_LAUNCH;
+    }
+    bound = dev;
+  }
+  return st;
+}
+
 // `mats` matrices of 16-bit values, `stride` elements apart.
 struct GrpStack {
   FfMat m;  // the first
@@ -77,7 +95,8 @@ tg_status grp_make_copies(FfMat* x, FfMat* y, GrpStack* w, uint8_t*& ws, cudaStr
   return st;
 }
 
-bool grp_encode3(CUtensorMap* map, const GrpStack& s, int box_cols, int box_rows) {
+bool grp_encode3(CUtensorMap* map, const GrpStack& s, int box_cols, int box_rows,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   auto fn = encode_fn();
   if (!fn) return false;
   const int64_t stride = s.mats == 1 ? round_up(s.m.rows * s.m.ld, 8) : s.stride;
@@ -87,7 +106,7 @@ bool grp_encode3(CUtensorMap* map, const GrpStack& s, int box_cols, int box_rows
   cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
   cuuint32_t estride[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(s.m.p), dims, strides, box, estride,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -340,9 +359,8 @@ tg_status run_grouped(GroupedArgs& a, const int32_t* ends, void* stream_ptr, voi
   if (!a.x.valid() || !a.w.valid(false) || !a.y.valid() || !e.valid() || need < 0) return TG_ERR_INVALID_ARG;
   const FfMat in[4] = {a.x, a.w.span(), e, a.y};
   if (!ff_disjoint(in, 3, &a.y, 1) || !ff_workspace_valid(ws_ptr, ws_bytes, need, in, 4)) return TG_ERR_INVALID_ARG;
-  int dev = 0;
   DeviceInfo* info = nullptr;
-  tg_status st = current_device(dev, info);
+  tg_status st = grp_device(info);
   if (st != TG_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (a.K == 0 || a.groups == 0) return grp_zero(a.y, ends, a.groups, a.rest, stream, info);
@@ -397,6 +415,7 @@ tg_status launch_grp_wgrad(const GroupedArgs& a, const int32_t* ends, cudaStream
   if (tiles > INT_MAX - 65536) return TG_ERR_INVALID_ARG;
   p.num_tiles = static_cast<int>(tiles);
   p.vec = a.dw.on16() ? 1 : 0;
+  if (p.vec && !grp_encode3(&maps.c, a.dw, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return TG_ERR_LAUNCH;
   p.bf16 = a.bf16 ? 1 : 0;
   p.idesc = make_idesc_ff(kFfF16, a.bf16, Cfg::TILE, Cfg::TILE, true, true);
   p.wait_budget_ns = wait_budget((a.M + 63) / 64);
@@ -446,9 +465,8 @@ tg_status run_grouped_grad(GroupedArgs& a, const int32_t* ends, void* stream_ptr
     all[n++] = a.dw.span();
   }
   if (!ff_disjoint(all, 4, all + 4, n - 4) || !ff_workspace_valid(ws_ptr, ws_bytes, need, all, n)) return TG_ERR_INVALID_ARG;
-  int dev = 0;
   DeviceInfo* info = nullptr;
-  tg_status st = current_device(dev, info);
+  tg_status st = grp_device(info);
   if (st != TG_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (a.M == 0 || a.N == 0 || a.groups == 0) {  // sums over nothing
@@ -586,9 +604,8 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
   for (int q = 0; q < 8; ++q)
     if (q != 5 && l.y.overlaps(all[q])) return TG_ERR_INVALID_ARG;
   if (!ff_workspace_valid(ws_ptr, ws_bytes, need, all, 8)) return TG_ERR_INVALID_ARG;
-  int dev = 0;
   DeviceInfo* info = nullptr;
-  tg_status st = current_device(dev, info);
+  tg_status st = grp_device(info);
   if (st != TG_OK) return st;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (l.K == 0) {

@@ -87,7 +87,7 @@ __device__ __forceinline__ int grp_end(const int* ends, int g, int M) {
 struct GrpCut {
   int tiles, whole, width;  // `whole` tiles of `most`, one of `width` rows, and the rest in the last
 };
-__device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
+__host__ __device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
   GrpCut c;
   c.tiles = (rows + most - 1) / most;  // `most` and `unit` are powers of two
   c.whole = c.tiles - 1;
@@ -100,8 +100,8 @@ __device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
   return c;
 }
 // First row and number of rows of tile i.
-__device__ __forceinline__ void grp_cut_tile(const GrpCut& c, int rows, int most, int i, int& first, int& count) {
-  first = min(i, c.whole) * most + (i > c.whole ? c.width : 0);
+__host__ __device__ __forceinline__ void grp_cut_tile(const GrpCut& c, int rows, int most, int i, int& first, int& count) {
+  first = (i < c.whole ? i : c.whole) * most + (i > c.whole ? c.width : 0);
   count = i < c.whole ? most : (i == c.whole && c.width != 0 ? c.width : rows - first);
 }
 
