@@ -473,6 +473,21 @@ int64_t ff_copy_bytes(const FfMat& m) {
   return (m.empty() || m.rows_on(16)) ? 0 : up256(2 * m.rows * round_up(m.cols, 8));
 }
 
+// m's padded copy at `ws`, which takes m's place; advances `ws`.
+void ff_copy_plan(FfMat& m, RepackParams& r, uint8_t*& ws) {
+  const int64_t ld = round_up(m.cols, 8);
+  r.src = static_cast<const __half*>(m.p);
+  r.dst = reinterpret_cast<__half*>(ws);
+  r.src_ld = m.ld;
+  r.rows = static_cast<int>(m.rows);
+  r.cols = static_cast<int>(m.cols);
+  r.cols_pad = static_cast<int>(ld);
+  r.chunks = m.rows * (ld / 8);
+  m.p = ws;
+  m.ld = ld;
+  ws += up256(2 * m.rows * ld);
+}
+
 // Replace those of `mats` that need one by their padded copies at `ws`, made by
 // one launch; advances `ws`.
 tg_status ff_make_copies(FfMat* const* mats, int count, uint8_t*& ws, cudaStream_t stream, DeviceInfo* info) {
@@ -482,21 +497,9 @@ tg_status ff_make_copies(FfMat* const* mats, int count, uint8_t*& ws, cudaStream
   int64_t most = 0;
   for (int i = 0; i < count; ++i) {
     FfMat& m = *mats[i];
-    const int64_t bytes = ff_copy_bytes(m);
-    if (bytes == 0) continue;
-    const int64_t ld = round_up(m.cols, 8);
-    RepackParams& r = p.m[n++];
-    r.src = static_cast<const __half*>(m.p);
-    r.dst = reinterpret_cast<__half*>(ws);
-    r.src_ld = m.ld;
-    r.rows = static_cast<int>(m.rows);
-    r.cols = static_cast<int>(m.cols);
-    r.cols_pad = static_cast<int>(ld);
-    r.chunks = m.rows * (ld / 8);
+    if (ff_copy_bytes(m) == 0) continue;
     most = m.rows > most ? m.rows : most;
-    m.p = ws;
-    m.ld = ld;
-    ws += bytes;
+    ff_copy_plan(m, p.m[n++], ws);
   }
   if (n == 0) return TG_OK;
   int64_t blocks = (most + 7) / 8;  // eight warps, a row each

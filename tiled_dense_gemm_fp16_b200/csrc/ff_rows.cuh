@@ -351,50 +351,52 @@ __device__ __forceinline__ uint4 load_block(uintptr_t at, uintptr_t lo, uintptr_
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Row `row` of m, by a warp.
+__device__ __forceinline__ void pad_row(const RepackParams& m, int row, int lane) {
+  const int chunks = m.cols_pad >> 3;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(m.src);
+  const uintptr_t hi = lo + 2 * static_cast<uintptr_t>((m.rows - 1) * m.src_ld + m.cols);
+  const uintptr_t start = lo + 2 * static_cast<uintptr_t>(row * m.src_ld);
+  const uintptr_t first = start & ~uintptr_t(15);
+  const uint32_t shift = static_cast<uint32_t>(start - first);
+  uint4* dst = reinterpret_cast<uint4*>(m.dst + static_cast<int64_t>(row) * m.cols_pad);
+  // Four blocks of a lane in flight.
+  for (int c0 = lane; c0 - lane < chunks; c0 += 128) {
+    uint4 v[4], last[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 32 * i;
+      v[i] = last[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (c - lane < chunks) {
+        v[i] = load_block(first + 16 * static_cast<uintptr_t>(c), lo, hi);
+        if (lane == 31) last[i] = load_block(first + 16 * static_cast<uintptr_t>(c + 1), lo, hi);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = c0 + 32 * i;
+      if (c - lane >= chunks) break;
+      uint4 b = make_uint4(__shfl_down_sync(0xffffffffu, v[i].x, 1), __shfl_down_sync(0xffffffffu, v[i].y, 1),
+                           __shfl_down_sync(0xffffffffu, v[i].z, 1), __shfl_down_sync(0xffffffffu, v[i].w, 1));
+      if (lane == 31) b = last[i];
+      uint4 o = edge_realign(v[i], b, shift);
+      const int n = m.cols - c * 8;
+      if (n < 8) {  // the row's last values, then zeros
+        uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) w[q] = n >= 2 * q + 2 ? w[q] : n == 2 * q + 1 ? w[q] & 0xffffu : 0u;
+        o = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (c < chunks) dst[c] = o;
+    }
+  }
+}
+
 __global__ void __launch_bounds__(256) pad_set_kernel(const __grid_constant__ PadSetParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const RepackParams& m = p.m[blockIdx.y];
-  const int lane = threadIdx.x & 31;
-  const int chunks = m.cols_pad >> 3;
-  const uintptr_t lo = reinterpret_cast<uintptr_t>(m.src);
-  const uintptr_t hi = lo + 2 * static_cast<uintptr_t>((m.rows - 1) * m.src_ld + m.cols);
-  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < m.rows; row += gridDim.x * 8) {
-    const uintptr_t start = lo + 2 * static_cast<uintptr_t>(row * m.src_ld);
-    const uintptr_t first = start & ~uintptr_t(15);
-    const uint32_t shift = static_cast<uint32_t>(start - first);
-    uint4* dst = reinterpret_cast<uint4*>(m.dst + static_cast<int64_t>(row) * m.cols_pad);
-    // Four blocks of a lane in flight.
-    for (int c0 = lane; c0 - lane < chunks; c0 += 128) {
-      uint4 v[4], last[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 32 * i;
-        v[i] = last[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (c - lane < chunks) {
-          v[i] = load_block(first + 16 * static_cast<uintptr_t>(c), lo, hi);
-          if (lane == 31) last[i] = load_block(first + 16 * static_cast<uintptr_t>(c + 1), lo, hi);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = c0 + 32 * i;
-        if (c - lane >= chunks) break;
-        uint4 b = make_uint4(__shfl_down_sync(0xffffffffu, v[i].x, 1), __shfl_down_sync(0xffffffffu, v[i].y, 1),
-                             __shfl_down_sync(0xffffffffu, v[i].z, 1), __shfl_down_sync(0xffffffffu, v[i].w, 1));
-        if (lane == 31) b = last[i];
-        uint4 o = edge_realign(v[i], b, shift);
-        const int n = m.cols - c * 8;
-        if (n < 8) {  // the row's last values, then zeros
-          uint32_t w[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = n >= 2 * q + 2 ? w[q] : n == 2 * q + 1 ? w[q] & 0xffffu : 0u;
-          o = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        if (c < chunks) dst[c] = o;
-      }
-    }
-  }
+  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < m.rows; row += gridDim.x * 8) pad_row(m, row, threadIdx.x & 31);
 }
 
 }  // namespace tg

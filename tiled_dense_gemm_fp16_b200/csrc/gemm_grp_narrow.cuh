@@ -40,7 +40,7 @@ struct GrpNarrowCfg {
     return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups);
   }
   static constexpr int lora_bytes(int tokens, int splits) {
-    return 4 * kLoraTBytes + delta_bytes(tokens, splits);
+    return delta_bytes(tokens, splits);
   }
   static_assert((2 * MAX_STAGES + 7) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
@@ -52,6 +52,11 @@ struct GrpTileAdapters {
   __device__ __forceinline__ void load(const LoraParams& l, int tok0, int cnt, int lane) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = 32 * i + lane < cnt ? lora_adapter(l, tok0 + 32 * i + lane) : -1;
+  }
+  // Of token t + lane, for 16 lanes and t a multiple of 16.
+  __device__ __forceinline__ int from(int t) const {
+    const int i = t >> 5, lane = threadIdx.x & 31;
+    return __shfl_sync(0xffffffffu, i == 0 ? a[0] : i == 1 ? a[1] : i == 2 ? a[2] : a[3], (t & 31) + (lane & 15));
   }
   // Of token t, the same in the whole warp.
   __device__ __forceinline__ int of(int t) const {
@@ -75,7 +80,7 @@ __device__ __forceinline__ void grp_narrow_store(const GrpParams& p, float (&v)[
 
 // LORA as in the pair kernel.
 template <int LORA>
-__global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
+__global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that makes T finds registers beside it
     grp_narrow_kernel(const __grid_constant__ GrpMaps maps, const GrpNarrowParams p) {
   using Cfg = GrpNarrowCfg;
   extern __shared__ uint8_t smem_raw[];
@@ -248,8 +253,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     __syncwarp();
   } else {
     const int quad = warp & 3;
-    uint8_t* tbuf = reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + quad * kLoraTBytes;  // adapters only
-    float* delta = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups) + 4 * kLoraTBytes);
+    float* delta = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(plan.lo) + grp_plan_align(p.g.groups));  // adapters only
     const int e = quad * 32 + lane;  // also the column of the panel that this thread sends
     const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
     const int pitch = p.tokens + 4;
@@ -263,7 +267,9 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
     for (int t = cluster_id; t < num_tiles; t += num_clusters) {
       const GrpTile f = walk.at(plan, t, p.g.col_tiles, p.g.super, p.tokens, Cfg::UNIT);
       const int n0 = f.col_blk * Cfg::PANEL + rank * own;
-      const int items = own * ((f.cnt + 7) / 8);  // (column, eight tokens)
+      // Units of 32 columns and TOK tokens, the warps in turn.
+      constexpr int TOK = LORA ? kLoraTokens : 8;
+      const int col_blocks = own / 32, units = col_blocks * ((f.cnt + TOK - 1) / TOK);
       if (f.g == p.g.groups) {
         const unsigned short zero = 0;
         for (int it = e; it < own * f.cnt; it += 128)
@@ -273,7 +279,7 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       }
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
       if (LORA && early) {
-        // The adapters' part, while the tile is computed: it is this thread's own
+        // The adapters' part, while the tile is computed: it is this warp's own
         // until the sums are there.  The first tile's rows of B come into L2 before
         // T is waited for.
         GrpTileAdapters adapters;
@@ -290,18 +296,10 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
           grid_launch_dependents();
           waited = true;
         }
-        for (int it = e; it < items; it += 128) {  // whole warps: own is a multiple of 32
-          const int col = it % own, tok = it / own * 8;
-          int a[kLoraTokens];
-          float d[kLoraTokens];
-#pragma unroll
-          for (int q = 0; q < kLoraTokens; ++q) {
-            a[q] = adapters.of(tok + q);
-            d[q] = 0.0f;
-          }
-          lora_add<LORA == 2>(p.g.lora, d, a, f.tok0 + tok, n0 + col, n0 + col < p.g.out, tbuf, lane);
-#pragma unroll
-          for (int q = 0; q < kLoraTokens; ++q) delta[col * pitch + tok + q] = d[q];
+        for (int u = quad; u < units; u += 4) {
+          const int col = u % col_blocks * 32, tok = u / col_blocks * TOK;
+          const int mine = adapters.from(tok);
+          lora_part<LORA == 2>(p.g.lora, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
         }
       }
       const int acc = local & 1;
@@ -340,24 +338,28 @@ __global__ void __launch_bounds__(GrpNarrowCfg::THREADS, 1)
       if (p.splits == 1) continue;
       ready = mbar_wait_cluster(part_full_bar, (local - 1) & 1, abort_flag, p.g.wait_budget_ns, 0xb8);
       if (!__all_sync(0xffffffffu, ready)) break;
-      for (int it = e; it < items; it += 128) {  // whole warps: own is a multiple of 32
-        const int col = it % own, tok = it / own * 8;
-        const float* at = recv + col * pitch + tok;
-        float v[8];
-        for (int q = 0; q < p.splits; ++q) {
+      for (int u = quad; u < units; u += 4) {
+        const int col = u % col_blocks * 32 + lane;
 #pragma unroll
-          for (int h = 0; h < 8; h += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(at + q * own * pitch + h);
-            v[h] = q == 0 ? x.x : v[h] + x.x;
-            v[h + 1] = q == 0 ? x.y : v[h + 1] + x.y;
-            v[h + 2] = q == 0 ? x.z : v[h + 2] + x.z;
-            v[h + 3] = q == 0 ? x.w : v[h + 3] + x.w;
+        for (int tok = u / col_blocks * TOK, i = 0; i < TOK; i += 8, tok += 8) {
+          if (tok >= f.cnt) break;
+          const float* at = recv + col * pitch + tok;
+          float v[8];
+          for (int q = 0; q < p.splits; ++q) {
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+              const float4 x = *reinterpret_cast<const float4*>(at + q * own * pitch + h);
+              v[h] = q == 0 ? x.x : v[h] + x.x;
+              v[h + 1] = q == 0 ? x.y : v[h + 1] + x.y;
+              v[h + 2] = q == 0 ? x.z : v[h + 2] + x.z;
+              v[h + 3] = q == 0 ? x.w : v[h + 3] + x.w;
+            }
           }
+          grp_narrow_store(p.g, v, f, tok, n0 + col, LORA && early ? delta + col * pitch + tok : nullptr,
+                           LORA && p.g.lora.bias != nullptr && n0 + col < p.g.out
+                               ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + col, p.g.bf16 != 0)
+                               : 0.0f);
         }
-        grp_narrow_store(p.g, v, f, tok, n0 + col, LORA && early ? delta + col * pitch + tok : nullptr,
-                         LORA && p.g.lora.bias != nullptr && n0 + col < p.g.out
-                             ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + col, p.g.bf16 != 0)
-                             : 0.0f);
       }
       __syncwarp();
       // Relaxed: the values read have been used, and nothing else is ordered.

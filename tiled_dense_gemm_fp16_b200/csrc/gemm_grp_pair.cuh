@@ -12,11 +12,11 @@
 // result leaves transposed: a lane of TMEM is a column of Y, so a warp stages
 // 32 x 32 boxes with a row per token.
 //
-// Adapters: each 32 tokens that share one get its product from the tensor cores,
-// as further k-blocks into their own 32 columns of the accumulator, so that no
-// adapter's values meet another request's rows, not even times zero.  Tokens of
-// several adapters within 32 (decoding requests beside each other, the ends of
-// prompts) get theirs in the epilogue, in fp32.
+// Adapters: each 32 tokens that share one get its product as further k-blocks into
+// their own 32 columns of the accumulator, so that no adapter's values meet
+// another request's rows, not even times zero.  Tokens of several adapters within
+// 32 (decoding requests beside each other, the ends of prompts) get theirs from the
+// epilogue's warps (lora_part).
 #pragma once
 
 #include "grp_ops.cuh"
@@ -88,64 +88,101 @@ __device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraR
   return true;
 }
 
-// v[q] += sum_j B_a[n][j] T[m][j] in fp32 for 8 tokens m = m0 + q, each with its adapter a[q] (negative: none), and this
-// lane's column n.  By a whole warp with the same tokens: T comes by way of `tbuf` (512 bytes of shared memory), 32 ranks at a
-// time, and B's rows from L2 with 16 loads of a lane in flight (8, one step ahead of the products, took twice the time).  Tokens
-// with the adapter of the one before them share its row.
-constexpr int kLoraTokens = 8;
-constexpr int kLoraTBytes = kLoraTokens * 32 * 2;
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8) on the warp-level tensor cores.
 template <bool BF16>
-__device__ __forceinline__ void lora_add(const LoraParams& l, float (&v)[kLoraTokens], const int (&a)[kLoraTokens], int m0, int n,
-                                         bool column, uint8_t* tbuf, int lane) {
-  bool any = false;
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if (BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The adapters' part of 32 columns from n0 on and 16 tokens from m0 on, by a warp
+// whose lane t < 16 holds token t's adapter (negative: none): sum_j B_a[n][j] T[m][j]
+// in fp32 to out[column * pitch + token].
+//
+// For each adapter among the tokens the warp multiplies its 32 rows of B by all 16
+// rows of T and keeps the columns of its own tokens: columns of a product do not
+// depend on each other, so nothing of one adapter reaches another's tokens.
+// Within 32 ranks a thread's fragments are 8 adjacent ones (the order of the sum
+// is free), so all loads are 16 bytes, and rows are read 64 bytes at a time; 32 ranks
+// of 4 adapters, or 128 of one, are in flight together.  (A thread a column, with
+// fused multiply-adds, read each row in pieces of its own: 3000 cycles for 16 ranks
+// of 8 tokens.)
+constexpr int kLoraTokens = 16;
+template <bool BF16>
+__device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0, int n0, int N, float* out, int pitch, int lane) {
+  const int row = lane >> 2, q = lane & 3;
+  const unsigned tokens = __ballot_sync(0xffffffffu, lane < kLoraTokens && mine >= 0);
+  const int steps = (l.rank + 31) >> 5;
+  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0 + row) * l.rank + q * 8;
+  const unsigned short* b = static_cast<const unsigned short*>(l.b) + (n0 + row) * l.ldb + q * 8;
+  float d[2][2][4], p[2][2][4];  // [16 columns][8 tokens]: the results, and the adapter's at hand
 #pragma unroll
-  for (int q = 0; q < kLoraTokens; ++q) any = any || a[q] >= 0;
-  if (!any) return;
-  const unsigned short* b = static_cast<const unsigned short*>(l.b) + n * l.ldb;
-  // Lane i fetches 8 ranks of token i / 4.
-  int ta = -1;
+  for (int i = 0; i < 16; ++i) d[i >> 3][i >> 2 & 1][i & 3] = 0.0f;
+  unsigned left = tokens, mask = 0;
+  int adapter = -1, step = steps;
+  while (left != 0 || step < steps) {
+    int at[4];         // first rank, negative: nothing
+    unsigned done[4];  // the tokens that take the sum after it
+    uint4 x[4][4], y[4][2];
 #pragma unroll
-  for (int q = 0; q < kLoraTokens; ++q) ta = (lane >> 2) == q ? a[q] : ta;
-  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0 + (lane >> 2)) * l.rank + (lane & 3) * 8;
-  float2 s[kLoraTokens];
-#pragma unroll
-  for (int q = 0; q < kLoraTokens; ++q) s[q] = make_float2(0.0f, 0.0f);
-#pragma unroll 1
-  for (int j = 0; j < l.rank; j += 16) {
-    uint4 x[kLoraTokens][2], tv = make_uint4(0u, 0u, 0u, 0u);
-    if ((j & 16) == 0 && ta >= 0 && j + (lane & 3) * 8 < l.rank) tv = ld_global_v4(t + j);
-#pragma unroll
-    for (int q = 0; q < kLoraTokens; ++q) {
-      if (q > 0 && a[q] == a[q - 1]) {
-        x[q][0] = x[q - 1][0];
-        x[q][1] = x[q - 1][1];
-        continue;
+    for (int i = 0; i < 4; ++i) {
+      if (step == steps && left != 0) {
+        adapter = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+        mask = __ballot_sync(0xffffffffu, mine == adapter) & tokens;
+        left &= ~mask;
+        step = 0;
       }
-      x[q][0] = x[q][1] = make_uint4(0u, 0u, 0u, 0u);
-      const unsigned short* row = b + a[q] * l.stride_b + j;
-      if (column && a[q] >= 0) x[q][0] = __ldg(reinterpret_cast<const uint4*>(row));
-      if (column && a[q] >= 0 && j + 8 < l.rank) x[q][1] = __ldg(reinterpret_cast<const uint4*>(row + 8));
-    }
-    if ((j & 16) == 0) {
-      __syncwarp();  // the ranks before have been read
-      *reinterpret_cast<uint4*>(tbuf + lane * 16) = tv;
-      __syncwarp();
-    }
+      at[i] = step < steps ? step * 32 : -1;
+      step = min(step + 1, steps);
+      done[i] = step == steps ? mask : 0u;
+      const bool in = at[i] >= 0 && at[i] + q * 8 < l.rank;
 #pragma unroll
-    for (int q = 0; q < kLoraTokens; ++q)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 y = *reinterpret_cast<const uint4*>(tbuf + q * 64 + (j & 16) * 2 + i * 16);
-        s[q] = fma2(unpack_16(x[q][i].x, BF16), unpack_16(y.x, BF16), s[q]);
-        s[q] = fma2(unpack_16(x[q][i].y, BF16), unpack_16(y.y, BF16), s[q]);
-        s[q] = fma2(unpack_16(x[q][i].z, BF16), unpack_16(y.z, BF16), s[q]);
-        s[q] = fma2(unpack_16(x[q][i].w, BF16), unpack_16(y.w, BF16), s[q]);
+      for (int r = 0; r < 4; ++r) {
+        x[i][r] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && n0 + row + 8 * r < N)
+          x[i][r] = __ldg(reinterpret_cast<const uint4*>(b + adapter * l.stride_b + 8 * r * l.ldb + at[i]));
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        y[i][h] = make_uint4(0u, 0u, 0u, 0u);
+        if (in && (tokens >> (row + 8 * h) & 1u)) y[i][h] = ld_global_v4(t + 8 * h * l.rank + at[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (at[i] < 0) break;
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (at[i] == 0)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[c][h][e] = 0.0f;
+          const uint4 &u = x[i][2 * c], &v = x[i][2 * c + 1], &w = y[i][h];
+          mma_16816<BF16>(p[c][h], u.x, v.x, u.y, v.y, w.x, w.y);
+          mma_16816<BF16>(p[c][h], u.z, v.z, u.w, v.w, w.z, w.w);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (done[i] >> (8 * h + 2 * q + (e & 1)) & 1u) d[c][h][e] = p[c][h][e];
+        }
+    }
   }
-  __syncwarp();
 #pragma unroll
-  for (int q = 0; q < kLoraTokens; ++q)
-    if (a[q] >= 0) v[q] += s[q].x + s[q].y;
+  for (int c = 0; c < 2; ++c)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) out[(16 * c + 8 * (e >> 1) + row) * pitch + 8 * h + 2 * q + (e & 1)] = d[c][h][e];
+  __syncwarp();
 }
 
 // A token's adapter, or -1.
@@ -153,6 +190,10 @@ __device__ __forceinline__ int lora_adapter(const LoraParams& l, int m) {
   const int a = __ldg(l.index + m);
   return a >= 0 && a < l.adapters ? a : -1;
 }
+
+// A warp's adapters' part: [32 columns][16 tokens + 1].
+constexpr int kPartPitch = kLoraTokens + 1;
+constexpr int kPartBytes = 32 * kPartPitch * 4;
 
 struct GrpPairCfg {
   static constexpr int STAGES = 6;                 // of the widest tiles; more of narrower ones
@@ -174,9 +215,10 @@ struct GrpPairCfg {
   static constexpr int BAR_BYTES = 256;
   static constexpr int FIXED_SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + STAGING + BAR_BYTES;
   static constexpr int smem_bytes(int groups, bool lora) {
-    return FIXED_SMEM + (lora ? grp_plan_align(1) + EPI_WARPS * kLoraTBytes : grp_plan_align(groups));
+    return FIXED_SMEM + (lora ? grp_plan_align(1) + EPI_WARPS * kPartBytes : grp_plan_align(groups));
   }
-  static_assert(FIXED_SMEM + (kGrpMaxGroups + 4) * 8 + WIDTHS * 4 <= 232448, "dynamic shared memory per CTA");
+  static_assert(FIXED_SMEM + (kGrpMaxGroups + 4) * 8 + WIDTHS * 4 <= 232448 &&
+                    FIXED_SMEM + 32 + EPI_WARPS * kPartBytes + WIDTHS * 4 <= 232448, "dynamic shared memory per CTA");
   static_assert((2 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(A_BYTES % 1024 == 0 && PANEL_BYTES % 1024 == 0 && B_BYTES % 1024 == 0 && UNIT / 2 * 128 % 1024 == 0,
                 "operand tiles, and the pieces of rows they are loaded in, start on the swizzle's 1024 bytes");
@@ -469,8 +511,8 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     constexpr int PARTS = Cfg::EPI_WARPS / 4;
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
     uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
-    uint8_t* tbuf = staging + Cfg::STAGING + Cfg::BAR_BYTES + grp_plan_align(p.groups) +
-                    (warp - Cfg::EPI_WARP0) * kLoraTBytes;  // adapters only
+    float* part_buf = reinterpret_cast<float*>(staging + Cfg::STAGING + Cfg::BAR_BYTES + grp_plan_align(p.groups) +
+                                               (warp - Cfg::EPI_WARP0) * kPartBytes);  // adapters only
     constexpr bool BF16 = LORA == 2;
     const bool bf16 = LORA ? BF16 : p.bf16 != 0;
     GrpWalk walk;
@@ -528,22 +570,13 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           bar_128(1 + part);
         if (mixed) {
           const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + e0 + lane) : -1;
-#pragma unroll 1
-          for (int e = 0; e < rows; e += kLoraTokens) {
-            uint32_t r[kLoraTokens];
-            float v[kLoraTokens];
-            int a[kLoraTokens];
-            tmem_ld_32x32b_x8(taddr + b * 32 + e0 + e, r);
-            tmem_ld_wait();
+          lora_part<BF16>(p.lora, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(taddr + b * 32 + e0, r);
+          tmem_ld_wait();
 #pragma unroll
-            for (int q = 0; q < kLoraTokens; ++q) {
-              v[q] = __uint_as_float(r[q]);
-              a[q] = __shfl_sync(0xffffffffu, mine, e + q);
-            }
-            lora_add<BF16>(p.lora, v, a, f.tok0 + b * 32 + e0 + e, n, n < p.out, tbuf, lane);
-#pragma unroll
-            for (int q = 0; q < kLoraTokens; ++q) put(e + q, v[q]);
-          }
+          for (int e = 0; e < kLoraTokens; ++e) put(e, __uint_as_float(r[e]) + part_buf[lane * kPartPitch + e]);
+          __syncwarp();  // read, before the next box's
         } else {
           uint32_t r[32];
           if (!zero) {

@@ -74,25 +74,67 @@ int64_t grp_copy_bytes(const GrpStack& s) {
   return up256(2 * s.mats * s.m.rows * round_up(s.m.cols, 8));
 }
 
-// The copies of x and w (either may be null) that a product needs, in one launch; advances `ws`.
-tg_status grp_make_copies(FfMat* x, FfMat* y, GrpStack* w, uint8_t*& ws, cudaStream_t stream, DeviceInfo* info) {
-  FfMat rows{nullptr, 0, 0, 1, 2};
-  FfMat* mats[3];
+// Padded copies, those of the weights of groups with rows only.
+struct GrpPadParams {
+  PadSetParams set;
+  const int* ends;
+  int M, weights, rows_each;  // which of the set are the weights, and rows of one
+};
+__global__ void __launch_bounds__(256) grp_pad_kernel(const __grid_constant__ GrpPadParams p) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const RepackParams& m = p.set.m[blockIdx.y];
+  for (int row = blockIdx.x * 8 + (threadIdx.x >> 5); row < m.rows; row += gridDim.x * 8) {
+    if (static_cast<int>(blockIdx.y) == p.weights) {
+      const int g = row / p.rows_each;
+      if (grp_end(p.ends, g, p.M) <= grp_end(p.ends, g - 1, p.M)) continue;
+    }
+    pad_row(m, row, threadIdx.x & 31);
+  }
+}
+
+// The copies of those of x, y and w (which may be null) that TMA cannot describe, in one launch; advances `ws`.
+tg_status grp_make_copies(FfMat* x, FfMat* y, GrpStack* w, const int32_t* ends, int64_t M, uint8_t*& ws, cudaStream_t stream,
+                          DeviceInfo* info) {
+  if (w == nullptr || w->empty() || w->on16()) {
+    FfMat* mats[2];
+    int n = 0;
+    if (x) mats[n++] = x;
+    if (y) mats[n++] = y;
+    return ff_make_copies(mats, n, ws, stream, info);
+  }
+  GrpPadParams p;
+  std::memset(&p, 0, sizeof p);
+  FfMat rows = w->rows();
+  FfMat* mats[3] = {x, y, &rows};
   int n = 0;
-  if (x) mats[n++] = x;
-  if (y) mats[n++] = y;
-  const bool copy_w = w && !w->empty() && !w->on16();
-  if (copy_w) {
-    rows = w->rows();
-    mats[n++] = &rows;
+  int64_t most = 0;
+  for (FfMat* m : mats) {
+    if (m == nullptr || (m != &rows && ff_copy_bytes(*m) == 0)) continue;
+    if (m == &rows) p.weights = n;
+    most = m->rows > most ? m->rows : most;
+    ff_copy_plan(*m, p.set.m[n++], ws);
   }
-  const tg_status st = ff_make_copies(mats, n, ws, stream, info);
-  if (copy_w) {
-    w->m.p = rows.p;
-    w->m.ld = rows.ld;
-    w->stride = w->m.rows * rows.ld;
+  w->m.p = rows.p;
+  w->m.ld = rows.ld;
+  w->stride = w->m.rows * rows.ld;
+  p.ends = ends;
+  p.M = static_cast<int>(M);
+  p.rows_each = static_cast<int>(w->m.rows);
+  int64_t blocks = (most + 7) / 8;  // eight warps, a row each
+  const int64_t cap = static_cast<int64_t>(info->sm_count) * 8;
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks > cap ? cap : blocks), static_cast<unsigned>(n), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 1);
+  if (cudaLaunchKernelEx(&cfg, grp_pad_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
   }
-  return st;
+  return TG_OK;
 }
 
 bool grp_encode3(CUtensorMap* map, const GrpStack& s, int box_cols, int box_rows,
@@ -212,18 +254,34 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
   return known;
 }
 
-// CTAs that share a sum.  Two keep the tiles of a decoding batch even over the
-// SMs (60 groups' weights of 2048 x 4096: 157 / 152 / 159 us with 1 / 2 / 4); where
-// few panels are all there is to do, four shorten the way through one (one token
-// through 4096 x 4096 with its adapter: 19 / 16 / 15).  Short sums do not pay for
-// the exchange.
-int grp_splits(const GrpProduct& f, int k_blocks) {
-  if (k_blocks < 8) return 1;
-  const int64_t panels = (f.out + 127) / 128 * (f.a.rows < f.groups ? f.a.rows : f.groups);
-  return k_blocks >= 16 && panels <= 40 ? 4 : 2;
+// Estimated times in us.  The pair kernel: a wave of tiles takes 0.222 a k-block, 5.2 before and after.
+double grp_pair_us(const GrpProduct& f, int64_t live, int k_blocks, DeviceInfo* info) {
+  const int64_t rows = f.a.rows, pairs = info->sm_count / 2;
+  const int64_t tiles = ((rows + 255) / 256 > live ? (rows + 255) / 256 : live) * ((f.out + 255) / 256);
+  const double work = static_cast<double>((tiles + pairs - 1) / pairs) * k_blocks * 0.222;
+  const double stream = static_cast<double>(live) * f.out * f.red * 2.0 / 5.6e6;  // of the weights from memory
+  return 5.2 + (work > stream ? work : stream);
 }
 
-tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream, DeviceInfo* info) {
+// The narrow kernel: a k-block takes 0.26 (up to 0.56 of 128 tokens); finishing a tile 1 + 0.03 a token alone,
+// 2.2 + 0.045 with the exchange, while the next one's sums are under way.  Measured,
+// us, narrow / pair, for g groups of n rows: 16 x 8 through 4096 x 512 (two splits)
+// 23.4 / 14.7, 4 x 32 through 256 x 4096 10.6 / 19.4, 16 x 128 through 1024 x 1024 29 /
+// 12, 16 x 8 through 2048 x 4096 44.5 / 48.2, 1 x 8 through 1024 x 1024 6.7 / 8.9.
+double grp_narrow_us(const GrpProduct& f, int64_t live, int k_blocks, int tokens, int splits, DeviceInfo* info) {
+  const int64_t rows = f.a.rows;
+  const int64_t tiles = ((rows + tokens - 1) / tokens > live ? (rows + tokens - 1) / tokens : live) * ((f.out + 127) / 128);
+  const int64_t fit = info->sm_count / splits - (splits > 2 ? 4 : 0);  // clusters of four leave some SMs out
+  const double rounds = static_cast<double>((tiles + fit - 1) / fit);
+  // Of 128 tokens the ring is short: felt where most SMs have a CTA.
+  const double main = (k_blocks + splits - 1) / splits * (tokens < 128 || tiles * splits <= info->sm_count / 2 ? 0.26 : 0.56);
+  const double finish = splits == 1 ? 1.0 + 0.03 * tokens : 2.2 + 0.045 * tokens;
+  const double work = (splits < 4 ? 2.9 : 3.5) + main + (rounds - 1.0) * (main > finish ? main : finish) + finish;
+  const double stream = 5.0 + static_cast<double>(live) * f.out * f.red * 2.0 / 6.3e6;
+  return work > stream ? work : stream;
+}
+
+tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = GrpNarrowCfg;
   const int kind = f.lora ? (f.bf16 ? 2 : 1) : 0;
   auto kernel = kind == 0 ? grp_narrow_kernel<0> : kind == 1 ? grp_narrow_kernel<1> : grp_narrow_kernel<2>;
@@ -239,7 +297,7 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
-  int splits = tune_int("TG_TUNE_GRP_SPLITS", grp_splits(f, p.g.k_blocks));
+  splits = tune_int("TG_TUNE_GRP_SPLITS", splits);
   while (splits > p.g.k_blocks) splits >>= 1;
   p.splits = splits;
   // As deep as fits a CTA an SM, or (adapters) beside the kernel that makes T, which is still at work.
@@ -270,18 +328,37 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, cudaStream_t stream
   return TG_OK;
 }
 
-// Few rows a group take the narrow kernel, and so do products whose tiles would
-// leave half the pairs without one.
+// Which kernel, by estimated time.  With adapters the host does not know how many
+// there are among the rows: where each row has its own, both kernels compute their
+// part outside the tensor cores; where runs share one, the pair kernel has it on
+// them.  So up to 96 rows, and 128 with long sums, take the narrow kernel, whose
+// CTAs share that part as well (us, narrow / pair: 64 rows through 4096 x 4096, rank
+// 64, 64 adapters 36 / 60, one 23 / 24; 128 rows 67 / 88 and 24 / 24; 96 rows through
+// 512 x 512, rank 16, 32 / 43 and 18 / 13; 128 rows 38 / 37 and 22 / 12).
 tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
   const int64_t rows = f.a.rows, live = rows < f.groups ? rows : f.groups;  // groups that can have rows
   const int64_t each = (rows + live - 1) / live;
-  const int64_t tiles = ((rows + 255) / 256 > live ? (rows + 255) / 256 : live) * ((f.out + 255) / 256);
-  const bool narrow = tune_int("TG_TUNE_GRP_NARROW", each <= 64 || 4 * tiles <= info->sm_count ? 1 : 0) != 0;
-  if (!narrow) return launch_grp_pair(f, stream, info);
+  const int k_blocks = static_cast<int>((f.red + 63) / 64);
   // Twice the even share, so that a group with more is one tile as a rule.
-  int tokens = 16;
+  int tokens = 16, splits = 1;
   while (tokens < 128 && tokens < (live > 1 ? 2 * each : each)) tokens <<= 1;
-  return launch_grp_narrow(f, tokens, stream, info);
+  bool narrow;
+  if (f.lora && f.l.adapters > 0) {
+    narrow = rows <= 96 || (rows <= 128 && k_blocks >= 32);
+    splits = k_blocks >= 8 && (f.out + 127) / 128 <= 40 ? 4 : 2;
+  } else {
+    double best = grp_narrow_us(f, live, k_blocks, tokens, 1, info);
+    for (int s = 2; s <= 4 && s <= k_blocks; s *= 2) {
+      const double us = grp_narrow_us(f, live, k_blocks, tokens, s, info);
+      if (us < best) {
+        best = us;
+        splits = s;
+      }
+    }
+    narrow = best < grp_pair_us(f, live, k_blocks, info);
+  }
+  if (tune_int("TG_TUNE_GRP_NARROW", narrow ? 1 : 0) == 0) return launch_grp_pair(f, stream, info);
+  return launch_grp_narrow(f, tokens, splits, stream, info);
 }
 
 // A result that is a sum over nothing: +0 in the rows of the groups, or in all with `rest`.
@@ -365,7 +442,7 @@ tg_status run_grouped(GroupedArgs& a, const int32_t* ends, void* stream_ptr, voi
   cudaStream_t stream = static_cast<cudaStream_t>(stream_ptr);
   if (a.K == 0 || a.groups == 0) return grp_zero(a.y, ends, a.groups, a.rest, stream, info);
   uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
-  if ((st = grp_make_copies(&a.x, nullptr, &a.w, ws, stream, info)) != TG_OK) return st;
+  if ((st = grp_make_copies(&a.x, nullptr, &a.w, ends, a.M, ws, stream, info)) != TG_OK) return st;
   GrpProduct f;
   f.a = a.x;
   f.c = a.y;
@@ -474,7 +551,7 @@ tg_status run_grouped_grad(GroupedArgs& a, const int32_t* ends, void* stream_ptr
     return want_x ? grp_zero(a.dx, ends, a.groups, a.rest, stream, info) : TG_OK;
   }
   uint8_t* ws = static_cast<uint8_t*>(ws_ptr);
-  if ((st = grp_make_copies(&a.y, want_w ? &a.x : nullptr, want_x ? &a.w : nullptr, ws, stream, info)) != TG_OK) return st;
+  if ((st = grp_make_copies(&a.y, want_w ? &a.x : nullptr, want_x ? &a.w : nullptr, ends, a.M, ws, stream, info)) != TG_OK) return st;
   if (want_w && (st = launch_grp_wgrad(a, ends, stream, info)) != TG_OK) return st;
   if (!want_x) return TG_OK;
   GrpProduct f;
@@ -551,21 +628,22 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.rank = static_cast<int>(l.rank);
   p.adapters = static_cast<int>(l.adapters);
   p.k_blocks = static_cast<int>((l.K + 63) / 64);
-  // Blocks of 16 tokens for a decoding batch, whose tokens have few neighbours of their own adapter.
-  p.tokens = l.M <= 16 ? 16 : l.M <= 128 ? 32 : 128;
+  // Small blocks for a decoding batch, whose tokens have few neighbours of their own
+  // adapter, and where whole ones would leave SMs without one.
+  p.tokens = l.M <= 16 ? 16 : l.M <= 128 ? 32 : l.M <= 64 * info->sm_count ? 64 : 128;
   for (int i = 0; i < 4 && 16 << i <= p.tokens; ++i)
     if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
   const int64_t deep = (l.rank + 127) / 128;
   p.splits = 1;
   const int64_t most = tune_int("TG_TUNE_SHRINK_SPLITS", 4);
-  while (p.splits < most && 4 * p.splits <= p.k_blocks && blocks * deep * p.splits * 2 <= 2 * info->sm_count) p.splits *= 2;
+  while (p.splits < most && 4 * p.splits <= p.k_blocks && blocks * deep * p.splits * 2 <= info->sm_count) p.splits *= 2;
   // Clusters for the items of a block: as many as it may have, while they find SMs.
   int64_t y = 4 * info->sm_count / (blocks * deep * p.splits);
   const int64_t items = l.M < p.tokens ? l.M : p.tokens;
   y = y < 1 ? 1 : y > items ? items : y;
   y = y > l.adapters ? l.adapters : y;
-  const int deepest = ((p.tokens == 128 ? 96 * 1024 : kShrinkSmem) - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  const int deepest = ((p.tokens > 32 ? 96 * 1024 : kShrinkSmem) - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
   p.per_stage = tune_int("TG_TUNE_SHRINK_PER", 2);
   while (p.per_stage > 1 && deepest < 4 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;

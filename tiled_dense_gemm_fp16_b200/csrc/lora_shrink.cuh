@@ -2,7 +2,7 @@
 // T[m][j] = scale_a sum_k A_a[j][k] X[m][k] with a = index[m].
 //
 // Bound by reading X and the used adapters' A.  An item is one adapter among a
-// block of 128 tokens, and up to 128 rows of its A: these are the MMA's M side
+// block of up to 128 tokens, and up to 128 rows of its A: these are the MMA's M side
 // (rows behind the rank are whatever lies in shared memory behind them, in lanes
 // that nobody reads), the tokens from the adapter's first to its last in the block the N side.
 // Columns of D are independent, so tokens of other adapters in between cost
@@ -283,7 +283,29 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
     for (int d = blockIdx.y; d < count; d += step) {
       const int adapter = items.adapter[d], t0 = items.first[d] & ~15, width = ((items.last[d] & ~15) + 16) - t0;
       const int fours = width / 4, mine = (fours - rank + p.splits - 1) / p.splits;  // those of this CTA: rank, rank + splits, ...
+      const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
       bool ready = mbar_wait(acc_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd6);
+      if (p.splits == 1) {  // nothing to exchange
+        if (!__all_sync(0xffffffffu, ready)) break;
+        tcgen05_fence_after_sync();
+        for (int c = 0; c < width && quad * 32 < rows; c += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c, r);
+          const int m = m0 + t0 + c;
+          const int owner = lane < 16 && m + lane < p.M ? __ldg(p.index + m + lane) : -1;
+          const unsigned mine_of = __ballot_sync(0xffffffffu, owner == adapter);
+          tmem_ld_wait();
+          unsigned short* dst = static_cast<unsigned short*>(p.t) + static_cast<int64_t>(m) * p.rank + j0 + j;
+#pragma unroll
+          for (int q = 0; q < 16; ++q)
+            if (j < rows && (mine_of >> q & 1u)) dst[q * p.rank] = round_16(__uint_as_float(r[q]) * scale, p.bf16 != 0);
+        }
+        tcgen05_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty_bar);
+        ++local;
+        continue;
+      }
       if (ready) ready = mbar_wait_cluster(part_empty_bar, (local & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xd7);
       if (!__all_sync(0xffffffffu, ready)) break;
       tcgen05_fence_after_sync();
@@ -312,7 +334,6 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
       }
       ready = mbar_wait_cluster(part_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd8);
       if (!__all_sync(0xffffffffu, ready)) break;
-      const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
       for (int it = e; it < mine * rows; it += 128) {
         const int four = it / rows, row = it - four * rows;
         float4 s = recv[four * p.a_rows + row];
