@@ -21,10 +21,10 @@ struct GrpWgradMaps {
 };
 
 // One box of results to matrix z of a stack.
-__device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap* map, const void* smem_src, int x, int y, int z, uint64_t policy) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int x, int y, int z) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
-               "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "l"(policy)
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z)
                : "memory");
 }
 
@@ -42,7 +42,7 @@ struct GrpWgradParams {
 };
 
 struct GrpWgradCfg {
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 5;
   static constexpr int BM = 128;
   static constexpr int TILE = 256;
   static constexpr int PANEL_BYTES = 64 * 128;
@@ -54,7 +54,8 @@ struct GrpWgradCfg {
   static constexpr int EPI_WARPS = 8;
   static constexpr int THREADS = (EPI_WARP0 + EPI_WARPS) * 32;
   static constexpr int TMEM_COLS = 512;
-  static constexpr int STAGING = EPI_WARPS * kGrpBoxBytes;
+  static constexpr int BOX_BYTES = 2 * kGrpBoxBytes;  // a warp's two staging boxes
+  static constexpr int STAGING = EPI_WARPS * BOX_BYTES;
   static constexpr int BAR_BYTES = 256;
   static constexpr int FIXED_SMEM = 1024 + STAGES * (A_BYTES + B_BYTES) + STAGING + BAR_BYTES;
   static constexpr int smem_bytes(int groups) { return FIXED_SMEM + (groups + 1) * 4; }
@@ -62,26 +63,42 @@ struct GrpWgradCfg {
   static_assert((3 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers");
 };
 
-// Tile t: group, place, rows of the sum.
+// The tiles of one cluster, in turn: group, place, rows of the sum.
 struct GrpWgradTile {
   int g, n_blk, k_blk;
   int lo, rows;
 };
-__device__ __forceinline__ GrpWgradTile grp_wgrad_tile(const GrpWgradParams& p, const int* ends, int t) {
-  GrpWgradTile f;
-  const int per = p.n_tiles * p.k_tiles;
-  f.g = t / per;
-  const int local = t - f.g * per;
-  // Eight tiles of dY's columns next to each other for one of X's.
-  const int s = local / (8 * p.k_tiles);
-  const int wide = min(8, p.n_tiles - 8 * s);
-  const int in = local - s * 8 * p.k_tiles;
-  f.k_blk = in / wide;
-  f.n_blk = 8 * s + in - f.k_blk * wide;
-  f.lo = uniform(ends[f.g]);
-  f.rows = max(0, uniform(ends[f.g + 1]) - f.lo);
-  return f;
-}
+struct GrpWgradWalk {
+  int g, local;  // tile of the group; from one tile to the next by subtraction
+  float inv_last;  // of the last, narrower strip
+
+  __device__ __forceinline__ GrpWgradWalk(const GrpWgradParams& p, int first) {
+    g = first / (p.n_tiles * p.k_tiles);
+    local = first - g * p.n_tiles * p.k_tiles;
+    inv_last = 1.0f / static_cast<float>(max(1, p.n_tiles % 8));
+  }
+  __device__ __forceinline__ void skip(const GrpWgradParams& p, int tiles) {
+    local += tiles;
+    for (const int per = p.n_tiles * p.k_tiles; local >= per; ++g) local -= per;
+  }
+  // By a whole warp.
+  __device__ __forceinline__ GrpWgradTile tile(const GrpWgradParams& p, const int* ends) const {
+    GrpWgradTile f;
+    f.g = g;
+    // Eight tiles of dY's columns next to each other for one of X's.
+    int s = 0, in = local;
+    while (in >= 8 * p.k_tiles && 8 * (s + 1) < p.n_tiles) {
+      in -= 8 * p.k_tiles;
+      ++s;
+    }
+    const int wide = min(8, p.n_tiles - 8 * s);
+    f.k_blk = wide == 8 ? in >> 3 : quick_div(in, wide, inv_last);
+    f.n_blk = 8 * s + in - f.k_blk * wide;
+    f.lo = uniform(ends[g]);
+    f.rows = max(0, uniform(ends[g + 1]) - f.lo);
+    return f;
+  }
+};
 
 __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     grp_wgrad_kernel(const __grid_constant__ GrpWgradMaps maps, const GrpWgradParams p) {
@@ -147,8 +164,9 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     bool ok = true;
     const uint64_t pol = l2_policy_evict_normal();
     const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
-    for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
-      const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
+    GrpWgradWalk walk(p, cluster_id);
+    for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters, walk.skip(p, num_clusters)) {
+      const GrpWgradTile f = walk.tile(p, ends);
       const int n0 = f.n_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
       const int k0 = f.k_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM;
       for (int r = 0; r < f.rows; r += 64) {
@@ -205,8 +223,9 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
       const uint64_t a_desc0 = make_sw128_desc(smem_u32(a_smem), Cfg::PANEL_BYTES, 1024);
       const uint64_t b_desc0 = make_sw128_desc(smem_u32(b_smem), Cfg::PANEL_BYTES, 1024);
       const uint32_t tmem = uniform(tmem_base);
-      for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters) {
-        const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
+      GrpWgradWalk walk(p, cluster_id);
+      for (int t = cluster_id; t < p.num_tiles && ok; t += num_clusters, walk.skip(p, num_clusters)) {
+        const GrpWgradTile f = walk.tile(p, ends);
         if (f.rows == 0) continue;
         const int acc = local & 1;
         if (!mbar_wait_warp(&acc_empty_bar[acc], ((local >> 1) & 1) ^ 1u, abort_flag, p.wait_budget_ns, 0xc3)) break;
@@ -248,8 +267,9 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
     const uint32_t full_even0 = mapa_shared(smem_u32(full_bar), 0);
     int stage = 0;
     uint32_t tail_phase = 0;  // a bit a stage
-    for (int t = cluster_id; t < p.num_tiles; t += num_clusters) {
-      const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
+    GrpWgradWalk walk(p, cluster_id);
+    for (int t = cluster_id; t < p.num_tiles; t += num_clusters, walk.skip(p, num_clusters)) {
+      const GrpWgradTile f = walk.tile(p, ends);
       const int blocks = (f.rows + 63) / 64;
       if (blocks == 0) continue;
       const int last = (stage + blocks - 1) % Cfg::STAGES;
@@ -273,12 +293,13 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
   } else {
     const int quad = warp & 3;
     const int part = (warp - Cfg::EPI_WARP0) >> 2;
-    uint8_t* box = staging + (warp - Cfg::EPI_WARP0) * kGrpBoxBytes;
+    uint8_t* boxes = staging + (warp - Cfg::EPI_WARP0) * Cfg::BOX_BYTES;
+    int turn = 0;
     const bool bf16 = p.bf16 != 0;
-    const uint64_t pol = l2_policy_evict_first();
     int local = 0;
-    for (int t = cluster_id; t < p.num_tiles; t += num_clusters) {
-      const GrpWgradTile f = grp_wgrad_tile(p, ends, t);
+    GrpWgradWalk walk(p, cluster_id);
+    for (int t = cluster_id; t < p.num_tiles; t += num_clusters, walk.skip(p, num_clusters)) {
+      const GrpWgradTile f = walk.tile(p, ends);
       const int n0 = f.n_blk * Cfg::TILE + static_cast<int>(rank) * Cfg::BM + quad * 32;
       const bool zero = f.rows == 0;
       const int acc = local & 1;
@@ -306,8 +327,9 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
           for (int e = 0; e < 16; ++e) h[e] = 0u;
         }
         // As ff_store_box, with TMA boxes of one matrix of the stack.
+        uint8_t* box = boxes + (turn++ & 1) * kGrpBoxBytes;
         if (p.vec && (k0 + 32 <= p.K || (p.K & 7) == 0)) {
-          if (lane == 0) bulk_wait_group_read<0>();  // the box before has left
+          if (lane == 0) bulk_wait_group_read<1>();  // the last but one has left
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 4; ++q)
@@ -315,11 +337,11 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d_hint(&maps.c, box, k0, n0, f.g, pol);
+            tma_store_3d(&maps.c, box, k0, n0, f.g);
             bulk_commit_group();
           }
         } else {
-          ff_store_box<1>(nullptr, dst - n0 * p.ldc, p.ldc, false, p.N, p.K, n0, k0, h, box, lane, pol);
+          ff_store_box<2>(nullptr, dst - n0 * p.ldc, p.ldc, false, p.N, p.K, n0, k0, h, box, lane, 0);
         }
       }
       if (!zero) {

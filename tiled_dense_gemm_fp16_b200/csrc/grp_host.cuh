@@ -12,7 +12,6 @@ namespace tg {
 namespace {
 
 constexpr int64_t kLoraMaxRank = 512;
-constexpr int kShrinkSmem = 48 * 1024;  // of the kernel that makes T for a decoding batch
 constexpr int64_t kLoraMaxAdapters = int64_t(1) << 20;
 
 // current_device, with the device's context bound to this host thread.  Encoding a
@@ -300,12 +299,11 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
   splits = tune_int("TG_TUNE_GRP_SPLITS", splits);
   while (splits > p.g.k_blocks) splits >>= 1;
   p.splits = splits;
-  // As deep as fits a CTA an SM, or (adapters) beside the kernel that makes T, which is still at work.
+  // As deep as fits a CTA an SM, less a little for the kernel that makes T, which is still at work beside it.
   const bool adapted = f.lora && f.l.adapters > 0;
   const int fixed = Cfg::smem_bytes(tokens, 0, f.groups) + (adapted ? Cfg::lora_bytes(tokens, splits) : 0);
   const int stage_bytes = Cfg::W_BYTES + tokens * 128;
-  int deepest = (232448 - fixed) / stage_bytes;
-  if (adapted && (232448 - fixed - kShrinkSmem - 2048) / stage_bytes >= 3) deepest = (232448 - fixed - kShrinkSmem - 2048) / stage_bytes;
+  const int deepest = (232448 - (adapted ? 4096 : 0) - fixed) / stage_bytes;
   p.per_stage = tune_int("TG_TUNE_GRP_PER", 2);
   while (p.per_stage > 1 && deepest < 3 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;
@@ -328,13 +326,16 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
   return TG_OK;
 }
 
-// Which kernel, by estimated time.  With adapters the host does not know how many
-// there are among the rows: where each row has its own, both kernels compute their
-// part outside the tensor cores; where runs share one, the pair kernel has it on
-// them.  So up to 96 rows, and 128 with long sums, take the narrow kernel, whose
-// CTAs share that part as well (us, narrow / pair: 64 rows through 4096 x 4096, rank
-// 64, 64 adapters 36 / 60, one 23 / 24; 128 rows 67 / 88 and 24 / 24; 96 rows through
-// 512 x 512, rank 16, 32 / 43 and 18 / 13; 128 rows 38 / 37 and 22 / 12).
+// With adapters the host does not know how many there are among the rows: where
+// each row has its own, both kernels compute their part outside the large tensor
+// cores; where runs share one, the pair kernel has it on them.  So up to 96 rows, and
+// 128 with long sums, take the narrow kernel, whose CTAs share that part as well (us,
+// narrow / pair: 64 rows through 4096 x 4096, rank 64, 64 adapters 36 / 60, one 23 / 24;
+// 128 rows 67 / 88 and 24 / 24; 96 rows through 512 x 512, rank 16, 32 / 43 and 18 / 13;
+// 128 rows 38 / 37 and 22 / 12).
+bool grp_lora_narrow(const GrpProduct& f) { return f.a.rows <= 96 || (f.a.rows <= 128 && f.red > 31 * 64); }
+
+// Which kernel, by estimated time.
 tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
   const int64_t rows = f.a.rows, live = rows < f.groups ? rows : f.groups;  // groups that can have rows
   const int64_t each = (rows + live - 1) / live;
@@ -344,7 +345,7 @@ tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info)
   while (tokens < 128 && tokens < (live > 1 ? 2 * each : each)) tokens <<= 1;
   bool narrow;
   if (f.lora && f.l.adapters > 0) {
-    narrow = rows <= 96 || (rows <= 128 && k_blocks >= 32);
+    narrow = grp_lora_narrow(f);
     splits = k_blocks >= 8 && (f.out + 127) / 128 <= 40 ? 4 : 2;
   } else {
     double best = grp_narrow_us(f, live, k_blocks, tokens, 1, info);
@@ -610,6 +611,35 @@ int64_t lora_workspace(const LoraArgs& l) {
   return inner + ff_copy_bytes(l.x) + ff_copy_bytes(l.w);
 }
 
+// T of few tokens.
+tg_status launch_lora_rows(const LoraArgs& l, const GrpProduct& f, const float* scale, cudaStream_t stream) {
+  LoraRowsParams p;
+  std::memset(&p, 0, sizeof p);
+  p.x = l.x.p;
+  p.a = l.a.m.p;
+  p.index = f.l.index;
+  p.scale = scale;
+  p.t = const_cast<void*>(f.l.t);
+  p.ldx = l.x.ld;
+  p.lda = l.a.m.ld;
+  p.stride_a = l.a.stride;
+  p.K = static_cast<int>(l.K);
+  p.rank = static_cast<int>(l.rank);
+  p.adapters = static_cast<int>(l.adapters);
+  cudaLaunchConfig_t cfg;
+  std::memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(static_cast<unsigned>(l.M), static_cast<unsigned>((l.rank + kLoraRowsWarps - 1) / kLoraRowsWarps), 1);
+  cfg.blockDim = dim3(kLoraRowsWarps * 32, 1, 1);
+  cfg.stream = stream;
+  LaunchAttrs la;
+  la.fill(cfg, 1);
+  if (cudaLaunchKernelEx(&cfg, l.bf16 ? lora_rows_kernel<true> : lora_rows_kernel<false>, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TG_ERR_LAUNCH;
+  }
+  return TG_OK;
+}
+
 // T and the kinds of 32 tokens.
 tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float* scale, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = LoraShrinkCfg;
@@ -628,9 +658,8 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.rank = static_cast<int>(l.rank);
   p.adapters = static_cast<int>(l.adapters);
   p.k_blocks = static_cast<int>((l.K + 63) / 64);
-  // Small blocks for a decoding batch, whose tokens have few neighbours of their own
-  // adapter, and where whole ones would leave SMs without one.
-  p.tokens = l.M <= 16 ? 16 : l.M <= 128 ? 32 : l.M <= 64 * info->sm_count ? 64 : 128;
+  // Small blocks where large ones would leave SMs without one.
+  p.tokens = l.M <= 32 * info->sm_count / 4 ? 32 : l.M <= 64 * info->sm_count ? 64 : 128;
   for (int i = 0; i < 4 && 16 << i <= p.tokens; ++i)
     if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
@@ -643,7 +672,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   const int64_t items = l.M < p.tokens ? l.M : p.tokens;
   y = y < 1 ? 1 : y > items ? items : y;
   y = y > l.adapters ? l.adapters : y;
-  const int deepest = ((p.tokens > 32 ? 96 * 1024 : kShrinkSmem) - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
+  const int deepest = (96 * 1024 - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
   p.per_stage = tune_int("TG_TUNE_SHRINK_PER", 2);
   while (p.per_stage > 1 && deepest < 4 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;
@@ -710,13 +739,16 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
   }
   FfMat* const operands[2] = {&l.x, &l.w};
   if ((st = ff_make_copies(operands, 2, ws, stream, info)) != TG_OK) return st;
-  if (adapted && (st = launch_lora_shrink(l, f, scale, stream, info)) != TG_OK) return st;
   f.a = l.x;
   f.c = l.y;
   f.w = GrpStack{l.w, 1, 0};
   f.out = l.N;
   f.red = l.K;
   f.bf16 = l.bf16;
+  if (adapted) {
+    st = grp_lora_narrow(f) ? launch_lora_rows(l, f, scale, stream) : launch_lora_shrink(l, f, scale, stream, info);
+    if (st != TG_OK) return st;
+  }
   return launch_grp(f, stream, info);
 }
 

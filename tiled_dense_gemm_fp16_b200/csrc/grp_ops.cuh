@@ -64,6 +64,23 @@ __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cl
 // ----------------------------------------------------------------------------
 // Groups
 // ----------------------------------------------------------------------------
+// n / d for n >= 0, d > 0 with inv = 1 / d: every warp of a kernel places its tiles
+// by divisions, and the compiler's takes 150 cycles or more one after the other.
+// The product is off by one where n / d < 2^22, and by little beyond.
+__device__ __forceinline__ int quick_div(int n, int d, float inv) {
+  int q = __float2int_rz(__int2float_rn(n) * inv);
+  int64_t r = n - static_cast<int64_t>(q) * d;
+  while (r < 0) {
+    --q;
+    r += d;
+  }
+  while (r >= d) {
+    ++q;
+    r -= d;
+  }
+  return q;
+}
+
 // Group g owns rows [ends[g - 1], ends[g]) of X (from 0 for g = 0).  The ends
 // are data on the device, so nothing on the host depends on them and a captured
 // graph may be replayed with others.  They are clamped to [0, M], and a group
@@ -82,7 +99,7 @@ struct GrpCut {
 };
 __host__ __device__ __forceinline__ GrpCut grp_cut(int rows, int most, int unit) {
   GrpCut c;
-  c.tiles = (rows + most - 1) / most;  // `most` and `unit` are powers of two
+  c.tiles = rows <= most ? 1 : (rows + most - 1) / most;
   c.whole = c.tiles - 1;
   c.width = 0;
   const int last = rows - c.whole * most;
@@ -163,7 +180,7 @@ struct GrpWalk {
       const int s = cut.tiles > super ? local / (super * col_tiles) : 0;
       const int wide = min(super, cut.tiles - s * super);
       const int in = local - s * super * col_tiles;
-      f.col_blk = in / wide;
+      f.col_blk = quick_div(in, wide, 1.0f / static_cast<float>(wide));
       i = s * super + in - f.col_blk * wide;
     }
     grp_cut_tile(cut, rows, most, i, f.tok0, f.cnt);
