@@ -299,7 +299,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
         for (int u = quad; u < units; u += 4) {
           const int col = u % col_blocks * 32, tok = u / col_blocks * TOK;
           const int mine = adapters.from(tok);
-          lora_part<LORA == 2>(p.g.lora, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
+          lora_part<LORA == 2, 4>(p.g.lora, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
         }
       }
       const int acc = local & 1;

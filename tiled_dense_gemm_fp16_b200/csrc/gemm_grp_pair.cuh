@@ -71,18 +71,19 @@ __device__ __forceinline__ int ld_global_s32(const int* p) {
   return v;
 }
 
-// Runs of 32-token groups of a tile that share an adapter, in order; for a whole warp.
+// Runs of 32-token groups of a tile that share an adapter, in order; for a whole
+// warp, whose lanes hold the groups' kinds.
 struct LoraRun {
   int first, count, adapter;
 };
-__device__ __forceinline__ bool lora_next_run(const int* kind, int groups, LoraRun& run) {
+__device__ __forceinline__ bool lora_next_run(int kinds, int groups, LoraRun& run) {
   int i = run.first + run.count;
   int r = kLoraNone;
-  while (i < groups && (r = uniform(ld_global_s32(kind + i))) < 0) ++i;
+  while (i < groups && (r = __shfl_sync(0xffffffffu, kinds, i)) < 0) ++i;
   if (i >= groups) return false;
   run.first = i;
   run.adapter = r;
-  while (++i < groups && uniform(ld_global_s32(kind + i)) == r) {
+  while (++i < groups && __shfl_sync(0xffffffffu, kinds, i) == r) {
   }
   run.count = i - run.first;
   return true;
@@ -113,11 +114,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // depend on each other, so nothing of one adapter reaches another's tokens.
 // Within 32 ranks a thread's fragments are 8 adjacent ones (the order of the sum
 // is free), so all loads are 16 bytes, and rows are read 64 bytes at a time; 32 ranks
-// of 4 adapters, or 128 of one, are in flight together.  (A thread a column, with
-// fused multiply-adds, read each row in pieces of its own: 3000 cycles for 16 ranks
-// of 8 tokens.)
+// of ITEMS adapters, or 32 ITEMS of one, are in flight together.  As many as the
+// registers hold: beside 220 KiB of shared memory a spill goes to L2 and back.  The
+// pair kernel takes 3 (7414 mixed rows, 880 x 1110, rank 112: 81 us, 2 take 79, 4
+// take 90; 16384 rows, 4096 x 4096, rank 64: 422, 436, 450), the narrow one 4.  (A
+// thread a column, with fused multiply-adds, read each row in pieces of its own: 3000
+// cycles for 16 ranks of 8 tokens.)
 constexpr int kLoraTokens = 16;
-template <bool BF16>
+template <bool BF16, int ITEMS>
 __device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0, int n0, int N, float* out, int pitch, int lane) {
   const int row = lane >> 2, q = lane & 3;
   const unsigned tokens = __ballot_sync(0xffffffffu, lane < kLoraTokens && mine >= 0);
@@ -130,11 +134,11 @@ __device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0,
   unsigned left = tokens, mask = 0;
   int adapter = -1, step = steps;
   while (left != 0 || step < steps) {
-    int at[4];         // first rank, negative: nothing
-    unsigned done[4];  // the tokens that take the sum after it
-    uint4 x[4][4], y[4][2];
+    int at[ITEMS];         // first rank, negative: nothing
+    unsigned done[ITEMS];  // the tokens that take the sum after it
+    uint4 x[ITEMS][4], y[ITEMS][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
       if (step == steps && left != 0) {
         adapter = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
         mask = __ballot_sync(0xffffffffu, mine == adapter) & tokens;
@@ -158,7 +162,7 @@ __device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0,
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < ITEMS; ++i) {
       if (at[i] < 0) break;
 #pragma unroll
       for (int c = 0; c < 2; ++c)
@@ -390,7 +394,8 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         if (!waited) grid_dependency_wait();
         waited = true;
         LoraRun run{0, 0, 0};
-        while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
+        const int kinds = lane < width / 32 ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone;
+        while (ok && lora_next_run(kinds, width / 32, run)) {
           for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
             if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
               ok = false;
@@ -470,7 +475,8 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           waited = true;
           const uint32_t idesc32 = p.idesc | (32u >> 3) << 17;
           LoraRun run{0, 0, 0};
-          while (ok && lora_next_run(p.lora.kind + f.tok0 / 32, width / 32, run)) {
+          const int kinds = lane < width / 32 ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone;
+          while (ok && lora_next_run(kinds, width / 32, run)) {
             for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
               if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
                 ok = false;
@@ -550,8 +556,10 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const int n = n0 + lane, cols = p.vec ? min(32, p.out - n0) : min(Cfg::BM, p.out - cta_n0);  // of a warp, or of four
       const float bias = LORA && p.lora.bias != nullptr && n < p.out
                              ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
+      unsigned mixed_boxes = 0;
+      if (early) mixed_boxes = __ballot_sync(0xffffffffu, (lane < boxes ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone) == kLoraMixed);
       for (int b = 0; b < boxes && cols > 0; ++b) {
-        const bool mixed = early && ld_global_s32(p.lora.kind + f.tok0 / 32 + b) == kLoraMixed;
+        const bool mixed = mixed_boxes >> b & 1u;
         if (!mixed && b % PARTS != part) continue;
         // A mixed box is shared: 16 tokens for each of the two warps that have these columns.
         const int e0 = mixed ? part * (32 / PARTS) : 0;
@@ -570,7 +578,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           bar_128(1 + part);
         if (mixed) {
           const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + e0 + lane) : -1;
-          lora_part<BF16>(p.lora, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
+          lora_part<BF16, 3>(p.lora, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
           uint32_t r[16];
           tmem_ld_32x32b_x16(taddr + b * 32 + e0, r);
           tmem_ld_wait();
