@@ -82,6 +82,28 @@ def test_strides(M, sizes, N, K, off):
         assert bool((rows[:, N:] == 9).all()) and bool((flat[:off + 16] == 9).all()) and bool((flat[off + 16 + M * (N + 5):] == 9).all())
 
 
+@pytest.mark.parametrize("stride", [8, 9, 40])
+@pytest.mark.parametrize("K", [5, 8])
+def test_weights_of_one_row(K, stride):
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    sizes = [30, 0, 34, 6]
+    x, w0, ends = _operands(70, sizes, 1, K, "f16")
+    dy = _randn(7, (70, 1), "f16")
+    w = _stack(w0, K, stride)
+    y, tol = ref.grouped(ref.f64(x), ref.f64(w0), sizes, "f16")
+    got = tg.grouped(x, w, ends)
+    grads = tg.grouped_backward(dy, x, w, ends)
+    leaf = w.detach().requires_grad_()
+    auto = tg.grouped_linear(x, leaf, ends)
+    auto.backward(dy)
+    _ok()
+    ref.check(ref.f64(got), y, tol, "y")
+    for name, g, o, t in zip(("dx", "dw"), grads, *ref.grouped_backward(ref.f64(dy), ref.f64(x), ref.f64(w0), sizes, "f16")):
+        ref.check(ref.f64(g), o, t, name)
+    assert torch.equal(auto, got) and torch.equal(leaf.grad, grads[1])
+
+
 @pytest.mark.parametrize("off", [0, 1, 4])
 @pytest.mark.parametrize("M,N,K", [(60, 72, 40), (60, 73, 41), (2700, 2311, 72)])
 def test_lora_strides(M, N, K, off):

@@ -140,6 +140,15 @@ def test_workspace_sizes():
     assert size(*P[:2], 0, M, N, K) == 0
 
 
+def test_weights_of_one_row():
+    """The row of each weight may lie anywhere: the distance between the weights is all that TMA or a copy needs."""
+    size = tg.grouped_workspace_size
+    assert size(*P[:2], 3, 16, 1, 5, tg.grouped_options(ldx=8, stride_w=8)) == 0
+    assert size(*P[:2], 3, 16, 1, 5, tg.grouped_options(ldx=8, stride_w=7)) == up(2 * 3 * 8)
+    assert size(*P[:2], 3, 16, 1, 5, tg.grouped_options(ldx=8, ldw=16)) == 0
+    assert size(*P[:2], 3, 16, 1, 8, tg.grouped_options(stride_w=9)) == up(2 * 3 * 8)
+
+
 def test_workspace_refusals():
     G, M, N, K = 5, 100, 41, 33
     need = tg.grouped_workspace_size(*P[:2], G, M, N, K)

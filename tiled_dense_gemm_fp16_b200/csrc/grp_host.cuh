@@ -63,6 +63,7 @@ GrpStack grp_stack(const void* p, int64_t mats, int64_t rows, int64_t cols, int6
   s.mats = mats;
   s.stride = stride;
   if (stride == 0) s.stride = rows <= kFfMaxSize && s.m.ld <= kFfMaxSpan / (rows + 1) ? rows * s.m.ld : 0;
+  if (rows == 1 && mats > 1 && s.stride >= cols) s.m.ld = s.stride;  // matrices of one row: the stack's rows
   return s;
 }
 
