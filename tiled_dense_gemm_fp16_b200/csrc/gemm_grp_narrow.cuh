@@ -137,8 +137,9 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
   cluster_sync();  // every CTA's barriers are initialised before any remote use
   tcgen05_fence_after_sync();
   const bool early = LORA != 0 && p.g.lora.adapters > 0;  // as in the pair kernel
+  const bool beside = LORA == 0 && p.g.beside != 0;
   if (!early) {
-    grid_dependency_wait();
+    if (!beside) grid_dependency_wait();
     grid_launch_dependents();
   }
   if (warp == Cfg::EPI_WARP0)
@@ -372,6 +373,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
     }
   }
 
+  if (beside) grid_dependency_wait();
   tcgen05_fence_before_sync();
   __syncthreads();
   cluster_sync();  // nobody writes to a CTA that has left

@@ -55,6 +55,7 @@ struct GrpParams {
   int adapt;                  // few tiles: their width is chosen in the kernel
   int vec;                    // rows of the result start on 16-byte boundaries
   int bf16;
+  int beside;                 // the kernel before this one writes nothing that it reads, and reads nothing that it writes
   uint32_t idesc;             // without N
   uint64_t wait_budget_ns;
   LoraParams lora;
@@ -298,8 +299,12 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
   // workspace's copies are there already; only T and kind are waited for, by
   // the threads that read them.
   const bool early = LORA != 0 && p.lora.adapters > 0;
+  // Gradients: the kernel before this one makes dW from the same dY.  It too waited
+  // for what came before it, so dX is computed beside its last tiles; only the end of
+  // this kernel waits for it, for those who wait for this one (see the end).
+  const bool beside = LORA == 0 && p.beside != 0;
   if (!early) {
-    grid_dependency_wait();
+    if (!beside) grid_dependency_wait();
     grid_launch_dependents();
   }
   // Tokens of a tile.  Few tiles leave pairs idle in the last wave, so the width is
@@ -624,6 +629,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
     }
   }
 
+  if (beside) grid_dependency_wait();
   tcgen05_fence_before_sync();
   __syncthreads();
   cluster_sync();  // the pair is done with each other's shared memory and barriers

@@ -160,6 +160,7 @@ struct GrpProduct {
   int groups = 1;
   int64_t out = 0, red = 0;
   bool transposed = false, rest = false, bf16 = false;
+  bool beside = false;  // see GrpParams
   bool lora = false;
   LoraParams l;
   GrpStack lb;  // with adapters
@@ -190,6 +191,7 @@ bool grp_fill(const GrpProduct& f, GrpMaps& maps, GrpParams& p, int weight_rows,
   p.w_mn = f.transposed ? 1 : 0;
   p.rest = f.rest ? 1 : 0;
   p.bf16 = f.bf16 ? 1 : 0;
+  p.beside = f.beside ? 1 : 0;
   p.wait_budget_ns = wait_budget(p.k_blocks);
   return true;
 }
@@ -565,6 +567,7 @@ tg_status run_grouped_grad(GroupedArgs& a, const int32_t* ends, void* stream_ptr
   f.out = a.K;
   f.red = a.N;
   f.transposed = true;
+  f.beside = want_w && tune_int("TG_TUNE_GRP_BESIDE", 1) != 0;
   f.rest = a.rest;
   f.bf16 = a.bf16;
   return launch_grp(f, stream, info);
