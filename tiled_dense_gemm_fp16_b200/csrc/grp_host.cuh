@@ -668,10 +668,14 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
     if (!ff_encode(&maps.x[i], l.x, 64, 16 << i, CU_TENSOR_MAP_SWIZZLE_128B)) return TG_ERR_LAUNCH;
   const int64_t blocks = (l.M + p.tokens - 1) / p.tokens;
   const int64_t deep = (l.rank + 127) / 128;
-  p.splits = 1;
-  const int64_t most = tune_int("TG_TUNE_SHRINK_SPLITS", 4);
-  while (p.splits < most && 4 * p.splits <= p.k_blocks && blocks * deep * p.splits * 2 <= info->sm_count) p.splits *= 2;
-  // Clusters for the items of a block: as many as it may have, while they find SMs.
+  // Two splits where that leaves SMs for both; four made the exchange between them dearer
+  // than what they saved (1049 rows of 40 requests, K = 2048, rank 32: 53.7 us against
+  // 58.2; 200 rows of one, K = 8192, rank 64: 42.5 / 46.9; no split 54.4 and 44.2).
+  p.splits = p.k_blocks >= 4 && blocks * deep * 2 <= info->sm_count ? 2 : 1;
+  // Clusters for the items of a block, as many as it may have, for four times the SMs at
+  // most: a batch of 60 adapters behind a prompt needs them (2048 rows: 195 us with
+  // half as many, 127 so), and one without an item costs a little (512 rows of 4
+  // requests through 4096 x 1024: 31.2 us, 28.9 with half as many, 33.9 with more).
   int64_t y = 4 * info->sm_count / (blocks * deep * p.splits);
   const int64_t items = l.M < p.tokens ? l.M : p.tokens;
   y = y < 1 ? 1 : y > items ? items : y;
