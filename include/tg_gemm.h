@@ -21,8 +21,9 @@
  * pointer to them after a call returns.  No call allocates or frees device
  * memory at run time.  Scratch memory comes from two places:
  *   - the caller: tg_gemm_relu_f16_ws, tg_gemm_relu_f16_ex,
- *     tg_gemm_relu_w4a16, tg_gated and tg_gated_backward take an optional (or,
- *     for some layouts, required) workspace pointer and size;
+ *     tg_gemm_relu_w4a16, tg_gated, tg_gated_backward, tg_grouped,
+ *     tg_grouped_backward and tg_lora take an optional (or, for some layouts
+ *     and calls, required) workspace pointer and size;
  *   - one fixed module buffer of TG_STATIC_WORKSPACE_BYTES (16 MiB) that the
  *     library holds on every GPU where it is loaded, until the process
  *     exits; only tg_gemm_relu_f16_static_ws uses it.

@@ -5,9 +5,14 @@
 // A cluster of S CTAs takes a panel of 128 weight rows and up to `tokens` rows of
 // one group and splits the sum over its CTAs.  Each CTA finishes 128 / S of the
 // panel's columns: the others write their partials into its shared memory, and
-// it adds them in rank order, so results do not depend on timing.  The kernel is persistent: which groups have rows is known on the device
-// only, so each cluster walks the tiles there are, its loads running ahead into
-// the next tile while the partials of the last one are added.
+// it adds them in rank order, so results do not depend on timing.  The kernel is
+// persistent: which groups have rows is known on the device only, so each cluster
+// walks the tiles there are, its loads running ahead into the next tile while the
+// partials of the last one are added.
+//
+// Bound by reading the weights that have rows: 512 rows in 60 of 64 groups of 2048 x
+// 4096 (1.01 GB) 155 us, 6.5 TB/s, the rate of a plain copy; 8 rows in 8 groups (134
+// MB) 26.7 us, 5.0 TB/s, of which 5 us are the launch and the first loads.
 #pragma once
 
 #include "gemm_ff_skinny.cuh"

@@ -17,6 +17,16 @@
 // another request's rows, not even times zero.  Tokens of several adapters within
 // 32 (decoding requests beside each other, the ends of prompts) get theirs from the
 // epilogue's warps (lora_part).
+//
+// Weights on the MMA's M side and tokens on its N side, since N may be any multiple
+// of 32: a group of 40 rows costs 64, not 256.
+//
+// Measured alone: 8192 rows, 8 groups, 4096 x 7168, 321 us, 1.50 PFLOP/s, tensor pipe
+// 83 % busy (one call after another the power cap holds it at 355-420).  Large tiles are
+// bound by the tensor pipe, narrower ones by their operands' way from L2 (about 50
+// bytes a cycle and SM), many groups of ~128 rows by reading the weights (64 of 1024 x
+// 2048, 268 MB, 60 us, 4.5 TB/s).  Adapters, 8192 rows of 8, 8192 x 4096, rank 64: 383
+// us, tensor pipe 77 % busy.
 #pragma once
 
 #include "grp_ops.cuh"
@@ -117,8 +127,8 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // is free), so all loads are 16 bytes, and rows are read 64 bytes at a time; 32 ranks
 // of ITEMS adapters, or 32 ITEMS of one, are in flight together.  As many as the
 // registers hold: beside 220 KiB of shared memory a spill goes to L2 and back.  The
-// pair kernel takes 3 (7414 mixed rows, 880 x 1110, rank 112: 81 us, 2 take 79, 4
-// take 90; 16384 rows, 4096 x 4096, rank 64: 422, 436, 450), the narrow one 4.  (A
+// pair kernel takes 3 (7414 mixed rows, 1110 x 880, rank 112: 81 us, 2 take 79, 4
+// take 90; 8192 rows of 8 requests, 8192 x 4096, rank 64: 422, 436, 450), the narrow one 4.  (A
 // thread a column, with fused multiply-adds, read each row in pieces of its own: 3000
 // cycles for 16 ranks of 8 tokens.)
 constexpr int kLoraTokens = 16;

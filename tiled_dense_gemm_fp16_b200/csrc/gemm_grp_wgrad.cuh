@@ -8,6 +8,13 @@
 // each CTA overwrites them with zeros in shared memory, in both operands (zeros
 // in one would still meet the other's infinities), before that block's MMAs; its
 // further 16-row steps are left out.  Groups without rows get zeros.
+//
+// Measured alone: 16384 rows in 8 groups, 4096 x 4096, 377 us, 1.46 PFLOP/s, tensor
+// pipe 81 % busy, which bounds it (and the power cap, in a row of calls).  8192 rows in 63 of 64 groups, 1024 x 2048: 83 us
+// for sums of two k-blocks a tile and 268 MB of results; bound by writing them (a plain
+// fill of as much memory takes 70 us here, 3.8 TB/s: writes have little more than half
+// of the rate of reads).  Not split over the rows: few tiles of long sums (one group of
+// 1992 rows, 128 x 104: 16 us) leave most pairs idle.
 #pragma once
 
 #include "grp_ops.cuh"

@@ -1,11 +1,14 @@
 // torch_calls.cpp -- the torch side of the feed-forward calls, the grouped
-// products and the adapters, as a CPython module: argument checks, allocation of results, and one call into the C ABI.
+// products and the adapters, as a CPython module: argument checks, allocation of
+// results, and one call into the C ABI.
 //
 // A decoding step makes these calls for 2-15 us of GPU work each, so what the
 // host spends on them counts.  Host time of a call at 16 x 64 x 64, written in
 // Python over ctypes and here: gated 8.8 and 4.3 us, with both projections
 // stored 11.9 and 5.7, the 8-bit product 9.2 and 4.2, quantization 8.3 and 4.4,
-// the backward pass (four launches) 21.6 and 11.4.  Two thirds and more of what
+// the backward pass (four launches) 21.6 and 11.4; here alone: a grouped product
+// 4.5, one row with an adapter (two launches) 7.3, a grouped product and its two
+// gradients 12.6.  Two thirds and more of what
 // is left are the launches themselves.  Nothing is computed here.
 #include <Python.h>
 
