@@ -298,6 +298,28 @@ def test_deep_adapters(rank):
         ref.check(ref.f64(got), y, tol, f"lora rank {rank} {kind}")
 
 
+# (rows, rank): few values of T, one and more a warp, ranks inside 32, rows whose values of T pass from one kernel to two.
+@pytest.mark.parametrize("M,rank", [(1, 8), (1, 16), (1, 128), (1, 512), (2, 40), (5, 8), (8, 16), (9, 16), (16, 8), (33, 8), (64, 8)])
+@pytest.mark.parametrize("N,K", [(72, 65), (264, 136), (2000, 4100), (5200, 1000), (129, 64), (40, 512)])
+@pytest.mark.parametrize("kind", ["random", "one", "none"])
+def test_few_rows(M, rank, N, K, kind):
+    """A value of T for each row and rank, by whichever kernel; twice in a row, since the second call may start early."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    R = 6
+    x, w, a0, b, index, ix = _lora_operands(M, N, K, rank, R, "bf16", kind, seed=M + rank)
+    lda = (K + 7) // 8 * 8
+    a = _stack(a0, lda, rank * lda)
+    scale = torch.rand(R, generator=torch.Generator().manual_seed(1)).cuda() + 0.5
+    bias = _randn(9, (N,), "bf16")
+    y, tol = ref.lora(ref.f64(x), ref.f64(w), ref.f64(a0), ref.f64(b), index, ref.f64(scale), ref.f64(bias), "bf16")
+    got = tg.lora(x, w, a, b, ix, scale=scale, bias=bias)
+    again = tg.lora(x, w, a, b, ix, scale=scale, bias=bias)
+    _ok()
+    ref.check(ref.f64(got), y, tol, f"lora {M} {rank} {N} {K} {kind}")
+    assert torch.equal(got, again)
+
+
 def test_many_groups():
     import tiled_dense_gemm_fp16_b200 as tg
     rng = np.random.default_rng(0)

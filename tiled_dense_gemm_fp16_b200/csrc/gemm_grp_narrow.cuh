@@ -25,6 +25,7 @@ struct GrpNarrowParams {
   int tokens;          // most of a tile: 16, 32, 64 or 128
   int splits, stages;  // 1, 2 or 4 splits
   int per_stage;       // k-blocks of a stage of the ring
+  int own_t;           // adapters: T is made here
   uint32_t tmem_cols;  // two accumulators
 };
 
@@ -44,10 +45,12 @@ struct GrpNarrowCfg {
   static constexpr int smem_bytes(int tokens, int stages, int groups) {
     return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups);
   }
-  static constexpr int lora_bytes(int tokens, int splits) {
-    return delta_bytes(tokens, splits);
+  // And T where it is made here, a value by each warp that finishes results.
+  static constexpr int own_t(int splits) { return 4 * splits; }
+  static constexpr int lora_bytes(int tokens, int splits, bool with_t) {
+    return delta_bytes(tokens, splits) + (with_t ? 2 * own_t(splits) : 0);
   }
-  static_assert((2 * MAX_STAGES + 7) * 8 + 8 <= BAR_BYTES, "barriers");
+  static_assert((2 * MAX_STAGES + 8) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
 };
 
@@ -83,6 +86,54 @@ __device__ __forceinline__ void grp_narrow_store(const GrpParams& p, float (&v)[
   }
 }
 
+// 8 values from p (on 16 bytes) on, of which n are in the row.
+__device__ __forceinline__ uint4 lora_row8(const unsigned short* p, int n) {
+  if (n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) w[e >> 1] |= static_cast<uint32_t>(__ldg(p + e)) << ((e & 1) * 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The inner product of two rows of K values, by a warp; DEEP times 256 values of each are in flight.
+template <bool BF16, int DEEP>
+__device__ __forceinline__ float lora_dot(const unsigned short* a, const unsigned short* x, int K, int lane) {
+  float2 s = make_float2(0.0f, 0.0f);
+  for (int k = lane * 8; k - lane * 8 < K; k += DEEP * 256) {
+    uint4 u[DEEP], v[DEEP];
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      u[i] = lora_row8(a + k + 256 * i, K - k - 256 * i);
+      v[i] = lora_row8(x + k + 256 * i, K - k - 256 * i);
+    }
+#pragma unroll
+    for (int i = 0; i < DEEP; ++i) {
+      s = fma2(unpack_16(u[i].x, BF16), unpack_16(v[i].x, BF16), s);
+      s = fma2(unpack_16(u[i].y, BF16), unpack_16(v[i].y, BF16), s);
+      s = fma2(unpack_16(u[i].z, BF16), unpack_16(v[i].z, BF16), s);
+      s = fma2(unpack_16(u[i].w, BF16), unpack_16(v[i].w, BF16), s);
+    }
+  }
+  float sum = s.x + s.y;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  return sum;
+}
+
+// T of all tokens, of which there are no more values than warps, into every CTA of
+// the cluster: value v by this warp.
+template <bool BF16>
+__device__ __forceinline__ void lora_own_t(const LoraParams& l, unsigned short* t, int M, int K, int v, int ctas, int lane) {
+  if (v >= M * l.rank) return;
+  const int m = v / l.rank, a = lora_adapter(l, m);
+  if (a < 0) return;
+  const float sum = lora_dot<BF16, 8>(static_cast<const unsigned short*>(l.a) + a * l.stride_a + (v - m * l.rank) * l.lda,
+                                      static_cast<const unsigned short*>(l.x) + m * l.ldx, K, lane);
+  const float scale = l.scale != nullptr ? __ldg(l.scale + a) : 1.0f;
+  if (lane < ctas) st_cluster_u16(mapa_shared(smem_u32(t + v), lane), round_16(sum * scale, BF16));
+}
+
 // LORA as in the pair kernel.
 template <int LORA>
 __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that makes T finds registers beside it
@@ -102,7 +153,8 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
   uint64_t* part_full_bar = acc_empty_bar + 2;   // every CTA's partials of this one's columns are here
   uint64_t* part_empty_bar = part_full_bar + 1;  // every CTA has added what this one sent
   uint64_t* mma_done_bar = part_empty_bar + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mma_done_bar + 1);
+  uint64_t* t_bar = mma_done_bar + 1;            // adapters: every CTA's values of T are here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(t_bar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   GrpPlan plan;
   plan.lo = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + Cfg::BAR_BYTES);
@@ -128,6 +180,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
     mbar_init(part_full_bar, 4);  // S sources, of each the 4 / S warps that hold this CTA's columns
     mbar_init(part_empty_bar, 4 * p.splits);
     mbar_init(mma_done_bar, 1);
+    mbar_init(t_bar, 4 * p.splits);
     *abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&maps.w);
@@ -141,7 +194,8 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
   __syncthreads();
   cluster_sync();  // every CTA's barriers are initialised before any remote use
   tcgen05_fence_after_sync();
-  const bool early = LORA != 0 && p.g.lora.adapters > 0;  // as in the pair kernel
+  const bool adapted = LORA != 0 && p.g.lora.adapters > 0;
+  const bool early = adapted && !p.own_t;  // as in the pair kernel
   const bool beside = LORA == 0 && p.g.beside != 0;
   if (!early) {
     if (!beside) grid_dependency_wait();
@@ -263,6 +317,8 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
     const int e = quad * 32 + lane;  // also the column of the panel that this thread sends
     const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
     const int pitch = p.tokens + 4;
+    unsigned short* own_t = reinterpret_cast<unsigned short*>(delta + own * pitch);
+    const void* const T = LORA && p.own_t ? own_t : p.g.lora.t;
     const int sent = e;
     const uint32_t owner = sent / own;
     const uint32_t to = mapa_shared(smem_u32(recv) + (rank * own + sent % own) * pitch * 4, owner);
@@ -284,7 +340,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
         continue;
       }
       const int width = (f.cnt + Cfg::UNIT - 1) / Cfg::UNIT * Cfg::UNIT;
-      if (LORA && early) {
+      if (LORA && adapted) {
         // The adapters' part, while the tile is computed: it is this warp's own
         // until the sums are there.  The first tile's rows of B come into L2 before
         // T is waited for.
@@ -298,14 +354,25 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
             for (int at = 0; at < p.g.lora.rank; at += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + at));
           }
           __syncwarp();
-          grid_dependency_wait();
-          grid_launch_dependents();
+          if (!p.own_t) {
+            grid_dependency_wait();
+            grid_launch_dependents();
+          } else {
+            lora_own_t<LORA == 2>(p.g.lora, own_t, p.g.M, p.g.red, rank * 4 + quad, p.splits, lane);
+            __syncwarp();
+            if (lane == 0) {
+              fence_cluster();
+              for (int q = 0; q < p.splits; ++q) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(t_bar), q));
+            }
+            const bool here = mbar_wait_cluster(t_bar, 0, abort_flag, p.g.wait_budget_ns, 0xb9);
+            if (!__all_sync(0xffffffffu, here)) break;
+          }
           waited = true;
         }
         for (int u = quad; u < units; u += 4) {
           const int col = u % col_blocks * 32, tok = u / col_blocks * TOK;
           const int mine = adapters.from(tok);
-          lora_part<LORA == 2, 4>(p.g.lora, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
+          lora_part<LORA == 2, 4>(p.g.lora, T, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
         }
       }
       const int acc = local & 1;
@@ -327,7 +394,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
             float v[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[h + q]);
-            grp_narrow_store(p.g, v, f, c + h, n0 + sent, LORA && early ? delta + sent * pitch + c + h : nullptr,
+            grp_narrow_store(p.g, v, f, c + h, n0 + sent, LORA && adapted ? delta + sent * pitch + c + h : nullptr,
                              LORA && p.g.lora.bias != nullptr && n0 + sent < p.g.out
                                  ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + sent, p.g.bf16 != 0)
                                  : 0.0f);
@@ -361,7 +428,7 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
               v[h + 3] = q == 0 ? x.w : v[h + 3] + x.w;
             }
           }
-          grp_narrow_store(p.g, v, f, tok, n0 + col, LORA && early ? delta + col * pitch + tok : nullptr,
+          grp_narrow_store(p.g, v, f, tok, n0 + col, LORA && adapted ? delta + col * pitch + tok : nullptr,
                            LORA && p.g.lora.bias != nullptr && n0 + col < p.g.out
                                ? load_16(static_cast<const unsigned short*>(p.g.lora.bias) + n0 + col, p.g.bf16 != 0)
                                : 0.0f);

@@ -49,6 +49,11 @@ struct LoraParams {
   const void* bias;           // N values, or nullptr
   int64_t ldb, stride_b;      // elements between rows and between adapters
   int rank, adapters;         // no adapters: only W's product and the bias
+  // Where the main product makes T itself:
+  const void* x;
+  const void* a;              // adapters' A
+  const float* scale;         // of each adapter, or nullptr
+  int64_t ldx, lda, stride_a;
 };
 enum { kLoraNone = -1, kLoraMixed = -2 };
 
@@ -71,9 +76,9 @@ struct GrpParams {
   LoraParams lora;
 };
 
-__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+__device__ __forceinline__ uint4 ld_v4(const void* p) {  // of any memory
   uint4 v;
-  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ int ld_global_s32(const int* p) {
@@ -133,11 +138,12 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // cycles for 16 ranks of 8 tokens.)
 constexpr int kLoraTokens = 16;
 template <bool BF16, int ITEMS>
-__device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0, int n0, int N, float* out, int pitch, int lane) {
+__device__ __forceinline__ void lora_part(const LoraParams& l, const void* T, int mine, int m0, int n0, int N, float* out, int pitch,
+                                          int lane) {
   const int row = lane >> 2, q = lane & 3;
   const unsigned tokens = __ballot_sync(0xffffffffu, lane < kLoraTokens && mine >= 0);
   const int steps = (l.rank + 31) >> 5;
-  const unsigned short* t = static_cast<const unsigned short*>(l.t) + static_cast<int64_t>(m0 + row) * l.rank + q * 8;
+  const unsigned short* t = static_cast<const unsigned short*>(T) + static_cast<int64_t>(m0 + row) * l.rank + q * 8;
   const unsigned short* b = static_cast<const unsigned short*>(l.b) + (n0 + row) * l.ldb + q * 8;
   float d[2][2][4], p[2][2][4];  // [16 columns][8 tokens]: the results, and the adapter's at hand
 #pragma unroll
@@ -169,7 +175,7 @@ __device__ __forceinline__ void lora_part(const LoraParams& l, int mine, int m0,
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         y[i][h] = make_uint4(0u, 0u, 0u, 0u);
-        if (in && (tokens >> (row + 8 * h) & 1u)) y[i][h] = ld_global_v4(t + 8 * h * l.rank + at[i]);
+        if (in && (tokens >> (row + 8 * h) & 1u)) y[i][h] = ld_v4(t + 8 * h * l.rank + at[i]);
       }
     }
 #pragma unroll
@@ -593,7 +599,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           bar_128(1 + part);
         if (mixed) {
           const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + e0 + lane) : -1;
-          lora_part<BF16, 3>(p.lora, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
+          lora_part<BF16, 3>(p.lora, p.lora.t, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
           uint32_t r[16];
           tmem_ld_32x32b_x16(taddr + b * 32 + e0, r);
           tmem_ld_wait();

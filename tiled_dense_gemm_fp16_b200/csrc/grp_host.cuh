@@ -299,14 +299,15 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
   p.tokens = tokens;
+  p.own_t = f.lora && f.l.adapters > 0 && f.l.t == nullptr ? 1 : 0;
   splits = tune_int("TG_TUNE_GRP_SPLITS", splits);
   while (splits > p.g.k_blocks) splits >>= 1;
   p.splits = splits;
   // As deep as fits a CTA an SM, less a little for the kernel that makes T, which is still at work beside it.
   const bool adapted = f.lora && f.l.adapters > 0;
-  const int fixed = Cfg::smem_bytes(tokens, 0, f.groups) + (adapted ? Cfg::lora_bytes(tokens, splits) : 0);
+  const int fixed = Cfg::smem_bytes(tokens, 0, f.groups) + (adapted ? Cfg::lora_bytes(tokens, splits, p.own_t != 0) : 0);
   const int stage_bytes = Cfg::W_BYTES + tokens * 128;
-  const int deepest = (232448 - (adapted ? 4096 : 0) - fixed) / stage_bytes;
+  const int deepest = (232448 - (adapted && !p.own_t ? 4096 : 0) - fixed) / stage_bytes;
   p.per_stage = tune_int("TG_TUNE_GRP_PER", 2);
   while (p.per_stage > 1 && deepest < 3 * p.per_stage) p.per_stage >>= 1;
   p.stages = deepest / p.per_stage;
@@ -338,6 +339,17 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
 // 128 rows 38 / 37 and 22 / 12).
 bool grp_lora_narrow(const GrpProduct& f) { return f.a.rows <= 96 || (f.a.rows <= 128 && f.red > 31 * 64); }
 
+// Splits of its sums then, of which there are at least two where it makes T itself.
+int grp_lora_splits(const GrpProduct& f) { return f.red > 7 * 64 && f.out <= 40 * 128 ? 4 : 2; }
+
+// Whether that kernel makes T itself, without a kernel before it: where that is a value
+// for each warp that waits for the sums anyway (us, so / with the kernel before: one
+// token through 4096 x 4096, rank 16, 12.6 / 13.5; with two values a warp 13.9 / 12.6,
+// four 15 / 12.8).
+bool grp_lora_own_t(const GrpProduct& f) {
+  return grp_lora_narrow(f) && f.red > 64 && f.a.rows * f.l.rank <= GrpNarrowCfg::own_t(grp_lora_splits(f));
+}
+
 // Which kernel, by estimated time.
 tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info) {
   const int64_t rows = f.a.rows, live = rows < f.groups ? rows : f.groups;  // groups that can have rows
@@ -349,7 +361,7 @@ tg_status launch_grp(const GrpProduct& f, cudaStream_t stream, DeviceInfo* info)
   bool narrow;
   if (f.lora && f.l.adapters > 0) {
     narrow = grp_lora_narrow(f);
-    splits = k_blocks >= 8 && (f.out + 127) / 128 <= 40 ? 4 : 2;
+    splits = grp_lora_splits(f);
   } else {
     double best = grp_narrow_us(f, live, k_blocks, tokens, 1, info);
     for (int s = 2; s <= 4 && s <= k_blocks; s *= 2) {
@@ -754,8 +766,18 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
   f.red = l.K;
   f.bf16 = l.bf16;
   if (adapted) {
-    st = grp_lora_narrow(f) ? launch_lora_rows(l, f, scale, stream) : launch_lora_shrink(l, f, scale, stream, info);
-    if (st != TG_OK) return st;
+    if (grp_lora_own_t(f)) {
+      f.l.t = nullptr;
+      f.l.x = l.x.p;
+      f.l.ldx = l.x.ld;
+      f.l.a = l.a.m.p;
+      f.l.lda = l.a.m.ld;
+      f.l.stride_a = l.a.stride;
+      f.l.scale = scale;
+    } else {
+      st = grp_lora_narrow(f) ? launch_lora_rows(l, f, scale, stream) : launch_lora_shrink(l, f, scale, stream, info);
+      if (st != TG_OK) return st;
+    }
   }
   return launch_grp(f, stream, info);
 }

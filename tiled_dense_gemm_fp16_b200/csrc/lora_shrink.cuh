@@ -17,7 +17,8 @@
 // there is no list, ring or exchange on the way from the index to T (whole call, one
 // token through 4096 x 4096, rank 16: 14.5 us with tiles, 13.4 so; 64 tokens of 64
 // adapters 29 and 24).  The main product runs meanwhile on the same SMs (it waits for
-// T only when its own sums are under way).
+// T only when its own sums are under way).  A token of up to 16 ranks goes without
+// either: the narrow kernel's warps make a value each.
 //
 // Measured: 8192 rows of 8 requests, K = 4096, rank 64, 30.9 us alone, 2.3 TB/s:
 // bound by the latency of a block's loads.  The main product hides most of it.
@@ -399,16 +400,6 @@ struct LoraRowsParams {
 
 constexpr int kLoraRowsWarps = 8;
 
-// 8 values from p (on 16 bytes) on, of which n are in the row.
-__device__ __forceinline__ uint4 lora_row8(const unsigned short* p, int n) {
-  if (n >= 8) return __ldg(reinterpret_cast<const uint4*>(p));
-  uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int e = 0; e < 7; ++e)
-    if (e < n) w[e >> 1] |= static_cast<uint32_t>(__ldg(p + e)) << ((e & 1) * 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 template <bool BF16>
 __global__ void __launch_bounds__(kLoraRowsWarps * 32) lora_rows_kernel(const LoraRowsParams p) {
   grid_dependency_wait();
@@ -420,26 +411,7 @@ __global__ void __launch_bounds__(kLoraRowsWarps * 32) lora_rows_kernel(const Lo
   const unsigned short* x = static_cast<const unsigned short*>(p.x) + m * p.ldx;
   const unsigned short* a = static_cast<const unsigned short*>(p.a) + adapter * p.stride_a + j * p.lda;
   const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
-  float2 s = make_float2(0.0f, 0.0f);
-  // Four times 256 values of K in flight.
-  for (int k = lane * 8; k - lane * 8 < p.K; k += 4 * 256) {
-    uint4 u[4], v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      u[i] = lora_row8(a + k + 256 * i, p.K - k - 256 * i);
-      v[i] = lora_row8(x + k + 256 * i, p.K - k - 256 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s = fma2(unpack_16(u[i].x, BF16), unpack_16(v[i].x, BF16), s);
-      s = fma2(unpack_16(u[i].y, BF16), unpack_16(v[i].y, BF16), s);
-      s = fma2(unpack_16(u[i].z, BF16), unpack_16(v[i].z, BF16), s);
-      s = fma2(unpack_16(u[i].w, BF16), unpack_16(v[i].w, BF16), s);
-    }
-  }
-  float sum = s.x + s.y;
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  const float sum = lora_dot<BF16, 4>(a, x, p.K, lane);
   if (lane == 0) static_cast<unsigned short*>(p.t)[static_cast<int64_t>(m) * p.rank + j] = round_16(sum * scale, BF16);
 }
 

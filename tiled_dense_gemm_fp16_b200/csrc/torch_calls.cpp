@@ -7,8 +7,8 @@
 // Python over ctypes and here: gated 8.8 and 4.3 us, with both projections
 // stored 11.9 and 5.7, the 8-bit product 9.2 and 4.2, quantization 8.3 and 4.4,
 // the backward pass (four launches) 21.6 and 11.4; here alone: a grouped product
-// 4.5, one row with an adapter (two launches) 7.3, a grouped product and its two
-// gradients 12.6.  Two thirds and more of what
+// 4.5, one row with an adapter 5.3, eight (two launches) 7.3, a grouped product and
+// its two gradients 12.  Two thirds and more of what
 // is left are the launches themselves.  Nothing is computed here.
 #include <Python.h>
 
