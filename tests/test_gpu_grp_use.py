@@ -402,6 +402,31 @@ def test_results_of_one_call_feed_the_next():
     _ok()
 
 
+def test_gradients_feed_the_next_call():
+    """dX is computed beside the last tiles of dW, and whoever reads either waits for both."""
+    import torch
+    import tiled_dense_gemm_fp16_b200 as tg
+    for M, G in ((24, 3), (900, 3), (4000, 5)):
+        w0 = _randn(1, (G, 256, 256), "f16", 256 ** -0.5)
+        ends = _ends([M // G] * (G - 1) + [M - M // G * (G - 1)])
+        x0, dy = _randn(4, (M, 256), "f16"), _randn(5, (M, 256), "f16", M ** -0.5 / 16)
+
+        def chain(wait):
+            x, w = x0, w0
+            for _ in range(6):
+                dx, dw = tg.grouped_backward(dy, x, w, ends)
+                wait()
+                y = tg.grouped(dx, dw, ends)
+                wait()
+                z, w = tg.grouped_backward(y, x0, w0, ends)
+                wait()
+                x = tg.grouped(z, dw, ends)
+                wait()
+            return x, w, dx, dw
+        assert _same(chain(torch.cuda.synchronize), chain(lambda: None))
+    _ok()
+
+
 def test_captured_calls_with_other_groups():
     import torch
     import tiled_dense_gemm_fp16_b200 as tg
