@@ -576,7 +576,8 @@ TG_API tg_status tg_gated_i8(const void *A, const float *a_scale, const void *Wg
  * set to +0.  No result may overlap an input or another result (as for tg_gated).
  * Workspace (256-byte aligned): only where TMA cannot describe an operand (a row
  * stride, a distance between weights or a base off 16 bytes), for padded copies;
- * weights that are copied must be evenly spaced rows (stride_w = N * ldw).
+ * weights that are copied must be evenly spaced rows (stride_w = N * ldw), fewer
+ * than 2^31 - 2^16 in all.
  * ------------------------------------------------------------------------- */
 /* A zero-initialised value (or NULL): fp16, dense rows, rows without a group left alone. */
 typedef struct tg_grouped_options {

@@ -149,6 +149,14 @@ def test_weights_of_one_row():
     assert size(*P[:2], 3, 16, 1, 8, tg.grouped_options(stride_w=9)) == up(2 * 3 * 8)
 
 
+def test_copies_of_many_rows():
+    """Rows of all weights are counted in 32 bits, and so are the steps over them."""
+    size = tg.grouped_workspace_size
+    assert size(*P[:2], 1000, 8, 2147000, 1) == up(2 * 8 * 8) + up(2 * 8 * 2147000000)
+    assert size(*P[:2], 1024, 8, 2097151, 1) == -1 and size(*P[:2], 1024, 8, 1 << 22, 1) == -1
+    assert size(*P[:2], 1024, 8, 2097151, 8) == 0  # no copy
+
+
 def test_workspace_refusals():
     G, M, N, K = 5, 100, 41, 33
     need = tg.grouped_workspace_size(*P[:2], G, M, N, K)

@@ -67,10 +67,11 @@ GrpStack grp_stack(const void* p, int64_t mats, int64_t rows, int64_t cols, int6
   return s;
 }
 
-// Bytes of the padded copy of a stack that TMA cannot describe, 0 where it can, -1 where it cannot be copied.
+// Bytes of the padded copy of a stack that TMA cannot describe, 0 where it can, -1 where it
+// cannot be copied: rows that are not evenly spaced, or so many that the kernel's steps over them would pass 32 bits.
 int64_t grp_copy_bytes(const GrpStack& s) {
   if (s.empty() || s.on16()) return 0;
-  if (!s.even_rows() || s.mats * s.m.rows > INT_MAX) return -1;
+  if (!s.even_rows() || s.mats * s.m.rows > INT_MAX - 65536) return -1;
   return up256(2 * s.mats * s.m.rows * round_up(s.m.cols, 8));
 }
 
