@@ -578,7 +578,9 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       const float bias = LORA && p.lora.bias != nullptr && n < p.out
                              ? load_16(static_cast<const unsigned short*>(p.lora.bias) + n, bf16) : 0.0f;
       unsigned mixed_boxes = 0;
-      if (early) mixed_boxes = __ballot_sync(0xffffffffu, (lane < boxes ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone) == kLoraMixed);
+      if (early)
+        mixed_boxes = __ballot_sync(
+            0xffffffffu, (lane < boxes ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone) == kLoraMixed);
       for (int b = 0; b < boxes && cols > 0; ++b) {
         const bool mixed = mixed_boxes >> b & 1u;
         if (!mixed && b % PARTS != part) continue;

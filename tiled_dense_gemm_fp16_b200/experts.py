@@ -42,12 +42,12 @@ def lora(x, w, a, b, index, scale=None, bias=None, out=None, stream=None, worksp
     """x @ w^T + scale[r] (x @ a[r]^T) @ b[r]^T + bias with an adapter r = index[row] for each row, float16 or bfloat16:
     x (..., K), w (N, K), a (adapters, rank, K), b (adapters, N, rank), index int32 with a value for each row of x.
 
-    Rows whose index is outside [0, adapters), -1 say, have no adapter.  Rows may come in any order; those of one request next to
-    each other are faster.  ``scale``: (adapters,) float32, or None for 1.  ``bias``: (N,) of x's type.  rank is a
-    multiple of 8, and rows of a and b start on 16-byte boundaries (pad a rank with zeros once); x, w and
-    ``out`` may have any row stride.  x @ a[r]^T, scaled, is rounded to the 16-bit type; sums are 32-bit.  A row depends on its own
-    adapter only.  For serving: nothing is recorded for autograd.  ``workspace`` ("auto" or a uint8 CUDA tensor) holds
-    those inner products; calls whose work may overlap need one each."""
+    Rows whose index is outside [0, adapters), -1 say, have no adapter.  Rows may come in any order; those of one
+    request next to each other are faster.  ``scale``: (adapters,) float32, or None for 1.  ``bias``: (N,) of x's type.
+    rank is a multiple of 8, at most 512, and rows of a and b start on 16-byte boundaries (pad a rank with zeros
+    once); x, w and ``out`` may have any row stride.  x @ a[r]^T, scaled, is rounded to the 16-bit type; sums are
+    32-bit.  A row depends on its own adapter only.  For serving: nothing is recorded for autograd.  ``workspace``
+    ("auto" or a uint8 CUDA tensor) holds those inner products; calls whose work may overlap need one each."""
     if stream is None:
         return _calls.lora(x, w, a, b, index, scale, bias, out, workspace)
     with _On(stream, x, w, a, b, index, scale, bias, out, workspace):
