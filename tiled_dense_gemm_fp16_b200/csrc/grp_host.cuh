@@ -690,8 +690,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   // half as many, 127 so), and one without an item costs a little (512 rows of 4
   // requests through 4096 x 1024: 31.2 us, 28.9 with half as many, 33.9 with more).
   int64_t y = 4 * info->sm_count / (blocks * deep * p.splits);
-  const int64_t items = l.M < p.tokens ? l.M : p.tokens;
-  y = y < 1 ? 1 : y > items ? items : y;
+  y = y < 1 ? 1 : y > p.tokens ? p.tokens : y;
   y = y > l.adapters ? l.adapters : y;
   const int deepest = (96 * 1024 - 1024 - Cfg::BAR_BYTES - Cfg::recv_bytes(p.tokens, p.splits, p.a_rows)) / ((p.a_rows + p.tokens) * 128);
   p.per_stage = tune_int("TG_TUNE_SHRINK_PER", 2);
@@ -700,7 +699,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
   if (p.stages < 2) p.stages = 2;
   p.bf16 = l.bf16 ? 1 : 0;
-  p.tmem_cols = p.tokens < 32 ? 32 : p.tokens;
+  p.tmem_cols = p.tokens;
   p.idesc = make_idesc_ff(kFfF16, l.bf16, 128, 0, false, false);
   p.wait_budget_ns = wait_budget(p.k_blocks);
   cudaLaunchConfig_t cfg;

@@ -41,7 +41,7 @@ struct LoraShrinkParams {
   int M, rank, adapters;
   int k_blocks, splits, stages;
   int per_stage;       // k-blocks of a stage of the ring
-  int tokens;          // most of an item, and rows of a block: 16, 32, 64 or 128
+  int tokens;          // most of an item, and rows of a block: 32, 64 or 128
   int a_rows;          // of a box: min(128, rank)
   int bf16;
   uint32_t tmem_cols;
@@ -54,9 +54,9 @@ struct LoraShrinkCfg {
   static constexpr int THREADS = 192;
   static constexpr int MAX_STAGES = 16;
   static constexpr int BAR_BYTES = 512;
-  // Partials: [source][four tokens][row of A] of 16 bytes, for this CTA's share of the tokens.
+  // Partials: [source][four tokens][row of A] of 16 bytes, for this CTA's share of the tokens; none without a split.
   __host__ __device__ static constexpr int recv_bytes(int tokens, int splits, int a_rows) {
-    return splits * ((tokens / 4 + splits - 1) / splits) * a_rows * 16;
+    return splits == 1 ? 0 : splits * ((tokens / 4 + splits - 1) / splits) * a_rows * 16;
   }
   // The MMAs read 128 rows from each stage's A on, the last ones of other stages and of X.
   static constexpr int smem_bytes(int tokens, int splits, int a_rows, int stages) {
