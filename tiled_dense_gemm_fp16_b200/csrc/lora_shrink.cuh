@@ -20,7 +20,7 @@
 // T only when its own sums are under way).  A token of up to 16 ranks goes without
 // either: the narrow kernel's warps make a value each.
 //
-// Measured: 8192 rows of 8 requests, K = 4096, rank 64, 30.9 us alone, 2.3 TB/s:
+// Measured: 8192 rows of 8 requests, K = 4096, rank 64, 29.5 us alone, 2.3 TB/s:
 // bound by the latency of a block's loads.  The main product hides most of it.
 #pragma once
 
