@@ -623,7 +623,11 @@ TG_API int64_t tg_grouped_backward_workspace_size(const void *dY, const void *X,
  * scale: one fp32 value for each adapter, or NULL (1).  bias: N values of the type, or NULL.
  *
  * Sums are fp32.  scale[a] A_a X[r] is rounded to the 16-bit type before it meets
- * B_a (the tensor cores read it so), the sum of all terms once more.  Each row's result
+ * B_a (the tensor cores read it so), the sum of all terms once more.  In fp16 that
+ * first rounding knows no range: eight ranks of a row whose largest magnitude is not
+ * in [2^-14, 2^15) are held times a power of two, so that each inner product is off
+ * by at most 2^-11 of itself or of the largest of its eight, from 2^-111 to 2^128 (in
+ * bf16 by 2^-8 of itself).  Such rows are slower.  Each row's result
  * depends on its own values and its own adapter only: infinities and NaN in other
  * rows or other adapters do not reach it.  Equal inputs give equal bits.
  *
@@ -631,7 +635,7 @@ TG_API int64_t tg_grouped_backward_workspace_size(const void *dY, const void *X,
  * start on 16-byte boundaries; X, W and Y may lie on any 2-byte boundary.  Sizes as
  * for tg_gated, 0 <= adapters <= 2^20.  M == 0 or N == 0: nothing is enqueued.  K == 0: every
  * row is the bias, or +0.  Y may overlap no input.  Workspace (256-byte aligned):
- * the inner products of M x rank, and padded copies as for tg_gated.
+ * the inner products of M x rank with their powers, and padded copies as for tg_gated.
  * ------------------------------------------------------------------------- */
 typedef struct tg_lora_options {
     int32_t type;          /* TG_TYPE_F16 or TG_TYPE_BF16                        */

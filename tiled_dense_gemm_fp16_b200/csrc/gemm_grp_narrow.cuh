@@ -46,10 +46,13 @@ struct GrpNarrowCfg {
   static constexpr int smem_bytes(int tokens, int stages, int groups) {
     return 1024 + stages * (W_BYTES + tokens * 128) + recv_bytes(tokens) + BAR_BYTES + grp_plan_align(groups);
   }
-  // And T where it is made here, a value by each warp that finishes results.
+  // And T where it is made here, a value by each warp that finishes results: up to 16
+  // of 16 bits in bf16, in fp16 of 32 bits, from which each warp makes its own of 16
+  // bits and their powers (48 bytes apart).
   static constexpr int own_t(int splits) { return 4 * splits; }
+  static constexpr int OWN_T_BYTES = 64 + 4 * 48;
   static constexpr int lora_bytes(int tokens, int splits, bool with_t) {
-    return delta_bytes(tokens, splits) + (with_t ? 2 * own_t(splits) : 0);
+    return delta_bytes(tokens, splits) + (with_t ? OWN_T_BYTES : 0);
   }
   static_assert((2 * MAX_STAGES + 8) * 8 + 8 <= BAR_BYTES, "barriers");
   static_assert(HALF_BYTES % 1024 == 0 && UNIT * 128 % 1024 == 0, "operands start on the swizzle's 1024 bytes");
@@ -123,16 +126,30 @@ __device__ __forceinline__ float lora_dot(const unsigned short* a, const unsigne
 }
 
 // T of all tokens, of which there are no more values than warps, into every CTA of
-// the cluster: value v by this warp.
+// the cluster: value v by this warp.  In fp16 still of 32 bits: the eight ranks
+// that share a power come from two CTAs.
 template <bool BF16>
-__device__ __forceinline__ void lora_own_t(const LoraParams& l, unsigned short* t, int M, int K, int v, int ctas, int lane) {
+__device__ __forceinline__ void lora_own_t(const LoraParams& l, void* t, int M, int K, int v, int ctas, int lane) {
   if (v >= M * l.rank) return;
   const int m = v / l.rank, a = lora_adapter(l, m);
   if (a < 0) return;
   const float sum = lora_dot<BF16, 8>(static_cast<const unsigned short*>(l.a) + a * l.stride_a + (v - m * l.rank) * l.lda,
                                       static_cast<const unsigned short*>(l.x) + m * l.ldx, K, lane);
   const float scale = l.scale != nullptr ? __ldg(l.scale + a) : 1.0f;
-  if (lane < ctas) st_cluster_u16(mapa_shared(smem_u32(t + v), lane), round_16(sum * scale, BF16));
+  if (lane < ctas) {
+    if (BF16)
+      st_cluster_u16(mapa_shared(smem_u32(static_cast<unsigned short*>(t) + v), lane), round_16(sum * scale, true));
+    else
+      st_cluster_f32(mapa_shared(smem_u32(static_cast<float*>(t) + v), lane), sum * scale);
+  }
+}
+// The 16-bit form of those n values and the powers of eight each, by a warp for itself.
+__device__ __forceinline__ void lora_own_round(const float* t, int n, unsigned short* to, signed char* exps, int lane) {
+  const float v = lane < n ? t[lane] : 0.0f;
+  const LoraRounded r = lora_round(v);
+  if (lane < n) to[lane] = r.y;
+  if (lane < n && (lane & 7) == 0) exps[lane >> 3] = static_cast<signed char>(r.e);
+  __syncwarp();
 }
 
 // LORA as in the pair kernel.
@@ -318,8 +335,10 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
     const int e = quad * 32 + lane;  // also the column of the panel that this thread sends
     const int own = Cfg::PANEL / p.splits;  // columns that this CTA finishes
     const int pitch = p.tokens + 4;
-    unsigned short* own_t = reinterpret_cast<unsigned short*>(delta + own * pitch);
-    const void* const T = LORA && p.own_t ? own_t : p.g.lora.t;
+    uint8_t* own_t = reinterpret_cast<uint8_t*>(delta + own * pitch);
+    uint8_t* own_16 = LORA == 2 ? own_t : own_t + 64 + quad * 48;
+    const void* const T = LORA && p.own_t ? own_16 : p.g.lora.t;
+    const signed char* const exps = LORA && p.own_t ? reinterpret_cast<signed char*>(own_16 + 32) : p.g.lora.exps;
     const int sent = e;
     const uint32_t owner = sent / own;
     const uint32_t to = mapa_shared(smem_u32(recv) + (rank * own + sent % own) * pitch * 4, owner);
@@ -367,13 +386,16 @@ __global__ void __maxnreg__(240)  // of 192 threads, so that the kernel that mak
             }
             const bool here = mbar_wait_cluster(t_bar, 0, abort_flag, p.g.wait_budget_ns, 0xb9);
             if (!__all_sync(0xffffffffu, here)) break;
+            if (LORA == 1)
+              lora_own_round(reinterpret_cast<const float*>(own_t), p.g.M * p.g.lora.rank, reinterpret_cast<unsigned short*>(own_16),
+                             reinterpret_cast<signed char*>(own_16 + 32), lane);
           }
           waited = true;
         }
         for (int u = quad; u < units; u += 4) {
           const int col = u % col_blocks * 32, tok = u / col_blocks * TOK;
           const int mine = adapters.from(tok);
-          lora_part<LORA == 2, 4>(p.g.lora, T, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
+          lora_part<LORA == 2, 4>(p.g.lora, T, exps, mine, f.tok0 + tok, n0 + col, p.g.out, delta + col * pitch + tok, pitch, lane);
         }
       }
       const int acc = local & 1;

@@ -45,6 +45,9 @@ struct LoraParams {
   const int* index;           // adapter of each token; outside [0, adapters): none
   const int* kind;            // of each 32 tokens: their adapter, kLoraNone or kLoraMixed
   const void* t;              // T: M x rank, 16-bit
+  const signed char* exps;    // fp16: powers of two that T was divided by, of each row and eight ranks
+  const uint2* misfits;       // fp16: of each 32 tokens, eight bytes per 128 ranks, all 0 if no value was divided
+  int deep;                   // ranks in 128s
   const void* b;              // adapters' B
   const void* bias;           // N values, or nullptr
   int64_t ldb, stride_b;      // elements between rows and between adapters
@@ -87,6 +90,66 @@ __device__ __forceinline__ int ld_global_s32(const int* p) {
   return v;
 }
 
+// T's range.  bf16 has that of fp32; fp16 has not: s A X of 1e5 would be infinite, of
+// 1e-7 lose its digits, where B T is an ordinary number.  So eight ranks of a row
+// whose largest finite value is outside fp16's normal numbers below 2^15 are divided
+// by the power of two that brings it to [2^15, 2^16), and its exponent stands beside
+// T: values from 2^15 on say that there may be one.  lora_part then multiplies the sums
+// of eight by it; 32 tokens of one adapter of which one has a power do not go through
+// the main accumulator, whose other terms know none.  All others keep their bits.  A
+// value of T is off by half a step, 2^-11 relative to it or to the largest of its
+// eight.  (A power for every row would close the accumulator's way to all.)
+constexpr float kLoraLeast = 6.103515625e-05f, kLoraMost = 32752.0f;  // below: still below 2^15 once rounded
+constexpr float kLoraNothing = 3.85185988877447e-34f;                 // 2^-111: below, B T is far below fp16, and T is 0
+__device__ __forceinline__ bool lora_fits(float v) { return fabsf(v) >= kLoraLeast && fabsf(v) < kLoraMost; }
+// Of eight ranks with the largest finite magnitude m: the power's exponent, -126 .. 112, 0 for none.
+__device__ __forceinline__ int lora_exponent(float m) {
+  return m < kLoraNothing || lora_fits(m) ? 0 : (__float_as_int(m) >> 23) - 127 - 15;
+}
+__device__ __forceinline__ float lora_power(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+// v of eight adjacent lanes, in a whole warp, as it stands in T, and its group's
+// exponent.  What is finite stays so (65504 for up to 65536: 2^-11 of it).
+struct LoraRounded {
+  unsigned short y;
+  int e;
+};
+__device__ __forceinline__ LoraRounded lora_round(float v) {
+  const float inf = __int_as_float(0x7f800000);
+  const bool finite = fabsf(v) < inf;
+  float m = finite ? fabsf(v) : 0.0f;
+#pragma unroll
+  for (int d = 1; d < 8; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  LoraRounded r;
+  r.e = lora_exponent(m);
+  if (finite) v = m < kLoraNothing ? 0.0f : fminf(fmaxf(v * lora_power(-r.e), -65504.0f), 65504.0f);
+  r.y = round_16(v, false);
+  return r;
+}
+// Whether one of eight values of fp16 is 2^15 or more, or not finite.
+__device__ __forceinline__ bool lora_powered(const uint4& w) {
+  const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+  return m >= 0x78000000u || (m & 0xffffu) >= 0x7800u;
+}
+
+__device__ __forceinline__ int ld_s8(const signed char* p) {  // of any memory
+  int v;
+  asm volatile("ld.s8 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+// The kind of 32 tokens, as the main product takes them: in one run only what fits the accumulator.
+template <bool BF16>
+__device__ __forceinline__ int lora_kind(const LoraParams& l, int block) {
+  const int kind = ld_global_s32(l.kind + block);
+  if (BF16) return kind;
+  uint32_t any = 0u;
+  for (int z = 0; z < l.deep; ++z) {
+    uint2 u;
+    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(u.x), "=r"(u.y) : "l"(l.misfits + static_cast<int64_t>(block) * l.deep + z));
+    any |= u.x | u.y;
+  }
+  return kind >= 0 && any != 0u ? kLoraMixed : kind;
+}
+
 // Runs of 32-token groups of a tile that share an adapter, in order; for a whole
 // warp, whose lanes hold the groups' kinds.
 struct LoraRun {
@@ -121,6 +184,36 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+constexpr int kLoraTokens = 16;
+// lora_part where T carries powers (fp16): a lane a column, eight ranks at a time in
+// fp32.  Such values are rare, and this form leaves the other's registers alone (two
+// forms on the tensor cores, or one with the powers in it, made the pair kernel spill:
+// 1049 rows of 40 requests 60-66 us, so 58).
+__device__ __forceinline__ void lora_part_powers(const LoraParams& l, const void* T, const signed char* exps, int mine, int m0, int n0,
+                                                 int N, float* out, int pitch, int lane) {
+  const int groups = l.rank >> 3, n = n0 + lane;
+  for (int tok = 0; tok < kLoraTokens; ++tok) {
+    const int adapter = __shfl_sync(0xffffffffu, mine, tok);
+    float sum = 0.0f;
+    if (adapter >= 0 && n < N) {
+      const unsigned short* b = static_cast<const unsigned short*>(l.b) + adapter * l.stride_b + n * l.ldb;
+      const unsigned short* t = static_cast<const unsigned short*>(T) + static_cast<int64_t>(m0 + tok) * l.rank;
+      const signed char* e = exps + static_cast<int64_t>(m0 + tok) * groups;
+#pragma unroll 2
+      for (int g = 0; g < groups; ++g) {
+        const uint4 u = __ldg(reinterpret_cast<const uint4*>(b + 8 * g)), v = ld_v4(t + 8 * g);
+        float2 s = mul2(unpack_16(u.x, false), unpack_16(v.x, false));
+        s = fma2(unpack_16(u.y, false), unpack_16(v.y, false), s);
+        s = fma2(unpack_16(u.z, false), unpack_16(v.z, false), s);
+        s = fma2(unpack_16(u.w, false), unpack_16(v.w, false), s);
+        sum = fmaf(s.x + s.y, lora_power(ld_s8(e + g)), sum);
+      }
+    }
+    out[lane * pitch + tok] = sum;
+  }
+  __syncwarp();
+}
+
 // The adapters' part of 32 columns from n0 on and 16 tokens from m0 on, by a warp
 // whose lane t < 16 holds token t's adapter (negative: none): sum_j B_a[n][j] T[m][j]
 // in fp32 to out[column * pitch + token].
@@ -136,10 +229,9 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 // take 90; 8192 rows of 8 requests, 8192 x 4096, rank 64: 422, 436, 450), the narrow one 4.  (A
 // thread a column, with fused multiply-adds, read each row in pieces of its own: 3000
 // cycles for 16 ranks of 8 tokens.)
-constexpr int kLoraTokens = 16;
 template <bool BF16, int ITEMS>
-__device__ __forceinline__ void lora_part(const LoraParams& l, const void* T, int mine, int m0, int n0, int N, float* out, int pitch,
-                                          int lane) {
+__device__ __forceinline__ void lora_part(const LoraParams& l, const void* T, const signed char* exps, int mine, int m0, int n0, int N,
+                                          float* out, int pitch, int lane) {
   const int row = lane >> 2, q = lane & 3;
   const unsigned tokens = __ballot_sync(0xffffffffu, lane < kLoraTokens && mine >= 0);
   const int steps = (l.rank + 31) >> 5;
@@ -195,6 +287,18 @@ __device__ __forceinline__ void lora_part(const LoraParams& l, const void* T, in
           for (int e = 0; e < 4; ++e)
             if (done[i] >> (8 * h + 2 * q + (e & 1)) & 1u) d[c][h][e] = p[c][h][e];
         }
+    }
+  }
+  if (!BF16) {  // T's rows again, which L1 holds by now (looked at in the loop: 64 rows of 64 requests 45.8 us, so 44.2)
+    bool powered = false;
+    for (int at = q * 8; at < l.rank; at += 32) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (tokens >> (row + 8 * h) & 1u) powered |= lora_powered(ld_v4(t + 8 * h * l.rank + at - q * 8));
+    }
+    if (__any_sync(0xffffffffu, powered)) {
+      lora_part_powers(l, T, exps, mine, m0, n0, N, out, pitch, lane);
+      return;
     }
   }
 #pragma unroll
@@ -415,7 +519,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
         if (!waited) grid_dependency_wait();
         waited = true;
         LoraRun run{0, 0, 0};
-        const int kinds = lane < width / 32 ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone;
+        const int kinds = lane < width / 32 ? lora_kind<LORA == 2>(p.lora, f.tok0 / 32 + lane) : kLoraNone;
         while (ok && lora_next_run(kinds, width / 32, run)) {
           for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
             if (!mbar_wait_warp(&empty_bar[stage], phase ^ 1u, abort_flag, p.wait_budget_ns, 0xa1)) {
@@ -496,7 +600,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           waited = true;
           const uint32_t idesc32 = p.idesc | (32u >> 3) << 17;
           LoraRun run{0, 0, 0};
-          const int kinds = lane < width / 32 ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone;
+          const int kinds = lane < width / 32 ? lora_kind<LORA == 2>(p.lora, f.tok0 / 32 + lane) : kLoraNone;
           while (ok && lora_next_run(kinds, width / 32, run)) {
             for (int j0 = 0; j0 < p.lora.rank; j0 += 64) {
               if (!mbar_wait_warp(&full_bar[stage], phase, abort_flag, p.wait_budget_ns, 0xa4)) {
@@ -580,7 +684,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
       unsigned mixed_boxes = 0;
       if (early)
         mixed_boxes = __ballot_sync(
-            0xffffffffu, (lane < boxes ? ld_global_s32(p.lora.kind + f.tok0 / 32 + lane) : kLoraNone) == kLoraMixed);
+            0xffffffffu, (lane < boxes ? lora_kind<BF16>(p.lora, f.tok0 / 32 + lane) : kLoraNone) == kLoraMixed);
       for (int b = 0; b < boxes && cols > 0; ++b) {
         const bool mixed = mixed_boxes >> b & 1u;
         if (!mixed && b % PARTS != part) continue;
@@ -601,7 +705,7 @@ __global__ void __launch_bounds__(GrpPairCfg::THREADS, 1)
           bar_128(1 + part);
         if (mixed) {
           const int mine = lane < rows ? lora_adapter(p.lora, f.tok0 + b * 32 + e0 + lane) : -1;
-          lora_part<BF16, 3>(p.lora, p.lora.t, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
+          lora_part<BF16, 3>(p.lora, p.lora.t, p.lora.exps, mine, f.tok0 + b * 32 + e0, n0, p.out, part_buf, kPartPitch, lane);
           uint32_t r[16];
           tmem_ld_32x32b_x16(taddr + b * 32 + e0, r);
           tmem_ld_wait();

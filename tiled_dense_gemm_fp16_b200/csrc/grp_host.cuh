@@ -620,12 +620,25 @@ bool lora_args(LoraArgs& l, const void* X, const void* W, const void* A, const v
   return true;
 }
 
-int64_t lora_inner_bytes(const LoraArgs& l) { return l.adapters == 0 ? 0 : up256(2 * l.M * l.rank); }
+// T, and behind it what stands beside it: the kinds of 32 rows and, in fp16, a byte
+// of power for each row and eight ranks and, before those, the misfits of 32 rows.
+struct LoraInner {
+  int64_t kind, misfits, exps, bytes;  // from T's start
+};
+LoraInner lora_inner(const LoraArgs& l) {
+  LoraInner n{0, 0, 0, 0};
+  if (l.adapters == 0) return n;
+  const int64_t blocks = (l.M + 31) / 32;
+  n.kind = up256(2 * l.M * l.rank);
+  n.misfits = n.kind + round_up(4 * blocks, 8);
+  n.exps = n.misfits + 8 * blocks * ((l.rank + 127) / 128);
+  n.bytes = n.kind + up256(l.bf16 ? 4 * blocks : n.exps + l.M * (l.rank / 8) - n.kind);
+  return n;
+}
 
 int64_t lora_workspace(const LoraArgs& l) {
   if (l.M == 0 || l.N == 0 || l.K == 0) return 0;
-  const int64_t inner = l.adapters == 0 ? 0 : lora_inner_bytes(l) + up256((l.M + 31) / 32 * 4);
-  return inner + ff_copy_bytes(l.x) + ff_copy_bytes(l.w);
+  return lora_inner(l).bytes + ff_copy_bytes(l.x) + ff_copy_bytes(l.w);
 }
 
 // T of few tokens.
@@ -637,6 +650,7 @@ tg_status launch_lora_rows(const LoraArgs& l, const GrpProduct& f, const float* 
   p.index = f.l.index;
   p.scale = scale;
   p.t = const_cast<void*>(f.l.t);
+  p.exps = const_cast<signed char*>(f.l.exps);
   p.ldx = l.x.ld;
   p.lda = l.a.m.ld;
   p.stride_a = l.a.stride;
@@ -660,7 +674,8 @@ tg_status launch_lora_rows(const LoraArgs& l, const GrpProduct& f, const float* 
 // T and the kinds of 32 tokens.
 tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float* scale, cudaStream_t stream, DeviceInfo* info) {
   using Cfg = LoraShrinkCfg;
-  if (!ff_set_smem(reinterpret_cast<const void*>(lora_shrink_kernel), info->grp_attr, 128u, 210 * 1024)) return TG_ERR_LAUNCH;
+  auto kernel = l.bf16 ? lora_shrink_kernel<true> : lora_shrink_kernel<false>;
+  if (!ff_set_smem(reinterpret_cast<const void*>(kernel), info->grp_attr, l.bf16 ? 128u : 256u, 210 * 1024)) return TG_ERR_LAUNCH;
   LoraShrinkMaps maps;
   std::memset(&maps, 0, sizeof maps);
   LoraShrinkParams p;
@@ -671,6 +686,8 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.scale = scale;
   p.t = const_cast<void*>(f.l.t);
   p.kind = const_cast<int*>(f.l.kind);
+  p.exps = const_cast<signed char*>(f.l.exps);
+  p.misfits = reinterpret_cast<uint8_t*>(const_cast<uint2*>(f.l.misfits));
   p.M = static_cast<int>(l.M);
   p.rank = static_cast<int>(l.rank);
   p.adapters = static_cast<int>(l.adapters);
@@ -698,7 +715,6 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   p.stages = deepest / p.per_stage;
   if (p.stages > Cfg::MAX_STAGES) p.stages = Cfg::MAX_STAGES;
   if (p.stages < 2) p.stages = 2;
-  p.bf16 = l.bf16 ? 1 : 0;
   p.tmem_cols = p.tokens;
   p.idesc = make_idesc_ff(kFfF16, l.bf16, 128, 0, false, false);
   p.wait_budget_ns = wait_budget(p.k_blocks);
@@ -710,7 +726,7 @@ tg_status launch_lora_shrink(const LoraArgs& l, const GrpProduct& f, const float
   cfg.stream = stream;
   LaunchAttrs la;
   la.fill(cfg, static_cast<unsigned>(p.splits));
-  if (cudaLaunchKernelEx(&cfg, lora_shrink_kernel, maps, p) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kernel, maps, p) != cudaSuccess) {
     cudaGetLastError();
     return TG_ERR_LAUNCH;
   }
@@ -747,7 +763,11 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
   if (adapted) {
     f.l.index = index;
     f.l.t = ws;
-    f.l.kind = reinterpret_cast<const int*>(ws + lora_inner_bytes(l));
+    const LoraInner inner = lora_inner(l);
+    f.l.kind = reinterpret_cast<const int*>(ws + inner.kind);
+    f.l.misfits = reinterpret_cast<const uint2*>(ws + inner.misfits);
+    f.l.exps = reinterpret_cast<const signed char*>(ws + inner.exps);
+    f.l.deep = static_cast<int>((l.rank + 127) / 128);
     f.l.b = l.b.m.p;
     f.l.ldb = l.b.m.ld;
     f.l.stride_b = l.b.stride;
@@ -755,7 +775,7 @@ tg_status run_lora(LoraArgs& l, const float* scale, const int32_t* index, const 
     f.l.adapters = static_cast<int>(l.adapters);
     f.lb = l.b;
     f.t = FfMat{ws, l.M, l.rank, l.rank, 2};
-    ws += lora_inner_bytes(l) + up256((l.M + 31) / 32 * 4);
+    ws += inner.bytes;
   }
   FfMat* const operands[2] = {&l.x, &l.w};
   if ((st = ff_make_copies(operands, 2, ws, stream, info)) != TG_OK) return st;

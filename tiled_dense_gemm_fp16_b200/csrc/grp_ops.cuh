@@ -59,6 +59,13 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a,
 __device__ __forceinline__ void st_cluster_u16(uint32_t cluster_addr, unsigned short v) {
   asm volatile("st.shared::cluster.u16 [%0], %1;" ::"r"(cluster_addr), "h"(v) : "memory");
 }
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
+}
+// This lane's value of one column.
+__device__ __forceinline__ void tmem_ld_32x32b_x1(uint32_t tmem, uint32_t& r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(tmem));
+}
 // What this thread (and, after __syncwarp, its warp) has written is seen by a
 // CTA of the cluster that acquires a later relaxed arrival.  One fence for several
 // arrivals: each release at cluster scope measured about 1 us.

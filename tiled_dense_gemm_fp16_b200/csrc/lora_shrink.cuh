@@ -10,7 +10,8 @@
 // sum over K; each finishes every S-th four tokens from the partials that the
 // others write into its shared memory, in rank order.  Blocks of a prompt have one item, those of a
 // decoding batch up to 128, spread over blockIdx.y.  T is rounded once to the
-// 16-bit type, as the tensor cores read it (and as two linear layers in a row would).
+// 16-bit type, as the tensor cores read it (and as two linear layers in a row would),
+// in fp16 with a power of two where its range needs one (gemm_grp_pair.cuh).
 //
 // A decoding batch takes the second kernel: a warp a value of T.  Its tokens rarely
 // share an adapter, so there is nothing to multiply by tiles, and without tiles
@@ -21,7 +22,10 @@
 // either: the narrow kernel's warps make a value each.
 //
 // Measured: 8192 rows of 8 requests, K = 4096, rank 64, 29.5 us alone, 2.3 TB/s:
-// bound by the latency of a block's loads.  The main product hides most of it.
+// bound by the latency of a block's loads.  The main product hides most of it.  fp16's
+// powers (looked for, none found) cost 2-4 us there and 2 of 30 with split sums: the
+// votes come after the stores, and full warps take part in them (votes among eight lanes
+// took 6 us more).
 #pragma once
 
 #include "gemm_grp_narrow.cuh"
@@ -38,12 +42,13 @@ struct LoraShrinkParams {
   const float* scale;  // of each adapter, or nullptr
   void* t;
   int* kind;
+  signed char* exps;   // fp16: T's powers, of each row and eight ranks
+  uint8_t* misfits;    // fp16: of each 32 tokens and 128 ranks, a byte of each warp of up to two CTAs: 1 where a power is not 0
   int M, rank, adapters;
   int k_blocks, splits, stages;
   int per_stage;       // k-blocks of a stage of the ring
   int tokens;          // most of an item, and rows of a block: 32, 64 or 128
   int a_rows;          // of a box: min(128, rank)
-  int bf16;
   uint32_t tmem_cols;
   uint32_t idesc;      // without N
   uint64_t wait_budget_ns;
@@ -73,7 +78,10 @@ struct LoraItems {
   int adapter[128], first[128], last[128];
 };
 
-__global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
+// Two CTAs an SM: their 6 warps take the registers of 8, so 128 a thread (with 150 of them the
+// split sums of 1049 rows took 35 us in the whole call instead of 30).
+template <bool BF16>
+__global__ void __launch_bounds__(256, 2)
     lora_shrink_kernel(const __grid_constant__ LoraShrinkMaps maps, const LoraShrinkParams p) {
   using Cfg = LoraShrinkCfg;
   extern __shared__ uint8_t smem_raw[];
@@ -131,6 +139,7 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
   const int rows = min(128, p.rank - j0);  // of A
   __shared__ __align__(16) int owner_of[128];
   __shared__ int firsts[4];
+  __shared__ int kinds[4];  // of each 32 tokens
   __shared__ LoraItems items;
   if (p.tokens <= 32) {  // each warp by itself finds what it needs; one keeps the list
     const bool valid = lane < p.tokens && m0 + lane < p.M;
@@ -150,7 +159,8 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
       const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
       if (lane == 0) {
         items.count = __popc(all);
-        if (blockIdx.y == 0 && blockIdx.z == 0 && rank == 0) p.kind[m0 / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
+        kinds[0] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
+        if (blockIdx.y == 0 && blockIdx.z == 0 && rank == 0) p.kind[m0 / 32] = kinds[0];
       }
     }
     __syncthreads();
@@ -165,8 +175,8 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
       const int r0 = __shfl_sync(0xffffffffu, mine, 0);
       const bool same = __all_sync(0xffffffffu, !valid || mine == r0);
       // What each 32 tokens are to the main product.
-      if (lane == 0 && valid && blockIdx.y == 0 && blockIdx.z == 0 && rank == 0)
-        p.kind[(m0 + tok) / 32] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
+      if (lane == 0) kinds[warp] = !same ? kLoraMixed : r0 < 0 ? kLoraNone : r0;
+      if (lane == 0 && valid && blockIdx.y == 0 && blockIdx.z == 0 && rank == 0) p.kind[(m0 + tok) / 32] = kinds[warp];
     }
     __syncthreads();
     int before = 128;  // the first token of this one's adapter, from the end of the search on
@@ -298,8 +308,26 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
     const int e = threadIdx.x - Cfg::EPI_WARP0 * 32;
     const int share = (p.tokens / 4 + p.splits - 1) / p.splits;  // four tokens each, of a source
     int local = 0;
+    constexpr bool powers = !BF16;
+    const int groups = p.rank >> 3;  // of eight ranks
+    // Whether the 32-token blocks that are the adapter's alone (bit i: tokens 32 i and
+    // on) hold what needs a power, as far as this warp has seen.
+    auto note = [&](int adapter, unsigned misfit) {
+      misfit = __reduce_or_sync(0xffffffffu, misfit);
+      for (int b = 0; b * 32 < p.tokens; ++b) {
+        if (kinds[b] != adapter || lane != 0) continue;
+        uint8_t* at = p.misfits + (static_cast<int64_t>((m0 >> 5) + b) * gridDim.z + blockIdx.z) * 8 + quad * 2;
+        const unsigned bit = misfit >> b & 1u;
+        if (p.splits == 1)
+          *reinterpret_cast<unsigned short*>(at) = static_cast<unsigned short>(bit);
+        else
+          at[rank] = static_cast<uint8_t>(bit);
+      }
+      __syncwarp();
+    };
     for (int d = blockIdx.y; d < count; d += step) {
       const int adapter = items.adapter[d], t0 = items.first[d] & ~15, width = ((items.last[d] & ~15) + 16) - t0;
+      unsigned misfit = 0;
       const int fours = width / 4, mine = (fours - rank + p.splits - 1) / p.splits;  // those of this CTA: rank, rank + splits, ...
       const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
       bool ready = mbar_wait(acc_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd6);
@@ -316,8 +344,45 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
           unsigned short* dst = static_cast<unsigned short*>(p.t) + static_cast<int64_t>(m) * p.rank + j0 + j;
 #pragma unroll
           for (int q = 0; q < 16; ++q)
-            if (j < rows && (mine_of >> q & 1u)) dst[q * p.rank] = round_16(__uint_as_float(r[q]) * scale, p.bf16 != 0);
+            if (j < rows && (mine_of >> q & 1u)) dst[q * p.rank] = round_16(__uint_as_float(r[q]) * scale, BF16);
+          if (powers) {
+            if (lane < 16 && (mine_of >> lane & 1u)) {
+              const int here = min(4, (rows - quad * 32) >> 3);
+              signed char* at = p.exps + static_cast<int64_t>(m + lane) * groups + (j0 >> 3) + quad * 4;
+              if (here == 4 && (groups & 3) == 0)
+                *reinterpret_cast<uint32_t*>(at) = 0u;
+              else
+                for (int g = 0; g < here; ++g) at[g] = 0;
+            }
+            // As a rule that was it: each eight ranks have a normal number, none passes the range.
+            unsigned lost = 0;
+            bool past = false;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const float v = fabsf(__uint_as_float(r[q]) * scale);
+              const unsigned normal = __ballot_sync(0xffffffffu, v >= kLoraLeast || j >= rows);
+              const unsigned none = (normal - 0x01010101u) & ~normal & 0x80808080u;  // a byte of zeros
+              lost |= mine_of >> q & 1u ? none : 0u;
+              past = past || ((mine_of >> q & 1u) && j < rows && v >= kLoraMost);
+            }
+            if (lost != 0 || __any_sync(0xffffffffu, past)) {
+              __syncwarp();
+#pragma unroll 1
+              for (int q = 0; q < 16; ++q) {  // short: it is read from memory when it is first needed
+                uint32_t one;
+                tmem_ld_32x32b_x1(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c + q, one);
+                tmem_ld_wait();
+                const LoraRounded t = lora_round(__uint_as_float(one) * scale);
+                if (j >= rows || !(mine_of >> q & 1u)) continue;
+                if (t.e != 0) misfit |= 1u << ((t0 + c) >> 5);
+                if ((lane & 7) == 0) p.exps[static_cast<int64_t>(m + q) * groups + ((j0 + j) >> 3)] = static_cast<signed char>(t.e);
+                dst[q * p.rank] = t.y;
+              }
+              __syncwarp();
+            }
+          }
         }
+        if (powers) note(adapter, misfit);
         tcgen05_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(acc_empty_bar);
@@ -352,24 +417,49 @@ __global__ void __launch_bounds__(LoraShrinkCfg::THREADS, 1)
       }
       ready = mbar_wait_cluster(part_full_bar, local & 1, abort_flag, p.wait_budget_ns, 0xd8);
       if (!__all_sync(0xffffffffu, ready)) break;
-      for (int it = e; it < mine * rows; it += 128) {
-        const int four = it / rows, row = it - four * rows;
-        float4 s = recv[four * p.a_rows + row];
-        for (int q = 1; q < p.splits; ++q) {
+      for (int it = e; it - lane < mine * rows; it += 128) {
+        const bool in = it < mine * rows;
+        const int four = in ? it / rows : 0, row = it - four * rows;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int q = 0; in && q < p.splits; ++q) {
           const float4 x = recv[(q * share + four) * p.a_rows + row];
-          s.x += x.x;
-          s.y += x.y;
-          s.z += x.z;
-          s.w += x.w;
+          s.x = q == 0 ? x.x : s.x + x.x;
+          s.y = q == 0 ? x.y : s.y + x.y;
+          s.z = q == 0 ? x.z : s.z + x.z;
+          s.w = q == 0 ? x.w : s.w + x.w;
         }
-        const float v[4] = {s.x, s.y, s.z, s.w};
+        const float v[4] = {s.x * scale, s.y * scale, s.z * scale, s.w * scale};
         const int m = m0 + t0 + (four * p.splits + rank) * 4;
+        unsigned short* dst = static_cast<unsigned short*>(p.t) + static_cast<int64_t>(m) * p.rank + j0 + row;
+        signed char* at = p.exps + static_cast<int64_t>(m) * groups + ((j0 + row) >> 3);
+        unsigned own = 0, odd = 0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (m + q < p.M && __ldg(p.index + m + q) == adapter)
-            static_cast<unsigned short*>(p.t)[static_cast<int64_t>(m + q) * p.rank + j0 + row] = round_16(v[q] * scale, p.bf16 != 0);
+        for (int q = 0; q < 4; ++q) {
+          const bool mine_q = in && m + q < p.M && __ldg(p.index + m + q) == adapter;
+          own |= mine_q ? 1u << q : 0u;
+          if (mine_q) dst[q * p.rank] = round_16(v[q], BF16);
+          if (!powers) continue;
+          if (mine_q && (lane & 7) == 0) at[q * groups] = 0;
+          // Rows of A come in eights: eight lanes have the same token.
+          const unsigned normal = __ballot_sync(0xffffffffu, !mine_q || fabsf(v[q]) >= kLoraLeast);
+          odd |= (normal - 0x01010101u) & ~normal & 0x80808080u;
+          odd |= mine_q && fabsf(v[q]) >= kLoraMost ? 1u : 0u;
+        }
+        if (powers && __any_sync(0xffffffffu, odd != 0)) {
+          __syncwarp();
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const LoraRounded t = lora_round(q == 0 ? v[0] : q == 1 ? v[1] : q == 2 ? v[2] : v[3]);
+            if (!(own >> q & 1u)) continue;
+            if (t.e != 0) misfit |= 1u << ((m - m0) >> 5);
+            if ((lane & 7) == 0) at[q * groups] = static_cast<signed char>(t.e);
+            dst[q * p.rank] = t.y;
+          }
+          __syncwarp();
+        }
       }
       __syncwarp();
+      if (powers) note(adapter, misfit);
       if (lane == 0)
         for (int q = 0; q < p.splits; ++q) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(part_empty_bar), q));
       ++local;
@@ -394,11 +484,12 @@ struct LoraRowsParams {
   const int* index;
   const float* scale;  // of each adapter, or nullptr
   void* t;
+  signed char* exps;   // fp16: T's powers, of each row and eight ranks
   int64_t ldx, lda, stride_a;
   int K, rank, adapters;
 };
 
-constexpr int kLoraRowsWarps = 8;
+constexpr int kLoraRowsWarps = 8;  // the ranks that share a power
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLoraRowsWarps * 32) lora_rows_kernel(const LoraRowsParams p) {
@@ -407,12 +498,24 @@ __global__ void __launch_bounds__(kLoraRowsWarps * 32) lora_rows_kernel(const Lo
   const int lane = threadIdx.x & 31, m = blockIdx.x;
   const int j = blockIdx.y * kLoraRowsWarps + (threadIdx.x >> 5);
   const int adapter = __ldg(p.index + m);
-  if (adapter < 0 || adapter >= p.adapters || j >= p.rank) return;
+  if (adapter < 0 || adapter >= p.adapters || j >= p.rank) return;  // the whole block: ranks come in eights
   const unsigned short* x = static_cast<const unsigned short*>(p.x) + m * p.ldx;
   const unsigned short* a = static_cast<const unsigned short*>(p.a) + adapter * p.stride_a + j * p.lda;
   const float scale = p.scale != nullptr ? __ldg(p.scale + adapter) : 1.0f;
   const float sum = lora_dot<BF16, 4>(a, x, p.K, lane);
-  if (lane == 0) static_cast<unsigned short*>(p.t)[static_cast<int64_t>(m) * p.rank + j] = round_16(sum * scale, BF16);
+  const float v = sum * scale;
+  unsigned short y;
+  if (!BF16) {
+    __shared__ float values[kLoraRowsWarps];
+    if (lane == 0) values[threadIdx.x >> 5] = v;
+    __syncthreads();
+    const LoraRounded r = lora_round(values[lane & 7]);
+    y = __shfl_sync(0xffffffffu, r.y, threadIdx.x >> 5);  // this warp's value's
+    if (threadIdx.x == 0) p.exps[static_cast<int64_t>(m) * (p.rank >> 3) + blockIdx.y] = static_cast<signed char>(r.e);
+  } else {
+    y = round_16(v, true);
+  }
+  if (lane == 0) static_cast<unsigned short*>(p.t)[static_cast<int64_t>(m) * p.rank + j] = y;
 }
 
 }  // namespace tg
