@@ -562,8 +562,9 @@ TG_API tg_status tg_gated_i8(const void *A, const float *a_scale, const void *Wg
  * row strides of their own, on any 2-byte boundary.  ends: G 32-bit integers in
  * DEVICE memory, not decreasing, at most M: groups may be empty, and rows behind
  * the last end belong to no group.  They are read by the kernels, never by the
- * host, so a captured graph may be replayed with other groups.  Values that
- * break the rule give wrong rows, but no access outside a matrix.
+ * host, so a captured graph may be replayed with other groups.  An end that
+ * breaks the rule counts as the greatest before it, or as M: a row never belongs to
+ * two groups, and no access leaves a matrix.
  *
  * Rows that belong to no group are left alone in Y and dX, or set to +0 with
  * options->rest = 1; nothing in them reaches a result.  dW_g of an empty group is +0.  Sums are

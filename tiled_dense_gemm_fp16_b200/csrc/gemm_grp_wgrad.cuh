@@ -102,7 +102,7 @@ struct GrpWgradWalk {
     f.k_blk = wide == 8 ? in >> 3 : quick_div(in, wide, inv_last);
     f.n_blk = 8 * s + in - f.k_blk * wide;
     f.lo = uniform(ends[g]);
-    f.rows = max(0, uniform(ends[g + 1]) - f.lo);
+    f.rows = uniform(ends[g + 1]) - f.lo;
     return f;
   }
 };
@@ -159,8 +159,19 @@ __global__ void __launch_bounds__(GrpWgradCfg::THREADS, 1)
   tcgen05_fence_after_sync();
   grid_dependency_wait();
   grid_launch_dependents();
-  for (int g = threadIdx.x; g <= p.groups; g += Cfg::THREADS) ends[g] = grp_end(p.ends, g - 1, p.M);
-  __syncthreads();
+  bool rising = true;
+  for (int g = threadIdx.x; g <= p.groups; g += Cfg::THREADS) {
+    ends[g] = grp_end(p.ends, g - 1, p.M);
+    rising = rising && ends[g] >= grp_end(p.ends, g - 2, p.M);
+  }
+  if (!__syncthreads_and(rising)) {
+    if (warp == Cfg::ZERO_WARP)
+      for (int g = lane, top = 0; g - lane <= p.groups; g += 32) {
+        const int lo = grp_raise(g <= p.groups ? ends[g] : p.M, top, lane);
+        if (g <= p.groups) ends[g] = lo;
+      }
+    __syncthreads();
+  }
   const uint32_t tmem_base = *tmem_slot;
 
   if (warp == 0) {

@@ -389,7 +389,9 @@ struct GrpZeroParams {
 __global__ void __launch_bounds__(256) grp_zero_kernel(const GrpZeroParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int rows = p.rest ? p.M : grp_end(p.ends, p.groups - 1, p.M);
+  int rows = p.rest ? p.M : 0;  // the greatest end
+  for (int g = threadIdx.x & 31; !p.rest && g < p.groups; g += 32) rows = max(rows, grp_end(p.ends, g, p.M));
+  rows = __reduce_max_sync(0xffffffffu, rows);
   const int64_t items = static_cast<int64_t>(rows) * p.cols;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < items;
        i += static_cast<int64_t>(gridDim.x) * blockDim.x) {

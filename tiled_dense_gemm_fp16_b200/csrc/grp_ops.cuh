@@ -93,12 +93,25 @@ __device__ __forceinline__ int quick_div(int n, int d, float inv) {
 
 // Group g owns rows [ends[g - 1], ends[g]) of X (from 0 for g = 0).  The ends
 // are data on the device, so nothing on the host depends on them and a captured
-// graph may be replayed with others.  They are clamped to [0, M], and a group
-// whose end lies before its start is empty: whatever they hold, no access leaves
-// a matrix.  Without ends (one weight for all rows) there is one group.
+// graph may be replayed with others.  They are clamped to [0, M] and raised to the
+// greatest before them (grp_raise): whatever they hold, no access leaves a matrix,
+// each row has one group, and the tiles of all groups are no more than the
+// host has counted in 32 bits.  Without ends (one weight for all rows) there is one group.
 __device__ __forceinline__ int grp_end(const int* ends, int g, int M) {
   if (g < 0) return 0;
   return ends == nullptr ? M : max(0, min(__ldg(ends + g), M));
+}
+
+// The starts of 32 groups in turn, a lane each, raised: `top` is that of the group
+// before.  As a rule none has to be.
+__device__ __forceinline__ int grp_raise(int lo, int& top, int lane) {
+  const int before = __shfl_up_sync(0xffffffffu, lo, 1);
+  if (!__all_sync(0xffffffffu, lo >= (lane == 0 ? top : before))) {
+    lo = max(lo, top);
+    for (int d = 1; d < 32; d <<= 1) lo = max(lo, __shfl_up_sync(0xffffffffu, lo, d));  // of lane < d: its own
+  }
+  top = __shfl_sync(0xffffffffu, lo, 31);
+  return lo;
 }
 
 // A group's rows as tiles of `most`, whose last two share what a short last one
@@ -138,12 +151,12 @@ __host__ __device__ constexpr int grp_plan_align(int groups) { return (grp_plan_
 // By one warp; the others wait for it.
 __device__ __forceinline__ void grp_make_plan(GrpPlan plan, const int* ends, int G, int M, int most, int col_tiles,
                                               bool rest, int lane) {
-  int before = 0;
+  int before = 0, top = 0;
   for (int base = 0; base <= G; base += 32) {
     const int g = base + lane;
-    int lo = 0, tiles = 0;
+    const int lo = grp_raise(g <= G ? grp_end(ends, g - 1, M) : M, top, lane);
+    int tiles = 0;
     if (g <= G) {
-      lo = grp_end(ends, g - 1, M);
       const int hi = g < G ? grp_end(ends, g, M) : (rest ? M : lo);
       tiles = hi > lo ? (hi - lo + most - 1) / most * col_tiles : 0;
     }
