@@ -627,8 +627,8 @@ TG_API int64_t tg_grouped_backward_workspace_size(const void *dY, const void *X,
  * B_a (the tensor cores read it so), the sum of all terms once more.  In fp16 that
  * first rounding knows no range: eight ranks of a row whose largest magnitude is not
  * in [2^-14, 2^15) are held times a power of two, so that each inner product is off
- * by at most 2^-11 of itself or of the largest of its eight, from 2^-111 to 2^128 (in
- * bf16 by 2^-8 of itself).  Such rows are slower.  Each row's result
+ * by at most 2^-11 of itself or of the largest of 32 neighbouring ones, from 2^-111 to
+ * 2^128 (in bf16 by 2^-8 of itself).  Such rows are slower.  Each row's result
  * depends on its own values and its own adapter only: infinities and NaN in other
  * rows or other adapters do not reach it.  Equal inputs give equal bits.
  *

@@ -94,11 +94,12 @@ __device__ __forceinline__ int ld_global_s32(const int* p) {
 // 1e-7 lose its digits, where B T is an ordinary number.  So eight ranks of a row
 // whose largest finite value is outside fp16's normal numbers below 2^15 are divided
 // by the power of two that brings it to [2^15, 2^16), and its exponent stands beside
-// T: values from 2^15 on say that there may be one.  lora_part then multiplies the sums
-// of eight by it; 32 tokens of one adapter of which one has a power do not go through
+// T: values from 2^15 on say that there may be one.  lora_part then multiplies its fp32
+// sums by it; 32 tokens of one adapter of which one has a power do not go through
 // the main accumulator, whose other terms know none.  All others keep their bits.  A
-// value of T is off by half a step, 2^-11 relative to it or to the largest of its
-// eight.  (A power for every row would close the accumulator's way to all.)
+// value of T is off by half a step, 2^-11 relative to it or to the largest of the 32
+// ranks that are summed with it.  (A power for every row would close the accumulator's way to
+// all: 8192 rows of 8 requests through 8192 x 4096, rank 64, 425 us, where all have one 957.)
 constexpr float kLoraLeast = 6.103515625e-05f, kLoraMost = 32752.0f;  // below: still below 2^15 once rounded
 constexpr float kLoraNothing = 3.85185988877447e-34f;                 // 2^-111: below, B T is far below fp16, and T is 0
 __device__ __forceinline__ bool lora_fits(float v) { return fabsf(v) >= kLoraLeast && fabsf(v) < kLoraMost; }
@@ -135,6 +136,17 @@ __device__ __forceinline__ int ld_s8(const signed char* p) {  // of any memory
   int v;
   asm volatile("ld.s8 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
+}
+// Eight values of fp16 times 2^e, e <= 0.
+__device__ __forceinline__ void lora_scale(uint4& w, int e) {
+  const float f = lora_power(max(e, -126));
+  uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = unpack_16(v[k], false);
+    v[k] = pack_f16(x.x * f, x.y * f);
+  }
+  w = make_uint4(v[0], v[1], v[2], v[3]);
 }
 // The kind of 32 tokens, as the main product takes them: in one run only what fits the accumulator.
 template <bool BF16>
@@ -185,31 +197,58 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
 }
 
 constexpr int kLoraTokens = 16;
-// lora_part where T carries powers (fp16): a lane a column, eight ranks at a time in
-// fp32.  Such values are rare, and this form leaves the other's registers alone (two
-// forms on the tensor cores, or one with the powers in it, made the pair kernel spill:
-// 1049 rows of 40 requests 60-66 us, so 58).
+// lora_part where T carries powers (fp16): of 32 ranks a token's four groups are brought
+// to the largest power among them (those without a value have no say), and the fp32
+// product of these ranks takes it.  Such values are rare, so this form goes over 16 columns
+// and 8 tokens at a time and leaves the other's registers alone: all at once the two made
+// the pair kernel spill (1049 rows of 40 requests 60-66 us, so 58).
 __device__ __forceinline__ void lora_part_powers(const LoraParams& l, const void* T, const signed char* exps, int mine, int m0, int n0,
                                                  int N, float* out, int pitch, int lane) {
-  const int groups = l.rank >> 3, n = n0 + lane;
-  for (int tok = 0; tok < kLoraTokens; ++tok) {
-    const int adapter = __shfl_sync(0xffffffffu, mine, tok);
-    float sum = 0.0f;
-    if (adapter >= 0 && n < N) {
-      const unsigned short* b = static_cast<const unsigned short*>(l.b) + adapter * l.stride_b + n * l.ldb;
-      const unsigned short* t = static_cast<const unsigned short*>(T) + static_cast<int64_t>(m0 + tok) * l.rank;
-      const signed char* e = exps + static_cast<int64_t>(m0 + tok) * groups;
+  const int row = lane >> 2, q = lane & 3;
+#pragma unroll 1
+  for (int part = 0; part < 4; ++part) {
+    const int col = (part & 1) * 16, tok = (part >> 1) * 8;
+    const int own = __shfl_sync(0xffffffffu, mine, tok + row);  // of this thread's row of T
+    const int64_t m = m0 + tok + row;
+    const unsigned short* t = static_cast<const unsigned short*>(T) + m * l.rank;
+    const signed char* ex = exps + m * (l.rank >> 3);
+    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    unsigned left = __ballot_sync(0xffffffffu, lane >= tok && lane < tok + 8 && mine >= 0);
+    while (left != 0) {
+      const int adapter = __shfl_sync(0xffffffffu, mine, __ffs(left) - 1);
+      const unsigned mask = __ballot_sync(0xffffffffu, mine == adapter) & left;
+      left &= ~mask;
+      const unsigned short* b = static_cast<const unsigned short*>(l.b) + adapter * l.stride_b + (n0 + col + row) * l.ldb;
+      float p[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 2
-      for (int g = 0; g < groups; ++g) {
-        const uint4 u = __ldg(reinterpret_cast<const uint4*>(b + 8 * g)), v = ld_v4(t + 8 * g);
-        float2 s = mul2(unpack_16(u.x, false), unpack_16(v.x, false));
-        s = fma2(unpack_16(u.y, false), unpack_16(v.y, false), s);
-        s = fma2(unpack_16(u.z, false), unpack_16(v.z, false), s);
-        s = fma2(unpack_16(u.w, false), unpack_16(v.w, false), s);
-        sum = fmaf(s.x + s.y, lora_power(ld_s8(e + g)), sum);
+      for (int at = q * 8; at - q * 8 < l.rank; at += 32) {
+        uint4 u = make_uint4(0u, 0u, 0u, 0u), v = u, w = u;
+        int top = -126;
+        if (at < l.rank && n0 + col + row < N) u = __ldg(reinterpret_cast<const uint4*>(b + at));
+        if (at < l.rank && n0 + col + row + 8 < N) v = __ldg(reinterpret_cast<const uint4*>(b + 8 * l.ldb + at));
+        if (at < l.rank && own >= 0) {
+          w = ld_v4(t + at);
+          top = ld_s8(ex + (at >> 3));
+        }
+        if (((w.x | w.y | w.z | w.w) & 0x7fff7fffu) == 0u) top = -126;
+        const int power = top;
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        lora_scale(w, power - top);
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_16816<false>(s, u.x, v.x, u.y, v.y, w.x, w.y);
+        mma_16816<false>(s, u.z, v.z, u.w, v.w, w.z, w.w);
+        // Columns of the product are tokens 2 q and 2 q + 1.
+        const float up0 = lora_power(__shfl_sync(0xffffffffu, top, 8 * q)), up1 = lora_power(__shfl_sync(0xffffffffu, top, 8 * q + 4));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = fmaf(s[e], e & 1 ? up1 : up0, p[e]);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (mask >> (tok + 2 * q + (e & 1)) & 1u) d[e] = p[e];
     }
-    out[lane * pitch + tok] = sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) out[(col + 8 * (e >> 1) + row) * pitch + tok + 2 * q + (e & 1)] = d[e];
   }
   __syncwarp();
 }
