@@ -295,7 +295,6 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
   GrpNarrowParams p;
   std::memset(&p, 0, sizeof p);
   if (!grp_fill(f, maps, p.g, Cfg::PANEL, tokens)) return TG_ERR_LAUNCH;
-  p.g.vec = f.c.rows_on(8) ? 1 : 0;
   p.g.idesc = make_idesc_ff(kFfF16, f.bf16, Cfg::PANEL, 0, f.transposed, false);
   p.g.super = 8;
   if (!grp_countable(p.g, tokens)) return TG_ERR_INVALID_ARG;
