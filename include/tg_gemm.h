@@ -630,7 +630,9 @@ TG_API int64_t tg_grouped_backward_workspace_size(const void *dY, const void *X,
  * by at most 2^-11 of itself or of the largest of 32 neighbouring ones, from 2^-111 to
  * 2^128 (in bf16 by 2^-8 of itself).  Such rows are slower.  Each row's result
  * depends on its own values and its own adapter only: infinities and NaN in other
- * rows or other adapters do not reach it.  Equal inputs give equal bits.
+ * rows or other adapters do not reach it.  Equal calls give equal bits; a row's last
+ * bits may change with the number of rows and with whether those beside it share its
+ * adapter, which decide how its terms are summed.
  *
  * rank is a multiple of 8, at most 512, or 0 (no adapters); rows of A and B, and their matrices,
  * start on 16-byte boundaries; X, W and Y may lie on any 2-byte boundary.  Sizes as

@@ -8,7 +8,8 @@
 // it adds them in rank order, so results do not depend on timing.  The kernel is
 // persistent: which groups have rows is known on the device only, so each cluster
 // walks the tiles there are, its loads running ahead into the next tile while the
-// partials of the last one are added.  Adapters' T of one token is made here too
+// partials of the last one are added.  Adapters' T is made here too where it is a
+// value a warp: one or two tokens, 8 values with clusters of two CTAs, 16 with four
 // (grp_lora_own_t).
 //
 // Bound by reading the weights that have rows: 512 rows in 60 of 64 groups of 2048 x

@@ -257,7 +257,10 @@ int grp_resident_clusters(int splits, DeviceInfo* info) {
   return known;
 }
 
-// Estimated times in us.  The pair kernel: a wave of tiles takes 0.222 a k-block, 5.2 before and after.
+// Estimated times in us.  The pair kernel: a wave of tiles takes 0.222 a k-block, 5.2
+// before and after.  The rate of the weights flatters it: it reads them at 4.5 TB/s (64
+// groups of 128 rows) or 3.3 (16 of 256, cold), which shifts the choice by some groups'
+// worth towards it where the weights bound both.
 double grp_pair_us(const GrpProduct& f, int64_t live, int k_blocks, DeviceInfo* info) {
   const int64_t rows = f.a.rows, pairs = info->sm_count / 2;
   const int64_t tiles = ((rows + 255) / 256 > live ? (rows + 255) / 256 : live) * ((f.out + 255) / 256);
@@ -336,14 +339,16 @@ tg_status launch_grp_narrow(const GrpProduct& f, int tokens, int splits, cudaStr
 // 128 with long sums, take the narrow kernel, whose CTAs share that part as well (us,
 // narrow / pair: 64 rows through 4096 x 4096, rank 64, 64 adapters 36 / 60, one 23 / 24;
 // 128 rows 67 / 88 and 24 / 24; 96 rows through 512 x 512, rank 16, 32 / 43 and 18 / 13;
-// 128 rows 38 / 37 and 22 / 12).
+// 128 rows 38 / 37 and 22 / 12).  Where rows share one adapter that is the slower choice
+// from about 96 rows on, which only the device could know.
 bool grp_lora_narrow(const GrpProduct& f) { return f.a.rows <= 96 || (f.a.rows <= 128 && f.red > 31 * 64); }
 
 // Splits of its sums then, of which there are at least two where it makes T itself.
 int grp_lora_splits(const GrpProduct& f) { return f.red > 7 * 64 && f.out <= 40 * 128 ? 4 : 2; }
 
 // Whether that kernel makes T itself, without a kernel before it: where that is a value
-// for each warp that waits for the sums anyway (us, so / with the kernel before: one
+// at most for each warp that waits for the sums anyway, of which a cluster of two CTAs has
+// 8 and one of four 16 (us, so / with the kernel before: one
 // token through 4096 x 4096, rank 16, 12.6 / 13.5; with two values a warp 13.9 / 12.6,
 // four 15 / 12.8).
 bool grp_lora_own_t(const GrpProduct& f) {

@@ -18,8 +18,9 @@
 // there is no list, ring or exchange on the way from the index to T (whole call, one
 // token through 4096 x 4096, rank 16: 14.5 us with tiles, 13.4 so; 64 tokens of 64
 // adapters 29 and 24).  The main product runs meanwhile on the same SMs (it waits for
-// T only when its own sums are under way).  A token of up to 16 ranks goes without
-// either: the narrow kernel's warps make a value each.
+// T only when its own sums are under way).  One token
+// or two with 8 or 16 values of T in all (grp_lora_own_t) go without either: the narrow
+// kernel's warps make a value each.
 //
 // Measured: 8192 rows of 8 requests, K = 4096, rank 64, 29.5 us alone, 2.3 TB/s:
 // bound by the latency of a block's loads.  The main product hides most of it.  fp16's

@@ -46,7 +46,7 @@ def lora(x, w, a, b, index, scale=None, bias=None, out=None, stream=None, worksp
     request next to each other are faster.  ``scale``: (adapters,) float32, or None for 1.  ``bias``: (N,) of x's type.
     rank is a multiple of 8, at most 512, and rows of a and b start on 16-byte boundaries (pad a rank with zeros
     once); x, w and ``out`` may have any row stride.  x @ a[r]^T, scaled, is rounded to the 16-bit type (in float16 times
-    a power of two where its range needs one; such rows are slower); sums are 32-bit.  A row depends on its own adapter only.  For serving: nothing is recorded for autograd.  ``workspace``
+    a power of two where its range needs one; such rows are slower); sums are 32-bit.  No value of another request or adapter reaches a row.  For serving: nothing is recorded for autograd.  ``workspace``
     ("auto" or a uint8 CUDA tensor) holds those inner products; calls whose work may overlap need one each."""
     if stream is None:
         return _calls.lora(x, w, a, b, index, scale, bias, out, workspace)
