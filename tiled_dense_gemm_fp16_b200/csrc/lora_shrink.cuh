@@ -374,12 +374,13 @@ __global__ void __launch_bounds__(256, 2)
                 tmem_ld_32x32b_x1(tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c + q, one);
                 tmem_ld_wait();
                 const LoraRounded t = lora_round(__uint_as_float(one) * scale);
-                if (j >= rows || !(mine_of >> q & 1u)) continue;
-                if (t.e != 0) misfit |= 1u << ((t0 + c) >> 5);
-                if ((lane & 7) == 0) p.exps[static_cast<int64_t>(m + q) * groups + ((j0 + j) >> 3)] = static_cast<signed char>(t.e);
-                dst[q * p.rank] = t.y;
+                if (j < rows && (mine_of >> q & 1u)) {
+                  if (t.e != 0) misfit |= 1u << ((t0 + c) >> 5);
+                  if ((lane & 7) == 0) p.exps[static_cast<int64_t>(m + q) * groups + ((j0 + j) >> 3)] = static_cast<signed char>(t.e);
+                  dst[q * p.rank] = t.y;
+                }
+                __syncwarp();  // the next load wants the whole warp
               }
-              __syncwarp();
             }
           }
         }
@@ -451,12 +452,13 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll 1
           for (int q = 0; q < 4; ++q) {
             const LoraRounded t = lora_round(q == 0 ? v[0] : q == 1 ? v[1] : q == 2 ? v[2] : v[3]);
-            if (!(own >> q & 1u)) continue;
-            if (t.e != 0) misfit |= 1u << ((m - m0) >> 5);
-            if ((lane & 7) == 0) at[q * groups] = static_cast<signed char>(t.e);
-            dst[q * p.rank] = t.y;
+            if (own >> q & 1u) {
+              if (t.e != 0) misfit |= 1u << ((m - m0) >> 5);
+              if ((lane & 7) == 0) at[q * groups] = static_cast<signed char>(t.e);
+              dst[q * p.rank] = t.y;
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       __syncwarp();
